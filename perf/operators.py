@@ -16,8 +16,9 @@ Two families, both on (tokens, channels) matrices with one row per token:
   quantisation of a matrix along its rows, its columns or both; reading back; and the
   product A B^T of two quantised matrices.
 
-A quantised matrix with K values a row holds K rounded up to 128 of them (zeros at the
-end): 64 code bytes (the first value of a pair in the low half) and 4 scale bytes per 128.
+A quantised row of K values holds K rounded up to 128 of them (zeros at the end): 64 code
+bytes per 128, the first value of a pair in the low half. Its scale bytes, one per 32
+values, are padded with zeros to a multiple of 16.
 """
 from __future__ import annotations
 
@@ -116,8 +117,8 @@ def _activations(g, rows, cols):
     return x
 
 
-def _pad128(k):
-    return (k + 127) // 128 * 128
+def _pad(k, unit):
+    return (k + unit - 1) // unit * unit
 
 
 def _quantized(g, rows, cols, weights):
@@ -158,12 +159,12 @@ def prepare(case, seed):
         r, c = case["rows"], case["cols"]
         st["x"] = _activations(g, r, c).to(DTYPE[case["src"]])
         if case["rowwise"]:
-            st["q"] = torch.empty(r, _pad128(c) // 2, dtype=torch.uint8, device=DEV)
-            st["s"] = torch.empty(r, _pad128(c) // 32, dtype=torch.uint8, device=DEV)
+            st["q"] = torch.empty(r, _pad(c, 128) // 2, dtype=torch.uint8, device=DEV)
+            st["s"] = torch.empty(r, _pad(c, 512) // 32, dtype=torch.uint8, device=DEV)
             st["v"] = torch.empty(r, c, dtype=torch.bfloat16, device=DEV)
         if case["colwise"]:
-            st["q_t"] = torch.empty(c, _pad128(r) // 2, dtype=torch.uint8, device=DEV)
-            st["s_t"] = torch.empty(c, _pad128(r) // 32, dtype=torch.uint8, device=DEV)
+            st["q_t"] = torch.empty(c, _pad(r, 128) // 2, dtype=torch.uint8, device=DEV)
+            st["s_t"] = torch.empty(c, _pad(r, 512) // 32, dtype=torch.uint8, device=DEV)
             st["v_t"] = torch.empty(c, r, dtype=torch.bfloat16, device=DEV)
     elif op == "dequantize":
         st["q"], st["s"] = _quantized(g, case["rows"], case["cols"], True)
@@ -180,7 +181,7 @@ def prepare(case, seed):
 def _plain_quantize(x):
     """E2M1 codes and E8M0 scales of x's rows: blocks of 32, the scale 2^(floor(log2 amax) - 2), values over 6 cut."""
     rows, cols = x.shape
-    kp = _pad128(cols)
+    kp = _pad(cols, 128)
     b = torch.nn.functional.pad(x.float(), (0, kp - cols)).view(rows, kp // 32, 32)
     amax = b.abs().amax(dim=2)
     e = (torch.frexp(amax).exponent - 3).clamp_(min=-127)
@@ -189,7 +190,8 @@ def _plain_quantize(x):
     a = v.abs()
     code = ((a > 0.25).to(torch.uint8) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0))
     code = (code + 8 * torch.signbit(v)).to(torch.uint8).view(rows, kp)
-    return code[:, 0::2] | (code[:, 1::2] << 4), (e + 127).to(torch.uint8)
+    s = torch.nn.functional.pad(e + 127, (0, _pad(cols, 512) // 32 - kp // 32))
+    return code[:, 0::2] | (code[:, 1::2] << 4), s.to(torch.uint8)
 
 
 def _plain_values(q, s, cols):
@@ -197,7 +199,7 @@ def _plain_values(q, s, cols):
     table = torch.tensor(GRID + tuple(-v for v in GRID), device=q.device)
     pairs = torch.stack((table[(q & 15).int()], table[(q >> 4).int()]), dim=2)
     v = pairs.view(q.shape[0], -1, 32)
-    v = torch.ldexp(v, s.int().unsqueeze(2) - 127)
+    v = torch.ldexp(v, s[:, :v.shape[1]].int().unsqueeze(2) - 127)
     return v.reshape(q.shape[0], -1)[:, :cols]
 
 
