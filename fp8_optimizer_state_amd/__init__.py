@@ -22,6 +22,7 @@ import torch
 
 FMT_E4M3 = 0
 FMT_E5M2 = 1
+FMT_MX4 = 2
 FMT_NO_EXPAND = 0x100
 
 COAT_OK, COAT_EINVAL, COAT_EALIGN, COAT_EHIP, COAT_ERANGE = 0, -1, -2, -3, -4
@@ -42,6 +43,12 @@ class _Tensor(ctypes.Structure):
                 ("grads", ctypes.c_void_p), ("m_q", ctypes.c_void_p), ("m_s", ctypes.c_void_p),
                 ("m_k", ctypes.c_void_p), ("v_q", ctypes.c_void_p), ("v_s", ctypes.c_void_p),
                 ("v_k", ctypes.c_void_p), ("n", ctypes.c_int64)]
+
+
+class _Border(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("rows_per_gate", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("scale", ctypes.c_float), ("post", ctypes.c_int32),
+                ("stream_type", ctypes.c_int32), ("param_type", ctypes.c_int32), ("grad_type", ctypes.c_int32)]
 
 
 class _Plan(ctypes.Structure):
@@ -77,13 +84,28 @@ def lib() -> ctypes.CDLL:
     L.coat_fp8_decode.argtypes = [P, i64, i32, P, P]
     L.coat_fp8_act_quantize.argtypes = [P, i64, i32, i32, P, P, P]
     L.coat_fp8_act_dequantize.argtypes = [P, P, i64, i32, i32, P, P]
+    L.coat_mx4_code_bytes.argtypes = [i64]
+    L.coat_mx4_scale_bytes.argtypes = [i64]
+    L.coat_mx4_quantize.argtypes = [P, i64, i64, i64, i32, P, P, P, P, P]
+    L.coat_mx4_dequantize.argtypes = [P, P, i64, i64, P, i64, i32, P]
+    L.coat_mx4_matmul_workspace_bytes.argtypes = [i64, i64, i64]
+    L.coat_mx4_matmul.argtypes = [P, P, i64, P, P, i64, i64, P, i64, i32, P, ctypes.c_size_t, P]
+    border = ctypes.POINTER(_Border)
+    L.coat_block_norm.argtypes = [border, P, P, P, P, P, P, P, P, P, i32, i32, P]
+    L.coat_block_norm_backward_workspace_bytes.argtypes = [border]
+    L.coat_block_norm_backward.argtypes = [border, P, P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+    for name in ("coat_mx4_code_bytes", "coat_mx4_scale_bytes"):
+        getattr(L, name).restype = i64
+    for name in ("coat_mx4_matmul_workspace_bytes", "coat_block_norm_backward_workspace_bytes"):
+        getattr(L, name).restype = ctypes.c_size_t
     L.coat_strerror.argtypes = [ctypes.c_int]
     L.coat_strerror.restype = ctypes.c_char_p
     L.coat_abi_version.restype = ctypes.c_int
     for name in ("coat_fp8_adamw_step", "coat_multi_plan_init", "coat_fp8_adamw_step_planned",
                  "coat_fp8_adamw_step_multi", "coat_fp8_adamw_step_multi_static", "coat_fp8_quantize", "coat_fp8_dequantize",
                  "coat_fp8_encode", "coat_fp8_decode", "coat_fp8_act_quantize",
-                 "coat_fp8_act_dequantize"):
+                 "coat_fp8_act_dequantize", "coat_mx4_quantize", "coat_mx4_dequantize", "coat_mx4_matmul",
+                 "coat_block_norm", "coat_block_norm_backward"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -197,6 +219,258 @@ def act_dequantize(q, scale, x, *, group: int, fmt: int, stream=None) -> None:
                                        _ptr(scale, torch.float32, act_nscales(n, group), "scale"), n,
                                        group, fmt, _ptr(x, torch.bfloat16, n, "x"), _stream(stream))
     _check(rc, "coat_fp8_act_dequantize")
+
+
+# ---------------------------------------------------------------- layer-input operators
+#
+# These work on (rows, channels) matrices, on the device that holds them: the
+# calls take `stream`, or that device's current stream, and may be made while
+# another device is current.
+
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _float_type(t: torch.Tensor, name: str) -> int:
+    kind = _TYPES.get(t.dtype)
+    if kind is None:
+        raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return kind
+
+
+def _operand(t: torch.Tensor, dtype: torch.dtype, shape, device: torch.device, name: str) -> int:
+    """Address of a tensor without gaps that has this type, shape and device."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU of the other tensors ({device}), got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _matrix(t: torch.Tensor, name: str) -> int:
+    """Elements from row to row of a GPU matrix whose rows have no gaps."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got {t.dim()} dimensions")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if rows > 1 and ld < cols or cols > 1 and step != 1:
+        raise ValueError(f"{name} must have rows without gaps, got strides {t.stride()}")
+    return ld if rows > 1 else max(cols, 1)
+
+
+def _run(device: torch.device, stream, call):
+    """call(stream handle) with `device` current."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors are on {device}")
+    if device.index == torch.cuda.current_device():
+        return call((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+    with torch.cuda.device(device):
+        return call((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+
+
+def _workspace(nbytes: int, workspace: Optional[torch.Tensor], device: torch.device, stream) -> Optional[torch.Tensor]:
+    """The caller's workspace, or one of torch's allocator that lasts until the call's work is done."""
+    if nbytes == 0:
+        return None
+    if workspace is not None:
+        if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+        if workspace.numel() < nbytes:
+            raise ValueError(f"workspace has {workspace.numel()} bytes, the call needs {nbytes}")
+        return workspace
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def mx4_code_bytes(k: int) -> int:
+    """Code bytes of a row of k values in 4-bit form."""
+    return (k + 127) // 128 * 64
+
+
+def mx4_scale_bytes(k: int) -> int:
+    """Scale bytes of a row of k values in 4-bit form."""
+    return (k + 511) // 512 * 16
+
+
+def mx4_empty(rows: int, k: int, device="cuda"):
+    """Uninitialised (q, s) of a quantized matrix: rows of k values."""
+    return (torch.empty(rows, mx4_code_bytes(k), dtype=torch.uint8, device=device),
+            torch.empty(rows, mx4_scale_bytes(k), dtype=torch.uint8, device=device))
+
+
+def _mx4_operand(q: torch.Tensor, s: torch.Tensor, rows: int, k: int, device: torch.device, name: str):
+    return (_operand(q, torch.uint8, (rows, mx4_code_bytes(k)), device, name + "q"),
+            _operand(s, torch.uint8, (rows, mx4_scale_bytes(k)), device, name + "s"))
+
+
+def mx4_quantize(x, q=None, s=None, q_t=None, s_t=None, *, stream=None) -> None:
+    """A bf16 or fp32 matrix -> microscaled 4-bit codes and scale bytes, along its
+    rows (q, s), its columns (q_t, s_t: the transposed matrix), or both in one pass."""
+    ld = _matrix(x, "x")
+    kind = _float_type(x, "x")
+    rows, cols = x.shape
+    if (q is None) != (s is None) or (q_t is None) != (s_t is None) or (q is None and q_t is None):
+        raise ValueError("codes and scales come in pairs: q with s, q_t with s_t, one pair at least")
+    along = (None, None) if q is None else _mx4_operand(q, s, rows, cols, x.device, "")
+    down = (None, None) if q_t is None else (
+        _operand(q_t, torch.uint8, (cols, mx4_code_bytes(rows)), x.device, "q_t"),
+        _operand(s_t, torch.uint8, (cols, mx4_scale_bytes(rows)), x.device, "s_t"))
+    rc = _run(x.device, stream, lambda st: lib().coat_mx4_quantize(x.data_ptr(), rows, cols, ld, kind, *along, *down, st))
+    _check(rc, "coat_mx4_quantize")
+
+
+def mx4_dequantize(q, s, x, *, stream=None) -> None:
+    """Microscaled 4-bit codes and scale bytes -> a bf16 or fp32 matrix."""
+    ld = _matrix(x, "x")
+    kind = _float_type(x, "x")
+    rows, cols = x.shape
+    qp, sp = _mx4_operand(q, s, rows, cols, x.device, "")
+    rc = _run(x.device, stream, lambda st: lib().coat_mx4_dequantize(qp, sp, rows, cols, x.data_ptr(), ld, kind, st))
+    _check(rc, "coat_mx4_dequantize")
+
+
+def mx4_matmul(a_q, a_s, b_q, b_s, y, *, workspace=None, stream=None) -> None:
+    """y (m, n) = A B^T of two quantized matrices, A m x k and B n x k; y bf16 or fp32.
+
+    k is taken from the codes, rounded up to 128 as they are. ``workspace``: uint8,
+    at least ``mx4_matmul_workspace_bytes`` long; without one the call takes one
+    from torch's allocator."""
+    ld = _matrix(y, "y")
+    kind = _float_type(y, "y")
+    m, n = y.shape
+    if a_q.dim() != 2:
+        raise ValueError("a_q must be a matrix")
+    k = a_q.shape[1] * 2
+    ap, asp = _mx4_operand(a_q, a_s, m, k, y.device, "a_")
+    bp, bsp = _mx4_operand(b_q, b_s, n, k, y.device, "b_")
+    nbytes = lib().coat_mx4_matmul_workspace_bytes(m, n, k)
+    ws = _workspace(nbytes, workspace, y.device, stream)
+    rc = _run(y.device, stream, lambda st: lib().coat_mx4_matmul(
+        ap, asp, m, bp, bsp, n, k, y.data_ptr(), ld, kind, ws.data_ptr() if ws is not None else None, nbytes, st))
+    _check(rc, "coat_mx4_matmul")
+
+
+def mx4_matmul_workspace_bytes(m: int, n: int, k: int) -> int:
+    return lib().coat_mx4_matmul_workspace_bytes(m, n, k)
+
+
+def _border(ref, w_post, w_pre, gate, rows_per_gate, scale, eps, post, res_type):
+    """The border's description, its parameters' type and the gate's shape."""
+    rows, cols = ref.shape
+    dtype = None
+    for t in (w_post, w_pre, gate):
+        if t is not None:
+            if dtype is not None and t.dtype is not dtype:
+                raise ValueError(f"w_post, w_pre and gate must have one type, got {dtype} and {t.dtype}")
+            dtype = t.dtype
+    kind = 0
+    if dtype is not None:
+        kind = _TYPES.get(dtype)
+        if kind is None:
+            raise ValueError(f"w_post, w_pre and gate must be bfloat16 or float32, got {dtype}")
+    if rows_per_gate is None:
+        rows_per_gate = rows
+    rpg = max(1, int(rows_per_gate)) if rows == 0 else int(rows_per_gate)
+    if rpg < 1:
+        raise ValueError("rows_per_gate must be at least 1")
+    gates = (rows + rpg - 1) // rpg
+    return _Border(rows, cols, rpg, eps, scale, 1 if post else 0, res_type, kind, 0), dtype, (gates, cols)
+
+
+def block_norm(y, r, r_out=None, h=None, *, w_post=None, w_pre=None, gate=None, rows_per_gate=None, scale=1.0,
+               eps=1e-5, post=None, q=None, q_scale=None, group: int = 0, fmt: int = 0, stream=None) -> None:
+    """The border between two blocks: r_out = r + scale gate (w_post N(y)), h = w_pre N(r_out),
+    N(a) = a / sqrt(mean(a^2) + eps) over the channels.
+
+    y None: no addition, r itself is normalised. post: whether y is normalised
+    (default: if w_post is given). gate: (ceil(rows / rows_per_gate), channels), token
+    t takes row t // rows_per_gate (default: one row for all). The layer input goes to
+    h (bf16) and/or to q, q_scale in a stored form: FP8 codes and fp32 scales as
+    ``act_quantize`` writes them for the bf16 h (group 16 .. 512, dividing the
+    channels), or with fmt FMT_MX4 as ``mx4_quantize`` does along the rows."""
+    if r.dim() != 2:
+        raise ValueError("r must be a matrix (tokens, channels)")
+    if post is None:
+        post = w_post is not None
+    shape, dev = r.shape, r.device
+    rows, cols = shape
+    b, pt, gate_shape = _border(r, w_post, w_pre, gate, rows_per_gate, scale, eps, post, _float_type(r, "r"))
+    bf16 = torch.bfloat16
+    qp = sp = None
+    if q is not None or q_scale is not None:
+        if q is None or q_scale is None:
+            raise ValueError("q and q_scale come as a pair")
+        if fmt == FMT_MX4:
+            group = 32
+            qp, sp = _mx4_operand(q, q_scale, rows, cols, dev, "")
+        else:
+            if group < 1 or cols % group:
+                raise ValueError(f"group {group} must divide the {cols} channels")
+            qp = _operand(q, torch.uint8, shape, dev, "q")
+            sp = _operand(q_scale, torch.float32, (rows, cols // group), dev, "q_scale")
+    args = (_operand(y, bf16, shape, dev, "y") if y is not None else None,
+            _operand(r, r.dtype, shape, dev, "r"),
+            _operand(w_post, pt, (cols,), dev, "w_post") if w_post is not None else None,
+            _operand(w_pre, pt, (cols,), dev, "w_pre") if w_pre is not None else None,
+            _operand(gate, pt, gate_shape, dev, "gate") if gate is not None else None,
+            _operand(r_out, r.dtype, shape, dev, "r_out") if r_out is not None else None,
+            _operand(h, bf16, shape, dev, "h") if h is not None else None)
+    rc = _run(dev, stream, lambda st: lib().coat_block_norm(ctypes.byref(b), *args, qp, sp, group, fmt, st))
+    _check(rc, "coat_block_norm")
+
+
+def block_norm_backward(y, r_out, dr_out, dh, dr, dy=None, *, w_post=None, w_pre=None, gate=None, rows_per_gate=None,
+                        scale=1.0, eps=1e-5, post=None, dw_post=None, dw_pre=None, dgate=None, workspace=None,
+                        stream=None) -> None:
+    """Backward of ``block_norm`` from the stored r_out (r, if y was None): the gradients
+    dr_out of r_out (None: zero) and dh of h (None: no norm before the next block) to dr
+    and dy, and to dw_post, dw_pre and dgate where they are given (all bf16 or all
+    fp32). ``workspace``: uint8, at least ``block_norm_backward_workspace_bytes`` long;
+    without one the call takes one from torch's allocator."""
+    if dr.dim() != 2:
+        raise ValueError("dr must be a matrix (tokens, channels)")
+    if post is None:
+        post = w_post is not None
+    shape, dev = dr.shape, dr.device
+    rows, cols = shape
+    b, pt, gate_shape = _border(dr, w_post, w_pre, gate, rows_per_gate, scale, eps, post, _float_type(dr, "dr"))
+    gt = None
+    for t in (dw_post, dw_pre, dgate):
+        if t is not None:
+            if gt is not None and t.dtype is not gt:
+                raise ValueError(f"dw_post, dw_pre and dgate must have one type, got {gt} and {t.dtype}")
+            gt = t.dtype
+            b.grad_type = _float_type(t, "a weight's gradient")
+    bf16 = torch.bfloat16
+    args = (_operand(y, bf16, shape, dev, "y") if y is not None else None,
+            _operand(r_out, dr.dtype, shape, dev, "r_out") if r_out is not None else None,
+            _operand(dr_out, dr.dtype, shape, dev, "dr_out") if dr_out is not None else None,
+            _operand(dh, bf16, shape, dev, "dh") if dh is not None else None,
+            _operand(w_post, pt, (cols,), dev, "w_post") if w_post is not None else None,
+            _operand(w_pre, pt, (cols,), dev, "w_pre") if w_pre is not None else None,
+            _operand(gate, pt, gate_shape, dev, "gate") if gate is not None else None,
+            _operand(dr, dr.dtype, shape, dev, "dr"),
+            _operand(dy, bf16, shape, dev, "dy") if dy is not None else None,
+            _operand(dw_post, gt, (cols,), dev, "dw_post") if dw_post is not None else None,
+            _operand(dw_pre, gt, (cols,), dev, "dw_pre") if dw_pre is not None else None,
+            _operand(dgate, gt, gate_shape, dev, "dgate") if dgate is not None else None)
+    nbytes = lib().coat_block_norm_backward_workspace_bytes(ctypes.byref(b)) if gt is not None else 0
+    ws = _workspace(nbytes, workspace, dev, stream)
+    rc = _run(dev, stream, lambda st: lib().coat_block_norm_backward(
+        ctypes.byref(b), *args, ws.data_ptr() if ws is not None else None, nbytes, st))
+    _check(rc, "coat_block_norm_backward")
+
+
+def block_norm_backward_workspace_bytes(rows: int, cols: int, rows_per_gate: Optional[int] = None) -> int:
+    b = _Border(rows, cols, max(1, rows if rows_per_gate is None else rows_per_gate), 1e-5, 1.0, 0, 0, 0, 0)
+    return lib().coat_block_norm_backward_workspace_bytes(ctypes.byref(b))
 
 
 # ---------------------------------------------------------------- parameter lists

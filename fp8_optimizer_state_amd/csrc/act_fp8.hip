@@ -1,89 +1,8 @@
 // HIP (gfx950) FP8 activation codec: bf16 values to E4M3 / E5M2 codes with
 // one fp32 scale per tensor or per group of G consecutive values, and back.
-#include "coat_common.h"
+#include "act_common.h"
 
 namespace {
-
-// ------------------------------------------------------------------ activation codec
-//
-// Article, section "Solution: mixed-granularity FP8 precision flow": layer
-// inputs are kept in FP8 for the backward pass, with a quantization
-// granularity that differs between layers. Plain absmax scaling of bf16
-// values with one fp32 scale per tensor or per group of G consecutive values:
-// s = RN32(amax / fpmax), code = encode(RN32(x / s)) (the sign alone when
-// s = 0), value = RN_bf16(RN32(decode(code) s)); a tensor or group holding a
-// NaN or Inf gets s = NaN and every code 0x7F.
-//
-// RN32(x / s) without a division per value: x has at most 8 significant bits
-// and s at most 24, so a quotient that is not an fp32 number lies at least
-// 2^-49 (relative) from every midpoint between fp32 neighbours (the distance
-// is a nonzero multiple of 2^(e-24) / s's integer significand in the binade
-// [2^e, 2^(e+1)), likewise in the subnormal range), while x * RN64(1 / s),
-// rounded to fp64, is within 2^-52 of it. Rounding that product to fp32 thus
-// gives RN32(x / s) exactly; the hardware converts round it to the FP8 grid,
-// nearest with ties to even, after a clamp to the largest finite magnitude.
-
-// bf16 magnitude bits of 16 values (two 16-byte words per 8 values) -> max.
-__device__ __forceinline__ uint32_t bf16_absmax_bits(const uint32_t (&w)[8]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t a = w[i] & 0x7FFF7FFFu;
-        const uint32_t lo = a & 0xFFFFu, hi = a >> 16;
-        m = m > lo ? m : lo;
-        m = m > hi ? m : hi;
-    }
-    return m;
-}
-
-__device__ __forceinline__ uint32_t group_umax(uint32_t v, int lanes) {
-    for (int d = 1; d < lanes; d <<= 1) {
-        const uint32_t o = xlane32(v, d);
-        v = v > o ? v : o;
-    }
-    return v;
-}
-
-// Codes of the 16 bf16 values in w (value i in half i & 1 of word i >> 1) for
-// a group with magnitude bits `amax_bits`; returns the four code words.
-template <int F>
-__device__ __forceinline__ void act_codes16(const uint32_t (&w)[8], uint32_t amax_bits, uint32_t (&out)[4]) {
-    using T = Fmt<F>;
-    if (amax_bits >= 0x7F80u) {  // Inf or NaN in the group
-#pragma unroll
-        for (int i = 0; i < 4; ++i) out[i] = 0x7F7F7F7Fu;
-        return;
-    }
-    const float amax = __builtin_bit_cast(float, amax_bits << 16);
-    const float sc = (float)((double)amax / T::FPMAX);
-    if (sc == 0.0f) {  // all zero: the sign alone
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t c = 0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int j = 4 * i + b;
-                c |= ((w[j >> 1] >> (16 * (j & 1) + 15)) & 1u) << (8 * b + 7);
-            }
-            out[i] = c;
-        }
-        return;
-    }
-    const double r = 1.0 / (double)sc;  // RN64(1 / s); fp64 holds it for a subnormal s too
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float y[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int j = 4 * i + b;
-            const float x = __builtin_bit_cast(float, (j & 1) ? (w[j >> 1] & 0xFFFF0000u) : (w[j >> 1] << 16));
-            const float q = (float)((double)x * r);  // RN32(x / s)
-            y[b] = __builtin_fminf(__builtin_fmaxf(q, -T::FPMAX_F), T::FPMAX_F);
-        }
-        uint32_t c = cvt_pk<F, false>(y[0], y[1], 0u);
-        out[i] = cvt_pk<F, true>(y[2], y[3], c);
-    }
-}
 
 // Loads the lane's 16 bf16 values of a tile (zeros past n).
 __device__ __forceinline__ void act_load16(const uint16_t* x, int64_t n, int64_t e0, uint32_t (&w)[8]) {
@@ -123,11 +42,10 @@ __global__ __launch_bounds__(kBlock) void act_quantize_group_kernel(const uint16
     auto code = [&](int64_t e0, const uint32_t (&w)[8]) {
         const uint32_t am = group_umax(bf16_absmax_bits(w), lpg);
         uint32_t c[4];
-        act_codes16<F>(w, am, c);
+        act_codes<F>(w, am, c);
         act_store16(q, n, e0, c);
         if ((lane & (lpg - 1)) == 0 && e0 < n) {
-            const float amax = __builtin_bit_cast(float, am << 16);
-            gp(s)[e0 >> lg2_group] = am >= 0x7F80u ? __builtin_nanf("") : (float)((double)amax / Fmt<F>::FPMAX);
+            gp(s)[e0 >> lg2_group] = act_scale<F>(am);
         }
     };
     // two tiles per iteration: both tiles' loads are in flight together
@@ -202,7 +120,7 @@ __global__ __launch_bounds__(kBlock) void act_quantize_tensor_kernel(const uint1
     const uint32_t am = __builtin_amdgcn_readfirstlane(gp(acc)[0]);
     auto code = [&](int64_t e0, const uint32_t (&w)[8]) {
         uint32_t c[4];
-        act_codes16<F>(w, am, c);
+        act_codes<F>(w, am, c);
         act_store16(q, n, e0, c);
     };
     // two tiles per iteration: both tiles' loads are in flight together
@@ -226,10 +144,7 @@ __global__ __launch_bounds__(kBlock) void act_quantize_tensor_kernel(const uint1
 template <int F>
 __global__ void act_finalize_kernel(uint32_t* acc) {
     if (threadIdx.x == 0) {
-        const uint32_t am = gp(acc)[0];
-        const float amax = __builtin_bit_cast(float, am << 16);
-        const float sc = am >= 0x7F80u ? __builtin_nanf("") : (float)((double)amax / Fmt<F>::FPMAX);
-        gp(acc)[0] = __builtin_bit_cast(uint32_t, sc);
+        gp(acc)[0] = __builtin_bit_cast(uint32_t, act_scale<F>(gp(acc)[0]));
     }
 }
 

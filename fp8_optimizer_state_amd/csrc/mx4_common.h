@@ -1,0 +1,142 @@
+// Microscaled 4-bit floating point (E2M1 codes, one power-of-two scale byte per
+// 32 values): the arithmetic and the memory access shared by the kernels.
+#pragma once
+
+#include "coat_common.h"
+#include "ops_host.h"
+
+namespace {
+
+// 16-byte accesses at an element's alignment: global memory takes them at any
+// byte address, in one instruction (rows of an odd width start anywhere).
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+typedef __attribute__((address_space(1))) u32x4_a2 gu32x4_a2;
+typedef __attribute__((address_space(1))) u32x4_a4 gu32x4_a4;
+typedef __attribute__((address_space(1))) u32x2 gu32x2;
+
+__device__ __forceinline__ float as_float(uint32_t w) { return __builtin_bit_cast(float, w); }
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
+// Round to nearest even; a NaN stays one.
+__device__ __forceinline__ uint32_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) { return bf16_bits(lo) | (bf16_bits(hi) << 16); }
+
+// 8 consecutive elements from p, of which the first n (maybe < 1) exist; the others are zero.
+__device__ __forceinline__ void load8(const uint16_t* p, int64_t n, float (&v)[8]) {
+    if (n >= 8) {
+        const u32x4 a = *reinterpret_cast<const gu32x4_a2*>(gp(p));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = bf16_lo(a[i]);
+            v[2 * i + 1] = bf16_hi(a[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        if (n < 1) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // the first element stands in for those past the end
+            const float e = bf16_lo(gp(p)[i < n ? i : 0]);
+            v[i] = i < n ? e : 0.0f;
+        }
+    }
+}
+__device__ __forceinline__ void load8(const float* p, int64_t n, float (&v)[8]) {
+    if (n >= 8) {
+        const u32x4 a = *reinterpret_cast<const gu32x4_a4*>(gp(p));
+        const u32x4 b = *reinterpret_cast<const gu32x4_a4*>(gp(p) + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = as_float(a[i]);
+            v[4 + i] = as_float(b[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        if (n < 1) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // the first element stands in for those past the end
+            const float e = gp(p)[i < n ? i : 0];
+            v[i] = i < n ? e : 0.0f;
+        }
+    }
+}
+
+// 8 consecutive elements to p, of which the first n exist.
+__device__ __forceinline__ void store8(uint16_t* p, int64_t n, const float (&v)[8]) {
+    if (n >= 8) {
+        *reinterpret_cast<gu32x4_a2*>(gp(p)) =
+            u32x4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) gp(p)[i] = (uint16_t)bf16_bits(v[i]);
+    }
+}
+__device__ __forceinline__ void store8(float* p, int64_t n, const float (&v)[8]) {
+    if (n >= 8) {
+        u32x4 a, b;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = __builtin_bit_cast(uint32_t, v[i]);
+            b[i] = __builtin_bit_cast(uint32_t, v[4 + i]);
+        }
+        *reinterpret_cast<gu32x4_a4*>(gp(p)) = a;
+        *reinterpret_cast<gu32x4_a4*>(gp(p) + 4) = b;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) gp(p)[i] = v[i];
+    }
+}
+
+__device__ __forceinline__ uint32_t magnitude_bits(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
+
+template <int N>
+__device__ __forceinline__ uint32_t absmax_bits(const float (&v)[N]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t a = magnitude_bits(v[i]);
+        m = m > a ? m : a;
+    }
+    return m;
+}
+
+// The scale byte of a block whose largest magnitude has these fp32 bits:
+// e + 127 with e = floor(log2 amax) - 2 >= -127, 0xFF for an Inf or NaN. The
+// exponent field of an fp32 subnormal (0) lies below the limit like its value.
+__device__ __forceinline__ uint32_t mx4_scale_byte(uint32_t amax_bits) {
+    const uint32_t f = amax_bits >> 23;
+    return f >= 255u ? 255u : (f > 2u ? f - 2u : 0u);
+}
+
+// Codes of 8 values of a block with scale byte b (not 0xFF), the first in the
+// low bits. x 2^-e is exact in fp32 wherever the result can be over the
+// smallest rounding border (1/4); the convert rounds to nearest, ties to the
+// even code, and cuts at 6.
+__device__ __forceinline__ uint32_t mx4_codes8(const float (&v)[8], uint32_t b) {
+    const float up = __builtin_bit_cast(float, (254u - b) << 23);  // 2^-e
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0] * up, v[1] * up, 1.0f, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2] * up, v[3] * up, 1.0f, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4] * up, v[5] * up, 1.0f, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6] * up, v[7] * up, 1.0f, 3);
+    return c;
+}
+
+// Values of 8 codes of a block with scale byte b.
+__device__ __forceinline__ void mx4_values8(uint32_t c, uint32_t b, float (&v)[8]) {
+    const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0);
+    const f32x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1);
+    const f32x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2);
+    const f32x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3);
+    v[0] = p0.x; v[1] = p0.y; v[2] = p1.x; v[3] = p1.y;
+    v[4] = p2.x; v[5] = p2.y; v[6] = p3.x; v[7] = p3.y;
+    const int e = (int)b - 127;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = b == 255u ? __builtin_nanf("") : __builtin_amdgcn_ldexpf(v[i], e);
+}
+
+}  // namespace

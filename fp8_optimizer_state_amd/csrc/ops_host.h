@@ -1,0 +1,173 @@
+// Host-side logic of the layer-input operators that touches no GPU: sizes,
+// argument checks and launch shapes. Plain C++ with no HIP dependency, so that
+// the same code runs in a host-only driver under AddressSanitizer and
+// UndefinedBehaviorSanitizer.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "coat_fp8.h"
+#include "coat_host.h"
+
+namespace {
+
+constexpr int64_t kMaxDim = 0x7FFFFFFF;
+constexpr int kCUs = 256;  // of an MI355X; launch shapes that decide an order of sums use this, not the device's count
+
+constexpr int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int64_t mx4_code_bytes(int64_t k) { return 64 * div_up(k, 128); }
+constexpr int64_t mx4_scale_bytes(int64_t k) { return 16 * div_up(k, 512); }
+
+inline bool type_ok(int32_t t) { return t == COAT_BF16 || t == COAT_FP32; }
+inline size_t type_bytes(int32_t t) { return t == COAT_FP32 ? 4 : 2; }
+
+// ------------------------------------------------------------------ 4-bit codec and product
+
+// A matrix of `rows` x `cols` elements with `ld` elements from row to row.
+inline int check_matrix(int64_t rows, int64_t cols, int64_t ld, int32_t dtype) {
+    if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim || ld < cols || !type_ok(dtype)) return COAT_EINVAL;
+    if (rows > 0 && ld > (INT64_MAX / 8) / rows) return COAT_EINVAL;
+    return COAT_OK;
+}
+
+inline int check_mx4_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, int32_t dtype, const uint8_t* q,
+                              const uint8_t* s, const uint8_t* q_t, const uint8_t* s_t) {
+    const int rc = check_matrix(rows, cols, ld, dtype);
+    if (rc) return rc;
+    if ((q == nullptr) != (s == nullptr) || (q_t == nullptr) != (s_t == nullptr)) return COAT_EINVAL;
+    if (rows == 0 || cols == 0) return COAT_OK;
+    if (!x || (!q && !q_t)) return COAT_EINVAL;
+    if (!aligned(x, type_bytes(dtype)) || !aligned16(q) || !aligned16(s) || !aligned16(q_t) || !aligned16(s_t))
+        return COAT_EALIGN;
+    return COAT_OK;
+}
+
+inline int check_mx4_dequantize(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t cols, const void* x,
+                                int64_t ld, int32_t dtype) {
+    const int rc = check_matrix(rows, cols, ld, dtype);
+    if (rc) return rc;
+    if (rows == 0 || cols == 0) return COAT_OK;
+    if (!x || !q || !s) return COAT_EINVAL;
+    if (!aligned(x, type_bytes(dtype)) || !aligned16(q) || !aligned16(s)) return COAT_EALIGN;
+    return COAT_OK;
+}
+
+inline int check_mx4_matmul(const uint8_t* a_q, const uint8_t* a_s, int64_t m, const uint8_t* b_q, const uint8_t* b_s,
+                            int64_t n, int64_t k, const void* y, int64_t ld, int32_t dtype) {
+    const int rc = check_matrix(m, n, ld, dtype);
+    if (rc) return rc;
+    if (k < 0 || k > kMaxDim) return COAT_EINVAL;
+    if (m == 0 || n == 0) return COAT_OK;
+    if (!y) return COAT_EINVAL;
+    if (k > 0 && (!a_q || !a_s || !b_q || !b_s)) return COAT_EINVAL;
+    if (!aligned16(a_q) || !aligned16(a_s) || !aligned16(b_q) || !aligned16(b_s) || !aligned(y, type_bytes(dtype)))
+        return COAT_EALIGN;
+    return COAT_OK;
+}
+
+// ------------------------------------------------------------------ block border
+
+inline int check_border(const coat_border* b) {
+    if (!b) return COAT_EINVAL;
+    if (b->rows < 0 || b->rows > kMaxDim || b->cols < 1 || b->cols > COAT_BORDER_MAX_COLS || b->rows_per_gate < 1)
+        return COAT_EINVAL;
+    if (!finite_f(b->eps) || !(b->eps > 0.0f) || !finite_f(b->scale)) return COAT_EINVAL;
+    if ((b->post != 0 && b->post != 1) || !type_ok(b->stream_type) || !type_ok(b->param_type) ||
+        !type_ok(b->grad_type))
+        return COAT_EINVAL;
+    return COAT_OK;
+}
+
+inline int check_block_norm(const coat_border* b, const void* y, const void* r, const void* w_post, const void* w_pre,
+                            const void* gate, const void* r_out, const void* h, const void* q, const void* q_scale,
+                            int32_t group, int32_t fmt) {
+    const int rc = check_border(b);
+    if (rc) return rc;
+    if ((q == nullptr) != (q_scale == nullptr)) return COAT_EINVAL;
+    if (q) {
+        if (fmt == COAT_FMT_MX4) {
+            if (group != 32) return COAT_EINVAL;
+        } else if (fmt == COAT_FMT_E4M3 || fmt == COAT_FMT_E5M2) {
+            if (lg2_group_of(group) < 0 || group > 512 || b->cols % group != 0) return COAT_EINVAL;
+        } else {
+            return COAT_EINVAL;
+        }
+    }
+    if (w_post && !b->post) return COAT_EINVAL;
+    if (b->rows == 0) return COAT_OK;  // a matrix without rows may have no address
+    if (!y && (gate || w_post || b->post || r_out)) return COAT_EINVAL;
+    if (w_pre && !h && !q) return COAT_EINVAL;
+    if (!r_out && !h && !q) return COAT_EINVAL;
+    if (!r) return COAT_EINVAL;
+    const size_t st = type_bytes(b->stream_type), pt = type_bytes(b->param_type);
+    if (!aligned(y, 2) || !aligned(r, st) || !aligned(r_out, st) || !aligned(h, 2) || !aligned(w_post, pt) ||
+        !aligned(w_pre, pt) || !aligned(gate, pt) || !aligned16(q) ||
+        !aligned(q_scale, fmt == COAT_FMT_MX4 ? 16 : 4))
+        return COAT_EALIGN;
+    return COAT_OK;
+}
+
+// How the backward pass deals the rows to blocks. A block sums the weight
+// gradients of its rows in registers and writes one row of partial sums, so
+// the blocks are few (kBorderBlocks at most, except where each gate row has
+// its own): more would fill the card no better and write more partial sums.
+// No block holds rows of two gate rows that both reach into other blocks:
+//   chunks > 0: a gate row's tokens are cut into `chunks` blocks of `step` rows
+//               (the last may be shorter or empty);
+//   chunks = 0: a block takes `step` rows, whole gate rows (or any rows, if no
+//               gate gradient is wanted).
+struct BorderSplit {
+    int64_t step, chunks, blocks;
+};
+constexpr int64_t kBorderBlocks = 512;
+
+inline BorderSplit border_split(int64_t rows, int64_t rows_per_gate, bool dgate) {
+    if (rows == 0) return BorderSplit{1, 0, 0};
+    const int64_t want = div_up(rows, kBorderBlocks);  // rows of a block
+    if (!dgate) return BorderSplit{want, 0, div_up(rows, want)};
+    const int64_t rpg = rows_per_gate < rows ? rows_per_gate : rows;
+    if (rpg <= want) {
+        const int64_t step = want / rpg * rpg;
+        return BorderSplit{step, 0, div_up(rows, step)};
+    }
+    const int64_t chunks = div_up(rpg, want);
+    return BorderSplit{div_up(rpg, chunks), chunks, div_up(rows, rpg) * chunks};
+}
+
+// Partial sums of the backward pass: up to three sections of blocks x cols fp32.
+inline size_t border_section_bytes(int64_t blocks, int64_t cols) {
+    return align_up((size_t)blocks * (size_t)cols * sizeof(float), 256);
+}
+inline size_t border_workspace_bytes(const coat_border* b) {
+    if (check_border(b) != COAT_OK) return 0;
+    const int64_t with = border_split(b->rows, b->rows_per_gate, true).blocks;
+    const int64_t without = border_split(b->rows, b->rows_per_gate, false).blocks;
+    return 3 * border_section_bytes(with > without ? with : without, b->cols);
+}
+
+inline int check_block_norm_backward(const coat_border* b, const void* y, const void* r_out, const void* dr_out,
+                                     const void* dh, const void* w_post, const void* w_pre, const void* gate,
+                                     const void* dr, const void* dy, const void* dw_post, const void* dw_pre,
+                                     const void* dgate, const void* workspace, size_t workspace_bytes) {
+    const int rc = check_border(b);
+    if (rc) return rc;
+    if (w_post && !b->post) return COAT_EINVAL;
+    if ((dw_post && !w_post) || (dw_pre && !w_pre) || (dgate && !gate)) return COAT_EINVAL;
+    const size_t st = type_bytes(b->stream_type), pt = type_bytes(b->param_type), gt = type_bytes(b->grad_type);
+    if (b->rows > 0) {  // a matrix without rows may have no address
+        if (!y && (gate || w_post || b->post || dy)) return COAT_EINVAL;
+        if (!dh && (w_pre || !dr_out)) return COAT_EINVAL;
+        if (!dr || (y && !dy) || (dh && !r_out)) return COAT_EINVAL;
+        const size_t need = border_workspace_bytes(b);
+        if ((dw_post || dw_pre || dgate) && (!workspace || workspace_bytes < need)) return COAT_EINVAL;
+    }
+    if (!aligned(y, 2) || !aligned(dh, 2) || !aligned(dy, 2) || !aligned(r_out, st) || !aligned(dr_out, st) ||
+        !aligned(dr, st) || !aligned(w_post, pt) || !aligned(w_pre, pt) || !aligned(gate, pt) ||
+        !aligned(dw_post, gt) || !aligned(dw_pre, gt) || !aligned(dgate, gt) || !aligned(workspace, 256))
+        return COAT_EALIGN;
+    return COAT_OK;
+}
+
+}  // namespace

@@ -242,6 +242,145 @@ int coat_fp8_act_quantize(const uint16_t* x, int64_t n, int32_t group, int32_t f
 int coat_fp8_act_dequantize(const uint8_t* q, const float* scale, int64_t n, int32_t group,
                             int32_t fmt, uint16_t* x, coat_stream_t stream);
 
+/* Element types of the entry points below. */
+enum { COAT_BF16 = 0, COAT_FP32 = 1 };
+
+/*
+ * Microscaled 4-bit floating point (OCP MX, E2M1 elements): a row is cut into
+ * blocks of 32 consecutive values; each block has one scale byte b and stands
+ * for code * 2^(b - 127), a code being a sign bit and one of the magnitudes
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *   - quantizing a block: e = floor(log2(amax)) - 2, at least -127; b = e + 127;
+ *     code = x / 2^e rounded to nearest, ties to the even code, magnitudes over
+ *     6 cut to 6. An all-zero block has b = 0 and signed-zero codes; a block
+ *     holding a NaN or Inf has b = 0xFF and codes 0, and reads back as NaN.
+ *   - a matrix of `rows` rows of k values is stored as
+ *       q[rows][coat_mx4_code_bytes(k)]   two codes a byte, the first in the low
+ *                                         half; k rounded up to 128 values,
+ *       s[rows][coat_mx4_scale_bytes(k)]  one byte a block, rounded up to 16,
+ *     both without gaps, the values, blocks and bytes past k zero.
+ */
+int64_t coat_mx4_code_bytes(int64_t k);  /* 64 ceil(k / 128) */
+int64_t coat_mx4_scale_bytes(int64_t k); /* 16 ceil(k / 512) */
+
+/*
+ * Quantize a matrix along its rows, its columns, or both in one pass.
+ *   x      rows x cols, bf16 or fp32 (dtype), row i at x + i ld, in
+ *   q, s   x's rows quantized (rows of cols values), out; both NULL to skip
+ *   q_t, s_t  x's columns quantized: the transposed matrix, cols rows of
+ *          `rows` values each, out; both NULL to skip
+ * ld >= cols counts elements. x needs its type's alignment, the byte arrays 16
+ * (COAT_EALIGN). rows = 0 or cols = 0 writes nothing. The sizes are limited to
+ * 2^31 - 1 each (COAT_EINVAL).
+ */
+int coat_mx4_quantize(const void* x, int64_t rows, int64_t cols, int64_t ld, int32_t dtype,
+                      uint8_t* q, uint8_t* s, uint8_t* q_t, uint8_t* s_t, coat_stream_t stream);
+
+/*
+ * Read a quantized matrix back: x (rows x cols, bf16 or fp32, row i at
+ * x + i ld) gets each code's value, rounded once (bf16 and fp32 hold every
+ * value of a matrix that coat_mx4_quantize wrote exactly). Elements of x
+ * between cols and ld are left as they are.
+ */
+int coat_mx4_dequantize(const uint8_t* q, const uint8_t* s, int64_t rows, int64_t cols, void* x,
+                        int64_t ld, int32_t dtype, coat_stream_t stream);
+
+/*
+ * Product of two quantized matrices on the matrix units:
+ *   y[i][j] = sum over k of A[i][k] B[j][k],  A m x k, B n x k, y m x n.
+ * With row-quantized activations X and weights W (out x in) a linear layer is
+ * Y = X W^T; with the column-quantized forms of coat_mx4_quantize its backward
+ * products are dX = dY (W^T)^T and dW = dY^T (X^T)^T. Sums are held in fp32,
+ * in an order that depends on (m, n, k) alone; y is rounded once.
+ *   y      bf16 or fp32 (dtype), row i at y + i ld, ld >= n, out
+ *   workspace  device memory, 256-byte aligned, at least
+ *          coat_mx4_matmul_workspace_bytes(m, n, k) bytes (may be NULL if that
+ *          is 0); calls that may overlap in time need one each.
+ * m = 0 or n = 0 writes nothing; k = 0 writes zeros. The byte arrays are
+ * 16-byte aligned, y has its type's alignment (COAT_EALIGN). m, n and k are
+ * limited to 2^31 - 1 (COAT_EINVAL). Elements of y between n and ld are left
+ * as they are.
+ */
+size_t coat_mx4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k);
+int coat_mx4_matmul(const uint8_t* a_q, const uint8_t* a_s, int64_t m, const uint8_t* b_q,
+                    const uint8_t* b_s, int64_t n, int64_t k, void* y, int64_t ld, int32_t dtype,
+                    void* workspace, size_t workspace_bytes, coat_stream_t stream);
+
+/*
+ * The border between two blocks of a transformer: the norm after a block, the
+ * gated and scaled residual addition, and the norm before the next block,
+ * whose result is that block's layer input. Per token (row) t, with
+ * N(a) = a / sqrt(mean(a^2) + eps) over the row and g the gate's row
+ * t / rows_per_gate,
+ *   z  = w_post N(y)            (z = y if post = 0)
+ *   r' = r + scale g z          rounded to the stream's type
+ *   h  = w_pre N(r')            computed from the rounded r'
+ * A missing weight or gate counts as ones.
+ */
+typedef struct coat_border {
+    int64_t rows;          /* tokens */
+    int64_t cols;          /* channels, 1 .. COAT_BORDER_MAX_COLS */
+    int64_t rows_per_gate; /* >= 1; the gate has ceil(rows / rows_per_gate) rows (1: one per token, rows: one for all) */
+    float eps;             /* > 0, finite */
+    float scale;           /* the residual scale, finite */
+    int32_t post;          /* 1: y is normalised, 0: it is not */
+    int32_t stream_type;   /* COAT_BF16 or COAT_FP32: r, r_out, dr_out, dr */
+    int32_t param_type;    /* of w_post, w_pre and gate */
+    int32_t grad_type;     /* of dw_post, dw_pre and dgate */
+} coat_border;
+
+#define COAT_BORDER_MAX_COLS 16384
+
+enum { COAT_FMT_MX4 = 2 }; /* a layer input stored as coat_mx4_quantize stores it */
+
+/*
+ * Forward. All matrices are rows x cols without gaps.
+ *   y      bf16, the block's output; NULL: no addition (the first block), r' = r
+ *   r      the residual stream
+ *   w_post, w_pre  cols values, may be NULL; w_post only with post
+ *   gate   ceil(rows / rows_per_gate) x cols, may be NULL; only with y
+ *   r_out  r', out; may be NULL, may be r itself
+ *   h      bf16 layer input, out; may be NULL
+ *   q, q_scale  the layer input in a stored form, out; both may be NULL. It is
+ *          exactly that of the bf16 h:
+ *          fmt COAT_FMT_E4M3 / COAT_FMT_E5M2: as coat_fp8_act_quantize with
+ *          `group` a power of two in [16, 512] that divides cols, fp32 scales;
+ *          fmt COAT_FMT_MX4: as coat_mx4_quantize along the rows, group = 32,
+ *          q_scale its scale bytes.
+ * With h and q both NULL there is no norm before the next block (w_pre NULL);
+ * at least one output is needed. Matrices of bf16 and fp32 need their type's
+ * alignment, q 16 bytes, q_scale 4, and 16 for COAT_FMT_MX4 (COAT_EALIGN).
+ * Sums of squares are held in fp32, so |values| over 1e19 overflow.
+ */
+int coat_block_norm(const coat_border* b, const uint16_t* y, const void* r, const void* w_post,
+                    const void* w_pre, const void* gate, void* r_out, uint16_t* h, uint8_t* q,
+                    void* q_scale, int32_t group, int32_t fmt, coat_stream_t stream);
+
+/*
+ * Backward, from the stored r' (the forward's r_out, or r if there was no
+ * addition). With D the whole gradient of r',
+ *   D  = dr_out + N'(r')^T (w_pre dh)     dw_pre  = sum_t dh N(r')
+ *   dr = D                                dgate   = sum over a gate row's tokens of scale z D
+ *   dy = N'(y)^T (w_post scale g D)       dw_post = sum_t scale g D N(y)
+ * (N'^T the transposed derivative of N; without the post-norm dy = scale g D).
+ *   dr_out  gradient of r' from later blocks; NULL: zero
+ *   dh      bf16 gradient of h; NULL: there was no norm before the next block
+ *   dr      out, the stream's type; may be dr_out itself
+ *   dy      bf16, out, with y; NULL without y
+ *   dw_post, dw_pre, dgate  out, grad_type; each may be NULL, and is only
+ *           allowed with its weight or gate; rows = 0 gives zeros. The sums are
+ *           held in fp32, in an order that depends on the sizes alone.
+ *   workspace  device memory, 256-byte aligned, at least
+ *           coat_block_norm_backward_workspace_bytes(b) bytes; calls that may
+ *           overlap in time need one each.
+ */
+size_t coat_block_norm_backward_workspace_bytes(const coat_border* b);
+int coat_block_norm_backward(const coat_border* b, const uint16_t* y, const void* r_out,
+                             const void* dr_out, const uint16_t* dh, const void* w_post,
+                             const void* w_pre, const void* gate, void* dr, uint16_t* dy,
+                             void* dw_post, void* dw_pre, void* dgate, void* workspace,
+                             size_t workspace_bytes, coat_stream_t stream);
+
 /* Static description of a status code. */
 const char* coat_strerror(int status);
 
