@@ -62,9 +62,243 @@ __global__ __launch_bounds__(kBlock) void mx4_matmul_small_kernel(const uint8_t*
     }
 }
 
+// ------------------------------------------------------------------ large tiles
+//
+// A workgroup of 2 x 2 wavefronts computes tiles of 64 FN rows of B by 64 FM
+// rows of A, one after the other; the steps of 128 values of k of all its tiles
+// form one stream. A step's codes (64 bytes a row, B's rows before A's) go
+// straight from global memory into one of four LDS slots, four steps before
+// they are used; the scale bytes of four steps (16 a row) likewise into one of
+// two. A step is computed in two halves of 64 values of k: while one half's
+// matrix instructions run, the next half's fragments are read from LDS. One
+// barrier a step, between its halves: behind it every wavefront has read step s
+// (its slot may be refilled) and step s + 1 has arrived.
+//
+// LDS reads are 16 bytes a lane from 32 rows 64 bytes apart; chunk c of row r
+// lies at position c ^ (r / 4 % 4), so that any 16 rows reach 16 different
+// 16-byte columns of the banks. The loads write LDS in lane order, so the lane
+// that fills position p of row r fetches chunk p ^ (r / 4 % 4).
+constexpr int kSlots = 4;
+
+template <int N>
+__device__ __forceinline__ void wait_vm_and_lds_then_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// 16 bytes a lane from base + off to LDS, lane after lane from the byte address `lds`.
+__device__ __forceinline__ void load_to_lds16(uint32_t lds, uint32_t off, const uint8_t* base) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+
+// Where a workgroup reads its next four steps.
+struct Stream {
+    const uint8_t *bq, *aq, *bs, *as;  // first rows of the tile, at the group's first step
+};
+
+template <int FN, int FM, class T>
+__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) void mx4_matmul_tile_kernel(
+    const uint8_t* __restrict__ aq, const uint8_t* __restrict__ as, int64_t m, const uint8_t* __restrict__ bq,
+    const uint8_t* __restrict__ bs, int64_t n, int64_t k, uint32_t tiles_m, uint32_t tiles_n, T* __restrict__ y,
+    int64_t ld) {
+    constexpr int BN = 64 * FN, BM = 64 * FM, D = FN + FM, SC = (FN + FM) / 4;
+    constexpr uint32_t kSlotBytes = (BN + BM) * 64, kScaleBytes = (BN + BM) * 16;
+    // stores of a whole tile, an exact count: later waits let them run
+    constexpr int kStores = FN * FM * (sizeof(T) == 4 ? 4 : 2);
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kSlots * kSlotBytes + 2 * kScaleBytes];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int half = lane >> 5, l32 = lane & 31;
+    const int64_t qb = mx4_code_bytes(k), sb = mx4_scale_bytes(k);
+    const uint32_t steps = (uint32_t)(qb / 64), groups = (steps + 3) / 4;
+    const uint32_t tiles = tiles_m * tiles_n;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+
+    // tile t: patches of 8 x 4 tiles are consecutive
+    auto place = [&](uint32_t t, int64_t& m0, int64_t& n0) {
+        const uint32_t per = 8 * tiles_n, band = t / per, in = t - band * per;
+        const uint32_t high = tiles_m - band * 8 < 8 ? tiles_m - band * 8 : 8;
+        m0 = (int64_t)(band * 8 + in % high) * BM;
+        n0 = (int64_t)(in / high) * BN;
+    };
+    // byte offsets of this lane's chunks and scale words from the tile's first rows
+    uint32_t off[D], soff[SC];
+    auto offsets = [&](int64_t m0, int64_t n0) {
+#pragma unroll
+        for (int i = 0; i < D; ++i) {
+            const uint32_t row = (uint32_t)(i * 4 + wave) * 16 + lane / 4 - (i < FN ? 0 : BN);
+            const int64_t left = (i < FN ? n - n0 : m - m0) - 1;  // the last row stands in for those past the end
+            const uint32_t r = row < left ? row : (uint32_t)left;
+            off[i] = r * (uint32_t)qb + (((lane & 3) ^ ((lane >> 4) & 3)) * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < SC; ++i) {
+            uint32_t row = (uint32_t)(i * 4 + wave) * 64 + lane;
+            const bool is_b = row < BN;
+            if (!is_b) row -= BN;
+            const int64_t left = (is_b ? n - n0 : m - m0) - 1;
+            soff[i] = (row < left ? row : (uint32_t)left) * (uint32_t)sb;
+        }
+    };
+    auto fetch_step = [&](const Stream& at, int u) {
+        // a step past the end of k is fetched from the last one and not used
+        const uint32_t d = u * 64;
+#pragma unroll
+        for (int i = 0; i < D; ++i)
+            load_to_lds16(lds0 + u * kSlotBytes + (i * 4 + wave) * 1024, off[i], (i < FN ? at.bq : at.aq) + d);
+    };
+    auto fetch_scales = [&](const Stream& at, int slot) {
+#pragma unroll
+        for (int i = 0; i < SC; ++i)
+            load_to_lds16(lds0 + kSlots * kSlotBytes + slot * kScaleBytes + (i * 4 + wave) * 1024, soff[i],
+                          (i * 4 + wave) * 64 < BN ? at.bs : at.as);
+    };
+    auto stream_of = [&](int64_t m0, int64_t n0, uint32_t g) {
+        return Stream{bq + n0 * qb + g * 256, aq + m0 * qb + g * 256, bs + n0 * sb + g * 16, as + m0 * sb + g * 16};
+    };
+
+    u32x4 fb[2][FN], fa[2][FM];    // fragments, by half
+    uint32_t cb[2][FN], ca[2][FM];  // scale words, by parity of the step
+    const int wn = (wave & 1) * FN * 32, wm = (wave >> 1) * FM * 32;
+    auto read_frags = [&](int u, int h) {
+        const uint8_t* slot = lds + u * kSlotBytes;
+        const int pos = ((2 * h + half) ^ ((l32 >> 2) & 3)) * 16;
+#pragma unroll
+        for (int i = 0; i < FN; ++i) fb[h][i] = *reinterpret_cast<const u32x4*>(slot + (wn + i * 32 + l32) * 64 + pos);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) fa[h][i] = *reinterpret_cast<const u32x4*>(slot + (BN + wm + i * 32 + l32) * 64 + pos);
+    };
+    auto read_scales = [&](int slot, int u, int p) {
+        const uint8_t* at = lds + kSlots * kSlotBytes + slot * kScaleBytes + u * 4;
+#pragma unroll
+        for (int i = 0; i < FN; ++i) cb[p][i] = *reinterpret_cast<const uint32_t*>(at + (wn + i * 32 + l32) * 16) >> (8 * half);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            ca[p][i] = *reinterpret_cast<const uint32_t*>(at + (BN + wm + i * 32 + l32) * 16) >> (8 * half);
+    };
+
+    // consecutive workgroups run on different XCDs: each XCD takes 32 consecutive tiles of a round
+    const uint32_t first = gridDim.x == kCUs ? (blockIdx.x & 7) * 32 + (blockIdx.x >> 3) : blockIdx.x;
+    if (first >= tiles) return;
+    int64_t m0, n0;
+    place(first, m0, n0);
+    offsets(m0, n0);
+    Stream next = stream_of(m0, n0, 0);
+    fetch_scales(next, 0);
+#pragma unroll
+    for (int u = 0; u < kSlots; ++u) {
+        if ((uint32_t)u < steps) fetch_step(next, u);
+        else fetch_step(Stream{next.bq - u * 64, next.aq - u * 64, next.bs, next.as}, u);
+    }
+    wait_vm_and_lds_then_barrier<0>();
+    read_frags(0, 0);
+    read_scales(0, 0, 0);
+    int par = 0;  // parity of the group
+
+    f32x16 acc[FN][FM];
+    for (uint32_t t = first; t < tiles; t += gridDim.x) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+        const int64_t cm0 = m0, cn0 = n0;
+        for (uint32_t g = 0; g < groups; ++g) {
+            uint32_t left = steps;  // steps that the next group may fetch
+            if (g + 1 < groups) {
+                next = stream_of(m0, n0, g + 1);
+                left = steps - 4 * (g + 1);
+            } else if (t + gridDim.x < tiles) {
+                place(t + gridDim.x, m0, n0);
+                offsets(m0, n0);
+                next = stream_of(m0, n0, 0);
+            } else {
+                next = stream_of(m0, n0, 0);  // fetched once more and not used
+            }
+            const bool after_stores = g == 0 && t != first;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                constexpr int kAllow0 = 2 * D, kAllow1 = 2 * D + SC;
+                constexpr int kLate0 = kAllow0 + kStores < 63 ? kAllow0 + kStores : 63;
+                constexpr int kLate1 = kAllow1 + kStores < 63 ? kAllow1 + kStores : 63;
+                const bool work = 4 * g + u < steps;
+                const int p = u & 1;
+                read_frags(u, 1);
+                if (work) {
+#pragma unroll
+                    for (int i = 0; i < FN; ++i)
+#pragma unroll
+                        for (int j = 0; j < FM; ++j) acc[i][j] = mfma_fp4<0>(fb[0][i], fa[0][j], acc[i][j], cb[p][i], ca[p][j]);
+                }
+                if (u == 0) {
+                    if (after_stores) wait_vm_and_lds_then_barrier<kLate0>();
+                    else wait_vm_and_lds_then_barrier<kAllow0>();
+                } else if (u == 3) {
+                    wait_vm_and_lds_then_barrier<kAllow0>();
+                } else {
+                    if (after_stores) wait_vm_and_lds_then_barrier<kLate1>();
+                    else wait_vm_and_lds_then_barrier<kAllow1>();
+                }
+                if (u == 0) fetch_scales(next, par ^ 1);
+                const int64_t back = (uint32_t)u < left ? 0 : (int64_t)(u + 1 - left) * 64;
+                fetch_step(Stream{next.bq - back, next.aq - back, next.bs, next.as}, u);
+                read_frags((u + 1) & 3, 0);
+                read_scales(u == 3 ? par ^ 1 : par, (u + 1) & 3, p ^ 1);
+                if (work) {
+#pragma unroll
+                    for (int i = 0; i < FN; ++i)
+#pragma unroll
+                        for (int j = 0; j < FM; ++j) acc[i][j] = mfma_fp4<2>(fb[1][i], fa[1][j], acc[i][j], cb[p][i], ca[p][j]);
+                }
+            }
+            par ^= 1;
+        }
+        // lanes l and l + 32 exchange so that each holds 8 consecutive columns
+        const bool whole = cm0 + BM <= m && cn0 + BN <= n;
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            const int64_t row = cm0 + wm + j * 32 + l32;
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+#pragma unroll
+                for (int q2 = 0; q2 < 2; ++q2) {
+                    float v[8];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float lo = acc[i][j][8 * q2 + r], hi = acc[i][j][8 * q2 + 4 + r];
+                        const u32x2 w = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, lo),
+                                                                         __builtin_bit_cast(uint32_t, hi), false, false);
+                        v[r] = as_float(w[0]);
+                        v[4 + r] = as_float(w[1]);
+                    }
+                    const int64_t col = cn0 + wn + i * 32 + q2 * 16 + half * 8;
+                    if (whole) store8(y + row * ld + col, 8, v);
+                    else if (row < m) store8(y + row * ld + col, n - col, v);
+                }
+            }
+        }
+        if (!whole) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    // nothing may still be on its way into LDS when the workgroup ends
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+template <int FN, int FM, class T>
+int launch_tile(const uint8_t* aq, const uint8_t* as, int64_t m, const uint8_t* bq, const uint8_t* bs, int64_t n,
+                int64_t k, T* y, int64_t ld, hipStream_t st) {
+    const int64_t tm = div_up(m, 64 * FM), tn = div_up(n, 64 * FN), tiles = tm * tn;
+    if (tiles > 0x7FFFFFFFll) return COAT_EINVAL;
+    const unsigned grid = (unsigned)(tiles < kCUs ? tiles : kCUs);
+    hipLaunchKernelGGL((mx4_matmul_tile_kernel<FN, FM, T>), dim3(grid), dim3(kBlock), 0, st, aq, as, m, bq, bs, n, k,
+                       (uint32_t)tm, (uint32_t)tn, y, ld);
+    return launch_status();
+}
+
 template <class T>
 int launch_matmul(const uint8_t* aq, const uint8_t* as, int64_t m, const uint8_t* bq, const uint8_t* bs, int64_t n,
                   int64_t k, T* y, int64_t ld, hipStream_t st) {
+    if (m >= 256 && n >= 256 && k > 0 && k < (1 << 22))
+        return launch_tile<4, 4>(aq, as, m, bq, bs, n, k, y, ld, st);
     const int64_t tn = div_up(n, 64), tiles = tn * div_up(m, 64);
     if (tiles > 0x7FFFFFFFll) return COAT_EINVAL;
     hipLaunchKernelGGL(mx4_matmul_small_kernel<T>, dim3((unsigned)tiles), dim3(kBlock), 0, st, aq, as, m, bq, bs, n, k,
