@@ -93,6 +93,7 @@ __device__ __forceinline__ void load_to_lds16(uint32_t lds, uint32_t off, const 
 // Where a workgroup reads its next four steps.
 struct Stream {
     const uint8_t *bq, *aq, *bs, *as;  // first rows of the tile, at the group's first step
+    uint32_t step[4];                  // byte offsets of the steps; one past the end of k is fetched from the last and not used
 };
 
 template <int FN, int FM, class T>
@@ -139,12 +140,8 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
             soff[i] = (row < left ? row : (uint32_t)left) * (uint32_t)sb;
         }
     };
-    auto fetch_step = [&](const Stream& at, int u) {
-        // a step past the end of k is fetched from the last one and not used
-        const uint32_t d = u * 64;
-#pragma unroll
-        for (int i = 0; i < D; ++i)
-            load_to_lds16(lds0 + u * kSlotBytes + (i * 4 + wave) * 1024, off[i], (i < FN ? at.bq : at.aq) + d);
+    auto fetch_part = [&](const Stream& at, int u, int i) {
+        load_to_lds16(lds0 + u * kSlotBytes + (i * 4 + wave) * 1024, off[i], (i < FN ? at.bq : at.aq) + at.step[u]);
     };
     auto fetch_scales = [&](const Stream& at, int slot) {
 #pragma unroll
@@ -153,27 +150,35 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
                           (i * 4 + wave) * 64 < BN ? at.bs : at.as);
     };
     auto stream_of = [&](int64_t m0, int64_t n0, uint32_t g) {
-        return Stream{bq + n0 * qb + g * 256, aq + m0 * qb + g * 256, bs + n0 * sb + g * 16, as + m0 * sb + g * 16};
+        const uint32_t last = steps - 4 * g - 1;
+        return Stream{bq + n0 * qb + g * 256, aq + m0 * qb + g * 256, bs + n0 * sb + g * 16, as + m0 * sb + g * 16,
+                      {0, 64 * (last < 1 ? last : 1), 64 * (last < 2 ? last : 2), 64 * (last < 3 ? last : 3)}};
     };
 
     u32x4 fb[2][FN], fa[2][FM];    // fragments, by half
     uint32_t cb[2][FN], ca[2][FM];  // scale words, by parity of the step
     const int wn = (wave & 1) * FN * 32, wm = (wave >> 1) * FM * 32;
-    auto read_frags = [&](int u, int h) {
-        const uint8_t* slot = lds + u * kSlotBytes;
+    // fragment i of a half step: A's first, which every row of matrix instructions needs
+    auto read_frag = [&](int u, int h, int i) {
         const int pos = ((2 * h + half) ^ ((l32 >> 2) & 3)) * 16;
-#pragma unroll
-        for (int i = 0; i < FN; ++i) fb[h][i] = *reinterpret_cast<const u32x4*>(slot + (wn + i * 32 + l32) * 64 + pos);
-#pragma unroll
-        for (int i = 0; i < FM; ++i) fa[h][i] = *reinterpret_cast<const u32x4*>(slot + (BN + wm + i * 32 + l32) * 64 + pos);
+        const uint8_t* slot = lds + u * kSlotBytes + pos + l32 * 64;
+        if (i < FM) fa[h][i] = *reinterpret_cast<const u32x4*>(slot + (BN + wm + i * 32) * 64);
+        else fb[h][i - FM] = *reinterpret_cast<const u32x4*>(slot + (wn + (i - FM) * 32) * 64);
     };
-    auto read_scales = [&](int slot, int u, int p) {
-        const uint8_t* at = lds + kSlots * kSlotBytes + slot * kScaleBytes + u * 4;
+    auto read_scale = [&](int slot, int u, int p, int i) {
+        const uint8_t* at = lds + kSlots * kSlotBytes + slot * kScaleBytes + u * 4 + l32 * 16;
+        if (i < FM) ca[p][i] = *reinterpret_cast<const uint32_t*>(at + (BN + wm + i * 32) * 16);
+        else cb[p][i - FM] = *reinterpret_cast<const uint32_t*>(at + (wn + (i - FM) * 32) * 16);
+    };
+    // Moves this half's scale bytes into place. A step past the end of k (its
+    // codes are those of the last one) gets scale bytes 0 instead: every product
+    // is at most 36 * 2^-254 then, and adds nothing to an fp32 sum.
+    auto shift_scales = [&](int p, bool work) {
+        const uint32_t width = work ? 24u : 0u;
 #pragma unroll
-        for (int i = 0; i < FN; ++i) cb[p][i] = *reinterpret_cast<const uint32_t*>(at + (wn + i * 32 + l32) * 16) >> (8 * half);
+        for (int i = 0; i < FM; ++i) ca[p][i] = __builtin_amdgcn_ubfe(ca[p][i], 8 * half, width);
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
-            ca[p][i] = *reinterpret_cast<const uint32_t*>(at + (BN + wm + i * 32 + l32) * 16) >> (8 * half);
+        for (int i = 0; i < FN; ++i) cb[p][i] = __builtin_amdgcn_ubfe(cb[p][i], 8 * half, width);
     };
 
     // consecutive workgroups run on different XCDs: each XCD takes 32 consecutive tiles of a round
@@ -185,16 +190,68 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
     Stream next = stream_of(m0, n0, 0);
     fetch_scales(next, 0);
 #pragma unroll
-    for (int u = 0; u < kSlots; ++u) {
-        if ((uint32_t)u < steps) fetch_step(next, u);
-        else fetch_step(Stream{next.bq - u * 64, next.aq - u * 64, next.bs, next.as}, u);
-    }
+    for (int u = 0; u < kSlots; ++u)
+#pragma unroll
+        for (int i = 0; i < D; ++i) fetch_part(next, u, i);
     wait_vm_and_lds_then_barrier<0>();
-    read_frags(0, 0);
-    read_scales(0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+        read_frag(0, 0, i);
+        read_scale(0, 0, 0, i);
+    }
+    shift_scales(0, true);
     int par = 0;  // parity of the group
 
     f32x16 acc[FN][FM];
+    // Four steps. The loads into LDS, the fragment reads and the matrix
+    // instructions are issued in turn, a few loads to every FM matrix
+    // instructions: a wavefront issues in order, so a run of loads would leave
+    // the matrix unit idle.
+    auto group_of_steps = [&](uint32_t g, uint32_t after_stores) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int p = u & 1;
+            constexpr int kReads = (D + FN - 1) / FN;  // a row of matrix instructions takes this many
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+#pragma unroll
+                for (int r = i * kReads; r < (i + 1) * kReads && r < D; ++r) read_frag(u, 1, r);
+#pragma unroll
+                for (int j = 0; j < FM; ++j) {
+                    acc[i][j] = mfma_fp4<0>(fb[0][i], fa[0][j], acc[i][j], cb[p][i], ca[p][j]);
+                    asm volatile("" : "+a"(acc[i][j]));
+                }
+            }
+            constexpr int kAllow0 = 2 * D, kAllow1 = 2 * D + SC;
+            constexpr int kLate0 = kAllow0 + kStores < 63 ? kAllow0 + kStores : 63;
+            constexpr int kLate1 = kAllow1 + kStores < 63 ? kAllow1 + kStores : 63;
+            if (u == 0) {
+                if (after_stores) wait_vm_and_lds_then_barrier<kLate0>();
+                else wait_vm_and_lds_then_barrier<kAllow0>();
+            } else if (u == 3) {
+                wait_vm_and_lds_then_barrier<kAllow0>();
+            } else {
+                if (after_stores) wait_vm_and_lds_then_barrier<kLate1>();
+                else wait_vm_and_lds_then_barrier<kAllow1>();
+            }
+            if (u == 0) fetch_scales(next, par ^ 1);
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+#pragma unroll
+                for (int r = i * kReads; r < (i + 1) * kReads && r < D; ++r) {
+                    read_frag((u + 1) & 3, 0, r);
+                    read_scale(u == 3 ? par ^ 1 : par, (u + 1) & 3, p ^ 1, r);
+                    fetch_part(next, u, r);
+                }
+#pragma unroll
+                for (int j = 0; j < FM; ++j) {
+                    acc[i][j] = mfma_fp4<2>(fb[1][i], fa[1][j], acc[i][j], cb[p][i], ca[p][j]);
+                    asm volatile("" : "+a"(acc[i][j]));
+                }
+            }
+            shift_scales(p ^ 1, u == 3 || 4 * g + u + 1 < steps);
+        }
+    };
     for (uint32_t t = first; t < tiles; t += gridDim.x) {
 #pragma unroll
         for (int i = 0; i < FN; ++i)
@@ -203,11 +260,10 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
         const int64_t cm0 = m0, cn0 = n0;
+#pragma nounroll
         for (uint32_t g = 0; g < groups; ++g) {
-            uint32_t left = steps;  // steps that the next group may fetch
             if (g + 1 < groups) {
                 next = stream_of(m0, n0, g + 1);
-                left = steps - 4 * (g + 1);
             } else if (t + gridDim.x < tiles) {
                 place(t + gridDim.x, m0, n0);
                 offsets(m0, n0);
@@ -215,42 +271,9 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
             } else {
                 next = stream_of(m0, n0, 0);  // fetched once more and not used
             }
-            const bool after_stores = g == 0 && t != first;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                constexpr int kAllow0 = 2 * D, kAllow1 = 2 * D + SC;
-                constexpr int kLate0 = kAllow0 + kStores < 63 ? kAllow0 + kStores : 63;
-                constexpr int kLate1 = kAllow1 + kStores < 63 ? kAllow1 + kStores : 63;
-                const bool work = 4 * g + u < steps;
-                const int p = u & 1;
-                read_frags(u, 1);
-                if (work) {
-#pragma unroll
-                    for (int i = 0; i < FN; ++i)
-#pragma unroll
-                        for (int j = 0; j < FM; ++j) acc[i][j] = mfma_fp4<0>(fb[0][i], fa[0][j], acc[i][j], cb[p][i], ca[p][j]);
-                }
-                if (u == 0) {
-                    if (after_stores) wait_vm_and_lds_then_barrier<kLate0>();
-                    else wait_vm_and_lds_then_barrier<kAllow0>();
-                } else if (u == 3) {
-                    wait_vm_and_lds_then_barrier<kAllow0>();
-                } else {
-                    if (after_stores) wait_vm_and_lds_then_barrier<kLate1>();
-                    else wait_vm_and_lds_then_barrier<kAllow1>();
-                }
-                if (u == 0) fetch_scales(next, par ^ 1);
-                const int64_t back = (uint32_t)u < left ? 0 : (int64_t)(u + 1 - left) * 64;
-                fetch_step(Stream{next.bq - back, next.aq - back, next.bs, next.as}, u);
-                read_frags((u + 1) & 3, 0);
-                read_scales(u == 3 ? par ^ 1 : par, (u + 1) & 3, p ^ 1);
-                if (work) {
-#pragma unroll
-                    for (int i = 0; i < FN; ++i)
-#pragma unroll
-                        for (int j = 0; j < FM; ++j) acc[i][j] = mfma_fp4<2>(fb[1][i], fa[1][j], acc[i][j], cb[p][i], ca[p][j]);
-                }
-            }
+            uint32_t after_stores = __builtin_amdgcn_readfirstlane(g == 0 && t != first ? 1 : 0);
+            asm volatile("" : "+s"(after_stores));  // the loop stays one loop
+            group_of_steps(g, after_stores);
             par ^= 1;
         }
         // lanes l and l + 32 exchange so that each holds 8 consecutive columns
