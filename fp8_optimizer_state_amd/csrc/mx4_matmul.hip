@@ -90,6 +90,28 @@ __device__ __forceinline__ void load_to_lds16(uint32_t lds, uint32_t off, const 
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
 }
 
+__device__ __forceinline__ uint32_t float_bits(float v) { return __builtin_bit_cast(uint32_t, v); }
+
+// A 16-byte chunk of y, of which the first n elements exist.
+__device__ __forceinline__ void store_chunk(float* p, int64_t n, const u32x4& w) {
+    if (n >= 4) {
+        *reinterpret_cast<gu32x4_a4*>(gp(p)) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) gp(p)[i] = as_float(w[i]);
+    }
+}
+__device__ __forceinline__ void store_chunk(uint16_t* p, int64_t n, const u32x4& w) {
+    if (n >= 8) {
+        *reinterpret_cast<gu32x4_a2*>(gp(p)) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) gp(p)[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    }
+}
+
 // Where a workgroup reads its next four steps.
 struct Stream {
     const uint8_t *bq, *aq, *bs, *as;  // first rows of the tile, at the group's first step
@@ -105,7 +127,7 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
     constexpr uint32_t kSlotBytes = (BN + BM) * 64, kScaleBytes = (BN + BM) * 16;
     // stores of a whole tile, an exact count: later waits let them run
     constexpr int kStores = FN * FM * (sizeof(T) == 4 ? 4 : 2);
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kSlots * kSlotBytes + 2 * kScaleBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kSlots * kSlotBytes + 2 * kScaleBytes + kWavesPerBlock * 4096];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int half = lane >> 5, l32 = lane & 31;
@@ -276,27 +298,47 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
             group_of_steps(g, after_stores);
             par ^= 1;
         }
-        // lanes l and l + 32 exchange so that each holds 8 consecutive columns
+        // Out through 4 KB of LDS of this wavefront's own, 32 rows of 128 bytes at
+        // a time, so that each store writes whole 128-byte lines: chunk c of row r
+        // lies at position c ^ (r % 8).
         const bool whole = cm0 + BM <= m && cn0 + BN <= n;
+        uint8_t* out = lds + kSlots * kSlotBytes + 2 * kScaleBytes + wave * 4096;
+        constexpr int kPer = 16 / sizeof(T);             // elements of a chunk
+        constexpr int kFrags = sizeof(T) == 4 ? 1 : 2;   // fragments that make 128 bytes of a row
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
-            const int64_t row = cm0 + wm + j * 32 + l32;
 #pragma unroll
-            for (int i = 0; i < FN; ++i) {
-#pragma unroll
-                for (int q2 = 0; q2 < 2; ++q2) {
-                    float v[8];
+            for (int i = 0; i < FN; i += kFrags) {
+                if constexpr (sizeof(T) == 4) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float lo = acc[i][j][8 * q2 + r], hi = acc[i][j][8 * q2 + 4 + r];
-                        const u32x2 w = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, lo),
-                                                                         __builtin_bit_cast(uint32_t, hi), false, false);
-                        v[r] = as_float(w[0]);
-                        v[4 + r] = as_float(w[1]);
+                        const u32x4 w{float_bits(acc[i][j][4 * r]), float_bits(acc[i][j][4 * r + 1]),
+                                      float_bits(acc[i][j][4 * r + 2]), float_bits(acc[i][j][4 * r + 3])};
+                        *reinterpret_cast<u32x4*>(out + l32 * 128 + (((2 * r + half) ^ (l32 & 7)) * 16)) = w;
                     }
-                    const int64_t col = cn0 + wn + i * 32 + q2 * 16 + half * 8;
-                    if (whole) store8(y + row * ld + col, 8, v);
-                    else if (row < m) store8(y + row * ld + col, n - col, v);
+                } else {
+#pragma unroll
+                    for (int f = 0; f < 2; ++f)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            // lanes l and l + 32 exchange so that each holds 8 consecutive columns
+                            const f32x16& v = acc[i + f][j];
+                            const u32x2 w0 = __builtin_amdgcn_permlane32_swap(bf16_pair(v[8 * q], v[8 * q + 1]),
+                                                                              bf16_pair(v[8 * q + 4], v[8 * q + 5]), false, false);
+                            const u32x2 w1 = __builtin_amdgcn_permlane32_swap(bf16_pair(v[8 * q + 2], v[8 * q + 3]),
+                                                                              bf16_pair(v[8 * q + 6], v[8 * q + 7]), false, false);
+                            *reinterpret_cast<u32x4*>(out + l32 * 128 + (((4 * f + 2 * q + half) ^ (l32 & 7)) * 16)) =
+                                u32x4{w0[0], w1[0], w0[1], w1[1]};
+                        }
+                }
+                const int r8 = lane >> 3, c8 = lane & 7;
+                const int64_t col = cn0 + wn + i * 32 + c8 * kPer;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const u32x4 w = *reinterpret_cast<const u32x4*>(out + (r * 8 + r8) * 128 + ((c8 ^ r8) * 16));
+                    const int64_t row = cm0 + wm + j * 32 + r * 8 + r8;
+                    if (whole) store_chunk(y + row * ld + col, kPer, w);
+                    else if (row < m) store_chunk(y + row * ld + col, n - col, w);
                 }
             }
         }
