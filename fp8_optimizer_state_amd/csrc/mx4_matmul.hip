@@ -1,4 +1,6 @@
 // HIP (gfx950) product of two matrices in microscaled 4-bit floating point.
+#include <type_traits>
+
 #include "mx4_common.h"
 
 namespace {
@@ -85,9 +87,11 @@ __device__ __forceinline__ void wait_vm_and_lds_then_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// 16 bytes a lane from base + off to LDS, lane after lane from the byte address `lds`.
+// 16 bytes a lane from base + off to LDS, lane after lane from byte address lds + AT.
+template <uint32_t AT>
 __device__ __forceinline__ void load_to_lds16(uint32_t lds, uint32_t off, const uint8_t* base) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+    asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base), "n"(AT)
+                 : "memory", "scc");
 }
 
 __device__ __forceinline__ uint32_t float_bits(float v) { return __builtin_bit_cast(uint32_t, v); }
@@ -109,6 +113,15 @@ __device__ __forceinline__ void store_chunk(uint16_t* p, int64_t n, const u32x4&
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i < n) gp(p)[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    }
+}
+
+// f(0), f(1), ... f(N - 1) with the index known to the compiler.
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void each(F&& f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        each<N, I + 1>(f);
     }
 }
 
@@ -162,14 +175,15 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
             soff[i] = (row < left ? row : (uint32_t)left) * (uint32_t)sb;
         }
     };
-    auto fetch_part = [&](const Stream& at, int u, int i) {
-        load_to_lds16(lds0 + u * kSlotBytes + (i * 4 + wave) * 1024, off[i], (i < FN ? at.bq : at.aq) + at.step[u]);
+    const uint32_t lds_wave = lds0 + wave * 1024;
+    auto fetch_part = [&](const Stream& at, auto u, auto i) {
+        load_to_lds16<u * kSlotBytes + i * 4096>(lds_wave, off[i], (i < FN ? at.bq : at.aq) + at.step[u]);
     };
     auto fetch_scales = [&](const Stream& at, int slot) {
-#pragma unroll
-        for (int i = 0; i < SC; ++i)
-            load_to_lds16(lds0 + kSlots * kSlotBytes + slot * kScaleBytes + (i * 4 + wave) * 1024, soff[i],
-                          (i * 4 + wave) * 64 < BN ? at.bs : at.as);
+        each<SC>([&](auto i) {
+            load_to_lds16<kSlots * kSlotBytes + i * 4096>(lds_wave + slot * kScaleBytes, soff[i],
+                                                          (i * 4 + wave) * 64 < BN ? at.bs : at.as);
+        });
     };
     auto stream_of = [&](int64_t m0, int64_t n0, uint32_t g) {
         const uint32_t last = steps - 4 * g - 1;
@@ -197,6 +211,11 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
     // is at most 36 * 2^-254 then, and adds nothing to an fp32 sum.
     auto shift_scales = [&](int p, bool work) {
         const uint32_t width = work ? 24u : 0u;
+        // not before here: the words are still on their way while matrix instructions can be issued
+#pragma unroll
+        for (int i = 0; i < FM; ++i) asm volatile("" : "+v"(ca[p][i]));
+#pragma unroll
+        for (int i = 0; i < FN; ++i) asm volatile("" : "+v"(cb[p][i]));
 #pragma unroll
         for (int i = 0; i < FM; ++i) ca[p][i] = __builtin_amdgcn_ubfe(ca[p][i], 8 * half, width);
 #pragma unroll
@@ -211,10 +230,7 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
     offsets(m0, n0);
     Stream next = stream_of(m0, n0, 0);
     fetch_scales(next, 0);
-#pragma unroll
-    for (int u = 0; u < kSlots; ++u)
-#pragma unroll
-        for (int i = 0; i < D; ++i) fetch_part(next, u, i);
+    each<kSlots>([&](auto u) { each<D>([&](auto i) { fetch_part(next, u, i); }); });
     wait_vm_and_lds_then_barrier<0>();
 #pragma unroll
     for (int i = 0; i < D; ++i) {
@@ -230,49 +246,43 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
     // instructions: a wavefront issues in order, so a run of loads would leave
     // the matrix unit idle.
     auto group_of_steps = [&](uint32_t g, uint32_t after_stores) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int p = u & 1;
-            constexpr int kReads = (D + FN - 1) / FN;  // a row of matrix instructions takes this many
-#pragma unroll
-            for (int i = 0; i < FN; ++i) {
-#pragma unroll
-                for (int r = i * kReads; r < (i + 1) * kReads && r < D; ++r) read_frag(u, 1, r);
-#pragma unroll
-                for (int j = 0; j < FM; ++j) {
+        each<4>([&](auto u) {
+            constexpr int p = u & 1;
+            constexpr int kReads = (D + FN - 1) / FN;  // fragments read to a row of matrix instructions
+            each<FN>([&](auto i) {
+                each<kReads>([&](auto r) {
+                    if constexpr (i * kReads + r < D) read_frag(u, 1, i * kReads + r);
+                });
+                __builtin_amdgcn_sched_barrier(0);
+                each<FM>([&](auto j) {
                     acc[i][j] = mfma_fp4<0>(fb[0][i], fa[0][j], acc[i][j], cb[p][i], ca[p][j]);
-                    asm volatile("" : "+a"(acc[i][j]));
-                }
-            }
-            constexpr int kAllow0 = 2 * D, kAllow1 = 2 * D + SC;
-            constexpr int kLate0 = kAllow0 + kStores < 63 ? kAllow0 + kStores : 63;
-            constexpr int kLate1 = kAllow1 + kStores < 63 ? kAllow1 + kStores : 63;
-            if (u == 0) {
-                if (after_stores) wait_vm_and_lds_then_barrier<kLate0>();
-                else wait_vm_and_lds_then_barrier<kAllow0>();
-            } else if (u == 3) {
-                wait_vm_and_lds_then_barrier<kAllow0>();
-            } else {
-                if (after_stores) wait_vm_and_lds_then_barrier<kLate1>();
-                else wait_vm_and_lds_then_barrier<kAllow1>();
-            }
-            if (u == 0) fetch_scales(next, par ^ 1);
-#pragma unroll
-            for (int i = 0; i < FN; ++i) {
-#pragma unroll
-                for (int r = i * kReads; r < (i + 1) * kReads && r < D; ++r) {
-                    read_frag((u + 1) & 3, 0, r);
-                    read_scale(u == 3 ? par ^ 1 : par, (u + 1) & 3, p ^ 1, r);
-                    fetch_part(next, u, r);
-                }
-#pragma unroll
-                for (int j = 0; j < FM; ++j) {
+                    asm volatile("" : "+a"(acc[i][j]));  // keeps the order
+                });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            constexpr int kAllow = 2 * D + (u == 1 || u == 2 ? SC : 0);
+            constexpr int kLate = kAllow + kStores < 63 ? kAllow + kStores : 63;
+            if (u < 3 && after_stores) wait_vm_and_lds_then_barrier<kLate>();
+            else wait_vm_and_lds_then_barrier<kAllow>();
+            if constexpr (u == 0) fetch_scales(next, par ^ 1);
+            each<FN>([&](auto i) {
+                each<kReads>([&](auto r) {
+                    constexpr int at = i * kReads + r;
+                    if constexpr (at < D) {
+                        read_frag((u + 1) & 3, 0, at);
+                        read_scale(u == 3 ? par ^ 1 : par, (u + 1) & 3, p ^ 1, at);
+                        fetch_part(next, u, std::integral_constant<int, at>{});
+                    }
+                });
+                __builtin_amdgcn_sched_barrier(0);
+                each<FM>([&](auto j) {
                     acc[i][j] = mfma_fp4<2>(fb[1][i], fa[1][j], acc[i][j], cb[p][i], ca[p][j]);
                     asm volatile("" : "+a"(acc[i][j]));
-                }
-            }
+                });
+                __builtin_amdgcn_sched_barrier(0);
+            });
             shift_scales(p ^ 1, u == 3 || 4 * g + u + 1 < steps);
-        }
+        });
     };
     for (uint32_t t = first; t < tiles; t += gridDim.x) {
 #pragma unroll
