@@ -230,7 +230,10 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
     offsets(m0, n0);
     Stream next = stream_of(m0, n0, 0);
     fetch_scales(next, 0);
-    each<kSlots>([&](auto u) { each<D>([&](auto i) { fetch_part(next, u, i); }); });
+    each<kSlots>([&](auto u) {
+        // the first half step fetches the rest of the last slot
+        each<(u < kSlots - 1 ? D : D / 2)>([&](auto i) { fetch_part(next, u, i); });
+    });
     wait_vm_and_lds_then_barrier<0>();
 #pragma unroll
     for (int i = 0; i < D; ++i) {
@@ -240,51 +243,70 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
     shift_scales(0, true);
     int par = 0;  // parity of the group
 
+    uint32_t t = first, g = 0;
+    // the group after (t, g): where its steps are fetched from
+    auto advance = [&] {
+        if (g + 1 < groups) {
+            next = stream_of(m0, n0, g + 1);
+            return;
+        }
+        if (t + gridDim.x < tiles) {
+            place(t + gridDim.x, m0, n0);
+            offsets(m0, n0);
+        }  // behind the last tile its first group is fetched once more and not used
+        next = stream_of(m0, n0, 0);
+    };
+
     f32x16 acc[FN][FM];
-    // Four steps. The loads into LDS, the fragment reads and the matrix
-    // instructions are issued in turn, a few loads to every FM matrix
-    // instructions: a wavefront issues in order, so a run of loads would leave
-    // the matrix unit idle.
-    auto group_of_steps = [&](uint32_t g, uint32_t after_stores) {
+    // Four steps. A wavefront issues in order, and a matrix instruction occupies
+    // its unit for 32 cycles: the few other instructions that a half step needs
+    // (reads of the next half's fragments, half of a step's loads into LDS, scale
+    // words) are dealt out between its FN FM matrix instructions, the reads first.
+    // The second half of a step's loads is issued in the next step's first half.
+    constexpr int kSlotsOfHalf = FN * FM, kItems = D + D / 2;
+    auto group_of_steps = [&](uint32_t after_stores) {
         each<4>([&](auto u) {
             constexpr int p = u & 1;
-            constexpr int kReads = (D + FN - 1) / FN;  // fragments read to a row of matrix instructions
-            each<FN>([&](auto i) {
-                each<kReads>([&](auto r) {
-                    if constexpr (i * kReads + r < D) read_frag(u, 1, i * kReads + r);
+            each<kSlotsOfHalf>([&](auto q) {
+                each<(q + 1) * kItems / kSlotsOfHalf - q * kItems / kSlotsOfHalf>([&](auto r) {
+                    constexpr int item = q * kItems / kSlotsOfHalf + r;
+                    if constexpr (item < D) read_frag(u, 1, item);
+                    else fetch_part(next, std::integral_constant<int, (u + 3) & 3>{}, std::integral_constant<int, item - D / 2>{});
                 });
                 __builtin_amdgcn_sched_barrier(0);
-                each<FM>([&](auto j) {
-                    acc[i][j] = mfma_fp4<0>(fb[0][i], fa[0][j], acc[i][j], cb[p][i], ca[p][j]);
-                    asm volatile("" : "+a"(acc[i][j]));  // keeps the order
-                });
+                constexpr int i = q / FM, j = q % FM;
+                acc[i][j] = mfma_fp4<0>(fb[0][i], fa[0][j], acc[i][j], cb[p][i], ca[p][j]);
+                asm volatile("" : "+a"(acc[i][j]));  // keeps the order
                 __builtin_amdgcn_sched_barrier(0);
             });
             constexpr int kAllow = 2 * D + (u == 1 || u == 2 ? SC : 0);
             constexpr int kLate = kAllow + kStores < 63 ? kAllow + kStores : 63;
             if (u < 3 && after_stores) wait_vm_and_lds_then_barrier<kLate>();
             else wait_vm_and_lds_then_barrier<kAllow>();
-            if constexpr (u == 0) fetch_scales(next, par ^ 1);
-            each<FN>([&](auto i) {
-                each<kReads>([&](auto r) {
-                    constexpr int at = i * kReads + r;
-                    if constexpr (at < D) {
-                        read_frag((u + 1) & 3, 0, at);
-                        read_scale(u == 3 ? par ^ 1 : par, (u + 1) & 3, p ^ 1, at);
-                        fetch_part(next, u, std::integral_constant<int, at>{});
+            if constexpr (u == 0) {
+                advance();
+                fetch_scales(next, par ^ 1);
+            }
+            each<kSlotsOfHalf>([&](auto q) {
+                each<(q + 1) * kItems / kSlotsOfHalf - q * kItems / kSlotsOfHalf>([&](auto r) {
+                    constexpr int item = q * kItems / kSlotsOfHalf + r;
+                    if constexpr (item < D) {
+                        read_scale(u == 3 ? par ^ 1 : par, (u + 1) & 3, p ^ 1, item);
+                        read_frag((u + 1) & 3, 0, item);
+                    } else {
+                        fetch_part(next, u, std::integral_constant<int, item - D>{});
                     }
                 });
+                if constexpr (q == kSlotsOfHalf - 1) shift_scales(p ^ 1, u == 3 || 4 * g + u + 1 < steps);
                 __builtin_amdgcn_sched_barrier(0);
-                each<FM>([&](auto j) {
-                    acc[i][j] = mfma_fp4<2>(fb[1][i], fa[1][j], acc[i][j], cb[p][i], ca[p][j]);
-                    asm volatile("" : "+a"(acc[i][j]));
-                });
+                constexpr int i = q / FM, j = q % FM;
+                acc[i][j] = mfma_fp4<2>(fb[1][i], fa[1][j], acc[i][j], cb[p][i], ca[p][j]);
+                asm volatile("" : "+a"(acc[i][j]));
                 __builtin_amdgcn_sched_barrier(0);
             });
-            shift_scales(p ^ 1, u == 3 || 4 * g + u + 1 < steps);
         });
     };
-    for (uint32_t t = first; t < tiles; t += gridDim.x) {
+    for (; t < tiles; t += gridDim.x) {
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
@@ -293,19 +315,10 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
         const int64_t cm0 = m0, cn0 = n0;
 #pragma nounroll
-        for (uint32_t g = 0; g < groups; ++g) {
-            if (g + 1 < groups) {
-                next = stream_of(m0, n0, g + 1);
-            } else if (t + gridDim.x < tiles) {
-                place(t + gridDim.x, m0, n0);
-                offsets(m0, n0);
-                next = stream_of(m0, n0, 0);
-            } else {
-                next = stream_of(m0, n0, 0);  // fetched once more and not used
-            }
+        for (g = 0; g < groups; ++g) {
             uint32_t after_stores = __builtin_amdgcn_readfirstlane(g == 0 && t != first ? 1 : 0);
             asm volatile("" : "+s"(after_stores));  // the loop stays one loop
-            group_of_steps(g, after_stores);
+            group_of_steps(after_stores);
             par ^= 1;
         }
         // Out through 4 KB of LDS of this wavefront's own, 32 rows of 128 bytes at
