@@ -96,10 +96,12 @@ __device__ __forceinline__ void load_to_lds16(uint32_t lds, uint32_t off, const 
 
 __device__ __forceinline__ uint32_t float_bits(float v) { return __builtin_bit_cast(uint32_t, v); }
 
-// A 16-byte chunk of y, of which the first n elements exist.
+// A 16-byte chunk of y, of which the first n elements exist. y is written past
+// the caches' usual order: kept there it would drive out the operands (16384 x
+// 16384 x 512 to bf16: 158 us against 214).
 __device__ __forceinline__ void store_chunk(float* p, int64_t n, const u32x4& w) {
     if (n >= 4) {
-        *reinterpret_cast<gu32x4_a4*>(gp(p)) = w;
+        __builtin_nontemporal_store(w, reinterpret_cast<gu32x4_a4*>(gp(p)));
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -108,7 +110,7 @@ __device__ __forceinline__ void store_chunk(float* p, int64_t n, const u32x4& w)
 }
 __device__ __forceinline__ void store_chunk(uint16_t* p, int64_t n, const u32x4& w) {
     if (n >= 8) {
-        *reinterpret_cast<gu32x4_a2*>(gp(p)) = w;
+        __builtin_nontemporal_store(w, reinterpret_cast<gu32x4_a2*>(gp(p)));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -131,22 +133,25 @@ struct Stream {
     uint32_t step[4];                  // byte offsets of the steps; one past the end of k is fetched from the last and not used
 };
 
-template <int FN, int FM, class T>
-__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) void mx4_matmul_tile_kernel(
+// With splits > 1 item t is the product over the groups of four steps
+// [s per_split, (s + 1) per_split), s = t / tiles, of tile t % tiles, and goes to
+// y + s part (partial sums, added by another kernel).
+template <int FN, int FM, int PER_EU, int PIECE, class T>
+__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(PER_EU, PER_EU))) void mx4_matmul_tile_kernel(
     const uint8_t* __restrict__ aq, const uint8_t* __restrict__ as, int64_t m, const uint8_t* __restrict__ bq,
-    const uint8_t* __restrict__ bs, int64_t n, int64_t k, uint32_t tiles_m, uint32_t tiles_n, T* __restrict__ y,
-    int64_t ld) {
+    const uint8_t* __restrict__ bs, int64_t n, int64_t k, uint32_t tiles_m, uint32_t tiles_n, uint32_t splits,
+    uint32_t per_split, T* __restrict__ y, int64_t ld, int64_t part) {
     constexpr int BN = 64 * FN, BM = 64 * FM, D = FN + FM, SC = (FN + FM) / 4;
     constexpr uint32_t kSlotBytes = (BN + BM) * 64, kScaleBytes = (BN + BM) * 16;
     // stores of a whole tile, an exact count: later waits let them run
     constexpr int kStores = FN * FM * (sizeof(T) == 4 ? 4 : 2);
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kSlots * kSlotBytes + 2 * kScaleBytes + kWavesPerBlock * 4096];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kSlots * kSlotBytes + 2 * kScaleBytes + kWavesPerBlock * 32 * PIECE];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int half = lane >> 5, l32 = lane & 31;
     const int64_t qb = mx4_code_bytes(k), sb = mx4_scale_bytes(k);
     const uint32_t steps = (uint32_t)(qb / 64), groups = (steps + 3) / 4;
-    const uint32_t tiles = tiles_m * tiles_n;
+    const uint32_t tiles = tiles_m * tiles_n, items = tiles * splits;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
 
     // tile t: patches of 8 x 4 tiles are consecutive
@@ -222,13 +227,13 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
         for (int i = 0; i < FN; ++i) cb[p][i] = __builtin_amdgcn_ubfe(cb[p][i], 8 * half, width);
     };
 
-    // consecutive workgroups run on different XCDs: each XCD takes 32 consecutive tiles of a round
-    const uint32_t first = gridDim.x == kCUs ? (blockIdx.x & 7) * 32 + (blockIdx.x >> 3) : blockIdx.x;
-    if (first >= tiles) return;
+    // consecutive workgroups run on different XCDs: each XCD takes consecutive items of a round
+    const uint32_t first = gridDim.x % 8 == 0 ? (blockIdx.x & 7) * (gridDim.x / 8) + (blockIdx.x >> 3) : blockIdx.x;
+    if (first >= items) return;
     int64_t m0, n0;
-    place(first, m0, n0);
+    place(first % tiles, m0, n0);
     offsets(m0, n0);
-    Stream next = stream_of(m0, n0, 0);
+    Stream next = stream_of(m0, n0, first / tiles * per_split);
     fetch_scales(next, 0);
     each<kSlots>([&](auto u) {
         // the first half step fetches the rest of the last slot
@@ -246,15 +251,15 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
     uint32_t t = first, g = 0;
     // the group after (t, g): where its steps are fetched from
     auto advance = [&] {
-        if (g + 1 < groups) {
-            next = stream_of(m0, n0, g + 1);
-            return;
-        }
-        if (t + gridDim.x < tiles) {
-            place(t + gridDim.x, m0, n0);
+        uint32_t at = t / tiles * per_split;
+        if (g + 1 < groups && g + 1 < at + per_split) {
+            at = g + 1;
+        } else if (t + gridDim.x < items) {
+            place((t + gridDim.x) % tiles, m0, n0);
             offsets(m0, n0);
-        }  // behind the last tile its first group is fetched once more and not used
-        next = stream_of(m0, n0, 0);
+            at = (t + gridDim.x) / tiles * per_split;
+        }  // behind the last item its first group is fetched once more and not used
+        next = stream_of(m0, n0, at);
     };
 
     f32x16 acc[FN][FM];
@@ -306,7 +311,7 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
             });
         });
     };
-    for (; t < tiles; t += gridDim.x) {
+    for (; t < items; t += gridDim.x) {
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
@@ -314,54 +319,54 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
         const int64_t cm0 = m0, cn0 = n0;
+        T* const yc = y + t / tiles * part;
+        const uint32_t g0 = t / tiles * per_split, g1 = g0 + per_split < groups ? g0 + per_split : groups;
 #pragma nounroll
-        for (g = 0; g < groups; ++g) {
-            uint32_t after_stores = __builtin_amdgcn_readfirstlane(g == 0 && t != first ? 1 : 0);
+        for (g = g0; g < g1; ++g) {
+            uint32_t after_stores = __builtin_amdgcn_readfirstlane(g == g0 && t != first ? 1 : 0);
             asm volatile("" : "+s"(after_stores));  // the loop stays one loop
             group_of_steps(after_stores);
             par ^= 1;
         }
-        // Out through 4 KB of LDS of this wavefront's own, 32 rows of 128 bytes at
-        // a time, so that each store writes whole 128-byte lines: chunk c of row r
-        // lies at position c ^ (r % 8).
+        // Out through LDS of this wavefront's own, 32 rows of PIECE bytes at a
+        // time, so that each store writes long runs of a row: chunk c of row r
+        // lies at position c ^ (r % chunks).
         const bool whole = cm0 + BM <= m && cn0 + BN <= n;
-        uint8_t* out = lds + kSlots * kSlotBytes + 2 * kScaleBytes + wave * 4096;
-        constexpr int kPer = 16 / sizeof(T);             // elements of a chunk
-        constexpr int kFrags = sizeof(T) == 4 ? 1 : 2;   // fragments that make 128 bytes of a row
+        uint8_t* out = lds + kSlots * kSlotBytes + 2 * kScaleBytes + wave * 32 * PIECE;
+        constexpr int kChunks = PIECE / 16, kPer = 16 / sizeof(T);  // chunks of a row, elements of a chunk
+        constexpr int kBlocks = PIECE / (int)sizeof(T) / 16;        // blocks of 16 columns of a piece
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
 #pragma unroll
-            for (int i = 0; i < FN; i += kFrags) {
-                if constexpr (sizeof(T) == 4) {
+            for (int pc = 0; pc < 2 * FN / kBlocks; ++pc) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const u32x4 w{float_bits(acc[i][j][4 * r]), float_bits(acc[i][j][4 * r + 1]),
-                                      float_bits(acc[i][j][4 * r + 2]), float_bits(acc[i][j][4 * r + 3])};
-                        *reinterpret_cast<u32x4*>(out + l32 * 128 + (((2 * r + half) ^ (l32 & 7)) * 16)) = w;
+                for (int b = 0; b < kBlocks; ++b) {
+                    const f32x16& v = acc[(pc * kBlocks + b) / 2][j];
+                    const int e = (pc * kBlocks + b) % 2 * 8;
+                    auto put = [&](int c, const u32x4& w) {
+                        *reinterpret_cast<u32x4*>(out + l32 * PIECE + ((c ^ (l32 & (kChunks - 1))) * 16)) = w;
+                    };
+                    if constexpr (sizeof(T) == 4) {
+                        put(4 * b + half, u32x4{float_bits(v[e]), float_bits(v[e + 1]), float_bits(v[e + 2]), float_bits(v[e + 3])});
+                        put(4 * b + 2 + half,
+                            u32x4{float_bits(v[e + 4]), float_bits(v[e + 5]), float_bits(v[e + 6]), float_bits(v[e + 7])});
+                    } else {
+                        // lanes l and l + 32 exchange so that each holds 8 consecutive columns
+                        const u32x2 w0 = __builtin_amdgcn_permlane32_swap(bf16_pair(v[e], v[e + 1]),
+                                                                          bf16_pair(v[e + 4], v[e + 5]), false, false);
+                        const u32x2 w1 = __builtin_amdgcn_permlane32_swap(bf16_pair(v[e + 2], v[e + 3]),
+                                                                          bf16_pair(v[e + 6], v[e + 7]), false, false);
+                        put(2 * b + half, u32x4{w0[0], w1[0], w0[1], w1[1]});
                     }
-                } else {
-#pragma unroll
-                    for (int f = 0; f < 2; ++f)
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            // lanes l and l + 32 exchange so that each holds 8 consecutive columns
-                            const f32x16& v = acc[i + f][j];
-                            const u32x2 w0 = __builtin_amdgcn_permlane32_swap(bf16_pair(v[8 * q], v[8 * q + 1]),
-                                                                              bf16_pair(v[8 * q + 4], v[8 * q + 5]), false, false);
-                            const u32x2 w1 = __builtin_amdgcn_permlane32_swap(bf16_pair(v[8 * q + 2], v[8 * q + 3]),
-                                                                              bf16_pair(v[8 * q + 6], v[8 * q + 7]), false, false);
-                            *reinterpret_cast<u32x4*>(out + l32 * 128 + (((4 * f + 2 * q + half) ^ (l32 & 7)) * 16)) =
-                                u32x4{w0[0], w1[0], w0[1], w1[1]};
-                        }
                 }
-                const int r8 = lane >> 3, c8 = lane & 7;
-                const int64_t col = cn0 + wn + i * 32 + c8 * kPer;
+                const int lr = lane / kChunks, lc = lane % kChunks;
+                const int64_t col = cn0 + wn + pc * kBlocks * 16 + lc * kPer;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const u32x4 w = *reinterpret_cast<const u32x4*>(out + (r * 8 + r8) * 128 + ((c8 ^ r8) * 16));
-                    const int64_t row = cm0 + wm + j * 32 + r * 8 + r8;
-                    if (whole) store_chunk(y + row * ld + col, kPer, w);
-                    else if (row < m) store_chunk(y + row * ld + col, n - col, w);
+                for (int r = 0; r < 32; r += kWave / kChunks) {
+                    const u32x4 w = *reinterpret_cast<const u32x4*>(out + (r + lr) * PIECE + ((lc ^ (lr & (kChunks - 1))) * 16));
+                    const int64_t row = cm0 + wm + j * 32 + r + lr;
+                    if (whole) store_chunk(yc + row * ld + col, kPer, w);
+                    else if (row < m) store_chunk(yc + row * ld + col, n - col, w);
                 }
             }
         }
@@ -371,26 +376,197 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-template <int FN, int FM, class T>
-int launch_tile(const uint8_t* aq, const uint8_t* as, int64_t m, const uint8_t* bq, const uint8_t* bs, int64_t n,
-                int64_t k, T* y, int64_t ld, hipStream_t st) {
-    const int64_t tm = div_up(m, 64 * FM), tn = div_up(n, 64 * FN), tiles = tm * tn;
-    if (tiles > 0x7FFFFFFFll) return COAT_EINVAL;
-    const unsigned grid = (unsigned)(tiles < kCUs ? tiles : kCUs);
-    hipLaunchKernelGGL((mx4_matmul_tile_kernel<FN, FM, T>), dim3(grid), dim3(kBlock), 0, st, aq, as, m, bq, bs, n, k,
-                       (uint32_t)tm, (uint32_t)tn, y, ld);
+// Adds the partial sums of the splits, in their order: four columns a thread.
+template <class T>
+__global__ __launch_bounds__(kBlock) void mx4_matmul_join_kernel(const float* __restrict__ ws, int64_t part, int64_t lw,
+                                                                 uint32_t splits, int64_t m, int64_t n,
+                                                                 T* __restrict__ y, int64_t ld) {
+    const int64_t quads = lw / 4, total = m * quads;
+    for (int64_t i = (int64_t)blockIdx.x * kBlock + threadIdx.x; i < total; i += (int64_t)gridDim.x * kBlock) {
+        const int64_t row = i / quads, col = (i - row * quads) * 4;
+        const float* p = ws + row * lw + col;
+        f32x4 sum = *reinterpret_cast<const gf32x4*>(gp(p));
+        for (uint32_t s = 1; s < splits; ++s) {
+            const f32x4 v = *reinterpret_cast<const gf32x4*>(gp(p + s * part));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[j] += v[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (col + j >= n) break;
+            if constexpr (sizeof(T) == 4) gp(y)[row * ld + col + j] = sum[j];
+            else gp(y)[row * ld + col + j] = (uint16_t)bf16_bits(sum[j]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ few rows of A
+//
+// Bound by reading B once. A workgroup takes 16 rows of B; its wavefronts take a
+// part of k each, straight from global memory into registers, and add their
+// sums through LDS in order. Up to 16 FM rows of A; rows past the end are read
+// as the last one and not stored.
+//
+// The matrix instruction here takes 16 rows of each operand over 128 values of
+// k: lane l holds the 32 codes of row l % 16 in block l / 16, and their scale
+// byte; accumulator r of lane l is y[l % 16][4 (l / 16) + r]. A load covers 64
+// consecutive bytes of each row (a 32-row form of the instruction would make it
+// 32), and a row's scale bytes of four steps come in one.
+constexpr int kFewWaves = 8;
+
+template <int FM, class T>
+__global__ __launch_bounds__(kFewWaves* kWave) void mx4_matmul_few_kernel(const uint8_t* __restrict__ aq,
+                                                                         const uint8_t* __restrict__ as, int64_t m,
+                                                                         const uint8_t* __restrict__ bq,
+                                                                         const uint8_t* __restrict__ bs, int64_t n,
+                                                                         int64_t k, int per, T* __restrict__ y, int64_t ld) {
+    __shared__ float sums[kFewWaves][4 * FM][kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int block = lane >> 4, l16 = lane & 15;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int64_t qb = mx4_code_bytes(k), sb = mx4_scale_bytes(k);
+    const int steps = (int)(qb / 64), groups = (steps + 3) / 4;  // groups of four steps
+    const int g0 = wave * per, g1 = g0 + per < groups ? g0 + per : groups;
+    const int64_t rb = n0 + l16 < n ? n0 + l16 : n - 1;
+    const uint8_t *pb = bq + rb * qb + block * 16, *psb = bs + rb * sb;
+    const uint8_t *pa[FM], *psa[FM];
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+        const int64_t ra = j * 16 + l16 < m ? j * 16 + l16 : m - 1;
+        pa[j] = aq + ra * qb + block * 16;
+        psa[j] = as + ra * sb;
+    }
+    f32x4 acc[FM];
+#pragma unroll
+    for (int j = 0; j < FM; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int kAhead = 2;  // groups whose loads are in flight together
+    for (int g = g0; g < g1; g += kAhead) {
+        u32x4 b[kAhead][4], a[kAhead][FM][4], cb[kAhead], ca[kAhead][FM];
+#pragma unroll
+        for (int v = 0; v < kAhead; ++v) {
+            const int gv = g + v < g1 ? g + v : g1 - 1;
+            cb[v] = *reinterpret_cast<const gu32x4*>(gp(psb) + gv * 16);
+#pragma unroll
+            for (int j = 0; j < FM; ++j) ca[v][j] = *reinterpret_cast<const gu32x4*>(gp(psa[j]) + gv * 16);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int at = 4 * gv + u < steps ? 4 * gv + u : steps - 1;
+                b[v][u] = *reinterpret_cast<const gu32x4*>(gp(pb) + at * 64);
+#pragma unroll
+                for (int j = 0; j < FM; ++j) a[v][j][u] = *reinterpret_cast<const gu32x4*>(gp(pa[j]) + at * 64);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < kAhead; ++v)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                // a step past this wavefront's part gets scale bytes 0, and adds nothing
+                const uint32_t width = g + v < g1 && 4 * (g + v) + u < steps ? 8u : 0u;
+                const uint32_t sbw = __builtin_amdgcn_ubfe(cb[v][u], 8 * block, width);
+                const i32x8 vb{(int)b[v][u].x, (int)b[v][u].y, (int)b[v][u].z, (int)b[v][u].w, 0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < FM; ++j) {
+                    const uint32_t sa = __builtin_amdgcn_ubfe(ca[v][j][u], 8 * block, width);
+                    const u32x4 w = a[v][j][u];
+                    const i32x8 va{(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
+                    acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(vb, va, acc[j], 4, 4, 0, (int)sbw, 0, (int)sa);
+                }
+            }
+    }
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sums[wave][j * 4 + r][lane] = acc[j][r];
+    __syncthreads();
+    const int rows = (int)(m < 16 * FM ? m : 16 * FM), waves = blockDim.x / kWave;
+    for (int i = threadIdx.x; i < rows * 16; i += blockDim.x) {
+        const int row = i / 16, col = i % 16;
+        const int r = row / 16 * 4 + col % 4, at = col / 4 * 16 + row % 16;
+        float sum = sums[0][r][at];
+        for (int w = 1; w < waves; ++w) sum += sums[w][r][at];
+        if (n0 + col < n) {
+            if constexpr (sizeof(T) == 4) gp(y)[row * ld + n0 + col] = sum;
+            else gp(y)[row * ld + n0 + col] = (uint16_t)bf16_bits(sum);
+        }
+    }
+}
+
+template <int FM, class T>
+int launch_few(const uint8_t* aq, const uint8_t* as, int64_t m, const uint8_t* bq, const uint8_t* bs, int64_t n, int64_t k,
+               T* y, int64_t ld, hipStream_t st) {
+    const int64_t groups = div_up(k, 512), per = div_up(groups, kFewWaves);
+    hipLaunchKernelGGL((mx4_matmul_few_kernel<FM, T>), dim3((unsigned)div_up(n, 16)), dim3((unsigned)div_up(groups, per) * kWave),
+                       0, st, aq, as, m, bq, bs, n, k, (int)per, y, ld);
     return launch_status();
+}
+
+// How a product is computed.
+enum class Way { kSmall, kFew, kTile128, kTile256 };
+struct Product {
+    Way way;
+    uint32_t tiles_m, tiles_n, splits, per_split;
+    int64_t lw, part;  // of the partial sums: elements of a row and of a split
+};
+
+inline Product product_of(int64_t m, int64_t n, int64_t k) {
+    Product p{Way::kSmall, 0, 0, 1, 0, 0, 0};
+    if (k == 0 || k >= (1 << 22)) return p;
+    if (m <= 32) {
+        p.way = Way::kFew;
+        return p;
+    }
+    if (div_up(m, 256) * div_up(n, 256) > 0x3FFFFFFF) return p;
+    const int64_t groups = div_up(k, 512);
+    p.per_split = (uint32_t)groups;
+    p.way = Way::kTile256;
+    p.tiles_m = (uint32_t)div_up(m, 256);
+    p.tiles_n = (uint32_t)div_up(n, 256);
+    if ((int64_t)p.tiles_m * p.tiles_n >= 160) return p;
+    p.way = Way::kTile128;
+    p.tiles_m = (uint32_t)div_up(m, 128);
+    p.tiles_n = (uint32_t)div_up(n, 128);
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    int64_t splits = 512 / tiles;
+    if (splits > groups / 2) splits = groups / 2;
+    if (splits < 2) return p;
+    p.per_split = (uint32_t)div_up(groups, splits);
+    p.splits = (uint32_t)div_up(groups, p.per_split);
+    p.lw = div_up(n, 64) * 64;
+    p.part = m * p.lw;
+    return p;
 }
 
 template <class T>
 int launch_matmul(const uint8_t* aq, const uint8_t* as, int64_t m, const uint8_t* bq, const uint8_t* bs, int64_t n,
-                  int64_t k, T* y, int64_t ld, hipStream_t st) {
-    if (m >= 256 && n >= 256 && k > 0 && k < (1 << 22))
-        return launch_tile<4, 4>(aq, as, m, bq, bs, n, k, y, ld, st);
-    const int64_t tn = div_up(n, 64), tiles = tn * div_up(m, 64);
-    if (tiles > 0x7FFFFFFFll) return COAT_EINVAL;
-    hipLaunchKernelGGL(mx4_matmul_small_kernel<T>, dim3((unsigned)tiles), dim3(kBlock), 0, st, aq, as, m, bq, bs, n, k,
-                       (uint32_t)tn, y, ld);
+                  int64_t k, T* y, int64_t ld, float* ws, hipStream_t st) {
+    const Product p = product_of(m, n, k);
+    if (p.way == Way::kFew) {
+        return m <= 16 ? launch_few<1>(aq, as, m, bq, bs, n, k, y, ld, st) : launch_few<2>(aq, as, m, bq, bs, n, k, y, ld, st);
+    }
+    if (p.way == Way::kSmall) {
+        const int64_t tn = div_up(n, 64), tiles = tn * div_up(m, 64);
+        if (tiles > 0x7FFFFFFFll) return COAT_EINVAL;
+        hipLaunchKernelGGL(mx4_matmul_small_kernel<T>, dim3((unsigned)tiles), dim3(kBlock), 0, st, aq, as, m, bq, bs, n, k,
+                           (uint32_t)tn, y, ld);
+        return launch_status();
+    }
+    const int64_t items = (int64_t)p.tiles_m * p.tiles_n * p.splits;
+    if (p.way == Way::kTile256) {
+        const unsigned grid = (unsigned)(items < kCUs ? items : kCUs);
+        hipLaunchKernelGGL((mx4_matmul_tile_kernel<4, 4, 1, 128, T>), dim3(grid), dim3(kBlock), 0, st, aq, as, m, bq, bs, n,
+                           k, p.tiles_m, p.tiles_n, 1u, p.per_split, y, ld, (int64_t)0);
+        return launch_status();
+    }
+    const unsigned grid = (unsigned)(items < 2 * kCUs ? items : 2 * kCUs);
+    if (p.splits == 1) {
+        hipLaunchKernelGGL((mx4_matmul_tile_kernel<2, 2, 2, 64, T>), dim3(grid), dim3(kBlock), 0, st, aq, as, m, bq, bs, n,
+                           k, p.tiles_m, p.tiles_n, 1u, p.per_split, y, ld, (int64_t)0);
+        return launch_status();
+    }
+    hipLaunchKernelGGL((mx4_matmul_tile_kernel<2, 2, 2, 64, float>), dim3(grid), dim3(kBlock), 0, st, aq, as, m, bq, bs, n,
+                       k, p.tiles_m, p.tiles_n, p.splits, p.per_split, ws, p.lw, p.part);
+    hipLaunchKernelGGL(mx4_matmul_join_kernel<T>, dim3((unsigned)(div_up(m * p.lw / 4, kBlock) < 8 * kCUs ? div_up(m * p.lw / 4, kBlock) : 8 * kCUs)),
+                       dim3(kBlock), 0, st, (const float*)ws, p.part, p.lw, p.splits, m, n, y, ld);
     return launch_status();
 }
 
@@ -398,19 +574,27 @@ int launch_matmul(const uint8_t* aq, const uint8_t* as, int64_t m, const uint8_t
 
 extern "C" {
 
-size_t coat_mx4_matmul_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+size_t coat_mx4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+    if (m < 1 || n < 1 || k < 1 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return 0;
+    const Product p = product_of(m, n, k);
+    return p.splits > 1 ? (size_t)p.splits * (size_t)p.part * sizeof(float) : 0;
+}
 
 int coat_mx4_matmul(const uint8_t* a_q, const uint8_t* a_s, int64_t m, const uint8_t* b_q, const uint8_t* b_s,
                     int64_t n, int64_t k, void* y, int64_t ld, int32_t dtype, void* workspace, size_t workspace_bytes,
                     coat_stream_t stream) {
     const int rc = check_mx4_matmul(a_q, a_s, m, b_q, b_s, n, k, y, ld, dtype);
     if (rc || m == 0 || n == 0) return rc;
-    (void)workspace;
-    (void)workspace_bytes;
+    const size_t need = coat_mx4_matmul_workspace_bytes(m, n, k);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return COAT_EINVAL;
+        if (!aligned(workspace, 256)) return COAT_EALIGN;
+    }
+    float* ws = static_cast<float*>(workspace);
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     if (dtype == COAT_FP32)
-        return launch_matmul(a_q, a_s, m, b_q, b_s, n, k, static_cast<float*>(y), ld, st);
-    return launch_matmul(a_q, a_s, m, b_q, b_s, n, k, static_cast<uint16_t*>(y), ld, st);
+        return launch_matmul(a_q, a_s, m, b_q, b_s, n, k, static_cast<float*>(y), ld, ws, st);
+    return launch_matmul(a_q, a_s, m, b_q, b_s, n, k, static_cast<uint16_t*>(y), ld, ws, st);
 }
 
 }  // extern "C"
