@@ -237,25 +237,30 @@ def _float_type(t: torch.Tensor, name: str) -> int:
     return kind
 
 
-def _operand(t: torch.Tensor, dtype: torch.dtype, shape, device: torch.device, name: str) -> int:
-    """Address of a tensor without gaps that has this type, shape and device."""
+def _operand(t: torch.Tensor, dtype: torch.dtype, shape, gpu: int, name: str) -> int:
+    """Address of a tensor without gaps that has this type and shape and is on GPU `gpu`."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == gpu and t.is_contiguous():
+        return t.data_ptr()
+    if t.get_device() != gpu:
+        raise ValueError(f"{name} must be on GPU {gpu} like the other tensors, got {t.device}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be on the GPU of the other tensors ({device}), got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _matrix(t: torch.Tensor, name: str) -> int:
-    """Elements from row to row of a GPU matrix whose rows have no gaps."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
+def _gpu_of(t: torch.Tensor, name: str) -> int:
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix, got {t.dim()} dimensions")
+    gpu = t.get_device()
+    if gpu < 0 or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return gpu
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements from row to row of a matrix whose rows have no gaps."""
     rows, cols = t.shape
     ld, step = t.stride()
     if rows > 1 and ld < cols or cols > 1 and step != 1:
@@ -263,30 +268,38 @@ def _matrix(t: torch.Tensor, name: str) -> int:
     return ld if rows > 1 else max(cols, 1)
 
 
-def _run(device: torch.device, stream, call):
-    """call(stream handle) with `device` current."""
-    if stream is not None and stream.device != device:
-        raise ValueError(f"the stream belongs to {stream.device}, the tensors are on {device}")
-    if device.index == torch.cuda.current_device():
-        return call((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
-    with torch.cuda.device(device):
-        return call((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+# torch.cuda.current_stream() builds a Stream object: 2 us, a fifth of a small call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda gpu: torch.cuda.current_stream(gpu).cuda_stream)
 
 
-def _workspace(nbytes: int, workspace: Optional[torch.Tensor], device: torch.device, stream) -> Optional[torch.Tensor]:
+def _call(gpu: int, stream, function, what: str, *args) -> None:
+    """function(*args, stream handle), with GPU `gpu` current."""
+    if stream is not None and stream.device_index != gpu:
+        raise ValueError(f"the stream belongs to GPU {stream.device_index}, the tensors are on GPU {gpu}")
+    if gpu == torch.cuda.current_device():
+        rc = function(*args, _raw_stream(gpu) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(gpu):
+            rc = function(*args, _raw_stream(gpu) if stream is None else stream.cuda_stream)
+    if rc != COAT_OK:
+        raise CoatError(rc, what)
+
+
+def _workspace(nbytes: int, workspace: Optional[torch.Tensor], gpu: int, stream) -> Optional[torch.Tensor]:
     """The caller's workspace, or one of torch's allocator that lasts until the call's work is done."""
     if nbytes == 0:
         return None
     if workspace is not None:
-        if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+        if workspace.get_device() != gpu or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous uint8 tensor on GPU {gpu}")
         if workspace.numel() < nbytes:
             raise ValueError(f"workspace has {workspace.numel()} bytes, the call needs {nbytes}")
         return workspace
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=gpu)
     with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=gpu)
 
 
 def mx4_code_bytes(k: int) -> int:
@@ -305,35 +318,29 @@ def mx4_empty(rows: int, k: int, device="cuda"):
             torch.empty(rows, mx4_scale_bytes(k), dtype=torch.uint8, device=device))
 
 
-def _mx4_operand(q: torch.Tensor, s: torch.Tensor, rows: int, k: int, device: torch.device, name: str):
-    return (_operand(q, torch.uint8, (rows, mx4_code_bytes(k)), device, name + "q"),
-            _operand(s, torch.uint8, (rows, mx4_scale_bytes(k)), device, name + "s"))
+def _mx4_operand(q: torch.Tensor, s: torch.Tensor, rows: int, k: int, gpu: int, names=("q", "s")):
+    return (_operand(q, torch.uint8, (rows, (k + 127) // 128 * 64), gpu, names[0]),
+            _operand(s, torch.uint8, (rows, (k + 511) // 512 * 16), gpu, names[1]))
 
 
 def mx4_quantize(x, q=None, s=None, q_t=None, s_t=None, *, stream=None) -> None:
     """A bf16 or fp32 matrix -> microscaled 4-bit codes and scale bytes, along its
     rows (q, s), its columns (q_t, s_t: the transposed matrix), or both in one pass."""
-    ld = _matrix(x, "x")
-    kind = _float_type(x, "x")
+    gpu, ld, kind = _gpu_of(x, "x"), _row_stride(x, "x"), _float_type(x, "x")
     rows, cols = x.shape
     if (q is None) != (s is None) or (q_t is None) != (s_t is None) or (q is None and q_t is None):
         raise ValueError("codes and scales come in pairs: q with s, q_t with s_t, one pair at least")
-    along = (None, None) if q is None else _mx4_operand(q, s, rows, cols, x.device, "")
-    down = (None, None) if q_t is None else (
-        _operand(q_t, torch.uint8, (cols, mx4_code_bytes(rows)), x.device, "q_t"),
-        _operand(s_t, torch.uint8, (cols, mx4_scale_bytes(rows)), x.device, "s_t"))
-    rc = _run(x.device, stream, lambda st: lib().coat_mx4_quantize(x.data_ptr(), rows, cols, ld, kind, *along, *down, st))
-    _check(rc, "coat_mx4_quantize")
+    along = (None, None) if q is None else _mx4_operand(q, s, rows, cols, gpu)
+    down = (None, None) if q_t is None else _mx4_operand(q_t, s_t, cols, rows, gpu, ("q_t", "s_t"))
+    _call(gpu, stream, lib().coat_mx4_quantize, "coat_mx4_quantize", x.data_ptr(), rows, cols, ld, kind, *along, *down)
 
 
 def mx4_dequantize(q, s, x, *, stream=None) -> None:
     """Microscaled 4-bit codes and scale bytes -> a bf16 or fp32 matrix."""
-    ld = _matrix(x, "x")
-    kind = _float_type(x, "x")
+    gpu, ld, kind = _gpu_of(x, "x"), _row_stride(x, "x"), _float_type(x, "x")
     rows, cols = x.shape
-    qp, sp = _mx4_operand(q, s, rows, cols, x.device, "")
-    rc = _run(x.device, stream, lambda st: lib().coat_mx4_dequantize(qp, sp, rows, cols, x.data_ptr(), ld, kind, st))
-    _check(rc, "coat_mx4_dequantize")
+    qp, sp = _mx4_operand(q, s, rows, cols, gpu)
+    _call(gpu, stream, lib().coat_mx4_dequantize, "coat_mx4_dequantize", qp, sp, rows, cols, x.data_ptr(), ld, kind)
 
 
 def mx4_matmul(a_q, a_s, b_q, b_s, y, *, workspace=None, stream=None) -> None:
@@ -342,19 +349,18 @@ def mx4_matmul(a_q, a_s, b_q, b_s, y, *, workspace=None, stream=None) -> None:
     k is taken from the codes, rounded up to 128 as they are. ``workspace``: uint8,
     at least ``mx4_matmul_workspace_bytes`` long; without one the call takes one
     from torch's allocator."""
-    ld = _matrix(y, "y")
-    kind = _float_type(y, "y")
+    gpu, ld, kind = _gpu_of(y, "y"), _row_stride(y, "y"), _float_type(y, "y")
     m, n = y.shape
     if a_q.dim() != 2:
         raise ValueError("a_q must be a matrix")
     k = a_q.shape[1] * 2
-    ap, asp = _mx4_operand(a_q, a_s, m, k, y.device, "a_")
-    bp, bsp = _mx4_operand(b_q, b_s, n, k, y.device, "b_")
-    nbytes = lib().coat_mx4_matmul_workspace_bytes(m, n, k)
-    ws = _workspace(nbytes, workspace, y.device, stream)
-    rc = _run(y.device, stream, lambda st: lib().coat_mx4_matmul(
-        ap, asp, m, bp, bsp, n, k, y.data_ptr(), ld, kind, ws.data_ptr() if ws is not None else None, nbytes, st))
-    _check(rc, "coat_mx4_matmul")
+    ap, asp = _mx4_operand(a_q, a_s, m, k, gpu, ("a_q", "a_s"))
+    bp, bsp = _mx4_operand(b_q, b_s, n, k, gpu, ("b_q", "b_s"))
+    L = lib()
+    nbytes = L.coat_mx4_matmul_workspace_bytes(m, n, k)
+    ws = _workspace(nbytes, workspace, gpu, stream)
+    _call(gpu, stream, L.coat_mx4_matmul, "coat_mx4_matmul", ap, asp, m, bp, bsp, n, k, y.data_ptr(), ld, kind,
+          ws.data_ptr() if ws is not None else None, nbytes)
 
 
 def mx4_matmul_workspace_bytes(m: int, n: int, k: int) -> int:
@@ -396,34 +402,34 @@ def block_norm(y, r, r_out=None, h=None, *, w_post=None, w_pre=None, gate=None, 
     ``act_quantize`` writes them for the bf16 h (group 16 .. 512, dividing the
     channels), or with fmt FMT_MX4 as ``mx4_quantize`` does along the rows."""
     if r.dim() != 2:
-        raise ValueError("r must be a matrix (tokens, channels)")
+        raise ValueError("r must be a matrix, one row per token")
     if post is None:
         post = w_post is not None
-    shape, dev = r.shape, r.device
+    shape = r.shape
     rows, cols = shape
     b, pt, gate_shape = _border(r, w_post, w_pre, gate, rows_per_gate, scale, eps, post, _float_type(r, "r"))
     bf16 = torch.bfloat16
+    if q_scale is None and q is not None or q is None and q_scale is not None:
+        raise ValueError("q and q_scale come as a pair")
+    if q is not None and fmt != FMT_MX4 and (group < 1 or cols % group):
+        raise ValueError(f"group {group} must divide the {cols} channels")
+    gpu = _gpu_of(r, "r")
     qp = sp = None
-    if q is not None or q_scale is not None:
-        if q is None or q_scale is None:
-            raise ValueError("q and q_scale come as a pair")
+    if q is not None:
         if fmt == FMT_MX4:
             group = 32
-            qp, sp = _mx4_operand(q, q_scale, rows, cols, dev, "")
+            qp, sp = _mx4_operand(q, q_scale, rows, cols, gpu, ("q", "q_scale"))
         else:
-            if group < 1 or cols % group:
-                raise ValueError(f"group {group} must divide the {cols} channels")
-            qp = _operand(q, torch.uint8, shape, dev, "q")
-            sp = _operand(q_scale, torch.float32, (rows, cols // group), dev, "q_scale")
-    args = (_operand(y, bf16, shape, dev, "y") if y is not None else None,
-            _operand(r, r.dtype, shape, dev, "r"),
-            _operand(w_post, pt, (cols,), dev, "w_post") if w_post is not None else None,
-            _operand(w_pre, pt, (cols,), dev, "w_pre") if w_pre is not None else None,
-            _operand(gate, pt, gate_shape, dev, "gate") if gate is not None else None,
-            _operand(r_out, r.dtype, shape, dev, "r_out") if r_out is not None else None,
-            _operand(h, bf16, shape, dev, "h") if h is not None else None)
-    rc = _run(dev, stream, lambda st: lib().coat_block_norm(ctypes.byref(b), *args, qp, sp, group, fmt, st))
-    _check(rc, "coat_block_norm")
+            qp = _operand(q, torch.uint8, shape, gpu, "q")
+            sp = _operand(q_scale, torch.float32, (rows, cols // group), gpu, "q_scale")
+    args = (_operand(y, bf16, shape, gpu, "y") if y is not None else None,
+            _operand(r, r.dtype, shape, gpu, "r"),
+            _operand(w_post, pt, (cols,), gpu, "w_post") if w_post is not None else None,
+            _operand(w_pre, pt, (cols,), gpu, "w_pre") if w_pre is not None else None,
+            _operand(gate, pt, gate_shape, gpu, "gate") if gate is not None else None,
+            _operand(r_out, r.dtype, shape, gpu, "r_out") if r_out is not None else None,
+            _operand(h, bf16, shape, gpu, "h") if h is not None else None)
+    _call(gpu, stream, lib().coat_block_norm, "coat_block_norm", ctypes.byref(b), *args, qp, sp, group, fmt)
 
 
 def block_norm_backward(y, r_out, dr_out, dh, dr, dy=None, *, w_post=None, w_pre=None, gate=None, rows_per_gate=None,
@@ -435,10 +441,10 @@ def block_norm_backward(y, r_out, dr_out, dh, dr, dy=None, *, w_post=None, w_pre
     fp32). ``workspace``: uint8, at least ``block_norm_backward_workspace_bytes`` long;
     without one the call takes one from torch's allocator."""
     if dr.dim() != 2:
-        raise ValueError("dr must be a matrix (tokens, channels)")
+        raise ValueError("dr must be a matrix, one row per token")
     if post is None:
         post = w_post is not None
-    shape, dev = dr.shape, dr.device
+    shape = dr.shape
     rows, cols = shape
     b, pt, gate_shape = _border(dr, w_post, w_pre, gate, rows_per_gate, scale, eps, post, _float_type(dr, "dr"))
     gt = None
@@ -448,24 +454,24 @@ def block_norm_backward(y, r_out, dr_out, dh, dr, dy=None, *, w_post=None, w_pre
                 raise ValueError(f"dw_post, dw_pre and dgate must have one type, got {gt} and {t.dtype}")
             gt = t.dtype
             b.grad_type = _float_type(t, "a weight's gradient")
+    gpu = _gpu_of(dr, "dr")
     bf16 = torch.bfloat16
-    args = (_operand(y, bf16, shape, dev, "y") if y is not None else None,
-            _operand(r_out, dr.dtype, shape, dev, "r_out") if r_out is not None else None,
-            _operand(dr_out, dr.dtype, shape, dev, "dr_out") if dr_out is not None else None,
-            _operand(dh, bf16, shape, dev, "dh") if dh is not None else None,
-            _operand(w_post, pt, (cols,), dev, "w_post") if w_post is not None else None,
-            _operand(w_pre, pt, (cols,), dev, "w_pre") if w_pre is not None else None,
-            _operand(gate, pt, gate_shape, dev, "gate") if gate is not None else None,
-            _operand(dr, dr.dtype, shape, dev, "dr"),
-            _operand(dy, bf16, shape, dev, "dy") if dy is not None else None,
-            _operand(dw_post, gt, (cols,), dev, "dw_post") if dw_post is not None else None,
-            _operand(dw_pre, gt, (cols,), dev, "dw_pre") if dw_pre is not None else None,
-            _operand(dgate, gt, gate_shape, dev, "dgate") if dgate is not None else None)
+    args = (_operand(y, bf16, shape, gpu, "y") if y is not None else None,
+            _operand(r_out, dr.dtype, shape, gpu, "r_out") if r_out is not None else None,
+            _operand(dr_out, dr.dtype, shape, gpu, "dr_out") if dr_out is not None else None,
+            _operand(dh, bf16, shape, gpu, "dh") if dh is not None else None,
+            _operand(w_post, pt, (cols,), gpu, "w_post") if w_post is not None else None,
+            _operand(w_pre, pt, (cols,), gpu, "w_pre") if w_pre is not None else None,
+            _operand(gate, pt, gate_shape, gpu, "gate") if gate is not None else None,
+            _operand(dr, dr.dtype, shape, gpu, "dr"),
+            _operand(dy, bf16, shape, gpu, "dy") if dy is not None else None,
+            _operand(dw_post, gt, (cols,), gpu, "dw_post") if dw_post is not None else None,
+            _operand(dw_pre, gt, (cols,), gpu, "dw_pre") if dw_pre is not None else None,
+            _operand(dgate, gt, gate_shape, gpu, "dgate") if dgate is not None else None)
     nbytes = lib().coat_block_norm_backward_workspace_bytes(ctypes.byref(b)) if gt is not None else 0
-    ws = _workspace(nbytes, workspace, dev, stream)
-    rc = _run(dev, stream, lambda st: lib().coat_block_norm_backward(
-        ctypes.byref(b), *args, ws.data_ptr() if ws is not None else None, nbytes, st))
-    _check(rc, "coat_block_norm_backward")
+    ws = _workspace(nbytes, workspace, gpu, stream)
+    _call(gpu, stream, lib().coat_block_norm_backward, "coat_block_norm_backward", ctypes.byref(b), *args,
+          ws.data_ptr() if ws is not None else None, nbytes)
 
 
 def block_norm_backward_workspace_bytes(rows: int, cols: int, rows_per_gate: Optional[int] = None) -> int:
