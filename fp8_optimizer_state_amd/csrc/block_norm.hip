@@ -1,6 +1,8 @@
 // HIP (gfx950) kernels of the border between two transformer blocks: the norm
 // after a block, the gated residual addition and the norm before the next block,
 // forward (with the layer input in bf16, FP8 or 4-bit form) and backward.
+#include <type_traits>
+
 #include "act_common.h"
 #include "mx4_common.h"
 
@@ -41,20 +43,19 @@ __device__ __forceinline__ void block_sum2(float (&scratch)[2][kMaxWaves][2], in
     }
 }
 
-// 8 values of a weight, gate or gradient array of run-time type.
-__device__ __forceinline__ void load_param8(const void* p, int32_t type, int64_t at, int64_t n, float (&v)[8]) {
-    if (!p) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 1.0f;
-    } else if (type == COAT_FP32) {
-        load8(static_cast<const float*>(p) + at, n, v);
-    } else {
-        load8(static_cast<const uint16_t*>(p) + at, n, v);
-    }
+// 8 values of a weight or gate that may be missing (ones).
+template <bool WHOLE, class P>
+__device__ __forceinline__ Raw8<P> load_param8(const void* p, int64_t at, int64_t n) {
+    if (p) return load_raw8<WHOLE>(static_cast<const P*>(p) + at, n);
+    Raw8<P> r;
+    if constexpr (sizeof(P) == 4) r.lo = r.hi = u32x4{0x3F800000u, 0x3F800000u, 0x3F800000u, 0x3F800000u};
+    else r.w = u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+    return r;
 }
+template <bool WHOLE>
 __device__ __forceinline__ void store_grad8(void* p, int32_t type, int64_t at, int64_t n, const float (&v)[8]) {
-    if (type == COAT_FP32) store8(static_cast<float*>(p) + at, n, v);
-    else store8(static_cast<uint16_t*>(p) + at, n, v);
+    if (type == COAT_FP32) store8<WHOLE>(static_cast<float*>(p) + at, n, v);
+    else store8<WHOLE>(static_cast<uint16_t*>(p) + at, n, v);
 }
 
 // The value a stored element of the stream stands for.
@@ -64,9 +65,9 @@ __device__ __forceinline__ float stored(float v, const uint16_t*) {
 __device__ __forceinline__ float stored(float v, const float*) { return v; }
 
 struct BorderForward {
-    int64_t rows, cols, rpg;
+    int64_t rows, cols, rpg, step;
     float eps, scale, inv_cols;
-    int32_t post, pre, param_type, fmt, lanes;  // lanes: threads that share a group of codes
+    int32_t post, pre, fmt, lanes;  // lanes: threads that share a group of codes
     const uint16_t* y;
     const void *r, *w_post, *w_pre, *gate;
     void* r_out;
@@ -109,47 +110,78 @@ __device__ __forceinline__ void store_codes8(const BorderForward& p, int64_t row
     if ((threadIdx.x & (p.lanes - 1)) == 0) gp(static_cast<float*>(p.q_scale))[at / (8 * p.lanes)] = sc;
 }
 
-template <class S, int NV, int MAXT>
-__global__ __launch_bounds__(MAXT) void border_forward_kernel(BorderForward p) {
+// S the stream's type, P the weights' and gate's, NV chunks a thread, WHOLE:
+// the channels are a multiple of 8. A workgroup takes `step` consecutive rows;
+// the weights, and the gate row while its tokens last, stay in registers.
+template <class S, class P, int NV, bool WHOLE>
+__global__ __launch_bounds__(1024) void border_forward_kernel(BorderForward p) {
     __shared__ float scratch[2][kMaxWaves][2];
     const int tid = threadIdx.x, threads = blockDim.x, waves = threads / kWave;
     int buf = 0;
-    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    int64_t row = (int64_t)blockIdx.x * p.step;
+    const int64_t end = row + p.step < p.rows ? row + p.step : p.rows;
+    Raw8<P> w_post[NV], w_pre[NV], gate[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int64_t c = (int64_t)(i * threads + tid) * 8, n = p.cols - c;
+        w_post[i] = load_param8<WHOLE, P>(p.w_post, c, n);
+        w_pre[i] = load_param8<WHOLE, P>(p.w_pre, c, n);
+        gate[i] = load_param8<WHOLE, P>(nullptr, c, n);
+    }
+    int64_t gate_end = p.gate ? row : end;  // first row that needs another gate row
+    for (; row < end; ++row) {
         const int64_t base = row * p.cols;
         float x[NV][8];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int64_t c = (int64_t)(i * threads + tid) * 8;
-            load8(static_cast<const S*>(p.r) + base + c, p.cols - c, x[i]);
-        }
         if (p.y) {
-            float y[NV][8], ss = 0.0f, none = 0.0f;
+            Raw8<uint16_t> y[NV];
+            Raw8<S> r[NV];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int64_t c = (int64_t)(i * threads + tid) * 8;
-                load8(p.y + base + c, p.cols - c, y[i]);
+                const int64_t c = (int64_t)(i * threads + tid) * 8, n = p.cols - c;
+                y[i] = load_raw8<WHOLE>(p.y + base + c, n);
+                r[i] = load_raw8<WHOLE>(static_cast<const S*>(p.r) + base + c, n);
+            }
+            if (row >= gate_end) {
+                const int64_t g = row / p.rpg;
+                gate_end = (g + 1) * p.rpg;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int64_t c = (int64_t)(i * threads + tid) * 8;
+                    gate[i] = load_param8<WHOLE, P>(p.gate, g * p.cols + c, p.cols - c);
+                }
             }
             float sig = p.scale;
             if (p.post) {
+                float ss = 0.0f, none = 0.0f;
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
+                for (int i = 0; i < NV; ++i) {
+                    float v[8];
+                    expand(y[i], v);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(y[i][j], y[i][j], ss);
+                    for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(v[j], v[j], ss);
+                }
                 block_sum2(scratch, buf, waves, ss, none);
                 buf ^= 1;
                 sig *= __builtin_amdgcn_rsqf(__builtin_fmaf(ss, p.inv_cols, p.eps));
             }
-            const int64_t grow = p.gate ? row / p.rpg : 0;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int64_t c = (int64_t)(i * threads + tid) * 8, n = p.cols - c;
-                float w[8], g[8];
-                load_param8(p.w_post, p.param_type, c, n, w);
-                load_param8(p.gate, p.param_type, grow * p.cols + c, n, g);
+                float v[8], w[8], g[8];
+                expand(y[i], v);
+                expand(w_post[i], w);
+                expand(gate[i], g);
+                expand(r[i], x[i]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    x[i][j] = stored(__builtin_fmaf(y[i][j] * sig * w[j], g[j], x[i][j]), static_cast<const S*>(nullptr));
-                if (p.r_out) store8(static_cast<S*>(p.r_out) + base + c, n, x[i]);
+                    x[i][j] = stored(__builtin_fmaf(v[j] * sig * w[j], g[j], x[i][j]), static_cast<const S*>(nullptr));
+                if (p.r_out) store8<WHOLE>(static_cast<S*>(p.r_out) + base + c, n, x[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int64_t c = (int64_t)(i * threads + tid) * 8;
+                expand(load_raw8<WHOLE>(static_cast<const S*>(p.r) + base + c, p.cols - c), x[i]);
             }
         }
         if (!p.pre) continue;
@@ -165,11 +197,12 @@ __global__ __launch_bounds__(MAXT) void border_forward_kernel(BorderForward p) {
         for (int i = 0; i < NV; ++i) {
             const int64_t c = (int64_t)(i * threads + tid) * 8, n = p.cols - c;
             float w[8];
-            load_param8(p.w_pre, p.param_type, c, n, w);
+            expand(w_pre[i], w);
+            // channels past the end are zeros even where rho is not finite
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                x[i][j] = __builtin_bit_cast(float, bf16_bits(j < n ? x[i][j] * rho * w[j] : 0.0f) << 16);
-            if (p.h) store8(p.h + base + c, n, x[i]);
+                x[i][j] = __builtin_bit_cast(float, bf16_bits((WHOLE ? n > 0 : j < n) ? x[i][j] * rho * w[j] : 0.0f) << 16);
+            if (p.h) store8<WHOLE>(p.h + base + c, n, x[i]);
             if (p.q) store_codes8(p, row, c, x[i]);
         }
     }
@@ -178,7 +211,7 @@ __global__ __launch_bounds__(MAXT) void border_forward_kernel(BorderForward p) {
 struct BorderBackward {
     int64_t rows, cols, rpg, step, chunks;
     float eps, scale, inv_cols;
-    int32_t post, param_type, grad_type;
+    int32_t post, grad_type;
     const uint16_t *y, *dh;
     const void *r, *dr_out, *w_post, *w_pre, *gate;
     void* dr;
@@ -191,8 +224,8 @@ struct BorderBackward {
 // of a gate row, while its tokens last) in registers.
 //   pre:  with u = w_pre dh, s2 = sum r u:  d = dr_out + rho u - r rho^3 s2 / cols
 //   post: with u = w_post scale g d, s4 = sum y u:  dy = sig u - y sig^3 s4 / cols
-template <class S, int NV, int MAXT>
-__global__ __launch_bounds__(MAXT) void border_backward_kernel(BorderBackward p) {
+template <class S, class P, int NV, bool WHOLE>
+__global__ __launch_bounds__(1024) void border_backward_kernel(BorderBackward p) {
     __shared__ float scratch[2][kMaxWaves][2];
     const int tid = threadIdx.x, threads = blockDim.x, waves = threads / kWave;
     int buf = 0;
@@ -206,81 +239,96 @@ __global__ __launch_bounds__(MAXT) void border_backward_kernel(BorderBackward p)
         end = row + p.step;
     }
     if (end > p.rows) end = p.rows;
+    Raw8<P> w_post[NV], w_pre[NV], gate[NV];
     float acc_pre[NV][8], acc_post[NV][8], acc_gate[NV][8];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+        const int64_t c = (int64_t)(i * threads + tid) * 8, n = p.cols - c;
+        w_post[i] = load_param8<WHOLE, P>(p.w_post, c, n);
+        w_pre[i] = load_param8<WHOLE, P>(p.w_pre, c, n);
+        gate[i] = load_param8<WHOLE, P>(nullptr, c, n);
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc_pre[i][j] = acc_post[i][j] = acc_gate[i][j] = 0.0f;
+    }
+    int64_t gate_end = p.gate ? row : end;  // first row that needs another gate row
     for (; row < end; ++row) {
         const int64_t base = row * p.cols;
-        float d[NV][8], x[NV][8], u[NV][8], y[NV][8];
-        float s1 = 0.0f, s2 = 0.0f;
+        Raw8<uint16_t> y[NV], u[NV];
+        Raw8<S> x[NV], dr[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int64_t c = (int64_t)(i * threads + tid) * 8, n = p.cols - c;
-            if (p.dr_out) {
-                load8(static_cast<const S*>(p.dr_out) + base + c, n, d[i]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) d[i][j] = 0.0f;
-            }
             if (p.dh) {
-                load8(static_cast<const S*>(p.r) + base + c, n, x[i]);
-                load8(p.dh + base + c, n, u[i]);
+                x[i] = load_raw8<WHOLE>(static_cast<const S*>(p.r) + base + c, n);
+                u[i] = load_raw8<WHOLE>(p.dh + base + c, n);
             }
-            if (p.y) load8(p.y + base + c, n, y[i]);
+            dr[i] = load_raw8<WHOLE>(static_cast<const S*>(p.dr_out) + base + c, p.dr_out ? n : 0);
+            y[i] = load_raw8<WHOLE>(p.y + base + c, p.y ? n : 0);
         }
-        if (p.dh) {
+        const int64_t g_row = p.gate ? row / p.rpg : 0;
+        if (row >= gate_end) {
+            gate_end = (g_row + 1) * p.rpg;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int64_t c = (int64_t)(i * threads + tid) * 8;
-                float w[8];
-                load_param8(p.w_pre, p.param_type, c, p.cols - c, w);
+                gate[i] = load_param8<WHOLE, P>(p.gate, g_row * p.cols + c, p.cols - c);
+            }
+        }
+        float rho = 0.0f, back = 0.0f;
+        if (p.dh) {
+            float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float xv[8], uv[8], w[8];
+                expand(x[i], xv);
+                expand(u[i], uv);
+                expand(w_pre[i], w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    s1 = __builtin_fmaf(x[i][j], x[i][j], s1);
-                    s2 = __builtin_fmaf(x[i][j] * w[j], u[i][j], s2);
+                    s1 = __builtin_fmaf(xv[j], xv[j], s1);
+                    s2 = __builtin_fmaf(xv[j] * w[j], uv[j], s2);
                 }
             }
             block_sum2(scratch, buf, waves, s1, s2);
             buf ^= 1;
-            const float rho = __builtin_amdgcn_rsqf(__builtin_fmaf(s1, p.inv_cols, p.eps));
-            const float back = rho * rho * rho * (s2 * p.inv_cols);
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int64_t c = (int64_t)(i * threads + tid) * 8;
-                float w[8];
-                load_param8(p.w_pre, p.param_type, c, p.cols - c, w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float ru = rho * u[i][j];
-                    acc_pre[i][j] = __builtin_fmaf(x[i][j], ru, acc_pre[i][j]);
-                    d[i][j] += __builtin_fmaf(ru, w[j], -x[i][j] * back);
-                }
-            }
+            rho = __builtin_amdgcn_rsqf(__builtin_fmaf(s1, p.inv_cols, p.eps));
+            back = rho * rho * rho * (s2 * p.inv_cols);
         }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int64_t c = (int64_t)(i * threads + tid) * 8;
-            store8(static_cast<S*>(p.dr) + base + c, p.cols - c, d[i]);
-        }
-        if (!p.y) continue;
-        const int64_t grow = p.gate ? row / p.rpg : 0;
+        float d[NV][8];
         float s3 = 0.0f, s4 = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int64_t c = (int64_t)(i * threads + tid) * 8, n = p.cols - c;
-            float w[8], g[8];
-            load_param8(p.w_post, p.param_type, c, n, w);
-            load_param8(p.gate, p.param_type, grow * p.cols + c, n, g);
+            expand(dr[i], d[i]);
+            if (p.dh) {
+                float xv[8], uv[8], w[8];
+                expand(x[i], xv);
+                expand(u[i], uv);
+                expand(w_pre[i], w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                d[i][j] *= p.scale;  // scale d, from here on
-                s3 = __builtin_fmaf(y[i][j], y[i][j], s3);
-                s4 = __builtin_fmaf(y[i][j] * w[j], g[j] * d[i][j], s4);
+                for (int j = 0; j < 8; ++j) {
+                    const float ru = rho * uv[j];
+                    acc_pre[i][j] = __builtin_fmaf(xv[j], ru, acc_pre[i][j]);
+                    d[i][j] += __builtin_fmaf(ru, w[j], -xv[j] * back);
+                }
+            }
+            store8<WHOLE>(static_cast<S*>(p.dr) + base + c, n, d[i]);
+            if (p.y) {
+                float yv[8], w[8], g[8];
+                expand(y[i], yv);
+                expand(w_post[i], w);
+                expand(gate[i], g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    d[i][j] *= p.scale;  // scale d, from here on
+                    s3 = __builtin_fmaf(yv[j], yv[j], s3);
+                    s4 = __builtin_fmaf(yv[j] * w[j], g[j] * d[i][j], s4);
+                }
             }
         }
-        float sig = 1.0f, back = 0.0f;
+        if (!p.y) continue;
+        float sig = 1.0f;
+        back = 0.0f;
         if (p.post) {
             block_sum2(scratch, buf, waves, s3, s4);
             buf ^= 1;
@@ -290,23 +338,24 @@ __global__ __launch_bounds__(MAXT) void border_backward_kernel(BorderBackward p)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int64_t c = (int64_t)(i * threads + tid) * 8, n = p.cols - c;
-            float w[8], g[8], out[8];
-            load_param8(p.w_post, p.param_type, c, n, w);
-            load_param8(p.gate, p.param_type, grow * p.cols + c, n, g);
+            float yv[8], w[8], g[8], out[8];
+            expand(y[i], yv);
+            expand(w_post[i], w);
+            expand(gate[i], g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float yn = y[i][j] * sig, gd = g[j] * d[i][j];
+                const float yn = yv[j] * sig, gd = g[j] * d[i][j];
                 acc_post[i][j] = __builtin_fmaf(gd, yn, acc_post[i][j]);
                 acc_gate[i][j] = __builtin_fmaf(d[i][j] * w[j], yn, acc_gate[i][j]);
-                out[j] = __builtin_fmaf(sig * w[j], gd, -y[i][j] * back);
+                out[j] = __builtin_fmaf(sig * w[j], gd, -yv[j] * back);
             }
-            store8(p.dy + base + c, n, out);
+            store8<WHOLE>(p.dy + base + c, n, out);
         }
-        if (p.dgate && p.chunks <= 1 && (row + 1 == end || (row + 1) % p.rpg == 0)) {
+        if (p.dgate && p.chunks <= 1 && (row + 1 == end || row + 1 == gate_end)) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int64_t c = (int64_t)(i * threads + tid) * 8;
-                store_grad8(p.dgate, p.grad_type, grow * p.cols + c, p.cols - c, acc_gate[i]);
+                store_grad8<WHOLE>(p.dgate, p.grad_type, g_row * p.cols + c, p.cols - c, acc_gate[i]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) acc_gate[i][j] = 0.0f;
             }
@@ -316,9 +365,9 @@ __global__ __launch_bounds__(MAXT) void border_backward_kernel(BorderBackward p)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int64_t c = (int64_t)(i * threads + tid) * 8, n = p.cols - c;
-        if (p.part_pre) store8(p.part_pre + part + c, n, acc_pre[i]);
-        if (p.part_post) store8(p.part_post + part + c, n, acc_post[i]);
-        if (p.part_gate) store8(p.part_gate + part + c, n, acc_gate[i]);
+        if (p.part_pre) store8<WHOLE>(p.part_pre + part + c, n, acc_pre[i]);
+        if (p.part_post) store8<WHOLE>(p.part_post + part + c, n, acc_post[i]);
+        if (p.part_gate) store8<WHOLE>(p.part_gate + part + c, n, acc_gate[i]);
     }
 }
 
@@ -365,31 +414,33 @@ __global__ __launch_bounds__(kBlock) void border_reduce_kernel(BorderReduce p) {
     }
 }
 
-// Threads of a workgroup that holds NV chunks a thread of a row.
-inline int border_threads(int64_t cols, int nv) { return (int)div_up(div_up(cols, 8), (int64_t)kWave * nv) * kWave; }
+// Calls launch(NV, WHOLE) as compile-time constants, and the workgroup's threads.
+template <class F>
+void border_shape(int64_t cols, F&& launch) {
+    const bool whole = cols % 8 == 0;
+    const int nv = cols <= 8 * 1024 ? 1 : 2;
+    const dim3 threads((unsigned)(div_up(div_up(cols, 8), (int64_t)kWave * nv) * kWave));
+    using one = std::integral_constant<int, 1>;
+    using two = std::integral_constant<int, 2>;
+    if (nv == 1) whole ? launch(one{}, std::true_type{}, threads) : launch(one{}, std::false_type{}, threads);
+    else whole ? launch(two{}, std::true_type{}, threads) : launch(two{}, std::false_type{}, threads);
+}
 
-template <class S>
-int launch_forward(const BorderForward& p, hipStream_t st) {
-    const int64_t most = (int64_t)kCUs * 8;
-    const dim3 grid((unsigned)(p.rows < most ? p.rows : most));
-    if (p.cols <= 4096)
-        hipLaunchKernelGGL((border_forward_kernel<S, 1, 512>), grid, dim3(border_threads(p.cols, 1)), 0, st, p);
-    else if (p.cols <= 8192)
-        hipLaunchKernelGGL((border_forward_kernel<S, 2, 512>), grid, dim3(border_threads(p.cols, 2)), 0, st, p);
-    else
-        hipLaunchKernelGGL((border_forward_kernel<S, 2, 1024>), grid, dim3(border_threads(p.cols, 2)), 0, st, p);
+template <class S, class P>
+int launch_forward(BorderForward& p, hipStream_t st) {
+    p.step = div_up(p.rows, (int64_t)kCUs * 3);
+    border_shape(p.cols, [&](auto nv, auto whole, dim3 threads) {
+        hipLaunchKernelGGL((border_forward_kernel<S, P, nv.value, whole.value>), dim3((unsigned)div_up(p.rows, p.step)), threads,
+                           0, st, p);
+    });
     return launch_status();
 }
 
-template <class S>
+template <class S, class P>
 int launch_backward(const BorderBackward& p, int64_t blocks, hipStream_t st) {
-    const dim3 grid((unsigned)blocks);
-    if (p.cols <= 4096)
-        hipLaunchKernelGGL((border_backward_kernel<S, 1, 512>), grid, dim3(border_threads(p.cols, 1)), 0, st, p);
-    else if (p.cols <= 8192)
-        hipLaunchKernelGGL((border_backward_kernel<S, 2, 512>), grid, dim3(border_threads(p.cols, 2)), 0, st, p);
-    else
-        hipLaunchKernelGGL((border_backward_kernel<S, 2, 1024>), grid, dim3(border_threads(p.cols, 2)), 0, st, p);
+    border_shape(p.cols, [&](auto nv, auto whole, dim3 threads) {
+        hipLaunchKernelGGL((border_backward_kernel<S, P, nv.value, whole.value>), dim3((unsigned)blocks), threads, 0, st, p);
+    });
     return launch_status();
 }
 
@@ -413,7 +464,6 @@ int coat_block_norm(const coat_border* b, const uint16_t* y, const void* r, cons
     p.inv_cols = (float)(1.0 / (double)b->cols);
     p.post = b->post;
     p.pre = h || q;
-    p.param_type = b->param_type;
     p.fmt = fmt;
     p.lanes = q ? group / 8 : 1;
     p.y = y;
@@ -426,7 +476,9 @@ int coat_block_norm(const coat_border* b, const uint16_t* y, const void* r, cons
     p.q = q;
     p.q_scale = q_scale;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-    return b->stream_type == COAT_FP32 ? launch_forward<float>(p, st) : launch_forward<uint16_t>(p, st);
+    if (b->param_type == COAT_FP32)
+        return b->stream_type == COAT_FP32 ? launch_forward<float, float>(p, st) : launch_forward<uint16_t, float>(p, st);
+    return b->stream_type == COAT_FP32 ? launch_forward<float, uint16_t>(p, st) : launch_forward<uint16_t, uint16_t>(p, st);
 }
 
 size_t coat_block_norm_backward_workspace_bytes(const coat_border* b) { return border_workspace_bytes(b); }
@@ -452,7 +504,6 @@ int coat_block_norm_backward(const coat_border* b, const uint16_t* y, const void
     p.scale = b->scale;
     p.inv_cols = (float)(1.0 / (double)b->cols);
     p.post = b->post;
-    p.param_type = b->param_type;
     p.grad_type = b->grad_type;
     p.y = y;
     p.dh = dh;
@@ -468,8 +519,11 @@ int coat_block_norm_backward(const coat_border* b, const uint16_t* y, const void
     p.part_post = dw_post ? ws + section : nullptr;
     p.part_gate = dgate && split.chunks > 1 ? ws + 2 * section : nullptr;
     if (b->rows > 0) {
-        const int run = b->stream_type == COAT_FP32 ? launch_backward<float>(p, split.blocks, st)
-                                                    : launch_backward<uint16_t>(p, split.blocks, st);
+        const bool s32 = b->stream_type == COAT_FP32;
+        const int run = b->param_type == COAT_FP32 ? (s32 ? launch_backward<float, float>(p, split.blocks, st)
+                                                          : launch_backward<uint16_t, float>(p, split.blocks, st))
+                                                   : (s32 ? launch_backward<float, uint16_t>(p, split.blocks, st)
+                                                          : launch_backward<uint16_t, uint16_t>(p, split.blocks, st));
         if (run) return run;
     }
     if (!dw_pre && !dw_post && !p.part_gate) return COAT_OK;

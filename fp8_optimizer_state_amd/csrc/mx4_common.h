@@ -22,58 +22,88 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __builtin_bit_cast
 __device__ __forceinline__ uint32_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) { return bf16_bits(lo) | (bf16_bits(hi) << 16); }
 
-// 8 consecutive elements from p, of which the first n (maybe < 1) exist; the others are zero.
-__device__ __forceinline__ void load8(const uint16_t* p, int64_t n, float (&v)[8]) {
-    if (n >= 8) {
-        const u32x4 a = *reinterpret_cast<const gu32x4_a2*>(gp(p));
+// 8 stored elements, as they come from memory.
+template <class E>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+    u32x4 w;
+};
+template <>
+struct Raw8<float> {
+    u32x4 lo, hi;
+};
+
+__device__ __forceinline__ void expand(const Raw8<uint16_t>& r, float (&v)[8]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = bf16_lo(a[i]);
-            v[2 * i + 1] = bf16_hi(a[i]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-        if (n < 1) return;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {  // the first element stands in for those past the end
-            const float e = bf16_lo(gp(p)[i < n ? i : 0]);
-            v[i] = i < n ? e : 0.0f;
-        }
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(r.w[i]);
+        v[2 * i + 1] = bf16_hi(r.w[i]);
     }
 }
-__device__ __forceinline__ void load8(const float* p, int64_t n, float (&v)[8]) {
-    if (n >= 8) {
-        const u32x4 a = *reinterpret_cast<const gu32x4_a4*>(gp(p));
-        const u32x4 b = *reinterpret_cast<const gu32x4_a4*>(gp(p) + 4);
+__device__ __forceinline__ void expand(const Raw8<float>& r, float (&v)[8]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = as_float(a[i]);
-            v[4 + i] = as_float(b[i]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-        if (n < 1) return;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {  // the first element stands in for those past the end
-            const float e = gp(p)[i < n ? i : 0];
-            v[i] = i < n ? e : 0.0f;
-        }
+    for (int i = 0; i < 4; ++i) {
+        v[i] = as_float(r.lo[i]);
+        v[4 + i] = as_float(r.hi[i]);
     }
 }
 
-// 8 consecutive elements to p, of which the first n exist.
+// 8 consecutive elements from p, of which the first n (maybe < 1) exist; the
+// others are zero. WHOLE: n is at least 8 or at most 0.
+template <bool WHOLE = false>
+__device__ __forceinline__ Raw8<uint16_t> load_raw8(const uint16_t* p, int64_t n) {
+    Raw8<uint16_t> r;
+    if (n >= 8) {
+        r.w = *reinterpret_cast<const gu32x4_a2*>(gp(p));
+        return r;
+    }
+    r.w = u32x4{0u, 0u, 0u, 0u};
+    if (WHOLE || n < 1) return r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // the first element stands in for those past the end
+        const uint32_t e = gp(p)[i < n ? i : 0];
+        r.w[i >> 1] |= i < n ? e << (16 * (i & 1)) : 0u;
+    }
+    return r;
+}
+template <bool WHOLE = false>
+__device__ __forceinline__ Raw8<float> load_raw8(const float* p, int64_t n) {
+    Raw8<float> r;
+    if (n >= 8) {
+        r.lo = *reinterpret_cast<const gu32x4_a4*>(gp(p));
+        r.hi = *reinterpret_cast<const gu32x4_a4*>(gp(p) + 4);
+        return r;
+    }
+    r.lo = r.hi = u32x4{0u, 0u, 0u, 0u};
+    if (WHOLE || n < 1) return r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float e = gp(p)[i < n ? i : 0];
+        const uint32_t b = i < n ? __builtin_bit_cast(uint32_t, e) : 0u;
+        if (i < 4) r.lo[i] = b;
+        else r.hi[i - 4] = b;
+    }
+    return r;
+}
+template <class E>
+__device__ __forceinline__ void load8(const E* p, int64_t n, float (&v)[8]) {
+    expand(load_raw8(p, n), v);
+}
+
+// 8 consecutive elements to p, of which the first n exist. WHOLE: as above.
+template <bool WHOLE = false>
 __device__ __forceinline__ void store8(uint16_t* p, int64_t n, const float (&v)[8]) {
     if (n >= 8) {
         *reinterpret_cast<gu32x4_a2*>(gp(p)) =
             u32x4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
-    } else {
+    } else if (!WHOLE) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i < n) gp(p)[i] = (uint16_t)bf16_bits(v[i]);
     }
 }
+template <bool WHOLE = false>
 __device__ __forceinline__ void store8(float* p, int64_t n, const float (&v)[8]) {
     if (n >= 8) {
         u32x4 a, b;
@@ -84,7 +114,7 @@ __device__ __forceinline__ void store8(float* p, int64_t n, const float (&v)[8])
         }
         *reinterpret_cast<gu32x4_a4*>(gp(p)) = a;
         *reinterpret_cast<gu32x4_a4*>(gp(p) + 4) = b;
-    } else {
+    } else if (!WHOLE) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i < n) gp(p)[i] = v[i];
