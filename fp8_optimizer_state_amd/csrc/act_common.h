@@ -47,24 +47,26 @@ __device__ __forceinline__ uint32_t group_umax(uint32_t v, int lanes) {
     return v;
 }
 
-// The scale of a group with magnitude bits `amax_bits`: RN32(amax / fpmax), NaN if the group holds an Inf or NaN.
+// The scale of a group with magnitude bits `amax_bits`: RN32(amax / fpmax), NaN
+// if the group holds an Inf or NaN. The product with RN64(1 / fpmax), rounded to
+// fp32, is that quotient by the argument above (amax has 8 significant bits).
 template <int F>
 __device__ __forceinline__ float act_scale(uint32_t amax_bits) {
     const float amax = __builtin_bit_cast(float, amax_bits << 16);
-    return amax_bits >= 0x7F80u ? __builtin_nanf("") : (float)((double)amax / Fmt<F>::FPMAX);
+    return amax_bits >= 0x7F80u ? __builtin_nanf("") : (float)((double)amax * (1.0 / Fmt<F>::FPMAX));
 }
 
 // Codes of the 2 NW bf16 values in w (value i in half i & 1 of word i >> 1) for
-// a group with magnitude bits `amax_bits`; returns the NW / 2 code words.
+// a group with magnitude bits `amax_bits` and their scale `sc`; returns the
+// NW / 2 code words.
 template <int F, int NW>
-__device__ __forceinline__ void act_codes(const uint32_t (&w)[NW], uint32_t amax_bits, uint32_t (&out)[NW / 2]) {
+__device__ __forceinline__ void act_codes(const uint32_t (&w)[NW], uint32_t amax_bits, float sc, uint32_t (&out)[NW / 2]) {
     using T = Fmt<F>;
     if (amax_bits >= 0x7F80u) {  // Inf or NaN in the group
 #pragma unroll
         for (int i = 0; i < NW / 2; ++i) out[i] = 0x7F7F7F7Fu;
         return;
     }
-    const float sc = act_scale<F>(amax_bits);
     if (sc == 0.0f) {  // all zero: the sign alone
 #pragma unroll
         for (int i = 0; i < NW / 2; ++i) {
@@ -78,7 +80,12 @@ __device__ __forceinline__ void act_codes(const uint32_t (&w)[NW], uint32_t amax
         }
         return;
     }
-    const double r = 1.0 / (double)sc;  // RN64(1 / s); fp64 holds it for a subnormal s too
+    // 1 / s by the hardware's estimate and two Newton steps: within 2^-51 of it,
+    // x times it within 2^-50, so the argument above holds
+    const double s = (double)sc;
+    double r = __builtin_amdgcn_rcp(s);
+    r = __builtin_fma(__builtin_fma(-s, r, 1.0), r, r);
+    r = __builtin_fma(__builtin_fma(-s, r, 1.0), r, r);
 #pragma unroll
     for (int i = 0; i < NW / 2; ++i) {
         float y[4];

@@ -42,11 +42,10 @@ __global__ __launch_bounds__(kBlock) void act_quantize_group_kernel(const uint16
     auto code = [&](int64_t e0, const uint32_t (&w)[8]) {
         const uint32_t am = group_umax(bf16_absmax_bits(w), lpg);
         uint32_t c[4];
-        act_codes<F>(w, am, c);
+        const float sc = act_scale<F>(am);
+        act_codes<F>(w, am, sc, c);
         act_store16(q, n, e0, c);
-        if ((lane & (lpg - 1)) == 0 && e0 < n) {
-            gp(s)[e0 >> lg2_group] = act_scale<F>(am);
-        }
+        if ((lane & (lpg - 1)) == 0 && e0 < n) gp(s)[e0 >> lg2_group] = sc;
     };
     // two tiles per iteration: both tiles' loads are in flight together
     int64_t tile = wave_id();
@@ -120,7 +119,7 @@ __global__ __launch_bounds__(kBlock) void act_quantize_tensor_kernel(const uint1
     const uint32_t am = __builtin_amdgcn_readfirstlane(gp(acc)[0]);
     auto code = [&](int64_t e0, const uint32_t (&w)[8]) {
         uint32_t c[4];
-        act_codes<F>(w, am, c);
+        act_codes<F>(w, am, act_scale<F>(am), c);
         act_store16(q, n, e0, c);
     };
     // two tiles per iteration: both tiles' loads are in flight together

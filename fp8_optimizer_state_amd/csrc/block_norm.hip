@@ -98,11 +98,11 @@ __device__ __forceinline__ void store_codes8(const BorderForward& p, int64_t row
     const uint32_t am = group_umax(bf16_absmax_bits(w), p.lanes);
     float sc;
     if (p.fmt == COAT_FMT_E4M3) {
-        act_codes<COAT_FMT_E4M3>(w, am, code);
         sc = act_scale<COAT_FMT_E4M3>(am);
+        act_codes<COAT_FMT_E4M3>(w, am, sc, code);
     } else {
-        act_codes<COAT_FMT_E5M2>(w, am, code);
         sc = act_scale<COAT_FMT_E5M2>(am);
+        act_codes<COAT_FMT_E5M2>(w, am, sc, code);
     }
     if (c >= p.cols) return;
     const int64_t at = row * p.cols + c;  // a multiple of 8: groups divide the row
@@ -239,16 +239,50 @@ __global__ __launch_bounds__(1024) void border_backward_kernel(BorderBackward p)
         end = row + p.step;
     }
     if (end > p.rows) end = p.rows;
+    // With two chunks a thread the registers do not hold everything (13824
+    // channels: 1667 us for 16384 rows with the spills): the weights are read for
+    // each row, and two of the three sums lie in LDS, each thread's own.
+    constexpr bool KEEP = NV == 1;
+    __shared__ f32x4 sums[KEEP ? 1 : 2 * NV * 2 * 1024];  // [array][chunk][half chunk][thread]
+    auto get = [&](int array, int i, const float (&kept)[8], float (&v)[8]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            f32x4 q;
+            if constexpr (!KEEP) q = sums[((array * NV + i) * 2 + h) * 1024 + tid];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[4 * h + j] = KEEP ? kept[4 * h + j] : q[j];
+        }
+    };
+    auto put = [&](int array, int i, float (&kept)[8], const float (&v)[8]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (!KEEP) {
+                sums[((array * NV + i) * 2 + h) * 1024 + tid] = f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) kept[4 * h + j] = v[4 * h + j];
+            }
+        }
+    };
+    const float zeros[8] = {};
     Raw8<P> w_post[NV], w_pre[NV], gate[NV];
+    auto weight = [&](const Raw8<P>& kept, const void* from, int64_t at, int64_t c, float (&v)[8]) {
+        if constexpr (KEEP) expand(kept, v);
+        else expand(load_param8<WHOLE, P>(from, at + c, p.cols - c), v);
+    };
     float acc_pre[NV][8], acc_post[NV][8], acc_gate[NV][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int64_t c = (int64_t)(i * threads + tid) * 8, n = p.cols - c;
-        w_post[i] = load_param8<WHOLE, P>(p.w_post, c, n);
-        w_pre[i] = load_param8<WHOLE, P>(p.w_pre, c, n);
-        gate[i] = load_param8<WHOLE, P>(nullptr, c, n);
+        if constexpr (KEEP) {
+            w_post[i] = load_param8<WHOLE, P>(p.w_post, c, n);
+            w_pre[i] = load_param8<WHOLE, P>(p.w_pre, c, n);
+            gate[i] = load_param8<WHOLE, P>(nullptr, c, n);
+        }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc_pre[i][j] = acc_post[i][j] = acc_gate[i][j] = 0.0f;
+        for (int j = 0; j < 8; ++j) acc_pre[i][j] = 0.0f;
+        put(0, i, acc_post[i], zeros);
+        put(1, i, acc_gate[i], zeros);
     }
     int64_t gate_end = p.gate ? row : end;  // first row that needs another gate row
     for (; row < end; ++row) {
@@ -268,10 +302,12 @@ __global__ __launch_bounds__(1024) void border_backward_kernel(BorderBackward p)
         const int64_t g_row = p.gate ? row / p.rpg : 0;
         if (row >= gate_end) {
             gate_end = (g_row + 1) * p.rpg;
+            if constexpr (KEEP) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int64_t c = (int64_t)(i * threads + tid) * 8;
-                gate[i] = load_param8<WHOLE, P>(p.gate, g_row * p.cols + c, p.cols - c);
+                for (int i = 0; i < NV; ++i) {
+                    const int64_t c = (int64_t)(i * threads + tid) * 8;
+                    gate[i] = load_param8<WHOLE, P>(p.gate, g_row * p.cols + c, p.cols - c);
+                }
             }
         }
         float rho = 0.0f, back = 0.0f;
@@ -279,10 +315,11 @@ __global__ __launch_bounds__(1024) void border_backward_kernel(BorderBackward p)
             float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
+                const int64_t c = (int64_t)(i * threads + tid) * 8;
                 float xv[8], uv[8], w[8];
                 expand(x[i], xv);
                 expand(u[i], uv);
-                expand(w_pre[i], w);
+                weight(w_pre[i], p.w_pre, 0, c, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     s1 = __builtin_fmaf(xv[j], xv[j], s1);
@@ -304,7 +341,7 @@ __global__ __launch_bounds__(1024) void border_backward_kernel(BorderBackward p)
                 float xv[8], uv[8], w[8];
                 expand(x[i], xv);
                 expand(u[i], uv);
-                expand(w_pre[i], w);
+                weight(w_pre[i], p.w_pre, 0, c, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float ru = rho * uv[j];
@@ -316,8 +353,8 @@ __global__ __launch_bounds__(1024) void border_backward_kernel(BorderBackward p)
             if (p.y) {
                 float yv[8], w[8], g[8];
                 expand(y[i], yv);
-                expand(w_post[i], w);
-                expand(gate[i], g);
+                weight(w_post[i], p.w_post, 0, c, w);
+                weight(gate[i], p.gate, g_row * p.cols, c, g);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     d[i][j] *= p.scale;  // scale d, from here on
@@ -338,26 +375,31 @@ __global__ __launch_bounds__(1024) void border_backward_kernel(BorderBackward p)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int64_t c = (int64_t)(i * threads + tid) * 8, n = p.cols - c;
-            float yv[8], w[8], g[8], out[8];
+            float yv[8], w[8], g[8], out[8], post[8], gates[8];
+            get(0, i, acc_post[i], post);
+            get(1, i, acc_gate[i], gates);
             expand(y[i], yv);
-            expand(w_post[i], w);
-            expand(gate[i], g);
+            weight(w_post[i], p.w_post, 0, c, w);
+            weight(gate[i], p.gate, g_row * p.cols, c, g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float yn = yv[j] * sig, gd = g[j] * d[i][j];
-                acc_post[i][j] = __builtin_fmaf(gd, yn, acc_post[i][j]);
-                acc_gate[i][j] = __builtin_fmaf(d[i][j] * w[j], yn, acc_gate[i][j]);
+                post[j] = __builtin_fmaf(gd, yn, post[j]);
+                gates[j] = __builtin_fmaf(d[i][j] * w[j], yn, gates[j]);
                 out[j] = __builtin_fmaf(sig * w[j], gd, -yv[j] * back);
             }
+            put(0, i, acc_post[i], post);
+            put(1, i, acc_gate[i], gates);
             store8<WHOLE>(p.dy + base + c, n, out);
         }
         if (p.dgate && p.chunks <= 1 && (row + 1 == end || row + 1 == gate_end)) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int64_t c = (int64_t)(i * threads + tid) * 8;
-                store_grad8<WHOLE>(p.dgate, p.grad_type, g_row * p.cols + c, p.cols - c, acc_gate[i]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) acc_gate[i][j] = 0.0f;
+                float gates[8];
+                get(1, i, acc_gate[i], gates);
+                store_grad8<WHOLE>(p.dgate, p.grad_type, g_row * p.cols + c, p.cols - c, gates);
+                put(1, i, acc_gate[i], zeros);
             }
         }
     }
@@ -366,22 +408,25 @@ __global__ __launch_bounds__(1024) void border_backward_kernel(BorderBackward p)
     for (int i = 0; i < NV; ++i) {
         const int64_t c = (int64_t)(i * threads + tid) * 8, n = p.cols - c;
         if (p.part_pre) store8<WHOLE>(p.part_pre + part + c, n, acc_pre[i]);
-        if (p.part_post) store8<WHOLE>(p.part_post + part + c, n, acc_post[i]);
-        if (p.part_gate) store8<WHOLE>(p.part_gate + part + c, n, acc_gate[i]);
+        float v[8];
+        get(0, i, acc_post[i], v);
+        if (p.part_post) store8<WHOLE>(p.part_post + part + c, n, v);
+        get(1, i, acc_gate[i], v);
+        if (p.part_gate) store8<WHOLE>(p.part_gate + part + c, n, v);
     }
 }
 
 // Sums the partial rows of each array, in the order of the workgroups: a
-// wavefront takes a quarter of the rows of 64 columns, the quarters are added
-// in order. blockIdx.y: 0 the pre-norm's weights, 1 the post-norm's, 2 + g gate row g.
+// wavefront takes a sixteenth of the rows of 64 columns, the parts are added in
+// order. blockIdx.y: 0 the pre-norm's weights, 1 the post-norm's, 2 + g gate row g.
 struct BorderReduce {
     const float *pre, *post, *gate;
     void *dw_pre, *dw_post, *dgate;
     int64_t blocks, chunks, cols;
     int32_t grad_type;
 };
-__global__ __launch_bounds__(kBlock) void border_reduce_kernel(BorderReduce p) {
-    __shared__ float sums[kWavesPerBlock][kWave];
+__global__ __launch_bounds__(kMaxWaves * kWave) void border_reduce_kernel(BorderReduce p) {
+    __shared__ float sums[kMaxWaves][kWave];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int64_t c = (int64_t)blockIdx.x * kWave + lane;
     const float* src = p.pre;
@@ -398,17 +443,19 @@ __global__ __launch_bounds__(kBlock) void border_reduce_kernel(BorderReduce p) {
         at += g * p.cols;
     }
     if (!dst) return;
-    const int64_t quarter = (count + kWavesPerBlock - 1) / kWavesPerBlock;
-    const int64_t b1 = (wave + 1) * quarter < count ? (wave + 1) * quarter : count;
+    const int64_t part = (count + kMaxWaves - 1) / kMaxWaves;
+    const int64_t b1 = (wave + 1) * part < count ? (wave + 1) * part : count;
     float sum = 0.0f;
     if (c < p.cols) {
 #pragma unroll 8
-        for (int64_t b = wave * quarter; b < b1; ++b) sum += gp(src)[b * p.cols + c];
+        for (int64_t b = wave * part; b < b1; ++b) sum += gp(src)[b * p.cols + c];
     }
     sums[wave][lane] = sum;
     __syncthreads();
     if (wave == 0 && c < p.cols) {
-        sum = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kMaxWaves; ++i) sum += sums[i][lane];
         if (p.grad_type == COAT_FP32) gp(static_cast<float*>(dst))[at] = sum;
         else gp(static_cast<uint16_t*>(dst))[at] = (uint16_t)bf16_bits(sum);
     }
@@ -418,8 +465,8 @@ __global__ __launch_bounds__(kBlock) void border_reduce_kernel(BorderReduce p) {
 template <class F>
 void border_shape(int64_t cols, F&& launch) {
     const bool whole = cols % 8 == 0;
-    const int nv = cols <= 8 * 1024 ? 1 : 2;
-    const dim3 threads((unsigned)(div_up(div_up(cols, 8), (int64_t)kWave * nv) * kWave));
+    const int nv = border_chunks(cols);
+    const dim3 threads((unsigned)(border_waves(cols) * kWave));
     using one = std::integral_constant<int, 1>;
     using two = std::integral_constant<int, 2>;
     if (nv == 1) whole ? launch(one{}, std::true_type{}, threads) : launch(one{}, std::false_type{}, threads);
@@ -428,8 +475,14 @@ void border_shape(int64_t cols, F&& launch) {
 
 template <class S, class P>
 int launch_forward(BorderForward& p, hipStream_t st) {
-    p.step = div_up(p.rows, (int64_t)kCUs * 3);
     border_shape(p.cols, [&](auto nv, auto whole, dim3 threads) {
+        // as many workgroups as run at once (24 wavefronts on a compute unit):
+        // 16384 x 5120 takes 144 us with 2 of 10 wavefronts each, 152 with 3, 162
+        // with 4; small ones hide their barriers better when there are twice as
+        // many (16384 x 1024: 28 us with 16 of 2 wavefronts, 45 with 3, 26 with 32)
+        const int64_t waves = threads.x / kWave;
+        const int64_t each = waves > 12 ? 1 : 24 / waves;
+        p.step = div_up(p.rows, kCUs * (waves <= 4 ? 2 * each : each));
         hipLaunchKernelGGL((border_forward_kernel<S, P, nv.value, whole.value>), dim3((unsigned)div_up(p.rows, p.step)), threads,
                            0, st, p);
     });
@@ -491,7 +544,7 @@ int coat_block_norm_backward(const coat_border* b, const uint16_t* y, const void
                                              dgate, workspace, workspace_bytes);
     if (rc) return rc;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-    const BorderSplit split = border_split(b->rows, b->rows_per_gate, dgate != nullptr);
+    const BorderSplit split = border_split(b->rows, b->cols, b->rows_per_gate, dgate != nullptr);
     const size_t section = border_section_bytes(split.blocks, b->cols) / sizeof(float);
     float* ws = static_cast<float*>(workspace);
     BorderBackward p;
@@ -539,7 +592,7 @@ int coat_block_norm_backward(const coat_border* b, const uint16_t* y, const void
     red.cols = b->cols;
     red.grad_type = b->grad_type;
     const unsigned gates = p.part_gate ? (unsigned)(split.blocks / split.chunks) : 0u;
-    hipLaunchKernelGGL(border_reduce_kernel, dim3((unsigned)div_up(b->cols, kWave), 2 + gates), dim3(kBlock), 0, st, red);
+    hipLaunchKernelGGL(border_reduce_kernel, dim3((unsigned)div_up(b->cols, kWave), 2 + gates), dim3(kMaxWaves * kWave), 0, st, red);
     return launch_status();
 }
 

@@ -123,7 +123,7 @@ def test_backward_workspace_is_enough_for_every_split():
     for rows in (1, 2, 511, 512, 513, 1024, 5000, 16384, 1 << 20):
         for rpg in (1, 2, 3, 7, 100, rows // 2 + 1, rows):
             most = max(most, coat.block_norm_backward_workspace_bytes(rows, 64, rpg))
-    assert 0 < most <= 3 * 1100 * 64 * 4
+    assert 0 < most <= 3 * 2 * 1024 * 64 * 4
 
 
 # ---------------------------------------------------------------- the binding (tensors without a GPU)
