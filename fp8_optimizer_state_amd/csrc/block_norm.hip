@@ -78,23 +78,20 @@ struct BorderForward {
 
 // Stores 8 channels of a layer input (given as their bf16 bits) in the stored form asked for.
 __device__ __forceinline__ void store_codes8(const BorderForward& p, int64_t row, int64_t c, const float (&v)[8]) {
+    Raw8<uint16_t> raw;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        raw.w[i] = (__builtin_bit_cast(uint32_t, v[2 * i]) >> 16) | (__builtin_bit_cast(uint32_t, v[2 * i + 1]) & 0xFFFF0000u);
     if (p.fmt == COAT_FMT_MX4) {
         const int64_t qb = mx4_code_bytes(p.cols), sb = mx4_scale_bytes(p.cols);
-        uint32_t am = absmax_bits(v);
-        uint32_t o = xlane32(am, 1);
-        am = am > o ? am : o;
-        o = xlane32(am, 2);
-        am = am > o ? am : o;
-        const uint32_t b = mx4_scale_byte(am);
-        const uint32_t code = b == 255u ? 0u : mx4_codes8(v, b);
+        const uint32_t b = mx4_scale_byte(block_max(absmax_bits(raw)));
+        const uint32_t code = b == 255u ? 0u : mx4_codes8(raw, b);
         if (c / 2 < qb) *reinterpret_cast<gu32*>(gp(p.q) + row * qb + c / 2) = code;
         if ((threadIdx.x & 3) == 0 && c / 32 < sb) gp(static_cast<uint8_t*>(p.q_scale))[row * sb + c / 32] = (uint8_t)b;
         return;
     }
-    uint32_t w[4], code[2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = (__builtin_bit_cast(uint32_t, v[2 * i]) >> 16) | (__builtin_bit_cast(uint32_t, v[2 * i + 1]) & 0xFFFF0000u);
+    const uint32_t w[4] = {raw.w[0], raw.w[1], raw.w[2], raw.w[3]};
+    uint32_t code[2];
     const uint32_t am = group_umax(bf16_absmax_bits(w), p.lanes);
     float sc;
     if (p.fmt == COAT_FMT_E4M3) {

@@ -27,18 +27,13 @@ __global__ __launch_bounds__(kBlock) void mx4_quantize_rows_kernel(const T* __re
         uint8_t* qr = q + (int64_t)row * qb;
         uint8_t* sr = s + (int64_t)row * sb;
         const int64_t c0 = (int64_t)seg * kSeg + lane * 8;
-        float v[4][8];
+        Raw8<T> v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) load8(xr + c0 + i * 8 * kWave, cols - (c0 + i * 8 * kWave), v[i]);
+        for (int i = 0; i < 4; ++i) v[i] = load_raw8(xr + c0 + i * 8 * kWave, cols - (c0 + i * 8 * kWave));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t c = c0 + i * 8 * kWave;
-            uint32_t am = absmax_bits(v[i]);
-            uint32_t o = xlane32(am, 1);
-            am = am > o ? am : o;
-            o = xlane32(am, 2);
-            am = am > o ? am : o;
-            const uint32_t b = mx4_scale_byte(am);
+            const uint32_t b = mx4_scale_byte(block_max(absmax_bits(v[i])));
             const uint32_t code = b == 255u ? 0u : mx4_codes8(v[i], b);
             if (c / 2 < qb) *reinterpret_cast<gu32*>(gp(qr) + c / 2) = code;
             if ((lane & 3) == 0 && c / 32 < sb) gp(sr)[c / 32] = (uint8_t)b;
@@ -59,20 +54,32 @@ __global__ __launch_bounds__(kBlock) void mx4_dequantize_kernel(const uint8_t* _
         T* xr = x + (int64_t)row * ld;
         const uint8_t* qr = q + (int64_t)row * qb;
         const uint8_t* sr = s + (int64_t)row * sb;
-        const int64_t c0 = (int64_t)seg * kSeg + lane * 8;
-        uint32_t code[4], b[4];
+        // a lane's values of a step fill 16 bytes, so that a store covers consecutive bytes
+        constexpr int kPer = 16 / sizeof(T), kSteps = kSeg / kPer / kWave;
+        const int64_t c0 = (int64_t)seg * kSeg + lane * kPer;
+        uint32_t code[kSteps], b[kSteps];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t c = c0 + i * 8 * kWave;
-            code[i] = c < cols ? *reinterpret_cast<const gu32*>(gp(qr) + c / 2) : 0u;
-            b[i] = c < cols ? gp(sr)[c / 32] : 0u;
+        for (int i = 0; i < kSteps; ++i) {
+            const int64_t c = c0 + i * kPer * kWave;
+            code[i] = b[i] = 0u;
+            if (c < cols) {
+                if constexpr (kPer == 8) code[i] = *reinterpret_cast<const gu32*>(gp(qr) + c / 2);
+                else code[i] = *reinterpret_cast<const gu16*>(gp(qr) + c / 2);
+                b[i] = gp(sr)[c / 32];
+            }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t c = c0 + i * 8 * kWave;
-            float v[8];
-            mx4_values8(code[i], b[i], v);
-            if (c < cols) store8(xr + c, cols - c, v);
+        for (int i = 0; i < kSteps; ++i) {
+            const int64_t c = c0 + i * kPer * kWave;
+            float v[kPer];
+#pragma unroll
+            for (int j = 0; j < kPer; j += 4) {
+                float w[4];
+                mx4_values4(code[i] >> (4 * j), b[i], w);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[j + k] = w[k];
+            }
+            if (c < cols) store16(xr + c, cols - c, v);
         }
     }
 }
@@ -84,20 +91,70 @@ __global__ __launch_bounds__(kBlock) void mx4_dequantize_kernel(const uint8_t* _
 // then each thread quantizes blocks of 32 values down a column.
 constexpr int kTileRows = 128, kTileCols = 128;
 
-__device__ __forceinline__ void to_lds8(uint16_t* p, const float (&v)[8]) {
-    // bf16 values read from bf16: the upper halves are the values
-    u32x4 w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = (__builtin_bit_cast(uint32_t, v[2 * i]) >> 16) | (__builtin_bit_cast(uint32_t, v[2 * i + 1]) & 0xFFFF0000u);
-    *reinterpret_cast<u32x4*>(p) = w;
+__device__ __forceinline__ void to_lds8(uint16_t* p, const Raw8<uint16_t>& r) { *reinterpret_cast<u32x4*>(p) = r.w; }
+__device__ __forceinline__ void to_lds8(float* p, const Raw8<float>& r) {
+    *reinterpret_cast<u32x4*>(p) = r.lo;
+    *reinterpret_cast<u32x4*>(p + 4) = r.hi;
 }
-__device__ __forceinline__ void to_lds8(float* p, const float (&v)[8]) {
+
+// Where a block of 32 values down column c goes.
+struct Down {
+    uint8_t *q, *s;
+    int64_t qb, sb, cols;
+    __device__ __forceinline__ void put(int64_t r, int64_t c, uint32_t b, const u32x4& code) const {
+        if (c >= cols) return;
+        if (r / 2 < qb) *reinterpret_cast<gu32x4*>(gp(q) + c * qb + r / 2) = b == 255u ? u32x4{0u, 0u, 0u, 0u} : code;
+        if (r / 32 < sb) gp(s)[c * sb + r / 32] = (uint8_t)b;
+    }
+};
+
+// Quantizes the blocks of a tile in LDS down its columns. bf16: a thread takes a
+// block of two columns, so that it reads whole words.
+__device__ __forceinline__ void quantize_down(const uint16_t (&tile)[kTileRows][kTileCols], int64_t r0, int64_t c0, const Down& to) {
+    for (int i = threadIdx.x; i < kTileCols / 2 * (kTileRows / 32); i += kBlock) {
+        const int lc = i % (kTileCols / 2) * 2, lr = i / (kTileCols / 2) * 32;
+        uint32_t w[32], m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = v[i];
+        for (int j = 0; j < 32; ++j) {
+            w[j] = *reinterpret_cast<const uint32_t*>(&tile[lr + j][lc]);
+            m = bf16_max2(m, w[j]);
+        }
+        const uint32_t b0 = mx4_scale_byte(m << 16), b1 = mx4_scale_byte(m & 0xFFFF0000u);
+        u32x4 q0, q1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            Raw8<uint16_t> x0, x1;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t even = w[8 * j + 2 * k], odd = w[8 * j + 2 * k + 1];
+                x0.w[k] = __builtin_amdgcn_perm(odd, even, 0x05040100u);
+                x1.w[k] = __builtin_amdgcn_perm(odd, even, 0x07060302u);
+            }
+            q0[j] = mx4_codes8(x0, b0);
+            q1[j] = mx4_codes8(x1, b1);
+        }
+        to.put(r0 + lr, c0 + lc, b0, q0);
+        to.put(r0 + lr, c0 + lc + 1, b1, q1);
+    }
 }
-__device__ __forceinline__ float from_lds(uint16_t h) { return __builtin_bit_cast(float, (uint32_t)h << 16); }
-__device__ __forceinline__ float from_lds(float f) { return f; }
+__device__ __forceinline__ void quantize_down(const float (&tile)[kTileRows][kTileCols], int64_t r0, int64_t c0, const Down& to) {
+    for (int i = threadIdx.x; i < kTileCols * (kTileRows / 32); i += kBlock) {
+        const int lc = i % kTileCols, lr = i / kTileCols * 32;
+        Raw8<float> x[4];
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[j].lo[k] = __builtin_bit_cast(uint32_t, tile[lr + 8 * j + k][lc]);
+                x[j].hi[k] = __builtin_bit_cast(uint32_t, tile[lr + 8 * j + 4 + k][lc]);
+            }
+            m = umax(m, absmax_bits(x[j]));
+        }
+        const uint32_t b = mx4_scale_byte(m);
+        to.put(r0 + lr, c0 + lc, b, u32x4{mx4_codes8(x[0], b), mx4_codes8(x[1], b), mx4_codes8(x[2], b), mx4_codes8(x[3], b)});
+    }
+}
 
 template <class T, bool ROWS>
 __global__ __launch_bounds__(kBlock) void mx4_quantize_tile_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
@@ -105,52 +162,31 @@ __global__ __launch_bounds__(kBlock) void mx4_quantize_tile_kernel(const T* __re
                                                                    uint8_t* __restrict__ q, uint8_t* __restrict__ s,
                                                                    uint8_t* __restrict__ qt, uint8_t* __restrict__ st) {
     __shared__ __attribute__((aligned(16))) T tile[kTileRows][kTileCols];
-    const int64_t r0 = (int64_t)(blockIdx.x % tiles_r) * kTileRows, c0 = (int64_t)(blockIdx.x / tiles_r) * kTileCols;
+    // Neighbouring tiles write parts of the same lines of codes and scale bytes
+    // (64 bytes and 4 a tile), so patches of 4 x 4 tiles are taken one after the
+    // other on one XCD: consecutive workgroups run on different XCDs.
+    uint32_t t = blockIdx.x;
+    if (gridDim.x % 8 == 0) t = (t & 7) * (gridDim.x / 8) + (t >> 3);
+    const uint32_t patch = t / 16, patches_r = tiles_r / 4;
+    const int64_t r0 = (int64_t)(patch % patches_r * 4 + t % 4) * kTileRows;
+    const int64_t c0 = (int64_t)(patch / patches_r * 4 + t / 4 % 4) * kTileCols;
     const int tid = threadIdx.x;
     const int64_t qb = mx4_code_bytes(cols), sb = mx4_scale_bytes(cols);
-    const int64_t qtb = mx4_code_bytes(rows), stb = mx4_scale_bytes(rows);
 #pragma unroll 4
     for (int i = 0; i < kTileRows * kTileCols / 8 / kBlock; ++i) {
         const int lr = i * (kBlock * 8 / kTileCols) + tid / (kTileCols / 8), lc = (tid % (kTileCols / 8)) * 8;
         const int64_t r = r0 + lr, c = c0 + lc;
-        float v[8];
-        load8(x + r * ld + c, r < rows ? cols - c : 0, v);
+        const Raw8<T> v = load_raw8(x + r * ld + c, r < rows ? cols - c : 0);
         to_lds8(&tile[lr][lc], v);
         if (ROWS) {
-            uint32_t am = absmax_bits(v);
-            uint32_t o = xlane32(am, 1);
-            am = am > o ? am : o;
-            o = xlane32(am, 2);
-            am = am > o ? am : o;
-            const uint32_t b = mx4_scale_byte(am);
+            const uint32_t b = mx4_scale_byte(block_max(absmax_bits(v)));
             const uint32_t code = b == 255u ? 0u : mx4_codes8(v, b);
             if (r < rows && c / 2 < qb) *reinterpret_cast<gu32*>(gp(q) + r * qb + c / 2) = code;
             if ((tid & 3) == 0 && r < rows && c / 32 < sb) gp(s)[r * sb + c / 32] = (uint8_t)b;
         }
     }
     __syncthreads();
-    for (int i = tid; i < kTileCols * (kTileRows / 32); i += kBlock) {
-        const int lc = i % kTileCols, rb = i / kTileCols;
-        const int64_t c = c0 + lc, r = r0 + rb * 32;
-        if (c >= cols) continue;
-        float v[4][8];
-        uint32_t am = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[j][k] = from_lds(tile[rb * 32 + j * 8 + k][lc]);
-            const uint32_t a = absmax_bits(v[j]);
-            am = am > a ? am : a;
-        }
-        const uint32_t b = mx4_scale_byte(am);
-        u32x4 code{0u, 0u, 0u, 0u};
-        if (b != 255u) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) code[j] = mx4_codes8(v[j], b);
-        }
-        if (r / 2 < qtb) *reinterpret_cast<gu32x4*>(gp(qt) + c * qtb + r / 2) = code;
-        if (r / 32 < stb) gp(st)[c * stb + r / 32] = (uint8_t)b;
-    }
+    quantize_down(tile, r0, c0, Down{qt, st, mx4_code_bytes(rows), mx4_scale_bytes(rows), cols});
 }
 
 template <class T>
@@ -164,7 +200,7 @@ int launch_quantize(const T* x, int64_t rows, int64_t cols, int64_t ld, uint8_t*
                            (uint32_t)items, (uint32_t)segs, cols, ld, q, s);
         return launch_status();
     }
-    // the tiles reach to the end of the scale bytes of either direction
+    // the tiles reach to the end of the scale bytes of either direction: four of them, 512 values
     const int64_t tr = div_up(32 * mx4_scale_bytes(rows), kTileRows), tc = div_up(32 * mx4_scale_bytes(cols), kTileCols);
     if (tr * tc > 0x7FFFFFFFll) return COAT_EINVAL;
     if (q)

@@ -16,6 +16,7 @@ typedef __attribute__((address_space(1))) u32x4_a4 gu32x4_a4;
 typedef __attribute__((address_space(1))) u32x2 gu32x2;
 
 __device__ __forceinline__ float as_float(uint32_t w) { return __builtin_bit_cast(float, w); }
+__device__ __forceinline__ bf16x2 word_bf16(uint32_t w) { return __builtin_bit_cast(bf16x2, w); }
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
 // Round to nearest even; a NaN stays one.
@@ -121,16 +122,39 @@ __device__ __forceinline__ void store8(float* p, int64_t n, const float (&v)[8])
     }
 }
 
-__device__ __forceinline__ uint32_t magnitude_bits(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
+// 16 bytes of elements to p, of which the first n exist.
+__device__ __forceinline__ void store16(uint16_t* p, int64_t n, const float (&v)[8]) { store8(p, n, v); }
+__device__ __forceinline__ void store16(float* p, int64_t n, const float (&v)[4]) {
+    if (n >= 4) {
+        *reinterpret_cast<gu32x4_a4*>(gp(p)) =
+            u32x4{__builtin_bit_cast(uint32_t, v[0]), __builtin_bit_cast(uint32_t, v[1]), __builtin_bit_cast(uint32_t, v[2]),
+                  __builtin_bit_cast(uint32_t, v[3])};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) gp(p)[i] = v[i];
+    }
+}
 
-template <int N>
-__device__ __forceinline__ uint32_t absmax_bits(const float (&v)[N]) {
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// Larger magnitude of each half of two words of bf16 (w's sign bits are dropped, m has none).
+__device__ __forceinline__ uint32_t bf16_max2(uint32_t m, uint32_t w) {
+    const u16x2 a = __builtin_bit_cast(u16x2, m), b = __builtin_bit_cast(u16x2, w & 0x7FFF7FFFu);
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(a, b));
+}
+
+// fp32 bits of the largest magnitude of 8 stored elements.
+__device__ __forceinline__ uint32_t absmax_bits(const Raw8<uint16_t>& r) {
+    uint32_t m = bf16_max2(bf16_max2(bf16_max2(bf16_max2(0u, r.w[0]), r.w[1]), r.w[2]), r.w[3]);
+    return umax(m << 16, m & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint32_t absmax_bits(const Raw8<float>& r) {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const uint32_t a = magnitude_bits(v[i]);
-        m = m > a ? m : a;
-    }
+    for (int i = 0; i < 4; ++i) m = umax(m, umax(r.lo[i] & 0x7FFFFFFFu, r.hi[i] & 0x7FFFFFFFu));
     return m;
 }
 
@@ -142,31 +166,41 @@ __device__ __forceinline__ uint32_t mx4_scale_byte(uint32_t amax_bits) {
     return f >= 255u ? 255u : (f > 2u ? f - 2u : 0u);
 }
 
-// Codes of 8 values of a block with scale byte b (not 0xFF), the first in the
-// low bits. x 2^-e is exact in fp32 wherever the result can be over the
-// smallest rounding border (1/4); the convert rounds to nearest, ties to the
-// even code, and cuts at 6.
-__device__ __forceinline__ uint32_t mx4_codes8(const float (&v)[8], uint32_t b) {
-    const float up = __builtin_bit_cast(float, (254u - b) << 23);  // 2^-e
-    uint32_t c = 0;
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0] * up, v[1] * up, 1.0f, 0);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2] * up, v[3] * up, 1.0f, 1);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4] * up, v[5] * up, 1.0f, 2);
-    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6] * up, v[7] * up, 1.0f, 3);
-    return c;
+// The largest fp32 bits of the four lanes that share a block of 32 values.
+__device__ __forceinline__ uint32_t block_max(uint32_t am) {
+    am = umax(am, xlane32(am, 1));
+    return umax(am, xlane32(am, 2));
 }
 
-// Values of 8 codes of a block with scale byte b.
-__device__ __forceinline__ void mx4_values8(uint32_t c, uint32_t b, float (&v)[8]) {
+// Codes of 8 elements of a block with scale byte b (not 0xFF), the first in the
+// low bits. The convert divides by the power of two whose exponent field is b
+// (2^-127 for b = 0), rounds to nearest, ties to the even code, and cuts at 6;
+// tests pin that for every bf16 value and for fp32 values about each border.
+__device__ __forceinline__ uint32_t mx4_codes8(const Raw8<uint16_t>& r, uint32_t b) {
+    const float scale = as_float(b << 23);
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, word_bf16(r.w[0]), scale, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, word_bf16(r.w[1]), scale, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, word_bf16(r.w[2]), scale, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, word_bf16(r.w[3]), scale, 3);
+}
+__device__ __forceinline__ uint32_t mx4_codes8(const Raw8<float>& r, uint32_t b) {
+    const float scale = as_float(b << 23);
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, as_float(r.lo[0]), as_float(r.lo[1]), scale, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, as_float(r.lo[2]), as_float(r.lo[3]), scale, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, as_float(r.hi[0]), as_float(r.hi[1]), scale, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, as_float(r.hi[2]), as_float(r.hi[3]), scale, 3);
+}
+
+// Values of 4 codes (the low half of c) of a block with scale byte b.
+__device__ __forceinline__ void mx4_values4(uint32_t c, uint32_t b, float (&v)[4]) {
     const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0);
     const f32x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1);
-    const f32x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2);
-    const f32x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3);
     v[0] = p0.x; v[1] = p0.y; v[2] = p1.x; v[3] = p1.y;
-    v[4] = p2.x; v[5] = p2.y; v[6] = p3.x; v[7] = p3.y;
     const int e = (int)b - 127;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = b == 255u ? __builtin_nanf("") : __builtin_amdgcn_ldexpf(v[i], e);
+    for (int i = 0; i < 4; ++i) v[i] = b == 255u ? __builtin_nanf("") : __builtin_amdgcn_ldexpf(v[i], e);
 }
 
 }  // namespace
