@@ -91,12 +91,6 @@ __global__ __launch_bounds__(kBlock) void mx4_dequantize_kernel(const uint8_t* _
 // then each thread quantizes blocks of 32 values down a column.
 constexpr int kTileRows = 128, kTileCols = 128;
 
-__device__ __forceinline__ void to_lds8(uint16_t* p, const Raw8<uint16_t>& r) { *reinterpret_cast<u32x4*>(p) = r.w; }
-__device__ __forceinline__ void to_lds8(float* p, const Raw8<float>& r) {
-    *reinterpret_cast<u32x4*>(p) = r.lo;
-    *reinterpret_cast<u32x4*>(p + 4) = r.hi;
-}
-
 // Where a block of 32 values down column c goes.
 struct Down {
     uint8_t *q, *s;
@@ -108,15 +102,29 @@ struct Down {
     }
 };
 
-// Quantizes the blocks of a tile in LDS down its columns. bf16: a thread takes a
-// block of two columns, so that it reads whole words.
+// Quantizes the blocks of a tile in LDS down its columns. Four consecutive lanes
+// take the four blocks of a column, so that they store 64 consecutive bytes; to
+// spread them over the banks, chunk c (16 bytes) of row r lies at position
+// c ^ (4 (r / 32)). bf16: a thread takes two columns, whole words.
+template <class T>
+__device__ __forceinline__ int tile_col(int r, int c) {
+    constexpr int kChunk = 16 / sizeof(T);
+    return c ^ (r / 32 * 4 * kChunk);
+}
+__device__ __forceinline__ void to_lds8(uint16_t* row, int r, int c, const Raw8<uint16_t>& v) {
+    *reinterpret_cast<u32x4*>(row + tile_col<uint16_t>(r, c)) = v.w;
+}
+__device__ __forceinline__ void to_lds8(float* row, int r, int c, const Raw8<float>& v) {
+    *reinterpret_cast<u32x4*>(row + tile_col<float>(r, c)) = v.lo;
+    *reinterpret_cast<u32x4*>(row + tile_col<float>(r, c + 4)) = v.hi;
+}
 __device__ __forceinline__ void quantize_down(const uint16_t (&tile)[kTileRows][kTileCols], int64_t r0, int64_t c0, const Down& to) {
     for (int i = threadIdx.x; i < kTileCols / 2 * (kTileRows / 32); i += kBlock) {
-        const int lc = i % (kTileCols / 2) * 2, lr = i / (kTileCols / 2) * 32;
+        const int lc = i / 4 * 2, lr = i % 4 * 32;
         uint32_t w[32], m = 0;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-            w[j] = *reinterpret_cast<const uint32_t*>(&tile[lr + j][lc]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&tile[lr + j][tile_col<uint16_t>(lr, lc)]);
             m = bf16_max2(m, w[j]);
         }
         const uint32_t b0 = mx4_scale_byte(m << 16), b1 = mx4_scale_byte(m & 0xFFFF0000u);
@@ -139,15 +147,15 @@ __device__ __forceinline__ void quantize_down(const uint16_t (&tile)[kTileRows][
 }
 __device__ __forceinline__ void quantize_down(const float (&tile)[kTileRows][kTileCols], int64_t r0, int64_t c0, const Down& to) {
     for (int i = threadIdx.x; i < kTileCols * (kTileRows / 32); i += kBlock) {
-        const int lc = i % kTileCols, lr = i / kTileCols * 32;
+        const int lc = i / 4, lr = i % 4 * 32, at = tile_col<float>(lr, lc);
         Raw8<float> x[4];
         uint32_t m = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                x[j].lo[k] = __builtin_bit_cast(uint32_t, tile[lr + 8 * j + k][lc]);
-                x[j].hi[k] = __builtin_bit_cast(uint32_t, tile[lr + 8 * j + 4 + k][lc]);
+                x[j].lo[k] = __builtin_bit_cast(uint32_t, tile[lr + 8 * j + k][at]);
+                x[j].hi[k] = __builtin_bit_cast(uint32_t, tile[lr + 8 * j + 4 + k][at]);
             }
             m = umax(m, absmax_bits(x[j]));
         }
@@ -177,7 +185,7 @@ __global__ __launch_bounds__(kBlock) void mx4_quantize_tile_kernel(const T* __re
         const int lr = i * (kBlock * 8 / kTileCols) + tid / (kTileCols / 8), lc = (tid % (kTileCols / 8)) * 8;
         const int64_t r = r0 + lr, c = c0 + lc;
         const Raw8<T> v = load_raw8(x + r * ld + c, r < rows ? cols - c : 0);
-        to_lds8(&tile[lr][lc], v);
+        to_lds8(tile[lr], lr, lc, v);
         if (ROWS) {
             const uint32_t b = mx4_scale_byte(block_max(absmax_bits(v)));
             const uint32_t code = b == 255u ? 0u : mx4_codes8(v, b);
