@@ -67,21 +67,22 @@ __global__ __launch_bounds__(kBlock) void mx4_matmul_small_kernel(const uint8_t*
 // ------------------------------------------------------------------ large tiles
 //
 // A workgroup of 2 x 2 wavefronts computes tiles of 64 FN rows of B by 64 FM
-// rows of A, one after the other; the steps of 128 values of k of all its tiles
-// form one stream. A step's codes (64 bytes a row, B's rows before A's) go
-// straight from global memory into one of four LDS slots, four steps before
-// they are used; the scale bytes of four steps (16 a row) likewise into one of
-// two. A step is computed in two halves of 64 values of k: while one half's
-// matrix instructions run, the next half's fragments are read from LDS. One
-// barrier a step, between its halves: behind it every wavefront has read step s
-// (its slot may be refilled) and step s + 1 has arrived.
+// rows of A, one after the other; the k of all its tiles forms one stream of
+// steps of 128 values, two steps a pair, four a group. A pair's codes (128
+// bytes a row, B's rows before A's) go straight from global memory into one of
+// PAIRS slots of LDS, PAIRS pairs before they are used; a group's scale bytes
+// (16 a row) likewise. 128 bytes a row, because a compute unit takes in 130
+// bytes a nanosecond in such runs and 80 in runs of 64.
 //
-// LDS reads are 16 bytes a lane from 32 rows 64 bytes apart; chunk c of row r
-// lies at position c ^ (r / 4 % 4), so that any 16 rows reach 16 different
+// A pair is computed in phases: while one phase's matrix instructions run, the
+// next one's fragments are read from LDS. One barrier a pair, before its last
+// phase: behind it every wavefront has read the pair (its slot may be refilled)
+// and the next pair has arrived.
+//
+// LDS reads are 16 bytes a lane from 32 rows 128 bytes apart; chunk c of row r
+// lies at position c ^ (r / 2 % 8), so that any 16 rows reach 16 different
 // 16-byte columns of the banks. The loads write LDS in lane order, so the lane
-// that fills position p of row r fetches chunk p ^ (r / 4 % 4).
-constexpr int kSlots = 4;
-
+// that fills position p of row r fetches chunk p ^ (r / 2 % 8).
 template <int N>
 __device__ __forceinline__ void wait_vm_and_lds_then_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
@@ -96,26 +97,39 @@ __device__ __forceinline__ void load_to_lds16(uint32_t lds, uint32_t off, const 
 
 __device__ __forceinline__ uint32_t float_bits(float v) { return __builtin_bit_cast(uint32_t, v); }
 
-// A 16-byte chunk of y, of which the first n elements exist. y is written past
-// the caches' usual order: kept there it would drive out the operands (16384 x
-// 16384 x 512 to bf16: 158 us against 214).
+// A 16-byte chunk of y, of which the first n elements exist. PAST: written past
+// the caches' usual order, where y would drive the operands out of them (16384 x
+// 16384 x 512 to bf16 in large tiles: 158 us against 214).
+template <bool PAST>
 __device__ __forceinline__ void store_chunk(float* p, int64_t n, const u32x4& w) {
     if (n >= 4) {
-        __builtin_nontemporal_store(w, reinterpret_cast<gu32x4_a4*>(gp(p)));
+        if constexpr (PAST) __builtin_nontemporal_store(w, reinterpret_cast<gu32x4_a4*>(gp(p)));
+        else *reinterpret_cast<gu32x4_a4*>(gp(p)) = w;
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (i < n) gp(p)[i] = as_float(w[i]);
     }
 }
+template <bool PAST>
 __device__ __forceinline__ void store_chunk(uint16_t* p, int64_t n, const u32x4& w) {
     if (n >= 8) {
-        __builtin_nontemporal_store(w, reinterpret_cast<gu32x4_a2*>(gp(p)));
+        if constexpr (PAST) __builtin_nontemporal_store(w, reinterpret_cast<gu32x4_a2*>(gp(p)));
+        else *reinterpret_cast<gu32x4_a2*>(gp(p)) = w;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i < n) gp(p)[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
     }
+}
+
+// The same, or nothing if `on` is 0 (one branch within a long run of code).
+template <uint32_t AT>
+__device__ __forceinline__ void load_to_lds16_if(uint32_t on, uint32_t lds, uint32_t off, const uint8_t* base) {
+    asm volatile(
+        "s_cmp_eq_u32 %4, 0\n\ts_cbranch_scc1 .Lskip%=\n\ts_add_u32 m0, %0, %3\n\ts_nop 0\n\t"
+        "global_load_lds_dwordx4 %1, %2\n.Lskip%=:" ::"s"(lds), "v"(off), "s"(base), "n"(AT), "s"(on)
+        : "memory", "scc");
 }
 
 // f(0), f(1), ... f(N - 1) with the index known to the compiler.
@@ -127,25 +141,32 @@ __device__ __forceinline__ void each(F&& f) {
     }
 }
 
-// Where a workgroup reads its next four steps.
+// Where a workgroup reads its next group of steps.
 struct Stream {
     const uint8_t *bq, *aq, *bs, *as;  // first rows of the tile, at the group's first step
-    uint32_t step[4];                  // byte offsets of the steps; one past the end of k is fetched from the last and not used
+    // Byte offset of the second pair, and for each pair whether its second step is
+    // past the end of k. What is past the end is not read: the first pair, or step,
+    // is fetched in its place and not used.
+    uint32_t second;
+    bool odd[2];
 };
 
 // With splits > 1 item t is the product over the groups of four steps
 // [s per_split, (s + 1) per_split), s = t / tiles, of tile t % tiles, and goes to
 // y + s part (partial sums, added by another kernel).
-template <int FN, int FM, int PER_EU, int PIECE, class T>
-__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(PER_EU, PER_EU))) void mx4_matmul_tile_kernel(
+template <int FN, int FM, int PAIRS, class T>
+__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) void mx4_matmul_tile_kernel(
     const uint8_t* __restrict__ aq, const uint8_t* __restrict__ as, int64_t m, const uint8_t* __restrict__ bq,
     const uint8_t* __restrict__ bs, int64_t n, int64_t k, uint32_t tiles_m, uint32_t tiles_n, uint32_t splits,
     uint32_t per_split, T* __restrict__ y, int64_t ld, int64_t part) {
-    constexpr int BN = 64 * FN, BM = 64 * FM, D = FN + FM, SC = (FN + FM) / 4;
-    constexpr uint32_t kSlotBytes = (BN + BM) * 64, kScaleBytes = (BN + BM) * 16;
+    // D fragments of a half step; 2 D loads of a pair and SC of a group's scale bytes by each wavefront
+    constexpr int BN = 64 * FN, BM = 64 * FM, D = FN + FM, SC = (FN + FM) / 4, SETS = PAIRS / 2;
+    constexpr bool AHEAD = FN * FM <= 4;  // a phase is a step, not half a step
+    constexpr int PHASES = AHEAD ? 2 : 4, PIECE = 128;
+    constexpr uint32_t kSlotBytes = (BN + BM) * 128, kScaleBytes = (BN + BM) * 16;
     // stores of a whole tile, an exact count: later waits let them run
     constexpr int kStores = FN * FM * (sizeof(T) == 4 ? 4 : 2);
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kSlots * kSlotBytes + 2 * kScaleBytes + kWavesPerBlock * 32 * PIECE];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[PAIRS * kSlotBytes + (SETS + 1) * kScaleBytes + kWavesPerBlock * 32 * PIECE];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int half = lane >> 5, l32 = lane & 31;
@@ -162,14 +183,15 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(PER_EU, 
         n0 = (int64_t)(in / high) * BN;
     };
     // byte offsets of this lane's chunks and scale words from the tile's first rows
-    uint32_t off[D], soff[SC];
+    const uint32_t chunk = (lane & 7) ^ ((wave & 1) * 4 + (lane >> 4));
+    const uint32_t back = chunk >= 4 ? 64 : 0;  // to the same chunk of the pair's first step
+    uint32_t off[2 * D], soff[SC];
     auto offsets = [&](int64_t m0, int64_t n0) {
 #pragma unroll
-        for (int i = 0; i < D; ++i) {
-            const uint32_t row = (uint32_t)(i * 4 + wave) * 16 + lane / 4 - (i < FN ? 0 : BN);
-            const int64_t left = (i < FN ? n - n0 : m - m0) - 1;  // the last row stands in for those past the end
-            const uint32_t r = row < left ? row : (uint32_t)left;
-            off[i] = r * (uint32_t)qb + (((lane & 3) ^ ((lane >> 4) & 3)) * 16);
+        for (int i = 0; i < 2 * D; ++i) {
+            const uint32_t row = (uint32_t)(i * 4 + wave) * 8 + lane / 8 - (i < 2 * FN ? 0 : BN);
+            const int64_t left = (i < 2 * FN ? n - n0 : m - m0) - 1;  // the last row stands in for those past the end
+            off[i] = (row < left ? row : (uint32_t)left) * (uint32_t)qb + chunk * 16;
         }
 #pragma unroll
         for (int i = 0; i < SC; ++i) {
@@ -181,38 +203,41 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(PER_EU, 
         }
     };
     const uint32_t lds_wave = lds0 + wave * 1024;
-    auto fetch_part = [&](const Stream& at, auto u, auto i) {
-        load_to_lds16<u * kSlotBytes + i * 4096>(lds_wave, off[i], (i < FN ? at.bq : at.aq) + at.step[u]);
+    auto fetch_part = [&](const Stream& at, int set, auto pair, auto i, uint32_t on = 1) {
+        const uint8_t* from = (i < 2 * FN ? at.bq : at.aq) + (pair == 1 ? at.second : 0);
+        const uint32_t to = lds_wave + set * 2 * kSlotBytes, lane_off = off[i] - (at.odd[pair] ? back : 0);
+        if (__builtin_constant_p(on)) load_to_lds16<pair * kSlotBytes + i * 4096>(to, lane_off, from);
+        else load_to_lds16_if<pair * kSlotBytes + i * 4096>(on, to, lane_off, from);
     };
     auto fetch_scales = [&](const Stream& at, int slot) {
         each<SC>([&](auto i) {
-            load_to_lds16<kSlots * kSlotBytes + i * 4096>(lds_wave + slot * kScaleBytes, soff[i],
-                                                          (i * 4 + wave) * 64 < BN ? at.bs : at.as);
+            load_to_lds16<PAIRS * kSlotBytes + i * 4096>(lds_wave + slot * kScaleBytes, soff[i],
+                                                         (i * 4 + wave) * 64 < BN ? at.bs : at.as);
         });
     };
     auto stream_of = [&](int64_t m0, int64_t n0, uint32_t g) {
-        const uint32_t last = steps - 4 * g - 1;
+        const uint32_t left = steps - 4 * g;
         return Stream{bq + n0 * qb + g * 256, aq + m0 * qb + g * 256, bs + n0 * sb + g * 16, as + m0 * sb + g * 16,
-                      {0, 64 * (last < 1 ? last : 1), 64 * (last < 2 ? last : 2), 64 * (last < 3 ? last : 3)}};
+                      left > 2 ? 128u : 0u, {left == 1, left == 1 || left == 3}};
     };
 
-    u32x4 fb[2][FN], fa[2][FM];    // fragments, by half
-    uint32_t cb[2][FN], ca[2][FM];  // scale words, by parity of the step
+    u32x4 fb[AHEAD ? 2 : 1][2][FN], fa[AHEAD ? 2 : 1][2][FM];  // fragments, [parity of the step][half]
+    uint32_t cb[2][FN], ca[2][FM];                             // scale words, by parity of the step
     const int wn = (wave & 1) * FN * 32, wm = (wave >> 1) * FM * 32;
-    // fragment i of a half step: A's first, which every row of matrix instructions needs
-    auto read_frag = [&](int u, int h, int i) {
-        const int pos = ((2 * h + half) ^ ((l32 >> 2) & 3)) * 16;
-        const uint8_t* slot = lds + u * kSlotBytes + pos + l32 * 64;
-        if (i < FM) fa[h][i] = *reinterpret_cast<const u32x4*>(slot + (BN + wm + i * 32) * 64);
-        else fb[h][i - FM] = *reinterpret_cast<const u32x4*>(slot + (wn + (i - FM) * 32) * 64);
+    // fragment i of half h of step sp of a pair: A's first, which every row of matrix instructions needs
+    auto read_frag = [&](int set, int pair, int sp, int h, int i) {
+        const int pos = ((4 * sp + 2 * h + half) ^ ((l32 >> 1) & 7)) * 16;
+        const uint8_t* slot = lds + (set * 2 + pair) * kSlotBytes + pos + l32 * 128;
+        if (i < FM) fa[AHEAD ? sp : 0][h][i] = *reinterpret_cast<const u32x4*>(slot + (BN + wm + i * 32) * 128);
+        else fb[AHEAD ? sp : 0][h][i - FM] = *reinterpret_cast<const u32x4*>(slot + (wn + (i - FM) * 32) * 128);
     };
-    auto read_scale = [&](int slot, int u, int p, int i) {
-        const uint8_t* at = lds + kSlots * kSlotBytes + slot * kScaleBytes + u * 4 + l32 * 16;
-        if (i < FM) ca[p][i] = *reinterpret_cast<const uint32_t*>(at + (BN + wm + i * 32) * 16);
-        else cb[p][i - FM] = *reinterpret_cast<const uint32_t*>(at + (wn + (i - FM) * 32) * 16);
+    auto read_scale = [&](int slot, int u, int i) {
+        const uint8_t* at = lds + PAIRS * kSlotBytes + slot * kScaleBytes + u * 4 + l32 * 16;
+        if (i < FM) ca[u & 1][i] = *reinterpret_cast<const uint32_t*>(at + (BN + wm + i * 32) * 16);
+        else cb[u & 1][i - FM] = *reinterpret_cast<const uint32_t*>(at + (wn + (i - FM) * 32) * 16);
     };
     // Moves this half's scale bytes into place. A step past the end of k (its
-    // codes are those of the last one) gets scale bytes 0 instead: every product
+    // codes are those of another one) gets scale bytes 0 instead: every product
     // is at most 36 * 2^-254 then, and adds nothing to an fp32 sum.
     auto shift_scales = [&](int p, bool work) {
         const uint32_t width = work ? 24u : 0u;
@@ -230,86 +255,102 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(PER_EU, 
     // consecutive workgroups run on different XCDs: each XCD takes consecutive items of a round
     const uint32_t first = gridDim.x % 8 == 0 ? (blockIdx.x & 7) * (gridDim.x / 8) + (blockIdx.x >> 3) : blockIdx.x;
     if (first >= items) return;
+    // the group that is fetched next, SETS groups before it is used: group fg of item ft
+    uint32_t ft = first, fg = first / tiles * per_split;
     int64_t m0, n0;
-    place(first % tiles, m0, n0);
+    place(ft % tiles, m0, n0);
     offsets(m0, n0);
-    Stream next = stream_of(m0, n0, first / tiles * per_split);
-    fetch_scales(next, 0);
-    each<kSlots>([&](auto u) {
-        // the first half step fetches the rest of the last slot
-        each<(u < kSlots - 1 ? D : D / 2)>([&](auto i) { fetch_part(next, u, i); });
+    Stream next = stream_of(m0, n0, fg);
+    auto advance = [&] {
+        const uint32_t g0 = ft / tiles * per_split;
+        if (fg + 1 < groups && fg + 1 < g0 + per_split) {
+            ++fg;
+        } else if (ft + gridDim.x < items) {
+            ft += gridDim.x;
+            place(ft % tiles, m0, n0);
+            offsets(m0, n0);
+            fg = ft / tiles * per_split;
+        } else {
+            fg = g0;  // behind the last item its groups are fetched once more and not used
+        }
+        next = stream_of(m0, n0, fg);
+    };
+    using zero = std::integral_constant<int, 0>;
+    using one = std::integral_constant<int, 1>;
+    // With two slots the last pair's later loads follow before the first phase.
+    constexpr int kLast = PAIRS > 2 ? D : 2 * D;
+    each<SETS>([&](auto set) {
+        if constexpr (set > 0) advance();
+        fetch_scales(next, set);
+        each<2 * D>([&](auto i) { fetch_part(next, set, zero{}, i); });
+        each<(set + 1 < SETS ? 2 * D : kLast)>([&](auto i) { fetch_part(next, set, one{}, i); });
     });
     wait_vm_and_lds_then_barrier<0>();
 #pragma unroll
     for (int i = 0; i < D; ++i) {
-        read_frag(0, 0, i);
-        read_scale(0, 0, 0, i);
+        read_frag(0, 0, 0, 0, i);
+        if constexpr (AHEAD) read_frag(0, 0, 0, 1, i);
+        read_scale(0, 0, i);
     }
     shift_scales(0, true);
-    int par = 0;  // parity of the group
-
+    // Set of slots and scale slot of the group in work, and of the next one; scales are
+    // fetched into the one scale slot that neither these nor the groups between hold.
+    int set = 0, sslot = 0;
+    auto next_set = [&] { return SETS == 1 ? 0 : (set + 1 < SETS ? set + 1 : 0); };
+    auto next_sslot = [&] { return sslot < SETS ? sslot + 1 : 0; };
+    auto free_sslot = [&] { return sslot > 0 ? sslot - 1 : SETS; };
     uint32_t t = first, g = 0;
-    // the group after (t, g): where its steps are fetched from
-    auto advance = [&] {
-        uint32_t at = t / tiles * per_split;
-        if (g + 1 < groups && g + 1 < at + per_split) {
-            at = g + 1;
-        } else if (t + gridDim.x < items) {
-            place((t + gridDim.x) % tiles, m0, n0);
-            offsets(m0, n0);
-            at = (t + gridDim.x) / tiles * per_split;
-        }  // behind the last item its first group is fetched once more and not used
-        next = stream_of(m0, n0, at);
-    };
 
     f32x16 acc[FN][FM];
-    // Four steps. A wavefront issues in order, and a matrix instruction occupies
-    // its unit for 32 cycles: the few other instructions that a half step needs
-    // (reads of the next half's fragments, half of a step's loads into LDS, scale
-    // words) are dealt out between its FN FM matrix instructions, the reads first.
-    // The second half of a step's loads is issued in the next step's first half.
-    constexpr int kSlotsOfHalf = FN * FM, kItems = D + D / 2;
-    auto group_of_steps = [&](uint32_t after_stores) {
-        each<4>([&](auto u) {
-            constexpr int p = u & 1;
-            each<kSlotsOfHalf>([&](auto q) {
-                each<(q + 1) * kItems / kSlotsOfHalf - q * kItems / kSlotsOfHalf>([&](auto r) {
-                    constexpr int item = q * kItems / kSlotsOfHalf + r;
-                    if constexpr (item < D) read_frag(u, 1, item);
-                    else fetch_part(next, std::integral_constant<int, (u + 3) & 3>{}, std::integral_constant<int, item - D / 2>{});
-                });
-                __builtin_amdgcn_sched_barrier(0);
-                constexpr int i = q / FM, j = q % FM;
-                acc[i][j] = mfma_fp4<0>(fb[0][i], fa[0][j], acc[i][j], cb[p][i], ca[p][j]);
-                asm volatile("" : "+a"(acc[i][j]));  // keeps the order
-                __builtin_amdgcn_sched_barrier(0);
+    // A phase. A wavefront issues in order, and a matrix instruction occupies its
+    // unit for 32 cycles: the few other instructions that the phase needs are dealt
+    // out between them, first the reads of the next phase's fragments (and scale
+    // words, if that begins a step), then loads into LDS: half of a pair's in its
+    // predecessor's last phase, the others (carry) in the phase behind that.
+    auto phase = [&](auto pair, auto f, uint32_t carry) {
+        constexpr int kInstr = AHEAD ? 2 * FN * FM : FN * FM;
+        constexpr bool last = f == PHASES - 1, new_step = AHEAD || f % 2 == 1;
+        constexpr int kReads = AHEAD ? 2 * D : D, kItems = kReads + (last || f == 0 ? D : 0);
+        constexpr int u = 2 * pair + (AHEAD ? f : f / 2), p = u & 1;  // step of the group
+        each<kInstr>([&](auto q) {
+            each<(q + 1) * kItems / kInstr - q * kItems / kInstr>([&](auto r) {
+                constexpr int item = q * kItems / kInstr + r;
+                if constexpr (item < kReads) {
+                    constexpr int nf = (f + 1) % PHASES;  // the phase that is read for
+                    constexpr int sp = AHEAD ? nf : nf / 2, h = AHEAD ? item / D : nf % 2;
+                    if constexpr (new_step && item < D)
+                        read_scale(u == 3 ? next_sslot() : sslot, (u + 1) & 3, item);
+                    read_frag(last && pair == 1 ? next_set() : set, last ? 1 - pair : pair, sp, h, item % D);
+                } else if constexpr (last) {
+                    fetch_part(next, set, pair, std::integral_constant<int, item - kReads>{});
+                } else {
+                    fetch_part(next, pair == 1 ? set : (set > 0 ? set - 1 : SETS - 1), std::integral_constant<int, 1 - pair>{},
+                               std::integral_constant<int, item - kReads + D>{}, PAIRS > 2 || pair == 1 ? 1 : carry);
+                }
             });
-            constexpr int kAllow = 2 * D + (u == 1 || u == 2 ? SC : 0);
-            constexpr int kLate = kAllow + kStores < 63 ? kAllow + kStores : 63;
-            if (u < 3 && after_stores) wait_vm_and_lds_then_barrier<kLate>();
-            else wait_vm_and_lds_then_barrier<kAllow>();
-            if constexpr (u == 0) {
-                advance();
-                fetch_scales(next, par ^ 1);
-            }
-            each<kSlotsOfHalf>([&](auto q) {
-                each<(q + 1) * kItems / kSlotsOfHalf - q * kItems / kSlotsOfHalf>([&](auto r) {
-                    constexpr int item = q * kItems / kSlotsOfHalf + r;
-                    if constexpr (item < D) {
-                        read_scale(u == 3 ? par ^ 1 : par, (u + 1) & 3, p ^ 1, item);
-                        read_frag((u + 1) & 3, 0, item);
-                    } else {
-                        fetch_part(next, u, std::integral_constant<int, item - D>{});
-                    }
-                });
-                if constexpr (q == kSlotsOfHalf - 1) shift_scales(p ^ 1, u == 3 || 4 * g + u + 1 < steps);
-                __builtin_amdgcn_sched_barrier(0);
-                constexpr int i = q / FM, j = q % FM;
-                acc[i][j] = mfma_fp4<2>(fb[1][i], fa[1][j], acc[i][j], cb[p][i], ca[p][j]);
-                asm volatile("" : "+a"(acc[i][j]));
-                __builtin_amdgcn_sched_barrier(0);
-            });
+            __builtin_amdgcn_sched_barrier(0);
+            constexpr int h = AHEAD ? q / (FN * FM) : f % 2, i = q / FM % FN, j = q % FM;
+            constexpr int r = AHEAD ? p : 0;
+            acc[i][j] = mfma_fp4<2 * h>(fb[r][h][i], fa[r][h][j], acc[i][j], cb[p][i], ca[p][j]);
+            asm volatile("" : "+a"(acc[i][j]));  // keeps the order
+            __builtin_amdgcn_sched_barrier(0);
         });
+        if constexpr (new_step) shift_scales(p ^ 1, u == 3 || 4 * g + u + 1 < steps);
+    };
+    // A pair. `after_stores`: the loads of the next one were all issued before the
+    // last item's stores, which may still run when it is needed.
+    auto pair_of_steps = [&](auto pair, uint32_t carry, uint32_t after_stores) {
+        each<PHASES - 1>([&](auto f) { phase(pair, f, carry); });
+        // still running at most: the loads of the pairs behind the next one, one group's scale bytes among them
+        constexpr int kAllow = (PAIRS - 2) * 2 * D + (PAIRS > 2 ? SC : 0);
+        constexpr int kLate = kAllow + kStores < 63 ? kAllow + kStores : 63;  // the counter's end
+        if (after_stores) wait_vm_and_lds_then_barrier<kLate>();
+        else wait_vm_and_lds_then_barrier<kAllow>();
+        if constexpr (pair == 0) {
+            advance();
+            fetch_scales(next, free_sslot());
+        }
+        phase(pair, std::integral_constant<int, PHASES - 1>{}, 0);
     };
     for (; t < items; t += gridDim.x) {
 #pragma unroll
@@ -318,21 +359,26 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(PER_EU, 
             for (int j = 0; j < FM; ++j)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-        const int64_t cm0 = m0, cn0 = n0;
+        int64_t cm0, cn0;
+        place(t % tiles, cm0, cn0);
         T* const yc = y + t / tiles * part;
         const uint32_t g0 = t / tiles * per_split, g1 = g0 + per_split < groups ? g0 + per_split : groups;
 #pragma nounroll
         for (g = g0; g < g1; ++g) {
+            uint32_t carry = __builtin_amdgcn_readfirstlane(g != g0 ? 1 : 0);
             uint32_t after_stores = __builtin_amdgcn_readfirstlane(g == g0 && t != first ? 1 : 0);
-            asm volatile("" : "+s"(after_stores));  // the loop stays one loop
-            group_of_steps(after_stores);
-            par ^= 1;
+            asm volatile("" : "+s"(after_stores), "+s"(carry));  // the loop stays one loop
+            pair_of_steps(zero{}, carry, after_stores);
+            pair_of_steps(one{}, 1, PAIRS > 2 ? after_stores : 0u);
+            set = next_set();
+            sslot = next_sslot();
         }
+        if constexpr (PAIRS == 2) each<D>([&](auto i) { fetch_part(next, 0, one{}, std::integral_constant<int, i + D>{}); });
         // Out through LDS of this wavefront's own, 32 rows of PIECE bytes at a
         // time, so that each store writes long runs of a row: chunk c of row r
         // lies at position c ^ (r % chunks).
         const bool whole = cm0 + BM <= m && cn0 + BN <= n;
-        uint8_t* out = lds + kSlots * kSlotBytes + 2 * kScaleBytes + wave * 32 * PIECE;
+        uint8_t* out = lds + PAIRS * kSlotBytes + (SETS + 1) * kScaleBytes + wave * 32 * PIECE;
         constexpr int kChunks = PIECE / 16, kPer = 16 / sizeof(T);  // chunks of a row, elements of a chunk
         constexpr int kBlocks = PIECE / (int)sizeof(T) / 16;        // blocks of 16 columns of a piece
 #pragma unroll
@@ -365,8 +411,8 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(PER_EU, 
                 for (int r = 0; r < 32; r += kWave / kChunks) {
                     const u32x4 w = *reinterpret_cast<const u32x4*>(out + (r + lr) * PIECE + ((lc ^ (lr & (kChunks - 1))) * 16));
                     const int64_t row = cm0 + wm + j * 32 + r + lr;
-                    if (whole) store_chunk(yc + row * ld + col, kPer, w);
-                    else if (row < m) store_chunk(yc + row * ld + col, n - col, w);
+                    if (whole) store_chunk<(FN * FM > 4)>(yc + row * ld + col, kPer, w);
+                    else if (row < m) store_chunk<(FN * FM > 4)>(yc + row * ld + col, n - col, w);
                 }
             }
         }
@@ -526,7 +572,7 @@ inline Product product_of(int64_t m, int64_t n, int64_t k) {
     p.tiles_m = (uint32_t)div_up(m, 128);
     p.tiles_n = (uint32_t)div_up(n, 128);
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-    int64_t splits = 512 / tiles;
+    int64_t splits = 256 / tiles;
     if (splits > groups / 2) splits = groups / 2;
     if (splits < 2) return p;
     p.per_split = (uint32_t)div_up(groups, splits);
@@ -553,17 +599,17 @@ int launch_matmul(const uint8_t* aq, const uint8_t* as, int64_t m, const uint8_t
     const int64_t items = (int64_t)p.tiles_m * p.tiles_n * p.splits;
     if (p.way == Way::kTile256) {
         const unsigned grid = (unsigned)(items < kCUs ? items : kCUs);
-        hipLaunchKernelGGL((mx4_matmul_tile_kernel<4, 4, 1, 128, T>), dim3(grid), dim3(kBlock), 0, st, aq, as, m, bq, bs, n,
+        hipLaunchKernelGGL((mx4_matmul_tile_kernel<4, 4, 2, T>), dim3(grid), dim3(kBlock), 0, st, aq, as, m, bq, bs, n,
                            k, p.tiles_m, p.tiles_n, 1u, p.per_split, y, ld, (int64_t)0);
         return launch_status();
     }
-    const unsigned grid = (unsigned)(items < 2 * kCUs ? items : 2 * kCUs);
+    const unsigned grid = (unsigned)(items < kCUs ? items : kCUs);
     if (p.splits == 1) {
-        hipLaunchKernelGGL((mx4_matmul_tile_kernel<2, 2, 2, 64, T>), dim3(grid), dim3(kBlock), 0, st, aq, as, m, bq, bs, n,
+        hipLaunchKernelGGL((mx4_matmul_tile_kernel<2, 2, 4, T>), dim3(grid), dim3(kBlock), 0, st, aq, as, m, bq, bs, n,
                            k, p.tiles_m, p.tiles_n, 1u, p.per_split, y, ld, (int64_t)0);
         return launch_status();
     }
-    hipLaunchKernelGGL((mx4_matmul_tile_kernel<2, 2, 2, 64, float>), dim3(grid), dim3(kBlock), 0, st, aq, as, m, bq, bs, n,
+    hipLaunchKernelGGL((mx4_matmul_tile_kernel<2, 2, 4, float>), dim3(grid), dim3(kBlock), 0, st, aq, as, m, bq, bs, n,
                        k, p.tiles_m, p.tiles_n, p.splits, p.per_split, ws, p.lw, p.part);
     hipLaunchKernelGGL(mx4_matmul_join_kernel<T>, dim3((unsigned)(div_up(m * p.lw / 4, kBlock) < 8 * kCUs ? div_up(m * p.lw / 4, kBlock) : 8 * kCUs)),
                        dim3(kBlock), 0, st, (const float*)ws, p.part, p.lw, p.splits, m, n, y, ld);
