@@ -67,7 +67,7 @@ __device__ __forceinline__ float stored(float v, const float*) { return v; }
 struct BorderForward {
     int64_t rows, cols, rpg, step;
     float eps, scale, inv_cols;
-    int32_t post, pre, fmt, lanes;  // lanes: threads that share a group of codes
+    int32_t post, pre, fmt, lg2_lanes;  // threads that share a group of codes
     const uint16_t* y;
     const void *r, *w_post, *w_pre, *gate;
     void* r_out;
@@ -91,8 +91,9 @@ __device__ __forceinline__ void store_codes8(const BorderForward& p, int64_t row
         return;
     }
     const uint32_t w[4] = {raw.w[0], raw.w[1], raw.w[2], raw.w[3]};
+    const int lanes = 1 << p.lg2_lanes;
     uint32_t code[2];
-    const uint32_t am = group_umax(bf16_absmax_bits(w), p.lanes);
+    const uint32_t am = group_umax(bf16_absmax_bits(w), lanes);
     float sc;
     if (p.fmt == COAT_FMT_E4M3) {
         sc = act_scale<COAT_FMT_E4M3>(am);
@@ -104,7 +105,7 @@ __device__ __forceinline__ void store_codes8(const BorderForward& p, int64_t row
     if (c >= p.cols) return;
     const int64_t at = row * p.cols + c;  // a multiple of 8: groups divide the row
     *reinterpret_cast<gu32x2*>(gp(p.q) + at) = u32x2{code[0], code[1]};
-    if ((threadIdx.x & (p.lanes - 1)) == 0) gp(static_cast<float*>(p.q_scale))[at / (8 * p.lanes)] = sc;
+    if ((threadIdx.x & (lanes - 1)) == 0) gp(static_cast<float*>(p.q_scale))[at >> (3 + p.lg2_lanes)] = sc;
 }
 
 // S the stream's type, P the weights' and gate's, NV chunks a thread, WHOLE:
@@ -515,7 +516,7 @@ int coat_block_norm(const coat_border* b, const uint16_t* y, const void* r, cons
     p.post = b->post;
     p.pre = h || q;
     p.fmt = fmt;
-    p.lanes = q ? group / 8 : 1;
+    p.lg2_lanes = q ? lg2_group_of(group) - 3 : 0;
     p.y = y;
     p.r = r;
     p.w_post = w_post;
