@@ -144,11 +144,11 @@ __device__ __forceinline__ void each(F&& f) {
 // Where a workgroup reads its next group of steps.
 struct Stream {
     const uint8_t *bq, *aq, *bs, *as;  // first rows of the tile, at the group's first step
-    // Byte offset of the second pair, and for each pair whether its second step is
-    // past the end of k. What is past the end is not read: the first pair, or step,
-    // is fetched in its place and not used.
-    uint32_t second;
-    bool odd[2];
+    uint32_t left;                     // steps from there to the end of k
+    // Byte offset of the second pair, and for each pair what this lane's offset is
+    // too large by, if the pair's second step is past the end of k. What is past
+    // the end is not read: the first pair, or step, is fetched instead and not used.
+    uint32_t second, back[2];
 };
 
 // With splits > 1 item t is the product over the groups of four steps
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
     const uint32_t lds_wave = lds0 + wave * 1024;
     auto fetch_part = [&](const Stream& at, int set, auto pair, auto i, uint32_t on = 1) {
         const uint8_t* from = (i < 2 * FN ? at.bq : at.aq) + (pair == 1 ? at.second : 0);
-        const uint32_t to = lds_wave + set * 2 * kSlotBytes, lane_off = off[i] - (at.odd[pair] ? back : 0);
+        const uint32_t to = lds_wave + set * 2 * kSlotBytes, lane_off = off[i] - at.back[pair];
         if (__builtin_constant_p(on)) load_to_lds16<pair * kSlotBytes + i * 4096>(to, lane_off, from);
         else load_to_lds16_if<pair * kSlotBytes + i * 4096>(on, to, lane_off, from);
     };
@@ -215,10 +215,16 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
                                                          (i * 4 + wave) * 64 < BN ? at.bs : at.as);
         });
     };
+    auto settle = [&](Stream& at) {
+        at.second = at.left > 2 ? 128 : 0;
+        at.back[0] = at.left == 1 ? back : 0;
+        at.back[1] = at.left == 1 || at.left == 3 ? back : 0;
+        asm volatile("" : "+v"(at.back[0]), "+v"(at.back[1]));  // held, not computed at each use
+    };
     auto stream_of = [&](int64_t m0, int64_t n0, uint32_t g) {
-        const uint32_t left = steps - 4 * g;
-        return Stream{bq + n0 * qb + g * 256, aq + m0 * qb + g * 256, bs + n0 * sb + g * 16, as + m0 * sb + g * 16,
-                      left > 2 ? 128u : 0u, {left == 1, left == 1 || left == 3}};
+        Stream at{bq + n0 * qb + g * 256, aq + m0 * qb + g * 256, bs + n0 * sb + g * 16, as + m0 * sb + g * 16, steps - 4 * g, 0, {0, 0}};
+        settle(at);
+        return at;
     };
 
     u32x4 fb[AHEAD ? 2 : 1][2][FN], fa[AHEAD ? 2 : 1][2][FM];  // fragments, [parity of the step][half]
@@ -261,18 +267,24 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
     place(ft % tiles, m0, n0);
     offsets(m0, n0);
     Stream next = stream_of(m0, n0, fg);
+    uint32_t group_end = fg + per_split < groups ? fg + per_split : groups;  // of item ft
     auto advance = [&] {
-        const uint32_t g0 = ft / tiles * per_split;
-        if (fg + 1 < groups && fg + 1 < g0 + per_split) {
-            ++fg;
-        } else if (ft + gridDim.x < items) {
+        if (++fg < group_end) {
+            next.bq += 256;
+            next.aq += 256;
+            next.bs += 16;
+            next.as += 16;
+            next.left -= 4;
+            settle(next);
+            return;
+        }
+        if (ft + gridDim.x < items) {  // behind the last item its groups are fetched once more and not used
             ft += gridDim.x;
             place(ft % tiles, m0, n0);
             offsets(m0, n0);
-            fg = ft / tiles * per_split;
-        } else {
-            fg = g0;  // behind the last item its groups are fetched once more and not used
         }
+        fg = ft / tiles * per_split;
+        group_end = fg + per_split < groups ? fg + per_split : groups;
         next = stream_of(m0, n0, fg);
     };
     using zero = std::integral_constant<int, 0>;
@@ -554,31 +566,47 @@ struct Product {
     int64_t lw, part;  // of the partial sums: elements of a row and of a split
 };
 
+// Estimated microseconds of 128 x 128 tiles with their k in `splits` parts: 0.27
+// a step of 128 values in each round of workgroups and 3 to begin and end; with
+// splits the second launch and the partial sums' way out and back on top.
+// Measured: 128 x 13824 x 5120 (108 tiles) 16.3 in one part, 19.2 in two;
+// 512 x 4096 x 4096 14.7 and 18.8; 333 x 5120 x 13824 36 and 32;
+// 64 x 5120 x 13824 34 and, in six, 17.5.
+inline double tile128_time(int64_t tiles, int64_t m, int64_t lw, int64_t steps, int64_t splits) {
+    const double rounds = (double)div_up(tiles * splits, kCUs);
+    const double work = rounds * (double)div_up(steps, splits) * 0.27 + 3.0;
+    return splits == 1 ? work : work + 6.0 + 8.0 * (double)splits * (double)m * (double)lw / 3.5e6;
+}
+
 inline Product product_of(int64_t m, int64_t n, int64_t k) {
     Product p{Way::kSmall, 0, 0, 1, 0, 0, 0};
-    if (k == 0 || k >= (1 << 22)) return p;
+    if (k == 0 || k >= (1 << 22)) return p;  // longer rows than 32-bit offsets within a tile reach
+    // Up to 32 rows of A: 1 x 13824 x 5120 takes 10 us, 32 17 us; 64 take 21 that
+    // way and 16 in tiles.
     if (m <= 32) {
         p.way = Way::kFew;
         return p;
     }
-    if (div_up(m, 256) * div_up(n, 256) > 0x3FFFFFFF) return p;
+    if (div_up(m, 128) * div_up(n, 128) > 0x3FFFFFFF) return p;
     const int64_t groups = div_up(k, 512);
     p.per_split = (uint32_t)groups;
     p.way = Way::kTile256;
     p.tiles_m = (uint32_t)div_up(m, 256);
     p.tiles_n = (uint32_t)div_up(n, 256);
+    // large tiles where they fill most of the card: 2048 x 5120 x 5120 (160 of them)
+    // takes 40 us and 46 in small ones, 1500 x 5120 x 13824 (120) 87 and 77
     if ((int64_t)p.tiles_m * p.tiles_n >= 160) return p;
     p.way = Way::kTile128;
     p.tiles_m = (uint32_t)div_up(m, 128);
     p.tiles_n = (uint32_t)div_up(n, 128);
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-    int64_t splits = 256 / tiles;
-    if (splits > groups / 2) splits = groups / 2;
-    if (splits < 2) return p;
-    p.per_split = (uint32_t)div_up(groups, splits);
-    p.splits = (uint32_t)div_up(groups, p.per_split);
     p.lw = div_up(n, 64) * 64;
     p.part = m * p.lw;
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, steps = div_up(k, 128);
+    int64_t best = 1;
+    for (int64_t s = 2; s <= groups / 2 && tiles * s <= kCUs; ++s)
+        if (tile128_time(tiles, m, p.lw, steps, s) < tile128_time(tiles, m, p.lw, steps, best)) best = s;
+    p.per_split = (uint32_t)div_up(groups, best);
+    p.splits = (uint32_t)div_up(groups, p.per_split);
     return p;
 }
 
