@@ -43,19 +43,48 @@ __device__ __forceinline__ void block_sum2(float (&scratch)[2][kMaxWaves][2], in
     }
 }
 
+// How a row ends: with a whole chunk, inside one, or before the first one's end.
+enum Edge { kWhole, kInside, kTiny };
+
+// 8 elements of a row; settle_row8 finishes what it began.
+template <int EDGE, class E>
+__device__ __forceinline__ Raw8<E> load_row8(const E* p, int64_t n) {
+    if constexpr (EDGE == kInside) return load_end8(p, n);
+    else return load_raw8<EDGE == kWhole>(p, n);
+}
+template <int EDGE, class E>
+__device__ __forceinline__ void settle_row8(Raw8<E>& r, int64_t n) {
+    if constexpr (EDGE == kInside) settle8(r, n);
+}
+
+// The same of a matrix that may be missing (zeros).
+template <int EDGE, class E>
+__device__ __forceinline__ Raw8<E> load_maybe8(const E* p, int64_t at, int64_t n) {
+    if constexpr (EDGE == kInside) {
+        if (p) return load_end8(p + at, n);
+        return load_raw8<true>(p, 0);
+    } else {
+        return load_row8<EDGE>(p + at, p ? n : 0);
+    }
+}
+
 // 8 values of a weight or gate that may be missing (ones).
-template <bool WHOLE, class P>
+template <int EDGE, class P>
 __device__ __forceinline__ Raw8<P> load_param8(const void* p, int64_t at, int64_t n) {
-    if (p) return load_raw8<WHOLE>(static_cast<const P*>(p) + at, n);
+    if (p) {
+        Raw8<P> r = load_row8<EDGE>(static_cast<const P*>(p) + at, n);
+        settle_row8<EDGE>(r, n);
+        return r;
+    }
     Raw8<P> r;
     if constexpr (sizeof(P) == 4) r.lo = r.hi = u32x4{0x3F800000u, 0x3F800000u, 0x3F800000u, 0x3F800000u};
     else r.w = u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
     return r;
 }
-template <bool WHOLE>
+template <int EDGE>
 __device__ __forceinline__ void store_grad8(void* p, int32_t type, int64_t at, int64_t n, const float (&v)[8]) {
-    if (type == COAT_FP32) store8<WHOLE>(static_cast<float*>(p) + at, n, v);
-    else store8<WHOLE>(static_cast<uint16_t*>(p) + at, n, v);
+    if (type == COAT_FP32) store8<EDGE == kWhole>(static_cast<float*>(p) + at, n, v);
+    else store8<EDGE == kWhole>(static_cast<uint16_t*>(p) + at, n, v);
 }
 
 // The value a stored element of the stream stands for.
@@ -108,10 +137,9 @@ __device__ __forceinline__ void store_codes8(const BorderForward& p, int64_t row
     if ((threadIdx.x & (lanes - 1)) == 0) gp(static_cast<float*>(p.q_scale))[at >> (3 + p.lg2_lanes)] = sc;
 }
 
-// S the stream's type, P the weights' and gate's, NV chunks a thread, WHOLE:
-// the channels are a multiple of 8. A workgroup takes `step` consecutive rows;
+// S the stream's type, P the weights' and gate's, NV chunks a thread. A workgroup takes `step` consecutive rows;
 // the weights, and the gate row while its tokens last, stay in registers.
-template <class S, class P, int NV, bool WHOLE>
+template <class S, class P, int NV, int EDGE>
 __global__ __launch_bounds__(1024) void border_forward_kernel(BorderForward p) {
     __shared__ float scratch[2][kMaxWaves][2];
     const int tid = threadIdx.x, threads = blockDim.x, waves = threads / kWave;
@@ -122,9 +150,9 @@ __global__ __launch_bounds__(1024) void border_forward_kernel(BorderForward p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int64_t c = (int64_t)(i * threads + tid) * 8, n = p.cols - c;
-        w_post[i] = load_param8<WHOLE, P>(p.w_post, c, n);
-        w_pre[i] = load_param8<WHOLE, P>(p.w_pre, c, n);
-        gate[i] = load_param8<WHOLE, P>(nullptr, c, n);
+        w_post[i] = load_param8<EDGE, P>(p.w_post, c, n);
+        w_pre[i] = load_param8<EDGE, P>(p.w_pre, c, n);
+        gate[i] = load_param8<EDGE, P>(nullptr, c, n);
     }
     int64_t gate_end = p.gate ? row : end;  // first row that needs another gate row
     for (; row < end; ++row) {
@@ -136,8 +164,14 @@ __global__ __launch_bounds__(1024) void border_forward_kernel(BorderForward p) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int64_t c = (int64_t)(i * threads + tid) * 8, n = p.cols - c;
-                y[i] = load_raw8<WHOLE>(p.y + base + c, n);
-                r[i] = load_raw8<WHOLE>(static_cast<const S*>(p.r) + base + c, n);
+                y[i] = load_row8<EDGE>(p.y + base + c, n);
+                r[i] = load_row8<EDGE>(static_cast<const S*>(p.r) + base + c, n);
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int64_t n = p.cols - (int64_t)(i * threads + tid) * 8;
+                settle_row8<EDGE>(y[i], n);
+                settle_row8<EDGE>(r[i], n);
             }
             if (row >= gate_end) {
                 const int64_t g = row / p.rpg;
@@ -145,7 +179,7 @@ __global__ __launch_bounds__(1024) void border_forward_kernel(BorderForward p) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int64_t c = (int64_t)(i * threads + tid) * 8;
-                    gate[i] = load_param8<WHOLE, P>(p.gate, g * p.cols + c, p.cols - c);
+                    gate[i] = load_param8<EDGE, P>(p.gate, g * p.cols + c, p.cols - c);
                 }
             }
             float sig = p.scale;
@@ -173,13 +207,15 @@ __global__ __launch_bounds__(1024) void border_forward_kernel(BorderForward p) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     x[i][j] = stored(__builtin_fmaf(v[j] * sig * w[j], g[j], x[i][j]), static_cast<const S*>(nullptr));
-                if (p.r_out) store8<WHOLE>(static_cast<S*>(p.r_out) + base + c, n, x[i]);
+                if (p.r_out) store8<EDGE == kWhole>(static_cast<S*>(p.r_out) + base + c, n, x[i]);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int64_t c = (int64_t)(i * threads + tid) * 8;
-                expand(load_raw8<WHOLE>(static_cast<const S*>(p.r) + base + c, p.cols - c), x[i]);
+                const int64_t c = (int64_t)(i * threads + tid) * 8, n = p.cols - c;
+                Raw8<S> r = load_row8<EDGE>(static_cast<const S*>(p.r) + base + c, n);
+                settle_row8<EDGE>(r, n);
+                expand(r, x[i]);
             }
         }
         if (!p.pre) continue;
@@ -199,8 +235,8 @@ __global__ __launch_bounds__(1024) void border_forward_kernel(BorderForward p) {
             // channels past the end are zeros even where rho is not finite
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                x[i][j] = __builtin_bit_cast(float, bf16_bits((WHOLE ? n > 0 : j < n) ? x[i][j] * rho * w[j] : 0.0f) << 16);
-            if (p.h) store8<WHOLE>(p.h + base + c, n, x[i]);
+                x[i][j] = __builtin_bit_cast(float, bf16_bits((EDGE == kWhole ? n > 0 : j < n) ? x[i][j] * rho * w[j] : 0.0f) << 16);
+            if (p.h) store8<EDGE == kWhole>(p.h + base + c, n, x[i]);
             if (p.q) store_codes8(p, row, c, x[i]);
         }
     }
@@ -222,8 +258,10 @@ struct BorderBackward {
 // of a gate row, while its tokens last) in registers.
 //   pre:  with u = w_pre dh, s2 = sum r u:  d = dr_out + rho u - r rho^3 s2 / cols
 //   post: with u = w_post scale g d, s4 = sum y u:  dy = sig u - y sig^3 s4 / cols
-template <class S, class P, int NV, bool WHOLE>
-__global__ __launch_bounds__(1024) void border_backward_kernel(BorderBackward p) {
+// MAXT: threads at most. Up to 768 leave registers for loading a row while the
+// one before it is worked on.
+template <class S, class P, int NV, int EDGE, int MAXT>
+__global__ __launch_bounds__(MAXT) void border_backward_kernel(BorderBackward p) {
     __shared__ float scratch[2][kMaxWaves][2];
     const int tid = threadIdx.x, threads = blockDim.x, waves = threads / kWave;
     int buf = 0;
@@ -266,16 +304,16 @@ __global__ __launch_bounds__(1024) void border_backward_kernel(BorderBackward p)
     Raw8<P> w_post[NV], w_pre[NV], gate[NV];
     auto weight = [&](const Raw8<P>& kept, const void* from, int64_t at, int64_t c, float (&v)[8]) {
         if constexpr (KEEP) expand(kept, v);
-        else expand(load_param8<WHOLE, P>(from, at + c, p.cols - c), v);
+        else expand(load_param8<EDGE, P>(from, at + c, p.cols - c), v);
     };
     float acc_pre[NV][8], acc_post[NV][8], acc_gate[NV][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int64_t c = (int64_t)(i * threads + tid) * 8, n = p.cols - c;
         if constexpr (KEEP) {
-            w_post[i] = load_param8<WHOLE, P>(p.w_post, c, n);
-            w_pre[i] = load_param8<WHOLE, P>(p.w_pre, c, n);
-            gate[i] = load_param8<WHOLE, P>(nullptr, c, n);
+            w_post[i] = load_param8<EDGE, P>(p.w_post, c, n);
+            w_pre[i] = load_param8<EDGE, P>(p.w_pre, c, n);
+            gate[i] = load_param8<EDGE, P>(nullptr, c, n);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc_pre[i][j] = 0.0f;
@@ -283,20 +321,49 @@ __global__ __launch_bounds__(1024) void border_backward_kernel(BorderBackward p)
         put(1, i, acc_gate[i], zeros);
     }
     int64_t gate_end = p.gate ? row : end;  // first row that needs another gate row
-    for (; row < end; ++row) {
-        const int64_t base = row * p.cols;
-        Raw8<uint16_t> y[NV], u[NV];
-        Raw8<S> x[NV], dr[NV];
+    constexpr bool EARLY = MAXT < 1024;
+    Raw8<uint16_t> y[NV], u[NV], y_next[NV], u_next[NV];
+    Raw8<S> x[NV], dr[NV], x_next[NV], dr_next[NV];
+    auto load_row = [&](int64_t at, Raw8<uint16_t> (&yv)[NV], Raw8<uint16_t> (&uv)[NV], Raw8<S> (&xv)[NV], Raw8<S> (&dv)[NV]) {
+        const int64_t from = at * p.cols;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int64_t c = (int64_t)(i * threads + tid) * 8, n = p.cols - c;
             if (p.dh) {
-                x[i] = load_raw8<WHOLE>(static_cast<const S*>(p.r) + base + c, n);
-                u[i] = load_raw8<WHOLE>(p.dh + base + c, n);
+                xv[i] = load_row8<EDGE>(static_cast<const S*>(p.r) + from + c, n);
+                uv[i] = load_row8<EDGE>(p.dh + from + c, n);
             }
-            dr[i] = load_raw8<WHOLE>(static_cast<const S*>(p.dr_out) + base + c, p.dr_out ? n : 0);
-            y[i] = load_raw8<WHOLE>(p.y + base + c, p.y ? n : 0);
+            dv[i] = load_maybe8<EDGE>(static_cast<const S*>(p.dr_out), from + c, n);
+            yv[i] = load_maybe8<EDGE>(p.y, from + c, n);
         }
+    };
+    auto settle_row = [&] {
+        if (EDGE != kInside) return;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int64_t n = p.cols - (int64_t)(i * threads + tid) * 8;
+            settle_row8<EDGE>(x[i], n);
+            settle_row8<EDGE>(u[i], n);
+            settle_row8<EDGE>(dr[i], n);
+            settle_row8<EDGE>(y[i], n);
+        }
+    };
+    if (EARLY && row < end) load_row(row, y_next, u_next, x_next, dr_next);
+    for (; row < end; ++row) {
+        const int64_t base = row * p.cols;
+        if constexpr (EARLY) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                y[i] = y_next[i];
+                u[i] = u_next[i];
+                x[i] = x_next[i];
+                dr[i] = dr_next[i];
+            }
+            if (row + 1 < end) load_row(row + 1, y_next, u_next, x_next, dr_next);
+        } else {
+            load_row(row, y, u, x, dr);
+        }
+        settle_row();
         const int64_t g_row = p.gate ? row / p.rpg : 0;
         if (row >= gate_end) {
             gate_end = (g_row + 1) * p.rpg;
@@ -304,7 +371,7 @@ __global__ __launch_bounds__(1024) void border_backward_kernel(BorderBackward p)
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int64_t c = (int64_t)(i * threads + tid) * 8;
-                    gate[i] = load_param8<WHOLE, P>(p.gate, g_row * p.cols + c, p.cols - c);
+                    gate[i] = load_param8<EDGE, P>(p.gate, g_row * p.cols + c, p.cols - c);
                 }
             }
         }
@@ -347,7 +414,7 @@ __global__ __launch_bounds__(1024) void border_backward_kernel(BorderBackward p)
                     d[i][j] += __builtin_fmaf(ru, w[j], -xv[j] * back);
                 }
             }
-            store8<WHOLE>(static_cast<S*>(p.dr) + base + c, n, d[i]);
+            store8<EDGE == kWhole>(static_cast<S*>(p.dr) + base + c, n, d[i]);
             if (p.y) {
                 float yv[8], w[8], g[8];
                 expand(y[i], yv);
@@ -388,7 +455,7 @@ __global__ __launch_bounds__(1024) void border_backward_kernel(BorderBackward p)
             }
             put(0, i, acc_post[i], post);
             put(1, i, acc_gate[i], gates);
-            store8<WHOLE>(p.dy + base + c, n, out);
+            store8<EDGE == kWhole>(p.dy + base + c, n, out);
         }
         if (p.dgate && p.chunks <= 1 && (row + 1 == end || row + 1 == gate_end)) {
 #pragma unroll
@@ -396,7 +463,7 @@ __global__ __launch_bounds__(1024) void border_backward_kernel(BorderBackward p)
                 const int64_t c = (int64_t)(i * threads + tid) * 8;
                 float gates[8];
                 get(1, i, acc_gate[i], gates);
-                store_grad8<WHOLE>(p.dgate, p.grad_type, g_row * p.cols + c, p.cols - c, gates);
+                store_grad8<EDGE>(p.dgate, p.grad_type, g_row * p.cols + c, p.cols - c, gates);
                 put(1, i, acc_gate[i], zeros);
             }
         }
@@ -405,12 +472,12 @@ __global__ __launch_bounds__(1024) void border_backward_kernel(BorderBackward p)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int64_t c = (int64_t)(i * threads + tid) * 8, n = p.cols - c;
-        if (p.part_pre) store8<WHOLE>(p.part_pre + part + c, n, acc_pre[i]);
+        if (p.part_pre) store8<EDGE == kWhole>(p.part_pre + part + c, n, acc_pre[i]);
         float v[8];
         get(0, i, acc_post[i], v);
-        if (p.part_post) store8<WHOLE>(p.part_post + part + c, n, v);
+        if (p.part_post) store8<EDGE == kWhole>(p.part_post + part + c, n, v);
         get(1, i, acc_gate[i], v);
-        if (p.part_gate) store8<WHOLE>(p.part_gate + part + c, n, v);
+        if (p.part_gate) store8<EDGE == kWhole>(p.part_gate + part + c, n, v);
     }
 }
 
@@ -459,21 +526,22 @@ __global__ __launch_bounds__(kMaxWaves * kWave) void border_reduce_kernel(Border
     }
 }
 
-// Calls launch(NV, WHOLE) as compile-time constants, and the workgroup's threads.
+// Calls launch(NV, EDGE, threads): the first two as compile-time constants.
 template <class F>
 void border_shape(int64_t cols, F&& launch) {
-    const bool whole = cols % 8 == 0;
-    const int nv = border_chunks(cols);
     const dim3 threads((unsigned)(border_waves(cols) * kWave));
     using one = std::integral_constant<int, 1>;
     using two = std::integral_constant<int, 2>;
-    if (nv == 1) whole ? launch(one{}, std::true_type{}, threads) : launch(one{}, std::false_type{}, threads);
-    else whole ? launch(two{}, std::true_type{}, threads) : launch(two{}, std::false_type{}, threads);
+    using whole = std::integral_constant<int, kWhole>;
+    using inside = std::integral_constant<int, kInside>;
+    if (cols < 8) launch(one{}, std::integral_constant<int, kTiny>{}, threads);
+    else if (border_chunks(cols) == 1) cols % 8 == 0 ? launch(one{}, whole{}, threads) : launch(one{}, inside{}, threads);
+    else cols % 8 == 0 ? launch(two{}, whole{}, threads) : launch(two{}, inside{}, threads);
 }
 
 template <class S, class P>
 int launch_forward(BorderForward& p, hipStream_t st) {
-    border_shape(p.cols, [&](auto nv, auto whole, dim3 threads) {
+    border_shape(p.cols, [&](auto nv, auto edge, dim3 threads) {
         // as many workgroups as run at once (24 wavefronts on a compute unit):
         // 16384 x 5120 takes 144 us with 2 of 10 wavefronts each, 152 with 3, 162
         // with 4; small ones hide their barriers better when there are twice as
@@ -481,7 +549,7 @@ int launch_forward(BorderForward& p, hipStream_t st) {
         const int64_t waves = threads.x / kWave;
         const int64_t each = waves > 12 ? 1 : 24 / waves;
         p.step = div_up(p.rows, kCUs * (waves <= 4 ? 2 * each : each));
-        hipLaunchKernelGGL((border_forward_kernel<S, P, nv.value, whole.value>), dim3((unsigned)div_up(p.rows, p.step)), threads,
+        hipLaunchKernelGGL((border_forward_kernel<S, P, nv.value, edge.value>), dim3((unsigned)div_up(p.rows, p.step)), threads,
                            0, st, p);
     });
     return launch_status();
@@ -489,8 +557,17 @@ int launch_forward(BorderForward& p, hipStream_t st) {
 
 template <class S, class P>
 int launch_backward(const BorderBackward& p, int64_t blocks, hipStream_t st) {
-    border_shape(p.cols, [&](auto nv, auto whole, dim3 threads) {
-        hipLaunchKernelGGL((border_backward_kernel<S, P, nv.value, whole.value>), dim3((unsigned)blocks), threads, 0, st, p);
+    border_shape(p.cols, [&](auto nv, auto edge, dim3 threads) {
+        if constexpr (nv.value == 2) {
+            hipLaunchKernelGGL((border_backward_kernel<S, P, 2, edge.value, 1024>), dim3((unsigned)blocks), threads, 0, st, p);
+        } else if (edge.value == kTiny || threads.x <= 512) {
+            hipLaunchKernelGGL((border_backward_kernel<S, P, 1, edge.value, 512>), dim3((unsigned)blocks), threads, 0, st, p);
+        } else if constexpr (edge.value == kTiny) {
+        } else if (threads.x <= 768) {
+            hipLaunchKernelGGL((border_backward_kernel<S, P, 1, edge.value, 768>), dim3((unsigned)blocks), threads, 0, st, p);
+        } else {
+            hipLaunchKernelGGL((border_backward_kernel<S, P, 1, edge.value, 1024>), dim3((unsigned)blocks), threads, 0, st, p);
+        }
     });
     return launch_status();
 }

@@ -87,9 +87,47 @@ __device__ __forceinline__ Raw8<float> load_raw8(const float* p, int64_t n) {
     }
     return r;
 }
-template <class E>
-__device__ __forceinline__ void load8(const E* p, int64_t n, float (&v)[8]) {
-    expand(load_raw8(p, n), v);
+
+// The same in two halves, for several loads that shall be under way together: the
+// load, of the row's last 8 elements where fewer than 8 are left (the row has
+// 8), and what moves those into place once they are there.
+__device__ __forceinline__ Raw8<uint16_t> load_end8(const uint16_t* p, int64_t n) {
+    return {*reinterpret_cast<const gu32x4_a2*>(gp(p) + (n < 8 ? n - 8 : 0))};
+}
+__device__ __forceinline__ Raw8<float> load_end8(const float* p, int64_t n) {
+    const auto q = gp(p) + (n < 8 ? n - 8 : 0);
+    return {*reinterpret_cast<const gu32x4_a4*>(q), *reinterpret_cast<const gu32x4_a4*>(q + 4)};
+}
+__device__ __forceinline__ void settle8(Raw8<uint16_t>& r, int64_t n) {
+    if (n >= 8) return;
+    const int k = n > 0 ? 8 - (int)n : 8;  // elements that belong before p
+    u32x4 w = r.w;
+    if (k & 4) w = u32x4{w[2], w[3], 0u, 0u};
+    if (k & 2) w = u32x4{w[1], w[2], w[3], 0u};
+    if (k & 1)
+        w = u32x4{__builtin_amdgcn_alignbit(w[1], w[0], 16), __builtin_amdgcn_alignbit(w[2], w[1], 16),
+                  __builtin_amdgcn_alignbit(w[3], w[2], 16), w[3] >> 16};
+    r.w = k < 8 ? w : u32x4{0u, 0u, 0u, 0u};
+}
+__device__ __forceinline__ void settle8(Raw8<float>& r, int64_t n) {
+    if (n >= 8) return;
+    const int k = n > 0 ? 8 - (int)n : 8;
+    u32x4 a = r.lo, b = r.hi;
+    const u32x4 none{0u, 0u, 0u, 0u};
+    if (k & 4) {
+        a = b;
+        b = none;
+    }
+    if (k & 2) {
+        a = u32x4{a[2], a[3], b[0], b[1]};
+        b = u32x4{b[2], b[3], 0u, 0u};
+    }
+    if (k & 1) {
+        a = u32x4{a[1], a[2], a[3], b[0]};
+        b = u32x4{b[1], b[2], b[3], 0u};
+    }
+    r.lo = k < 8 ? a : none;
+    r.hi = k < 8 ? b : none;
 }
 
 // 8 consecutive elements to p, of which the first n exist. WHOLE: as above.
