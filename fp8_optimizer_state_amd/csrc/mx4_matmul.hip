@@ -97,30 +97,18 @@ __device__ __forceinline__ void load_to_lds16(uint32_t lds, uint32_t off, const 
 
 __device__ __forceinline__ uint32_t float_bits(float v) { return __builtin_bit_cast(uint32_t, v); }
 
-// A 16-byte chunk of y, of which the first n elements exist. PAST: written past
-// the caches' usual order, where y would drive the operands out of them (16384 x
-// 16384 x 512 to bf16 in large tiles: 158 us against 214).
+// A 16-byte chunk of y. PAST: written past the caches' usual order, where y would
+// drive the operands out of them (16384 x 16384 x 512 to bf16 in large tiles: 158
+// us against 214).
 template <bool PAST>
-__device__ __forceinline__ void store_chunk(float* p, int64_t n, const u32x4& w) {
-    if (n >= 4) {
-        if constexpr (PAST) __builtin_nontemporal_store(w, reinterpret_cast<gu32x4_a4*>(gp(p)));
-        else *reinterpret_cast<gu32x4_a4*>(gp(p)) = w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < n) gp(p)[i] = as_float(w[i]);
-    }
+__device__ __forceinline__ void store_chunk(float* p, const u32x4& w) {
+    if constexpr (PAST) __builtin_nontemporal_store(w, reinterpret_cast<gu32x4_a4*>(gp(p)));
+    else *reinterpret_cast<gu32x4_a4*>(gp(p)) = w;
 }
 template <bool PAST>
-__device__ __forceinline__ void store_chunk(uint16_t* p, int64_t n, const u32x4& w) {
-    if (n >= 8) {
-        if constexpr (PAST) __builtin_nontemporal_store(w, reinterpret_cast<gu32x4_a2*>(gp(p)));
-        else *reinterpret_cast<gu32x4_a2*>(gp(p)) = w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) gp(p)[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-    }
+__device__ __forceinline__ void store_chunk(uint16_t* p, const u32x4& w) {
+    if constexpr (PAST) __builtin_nontemporal_store(w, reinterpret_cast<gu32x4_a2*>(gp(p)));
+    else *reinterpret_cast<gu32x4_a2*>(gp(p)) = w;
 }
 
 // The same, or nothing if `on` is 0 (one branch within a long run of code).
@@ -418,13 +406,22 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
                     }
                 }
                 const int lr = lane / kChunks, lc = lane % kChunks;
-                const int64_t col = cn0 + wn + pc * kBlocks * 16 + lc * kPer;
+                const int64_t row0 = cm0 + wm + j * 32, col0 = cn0 + wn + pc * kBlocks * 16;
+                if (whole) {
+                    T* to = yc + (row0 + lr) * ld + col0 + lc * kPer;
 #pragma unroll
-                for (int r = 0; r < 32; r += kWave / kChunks) {
-                    const u32x4 w = *reinterpret_cast<const u32x4*>(out + (r + lr) * PIECE + ((lc ^ (lr & (kChunks - 1))) * 16));
-                    const int64_t row = cm0 + wm + j * 32 + r + lr;
-                    if (whole) store_chunk<(FN * FM > 4)>(yc + row * ld + col, kPer, w);
-                    else if (row < m) store_chunk<(FN * FM > 4)>(yc + row * ld + col, n - col, w);
+                    for (int r = 0; r < 32; r += kWave / kChunks) {
+                        const u32x4 w = *reinterpret_cast<const u32x4*>(out + (r + lr) * PIECE + ((lc ^ (lr & (kChunks - 1))) * 16));
+                        store_chunk<(FN * FM > 4)>(to + r * ld, w);
+                    }
+                } else {  // element by element, a row or two at a time
+                    constexpr int kCols = PIECE / sizeof(T), kRows = kWave / kCols;
+                    const int er = lane / kCols, ec = lane % kCols;
+#pragma nounroll
+                    for (int r = er; r < 32; r += kRows) {
+                        const T v = *reinterpret_cast<const T*>(out + r * PIECE + (((ec / kPer) ^ (r & (kChunks - 1))) * kPer + ec % kPer) * sizeof(T));
+                        if (row0 + r < m && col0 + ec < n) gp(yc)[(row0 + r) * ld + col0 + ec] = v;
+                    }
                 }
             }
         }
