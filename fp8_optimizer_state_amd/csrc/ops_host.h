@@ -67,6 +67,64 @@ inline int check_mx4_matmul(const uint8_t* a_q, const uint8_t* a_s, int64_t m, c
     return COAT_OK;
 }
 
+// How a product is computed.
+enum class Way { kSmall, kFew, kTile128, kTile256 };
+struct Product {
+    Way way;
+    uint32_t tiles_m, tiles_n, splits, per_split;
+    int64_t lw, part;  // of the partial sums: elements of a row and of a split
+};
+
+// Estimated microseconds of 128 x 128 tiles with their k in `splits` parts: 0.27
+// a step of 128 values in each round of workgroups and 3 to begin and end; with
+// splits the second launch and the partial sums' way out and back on top.
+// Measured: 128 x 13824 x 5120 (108 tiles) 16.3 in one part, 19.2 in two;
+// 512 x 4096 x 4096 14.7 and 18.8; 333 x 5120 x 13824 36 and 32;
+// 64 x 5120 x 13824 34 and, in six, 17.5.
+inline double tile128_time(int64_t tiles, int64_t m, int64_t lw, int64_t steps, int64_t splits) {
+    const double rounds = (double)div_up(tiles * splits, kCUs);
+    const double work = rounds * (double)div_up(steps, splits) * 0.27 + 3.0;
+    return splits == 1 ? work : work + 6.0 + 8.0 * (double)splits * (double)m * (double)lw / 3.5e6;
+}
+
+inline Product product_of(int64_t m, int64_t n, int64_t k) {
+    Product p{Way::kSmall, 0, 0, 1, 0, 0, 0};
+    if (k == 0 || k >= (1 << 22)) return p;  // longer rows than 32-bit offsets within a tile reach
+    // Up to 32 rows of A: 1 x 13824 x 5120 takes 10 us, 32 17 us; 64 take 21 that
+    // way and 16 in tiles.
+    if (m <= 32) {
+        p.way = Way::kFew;
+        return p;
+    }
+    if (div_up(m, 128) * div_up(n, 128) > 0x3FFFFFFF) return p;
+    const int64_t groups = div_up(k, 512);
+    p.per_split = (uint32_t)groups;
+    p.way = Way::kTile256;
+    p.tiles_m = (uint32_t)div_up(m, 256);
+    p.tiles_n = (uint32_t)div_up(n, 256);
+    // large tiles where they fill most of the card: 2048 x 5120 x 5120 (160 of them)
+    // takes 40 us and 46 in small ones, 1500 x 5120 x 13824 (120) 87 and 77
+    if ((int64_t)p.tiles_m * p.tiles_n >= 160) return p;
+    p.way = Way::kTile128;
+    p.tiles_m = (uint32_t)div_up(m, 128);
+    p.tiles_n = (uint32_t)div_up(n, 128);
+    p.lw = div_up(n, 64) * 64;
+    p.part = m * p.lw;
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, steps = div_up(k, 128);
+    int64_t best = 1;
+    for (int64_t s = 2; s <= groups / 2 && tiles * s <= kCUs; ++s)
+        if (tile128_time(tiles, m, p.lw, steps, s) < tile128_time(tiles, m, p.lw, steps, best)) best = s;
+    p.per_split = (uint32_t)div_up(groups, best);
+    p.splits = (uint32_t)div_up(groups, p.per_split);
+    return p;
+}
+
+inline size_t product_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+    if (m < 1 || n < 1 || k < 1 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return 0;
+    const Product p = product_of(m, n, k);
+    return p.splits > 1 ? (size_t)p.splits * (size_t)p.part * sizeof(float) : 0;
+}
+
 // ------------------------------------------------------------------ block border
 
 inline int check_border(const coat_border* b) {
