@@ -66,9 +66,9 @@ __global__ __launch_bounds__(kBlock) void mx4_matmul_small_kernel(const uint8_t*
 
 // ------------------------------------------------------------------ large tiles
 //
-// A workgroup of 2 x 2 wavefronts computes tiles of 64 FN rows of B by 64 FM
-// rows of A, one after the other; the k of all its tiles forms one stream of
-// steps of 128 values, two steps a pair, four a group. A pair's codes (128
+// A workgroup of WN x WM wavefronts, each with 32 FN rows of B by 32 FM rows of
+// A, computes tiles one after the other; the k of all its tiles forms one stream
+// of steps of 128 values, two steps a pair, four a group. A pair's codes (128
 // bytes a row, B's rows before A's) go straight from global memory into one of
 // PAIRS slots of LDS, PAIRS pairs before they are used; a group's scale bytes
 // (16 a row) likewise. 128 bytes a row, because a compute unit takes in 130
@@ -142,19 +142,23 @@ struct Stream {
 // With splits > 1 item t is the product over the groups of four steps
 // [s per_split, (s + 1) per_split), s = t / tiles, of tile t % tiles, and goes to
 // y + s part (partial sums, added by another kernel).
-template <int FN, int FM, int PAIRS, class T>
-__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) void mx4_matmul_tile_kernel(
+template <int WN, int WM, int FN, int FM, int PAIRS, int PIECE, class T>
+__global__ __launch_bounds__(WN* WM* kWave) __attribute__((amdgpu_waves_per_eu(WN* WM / 4, WN* WM / 4))) void mx4_matmul_tile_kernel(
     const uint8_t* __restrict__ aq, const uint8_t* __restrict__ as, int64_t m, const uint8_t* __restrict__ bq,
     const uint8_t* __restrict__ bs, int64_t n, int64_t k, uint32_t tiles_m, uint32_t tiles_n, uint32_t splits,
     uint32_t per_split, T* __restrict__ y, int64_t ld, int64_t part) {
-    // D fragments of a half step; 2 D loads of a pair and SC of a group's scale bytes by each wavefront
-    constexpr int BN = 64 * FN, BM = 64 * FM, D = FN + FM, SC = (FN + FM) / 4, SETS = PAIRS / 2;
+    // D fragments of a half step; L loads of a pair (LB of them B's) and SC of a group's scale bytes by each wavefront
+    constexpr int WAVES = WN * WM, BN = 32 * WN * FN, BM = 32 * WM * FM, D = FN + FM, SETS = PAIRS / 2;
+    constexpr int L = (BN + BM) / 8 / WAVES, LB = BN / 8 / WAVES, kScaleLoads = (BN + BM) / 64;
+    constexpr int SC = kScaleLoads < WAVES ? 1 : kScaleLoads / WAVES;
+    static_assert(LB * 8 * WAVES == BN && L * 8 * WAVES == BN + BM && L % 2 == 0 && BN % 64 == 0, "loads are dealt evenly");
+    static_assert(kScaleLoads % WAVES == 0 || WAVES % kScaleLoads == 0, "scale loads too, or repeated");
     constexpr bool AHEAD = FN * FM <= 4;  // a phase is a step, not half a step
-    constexpr int PHASES = AHEAD ? 2 : 4, PIECE = 128;
+    constexpr int PHASES = AHEAD ? 2 : 4;
     constexpr uint32_t kSlotBytes = (BN + BM) * 128, kScaleBytes = (BN + BM) * 16;
     // stores of a whole tile, an exact count: later waits let them run
     constexpr int kStores = FN * FM * (sizeof(T) == 4 ? 4 : 2);
-    __shared__ __attribute__((aligned(16))) uint8_t lds[PAIRS * kSlotBytes + (SETS + 1) * kScaleBytes + kWavesPerBlock * 32 * PIECE];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[PAIRS * kSlotBytes + (SETS + 1) * kScaleBytes + WAVES * 32 * PIECE];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int half = lane >> 5, l32 = lane & 31;
@@ -173,17 +177,19 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
     // byte offsets of this lane's chunks and scale words from the tile's first rows
     const uint32_t chunk = (lane & 7) ^ ((wave & 1) * 4 + (lane >> 4));
     const uint32_t back = chunk >= 4 ? 64 : 0;  // to the same chunk of the pair's first step
-    uint32_t off[2 * D], soff[SC];
+    uint32_t off[L], soff[SC];
+    // with more wavefronts than loads of scale bytes they are made twice, so that every wavefront counts alike
+    const int swave = wave % kScaleLoads;
     auto offsets = [&](int64_t m0, int64_t n0) {
 #pragma unroll
-        for (int i = 0; i < 2 * D; ++i) {
-            const uint32_t row = (uint32_t)(i * 4 + wave) * 8 + lane / 8 - (i < 2 * FN ? 0 : BN);
-            const int64_t left = (i < 2 * FN ? n - n0 : m - m0) - 1;  // the last row stands in for those past the end
+        for (int i = 0; i < L; ++i) {
+            const uint32_t row = (uint32_t)(i * WAVES + wave) * 8 + lane / 8 - (i < LB ? 0 : BN);
+            const int64_t left = (i < LB ? n - n0 : m - m0) - 1;  // the last row stands in for those past the end
             off[i] = (row < left ? row : (uint32_t)left) * (uint32_t)qb + chunk * 16;
         }
 #pragma unroll
         for (int i = 0; i < SC; ++i) {
-            uint32_t row = (uint32_t)(i * 4 + wave) * 64 + lane;
+            uint32_t row = (uint32_t)(i * WAVES + swave) * 64 + lane;
             const bool is_b = row < BN;
             if (!is_b) row -= BN;
             const int64_t left = (is_b ? n - n0 : m - m0) - 1;
@@ -192,15 +198,15 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
     };
     const uint32_t lds_wave = lds0 + wave * 1024;
     auto fetch_part = [&](const Stream& at, int set, auto pair, auto i, uint32_t on = 1) {
-        const uint8_t* from = (i < 2 * FN ? at.bq : at.aq) + (pair == 1 ? at.second : 0);
+        const uint8_t* from = (i < LB ? at.bq : at.aq) + (pair == 1 ? at.second : 0);
         const uint32_t to = lds_wave + set * 2 * kSlotBytes, lane_off = off[i] - at.back[pair];
-        if (__builtin_constant_p(on)) load_to_lds16<pair * kSlotBytes + i * 4096>(to, lane_off, from);
-        else load_to_lds16_if<pair * kSlotBytes + i * 4096>(on, to, lane_off, from);
+        if (__builtin_constant_p(on)) load_to_lds16<pair * kSlotBytes + i * WAVES * 1024>(to, lane_off, from);
+        else load_to_lds16_if<pair * kSlotBytes + i * WAVES * 1024>(on, to, lane_off, from);
     };
     auto fetch_scales = [&](const Stream& at, int slot) {
         each<SC>([&](auto i) {
-            load_to_lds16<PAIRS * kSlotBytes + i * 4096>(lds_wave + slot * kScaleBytes, soff[i],
-                                                         (i * 4 + wave) * 64 < BN ? at.bs : at.as);
+            load_to_lds16<PAIRS * kSlotBytes + i * WAVES * 1024>(lds0 + swave * 1024 + slot * kScaleBytes, soff[i],
+                                                                 (i * WAVES + swave) * 64 < BN ? at.bs : at.as);
         });
     };
     auto settle = [&](Stream& at) {
@@ -217,7 +223,7 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
 
     u32x4 fb[AHEAD ? 2 : 1][2][FN], fa[AHEAD ? 2 : 1][2][FM];  // fragments, [parity of the step][half]
     uint32_t cb[2][FN], ca[2][FM];                             // scale words, by parity of the step
-    const int wn = (wave & 1) * FN * 32, wm = (wave >> 1) * FM * 32;
+    const int wn = wave % WN * FN * 32, wm = wave / WN * FM * 32;
     // fragment i of half h of step sp of a pair: A's first, which every row of matrix instructions needs
     auto read_frag = [&](int set, int pair, int sp, int h, int i) {
         const int pos = ((4 * sp + 2 * h + half) ^ ((l32 >> 1) & 7)) * 16;
@@ -278,12 +284,12 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
     using zero = std::integral_constant<int, 0>;
     using one = std::integral_constant<int, 1>;
     // With two slots the last pair's later loads follow before the first phase.
-    constexpr int kLast = PAIRS > 2 ? D : 2 * D;
+    constexpr int kLast = PAIRS > 2 ? L / 2 : L;
     each<SETS>([&](auto set) {
         if constexpr (set > 0) advance();
         fetch_scales(next, set);
-        each<2 * D>([&](auto i) { fetch_part(next, set, zero{}, i); });
-        each<(set + 1 < SETS ? 2 * D : kLast)>([&](auto i) { fetch_part(next, set, one{}, i); });
+        each<L>([&](auto i) { fetch_part(next, set, zero{}, i); });
+        each<(set + 1 < SETS ? L : kLast)>([&](auto i) { fetch_part(next, set, one{}, i); });
     });
     wait_vm_and_lds_then_barrier<0>();
 #pragma unroll
@@ -310,7 +316,7 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
     auto phase = [&](auto pair, auto f, uint32_t carry) {
         constexpr int kInstr = AHEAD ? 2 * FN * FM : FN * FM;
         constexpr bool last = f == PHASES - 1, new_step = AHEAD || f % 2 == 1;
-        constexpr int kReads = AHEAD ? 2 * D : D, kItems = kReads + (last || f == 0 ? D : 0);
+        constexpr int kReads = AHEAD ? 2 * D : D, kItems = kReads + (last || f == 0 ? L / 2 : 0);
         constexpr int u = 2 * pair + (AHEAD ? f : f / 2), p = u & 1;  // step of the group
         each<kInstr>([&](auto q) {
             each<(q + 1) * kItems / kInstr - q * kItems / kInstr>([&](auto r) {
@@ -325,7 +331,7 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
                     fetch_part(next, set, pair, std::integral_constant<int, item - kReads>{});
                 } else {
                     fetch_part(next, pair == 1 ? set : (set > 0 ? set - 1 : SETS - 1), std::integral_constant<int, 1 - pair>{},
-                               std::integral_constant<int, item - kReads + D>{}, PAIRS > 2 || pair == 1 ? 1 : carry);
+                               std::integral_constant<int, item - kReads + L / 2>{}, PAIRS > 2 || pair == 1 ? 1 : carry);
                 }
             });
             __builtin_amdgcn_sched_barrier(0);
@@ -342,7 +348,7 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
     auto pair_of_steps = [&](auto pair, uint32_t carry, uint32_t after_stores) {
         each<PHASES - 1>([&](auto f) { phase(pair, f, carry); });
         // still running at most: the loads of the pairs behind the next one, one group's scale bytes among them
-        constexpr int kAllow = (PAIRS - 2) * 2 * D + (PAIRS > 2 ? SC : 0);
+        constexpr int kAllow = (PAIRS - 2) * L + (PAIRS > 2 ? SC : 0);
         constexpr int kLate = kAllow + kStores < 63 ? kAllow + kStores : 63;  // the counter's end
         if (after_stores) wait_vm_and_lds_then_barrier<kLate>();
         else wait_vm_and_lds_then_barrier<kAllow>();
@@ -373,7 +379,7 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(1, 1))) 
             set = next_set();
             sslot = next_sslot();
         }
-        if constexpr (PAIRS == 2) each<D>([&](auto i) { fetch_part(next, 0, one{}, std::integral_constant<int, i + D>{}); });
+        if constexpr (PAIRS == 2) each<L / 2>([&](auto i) { fetch_part(next, 0, one{}, std::integral_constant<int, i + L / 2>{}); });
         // Out through LDS of this wavefront's own, 32 rows of PIECE bytes at a
         // time, so that each store writes long runs of a row: chunk c of row r
         // lies at position c ^ (r % chunks).
@@ -572,17 +578,21 @@ int launch_matmul(const uint8_t* aq, const uint8_t* as, int64_t m, const uint8_t
     const int64_t items = (int64_t)p.tiles_m * p.tiles_n * p.splits;
     if (p.way == Way::kTile256) {
         const unsigned grid = (unsigned)(items < kCUs ? items : kCUs);
-        hipLaunchKernelGGL((mx4_matmul_tile_kernel<4, 4, 2, T>), dim3(grid), dim3(kBlock), 0, st, aq, as, m, bq, bs, n,
+        hipLaunchKernelGGL((mx4_matmul_tile_kernel<2, 2, 4, 4, 2, 128, T>), dim3(grid), dim3(kBlock), 0, st, aq, as, m, bq, bs, n,
                            k, p.tiles_m, p.tiles_n, 1u, p.per_split, y, ld, (int64_t)0);
         return launch_status();
     }
     const unsigned grid = (unsigned)(items < kCUs ? items : kCUs);
     if (p.splits == 1) {
-        hipLaunchKernelGGL((mx4_matmul_tile_kernel<2, 2, 4, T>), dim3(grid), dim3(kBlock), 0, st, aq, as, m, bq, bs, n,
+        hipLaunchKernelGGL((mx4_matmul_tile_kernel<2, 2, 2, 2, 4, 128, T>), dim3(grid), dim3(kBlock), 0, st, aq, as, m, bq, bs, n,
                            k, p.tiles_m, p.tiles_n, 1u, p.per_split, y, ld, (int64_t)0);
         return launch_status();
     }
-    hipLaunchKernelGGL((mx4_matmul_tile_kernel<2, 2, 4, float>), dim3(grid), dim3(kBlock), 0, st, aq, as, m, bq, bs, n,
+    // Bound by LDS: eight wavefronts of 32 x 64 read half as much again from it as
+    // four of 64 x 64, but hide its latency. One round of split tiles gains (64 x
+    // 5120 x 13824 22 -> 20 us, 700 x 1000 x 8192 23 -> 20), whole ones lose (1500 x
+    // 5120 x 13824 79 -> 86).
+    hipLaunchKernelGGL((mx4_matmul_tile_kernel<4, 2, 1, 2, 4, 64, float>), dim3(grid), dim3(2 * kBlock), 0, st, aq, as, m, bq, bs, n,
                        k, p.tiles_m, p.tiles_n, p.splits, p.per_split, ws, p.lw, p.part);
     hipLaunchKernelGGL(mx4_matmul_join_kernel<T>, dim3((unsigned)(div_up(m * p.lw / 4, kBlock) < 8 * kCUs ? div_up(m * p.lw / 4, kBlock) : 8 * kCUs)),
                        dim3(kBlock), 0, st, (const float*)ws, p.part, p.lw, p.splits, m, n, y, ld);
