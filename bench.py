@@ -8,7 +8,7 @@ whole list. Prints one JSON line on stdout; progress goes to stderr.
 
   python bench.py [--gpus 1] [--steps 20] [--warmup 3] [--workload llama13b]
                   [--no-cpu-baseline] [--no-reference] [--copy-calibration]
-                  [--sweep | --act | --codec | --ceiling]
+                  [--sweep | --act | --layer-input | --codec | --ceiling]
 
 After the measured steps it also times, unless --no-reference, the same step
 without expansion (every group k = 1: the same bytes with the least
@@ -36,6 +36,11 @@ E4M3 and v in E5M2) on 2^30 values: one JSON line per launch kind.
 With --act it times the FP8 activation codec (per tensor and per group of 128,
 E4M3 and E5M2) on a 16384 x 13824 bf16 activation matrix (the input of
 Llama-2-13B's down projection for 16k tokens): one JSON line per launch kind.
+
+With --layer-input it times what makes and multiplies a layer input, on 16384
+tokens at Llama-2-13B's widths: the norms at a block's border (5120 channels;
+to bf16, FP8 and 4-bit form, and backward), the 4-bit codec and the gate
+projection's 4-bit products: one JSON line per launch kind.
 """
 from __future__ import annotations
 
@@ -229,6 +234,65 @@ def act_bench(args) -> int:
                        "bytes_per_element": bpe, "achieved_GBps": gbps, "frac_of_8TBps": gbps / PEAK_HBM_GBPS}
                 print(json.dumps(row), flush=True)
                 log(f"act {name} {row['granularity']} {fname}: {ms:.3f} ms, {gbps:.0f} GB/s")
+    return 0
+
+
+def layer_input_bench(args) -> int:
+    """Times of the layer-input operators' entry points, inputs resident in HBM."""
+    import torch
+
+    import fp8_optimizer_state_amd as coat
+    import synth
+
+    dev = torch.device("cuda:0")
+    torch.cuda.set_device(dev)
+    coat.lib()
+    t, c, f = 16384, 5120, 13824
+    bf16 = torch.bfloat16
+    y, r, dh, d_out = (synth.activations(t, c, seed=20 + i, device=dev).view(t, c) for i in range(4))
+    w_post, w_pre, gate = (torch.ones(c, dtype=bf16, device=dev) for _ in range(3))
+    r_out, h, dr, dy = (torch.empty(t, c, dtype=bf16, device=dev) for _ in range(4))
+    q8, s8 = torch.empty(t, c, dtype=torch.uint8, device=dev), torch.empty(t, c // 128, device=dev)
+    dw_post, dw_pre, dgate = (torch.empty(c, dtype=bf16, device=dev) for _ in range(3))
+    w = synth.params(f * c, 13, device=dev).view(f, c).to(bf16)
+    xq, xtq, wq, wtq = (coat.mx4_empty(*s, device=dev) for s in ((t, c), (c, t), (f, c), (c, f)))
+    dzq, dztq = coat.mx4_empty(t, f, device=dev), coat.mx4_empty(f, t, device=dev)
+    z, dx, dw = (torch.empty(*s, dtype=bf16, device=dev) for s in ((t, f), (t, c), (f, c)))
+    how = dict(w_post=w_post, w_pre=w_pre, gate=gate.view(1, c), scale=0.5, eps=1e-5)
+    n, mx = t * c, 17 / 32
+    ops = (
+        ("block_norm to bf16", lambda: coat.block_norm(y, r, r_out, h, **how), 8 * n, 0),
+        ("block_norm to E4M3, group 128",
+         lambda: coat.block_norm(y, r, r_out, None, q=q8, q_scale=s8, group=128, fmt=coat.FMT_E4M3, **how), (7 + 4 / 128) * n, 0),
+        ("block_norm to 4 bits", lambda: coat.block_norm(y, r, r_out, None, q=xq[0], q_scale=xq[1], fmt=coat.FMT_MX4, **how),
+         (6 + mx) * n, 0),
+        ("block_norm_backward",
+         lambda: coat.block_norm_backward(y, r_out, d_out, dh, dr, dy, dw_post=dw_post, dw_pre=dw_pre, dgate=dgate.view(1, c), **how),
+         12 * n, 0),
+        ("mx4_quantize along rows and columns", lambda: coat.mx4_quantize(h, *xq, *xtq), (2 + 2 * mx) * n, 0),
+        ("mx4_quantize weights, both", lambda: coat.mx4_quantize(w, *wq, *wtq), (2 + 2 * mx) * f * c, 0),
+        ("mx4_matmul Y = X W^T", lambda: coat.mx4_matmul(*xq, *wq, z), (n + f * c) * mx + 2 * t * f, 2 * t * f * c),
+        ("mx4_quantize gradient, both", lambda: coat.mx4_quantize(z, *dzq, *dztq), (2 + 2 * mx) * t * f, 0),
+        ("mx4_matmul dX = dY W", lambda: coat.mx4_matmul(*dzq, *wtq, dx), (t * f + f * c) * mx + 2 * n, 2 * t * f * c),
+        ("mx4_matmul dW = dY^T X", lambda: coat.mx4_matmul(*dztq, *xtq, dw), (t * f + n) * mx + 2 * f * c, 2 * t * f * c),
+        ("mx4_dequantize weights", lambda: coat.mx4_dequantize(*wq, w), (2 + mx) * f * c, 0),
+    )
+    stream = torch.cuda.current_stream()
+    for name, fn, nbytes, flops in ops:
+        for _ in range(args.warmup):
+            fn()
+        ev0, ev1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        ev0.record(stream)
+        for _ in range(args.steps):
+            fn()
+        ev1.record(stream)
+        torch.cuda.synchronize()
+        ms = ev0.elapsed_time(ev1) / args.steps
+        row = {"layer_input": name, "tokens": t, "channels": c, "features": f, "ms": ms,
+               "achieved_GBps": nbytes / (ms * 1e-3) / 1e9, "achieved_TFLOPps": flops / (ms * 1e-3) / 1e12}
+        print(json.dumps(row), flush=True)
+        log(f"{name}: {ms * 1e3:.1f} us, {row['achieved_GBps']:.0f} GB/s, {row['achieved_TFLOPps']:.0f} TFLOP/s")
     return 0
 
 
@@ -500,6 +564,8 @@ def main() -> int:
     ap.add_argument("--sweep", action="store_true",
                     help="time and measure the codec error of every group size / format / expansion variant")
     ap.add_argument("--act", action="store_true", help="time the FP8 activation codec instead of the step")
+    ap.add_argument("--layer-input", action="store_true",
+                    help="time the block-border norms, the 4-bit codec and its products instead of the step")
     ap.add_argument("--codec", action="store_true",
                     help="time the FP8 state codec (quantize / dequantize of moments) instead of the step")
     ap.add_argument("--ceiling", action="store_true",
@@ -517,6 +583,8 @@ def main() -> int:
         return sweep(args)
     if args.act:
         return act_bench(args)
+    if args.layer_input:
+        return layer_input_bench(args)
     if args.codec:
         return codec_bench(args)
     if args.ceiling:
