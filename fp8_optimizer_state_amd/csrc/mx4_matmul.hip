@@ -587,24 +587,31 @@ int launch_matmul(const uint8_t* aq, const uint8_t* as, int64_t m, const uint8_t
                            (uint32_t)tn, y, ld);
         return launch_status();
     }
-    const int64_t items = (int64_t)p.tiles_m * p.tiles_n * p.splits;
+    auto grid_of = [](int64_t items) { return dim3((unsigned)(items < kCUs ? items : kCUs)); };
+    auto small_tiles = [&](int64_t m0, int64_t n0) {  // rows of y from m0 and columns from n0
+        const int64_t tm = div_up(m - m0, 128), tn = div_up(n - n0, 128), qb = mx4_code_bytes(k), sb = mx4_scale_bytes(k);
+        hipLaunchKernelGGL((mx4_matmul_tile_kernel<2, 2, 2, 2, 4, 128, T>), grid_of(tm * tn), dim3(kBlock), 0, st, aq + m0 * qb,
+                           as + m0 * sb, m - m0, bq + n0 * qb, bs + n0 * sb, n - n0, k, (uint32_t)tm, (uint32_t)tn, 1u,
+                           p.per_split, y + m0 * ld + n0, ld, (int64_t)0);
+    };
     if (p.way == Way::kTile256) {
-        const unsigned grid = (unsigned)(items < kCUs ? items : kCUs);
-        hipLaunchKernelGGL((mx4_matmul_tile_kernel<2, 2, 4, 4, 2, 128, T>), dim3(grid), dim3(kBlock), 0, st, aq, as, m, bq, bs, n,
-                           k, p.tiles_m, p.tiles_n, 1u, p.per_split, y, ld, (int64_t)0);
+        const int64_t tm = div_up(p.head_m, 256), tn = div_up(p.head_n, 256);
+        hipLaunchKernelGGL((mx4_matmul_tile_kernel<2, 2, 4, 4, 2, 128, T>), grid_of(tm * tn), dim3(kBlock), 0, st, aq, as,
+                           p.head_m, bq, bs, p.head_n, k, (uint32_t)tm, (uint32_t)tn, 1u, p.per_split, y, ld, (int64_t)0);
+        if (p.head_m < m) small_tiles(p.head_m, 0);
+        else if (p.head_n < n) small_tiles(0, p.head_n);
         return launch_status();
     }
-    const unsigned grid = (unsigned)(items < kCUs ? items : kCUs);
     if (p.splits == 1) {
-        hipLaunchKernelGGL((mx4_matmul_tile_kernel<2, 2, 2, 2, 4, 128, T>), dim3(grid), dim3(kBlock), 0, st, aq, as, m, bq, bs, n,
-                           k, p.tiles_m, p.tiles_n, 1u, p.per_split, y, ld, (int64_t)0);
+        small_tiles(0, 0);
         return launch_status();
     }
+    const dim3 grid = grid_of((int64_t)p.tiles_m * p.tiles_n * p.splits);
     // Bound by LDS: eight wavefronts of 32 x 64 read half as much again from it as
     // four of 64 x 64, but hide its latency. One round of split tiles gains (64 x
     // 5120 x 13824 22 -> 20 us, 700 x 1000 x 8192 23 -> 20), whole ones lose (1500 x
     // 5120 x 13824 79 -> 86).
-    hipLaunchKernelGGL((mx4_matmul_tile_kernel<4, 2, 1, 2, 4, 64, float>), dim3(grid), dim3(2 * kBlock), 0, st, aq, as, m, bq, bs, n,
+    hipLaunchKernelGGL((mx4_matmul_tile_kernel<4, 2, 1, 2, 4, 64, float>), grid, dim3(2 * kBlock), 0, st, aq, as, m, bq, bs, n,
                        k, p.tiles_m, p.tiles_n, p.splits, p.per_split, ws, p.lw, p.part);
     hipLaunchKernelGGL(mx4_matmul_join_kernel<T>, dim3((unsigned)(div_up(m * p.lw / 4, kBlock) < 8 * kCUs ? div_up(m * p.lw / 4, kBlock) : 8 * kCUs)),
                        dim3(kBlock), 0, st, (const float*)ws, p.part, p.lw, p.splits, m, n, y, ld);

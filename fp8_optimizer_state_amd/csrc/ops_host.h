@@ -73,6 +73,7 @@ struct Product {
     Way way;
     uint32_t tiles_m, tiles_n, splits, per_split;
     int64_t lw, part;  // of the partial sums: elements of a row and of a split
+    int64_t head_m, head_n;  // kTile256: the part of y in large tiles; the rest, rows or columns, follows in small ones
 };
 
 // Estimated microseconds of 128 x 128 tiles with their k in `splits` parts: 0.27
@@ -87,8 +88,14 @@ inline double tile128_time(int64_t tiles, int64_t m, int64_t lw, int64_t steps, 
     return splits == 1 ? work : work + 6.0 + 8.0 * (double)splits * (double)m * (double)lw / 3.5e6;
 }
 
+// The same of 256 x 256 tiles, with all compute units at work: 13824 x 5120 x 8191
+// (five rounds of 64 steps) takes 294, 16384 x 13824 x 5120 (14 of 40) 550.
+inline double tile256_time(int64_t tiles, int64_t steps) {
+    return (double)div_up(tiles, kCUs) * (0.81 * (double)steps + 7.0);
+}
+
 inline Product product_of(int64_t m, int64_t n, int64_t k) {
-    Product p{Way::kSmall, 0, 0, 1, 0, 0, 0};
+    Product p{Way::kSmall, 0, 0, 1, 0, 0, 0, m, n};
     if (k == 0 || k >= (1 << 22)) return p;  // longer rows than 32-bit offsets within a tile reach
     // Up to 32 rows of A: 1 x 13824 x 5120 takes 10 us, 32 17 us; 64 take 21 that
     // way and 16 in tiles.
@@ -104,13 +111,34 @@ inline Product product_of(int64_t m, int64_t n, int64_t k) {
     p.tiles_n = (uint32_t)div_up(n, 256);
     // large tiles where they fill most of the card: 2048 x 5120 x 5120 (160 of them)
     // takes 40 us and 46 in small ones, 1500 x 5120 x 13824 (120) 87 and 77
-    if ((int64_t)p.tiles_m * p.tiles_n >= 160) return p;
+    const int64_t large = (int64_t)p.tiles_m * p.tiles_n, steps = div_up(k, 128);
+    if (large >= 160) {
+        const int64_t full = large / kCUs * kCUs;  // of them in whole rounds of workgroups
+        // A last round of few large tiles is done in small ones instead, if the
+        // estimate gains 6 % or more (the card is bound by power, and a round with
+        // few workgroups runs faster than the estimate): 4096 x 5120 x 5120 takes 86
+        // us whole and 67 so, 2600 x 13824 x 5120 134 and 121, 13824 x 5120 x 16384
+        // 582 and 556; 10000 x 7000 x 2000 (4.5 % by the estimate) 131 and 141.
+        double best = 0.94 * tile256_time(large, steps);
+        for (const bool rows : {true, false}) {
+            const int64_t across = rows ? p.tiles_n : p.tiles_m, lines = full / across;
+            if (lines == 0 || full == large) continue;
+            const int64_t left_m = rows ? m - 256 * lines : m, left_n = rows ? n : n - 256 * lines;
+            const double t = tile256_time(lines * across, steps) + 4.0 +
+                             tile128_time(div_up(left_m, 128) * div_up(left_n, 128), 0, 0, steps, 1);
+            if (t >= best) continue;
+            best = t;
+            p.head_m = rows ? 256 * lines : m;
+            p.head_n = rows ? n : 256 * lines;
+        }
+        return p;
+    }
     p.way = Way::kTile128;
     p.tiles_m = (uint32_t)div_up(m, 128);
     p.tiles_n = (uint32_t)div_up(n, 128);
     p.lw = div_up(n, 64) * 64;
     p.part = m * p.lw;
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, steps = div_up(k, 128);
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
     int64_t best = 1;
     for (int64_t s = 2; s <= groups / 2 && tiles * s <= kCUs; ++s)
         if (tile128_time(tiles, m, p.lw, steps, s) < tile128_time(tiles, m, p.lw, steps, best)) best = s;

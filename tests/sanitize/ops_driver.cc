@@ -65,6 +65,9 @@ static void product(int64_t m, int64_t n, int64_t k) {
     EXPECT((int64_t)p.tiles_n * tile >= n && ((int64_t)p.tiles_n - 1) * tile < n);
     EXPECT((int64_t)p.splits * p.per_split >= groups && ((int64_t)p.splits - 1) * p.per_split < groups);
     EXPECT((int64_t)p.tiles_m * p.tiles_n * p.splits <= 0x7FFFFFFF);
+    EXPECT(p.head_m >= 1 && p.head_m <= m && p.head_n >= 1 && p.head_n <= n && (p.head_m == m || p.head_n == n));
+    if (p.head_m < m) EXPECT(p.way == Way::kTile256 && p.head_m % 256 == 0);
+    if (p.head_n < n) EXPECT(p.way == Way::kTile256 && p.head_n % 256 == 0);
     if (p.splits > 1) EXPECT(p.lw >= n && p.lw % 4 == 0 && need == (size_t)p.splits * (size_t)m * (size_t)p.lw * 4);
 }
 
@@ -78,6 +81,8 @@ int main() {
     for (int64_t m : {1, 32, 33, 64, 100, 333, 2048, 16384, 1 << 20, 0x7FFFFFFF})
         for (int64_t n : {1, 17, 300, 5120, 13824, 0x7FFFFFFF})
             for (int64_t k : {1, 128, 511, 513, 5120, 13824, (1 << 22) - 1, 1 << 22, 0x7FFFFFFF}) product(m, n, k);
+    EXPECT(product_of(4096, 5120, 5120).head_n == 16 * 256 && product_of(5120, 4096, 5120).head_m == 16 * 256);
+    EXPECT(product_of(16384, 5120, 13824).head_n == 5120);  // whole rounds
     EXPECT(product_workspace_bytes(0, 5, 5) == 0 && product_workspace_bytes(5, 5, -1) == 0);
 
     EXPECT(mx4_code_bytes(1) == 64 && mx4_code_bytes(129) == 128 && mx4_scale_bytes(512) == 16 && mx4_scale_bytes(513) == 32);

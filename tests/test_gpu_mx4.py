@@ -185,7 +185,7 @@ def test_round_trip(coat, rows, cols, dtype):
 PRODUCTS = [(1, 1, 1), (1, 32, 64), (2, 3, 129), (16, 16, 128), (17, 33, 500), (31, 64, 513), (33, 31, 640), (64, 65, 1024),
             (1, 257, 2731), (5, 700, 1000), (65, 130, 4097), (128, 128, 256), (129, 255, 384), (257, 256, 512), (300, 513, 2048),
             (256, 256, 1), (512, 768, 640), (2600, 1300, 1030), (1030, 4100, 520),
-            (70, 200, 5000), (129, 300, 13824), (33, 5120, 2731), (64, 65, 6000), (333, 640, 4100), (4100, 4100, 300), (300, 300, 3000)]
+            (70, 200, 5000), (129, 300, 13824), (33, 5120, 2731), (64, 65, 6000), (333, 640, 4100), (4100, 4100, 300), (300, 300, 3000), (4090, 4950, 300)]
 
 
 def operand(rows, k, seed):
