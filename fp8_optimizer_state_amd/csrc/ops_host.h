@@ -217,13 +217,31 @@ inline BorderSplit border_split(int64_t rows, int64_t cols, int64_t rows_per_gat
     const int64_t waves = border_waves(cols), each = waves > 8 ? 1 : (waves > 4 ? 2 : 4);
     const int64_t want = div_up(rows, kCUs * each);  // rows of a workgroup
     if (!dgate) return BorderSplit{want, 0, div_up(rows, want)};
-    const int64_t rpg = rows_per_gate < rows ? rows_per_gate : rows;
-    if (rpg <= want) {
-        const int64_t step = want / rpg * rpg;
-        return BorderSplit{step, 0, div_up(rows, step)};
+    const int64_t rpg = rows_per_gate < rows ? rows_per_gate : rows, gates = div_up(rows, rpg);
+    // Gate rows seldom divide evenly. Of the ways that fill one to three rounds of
+    // workgroups the one with the fewest rows after one another is taken, a
+    // workgroup's beginning and end counting as two: 8000 x 8000 with 301 tokens a
+    // gate row takes 194 us in 243 workgroups of 34 rows, 303 in 270 of 31.
+    BorderSplit best{0, 0, 0};
+    int64_t least = INT64_MAX;
+    auto consider = [&](int64_t step, int64_t chunks, int64_t blocks) {
+        const int64_t cost = div_up(blocks, kCUs * each) * (step + 2);
+        if (cost < least) {
+            least = cost;
+            best = BorderSplit{step, chunks, blocks};
+        }
+    };
+    for (int64_t round = 1; round <= 3; ++round) {
+        const int64_t slots = round * kCUs * each;
+        if (gates <= slots) {
+            const int64_t chunks = slots / gates < rpg ? slots / gates : rpg;
+            consider(div_up(rpg, chunks), chunks, gates * chunks);
+        } else {
+            const int64_t step = div_up(gates, slots) * rpg;
+            consider(step, 0, div_up(rows, step));
+        }
     }
-    const int64_t chunks = div_up(rpg, want);
-    return BorderSplit{div_up(rpg, chunks), chunks, div_up(rows, rpg) * chunks};
+    return best;
 }
 
 // Partial sums of the backward pass: up to three sections of blocks x cols fp32.
