@@ -431,13 +431,18 @@ __global__ __launch_bounds__(WN* WM* kWave) __attribute__((amdgpu_waves_per_eu(W
                         const u32x4 w = *reinterpret_cast<const u32x4*>(out + (r + lr) * PIECE + ((lc ^ (lr & (kChunks - 1))) * 16));
                         store_chunk<(FN * FM > 4)>(to + r * ld, w);
                     }
-                } else {  // element by element, a row or two at a time
-                    constexpr int kCols = PIECE / sizeof(T), kRows = kWave / kCols;
-                    const int er = lane / kCols, ec = lane % kCols;
+                } else {  // what exists of each chunk
+                    const int64_t left = n - (col0 + lc * kPer);
 #pragma nounroll
-                    for (int r = er; r < 32; r += kRows) {
-                        const T v = *reinterpret_cast<const T*>(out + r * PIECE + (((ec / kPer) ^ (r & (kChunks - 1))) * kPer + ec % kPer) * sizeof(T));
-                        if (row0 + r < m && col0 + ec < n) gp(yc)[(row0 + r) * ld + col0 + ec] = v;
+                    for (int r = lr; r < 32 && row0 + r < m; r += kWave / kChunks) {
+                        const uint8_t* from = out + r * PIECE + ((lc ^ (r & (kChunks - 1))) * 16);
+                        T* to = yc + (row0 + r) * ld + col0 + lc * kPer;
+                        if (left >= kPer) {
+                            store_chunk<false>(to, *reinterpret_cast<const u32x4*>(from));
+                        } else {
+#pragma nounroll
+                            for (int e = 0; e < (int)left; ++e) gp(to)[e] = reinterpret_cast<const T*>(from)[e];
+                        }
                     }
                 }
             }
