@@ -110,7 +110,9 @@ __device__ __forceinline__ uint32_t float_bits(float v) { return __builtin_bit_c
 
 // A 16-byte chunk of y. PAST: written past the caches' usual order, where y would
 // drive the operands out of them (16384 x 16384 x 512 to bf16 in large tiles: 158
-// us against 214).
+// us against 214). Not where the pieces of a row end within a line, whose halves
+// would go to memory one by one (4097 x 5001 x 2000 to fp32: 77 us against 50;
+// 16384 x 13823 x 5120 643 against 594).
 template <bool PAST>
 __device__ __forceinline__ void store_chunk(float* p, const u32x4& w) {
     if constexpr (PAST) __builtin_nontemporal_store(w, reinterpret_cast<gu32x4_a4*>(gp(p)));
@@ -317,6 +319,7 @@ __global__ __launch_bounds__(WN* WM* kWave) __attribute__((amdgpu_waves_per_eu(W
     auto next_sslot = [&] { return sslot < SETS ? sslot + 1 : 0; };
     auto free_sslot = [&] { return sslot > 0 ? sslot - 1 : SETS; };
     uint32_t t = first, g = 0;
+    const bool lines = FN * FM <= 4 || (((uintptr_t)y | ((uint64_t)ld * sizeof(T))) & 127) == 0;  // a piece fills lines of y
 
     f32x16 acc[FN][FM];
     // A phase. A wavefront issues in order, and a matrix instruction occupies its
@@ -424,13 +427,18 @@ __global__ __launch_bounds__(WN* WM* kWave) __attribute__((amdgpu_waves_per_eu(W
                 }
                 const int lr = lane / kChunks, lc = lane % kChunks;
                 const int64_t row0 = cm0 + wm + j * 32, col0 = cn0 + wn + pc * kBlocks * 16;
-                if (whole) {
+                auto store_rows = [&](auto past) {
                     T* to = yc + (row0 + lr) * ld + col0 + lc * kPer;
 #pragma unroll
                     for (int r = 0; r < 32; r += kWave / kChunks) {
                         const u32x4 w = *reinterpret_cast<const u32x4*>(out + (r + lr) * PIECE + ((lc ^ (lr & (kChunks - 1))) * 16));
-                        store_chunk<(FN * FM > 4)>(to + r * ld, w);
+                        store_chunk<past.value>(to + r * ld, w);
                     }
+                };
+                if (whole && lines) {
+                    store_rows(std::bool_constant<(FN * FM > 4)>{});
+                } else if (whole) {
+                    store_rows(std::false_type{});
                 } else {  // what exists of each chunk
                     const int64_t left = n - (col0 + lc * kPer);
 #pragma nounroll
@@ -480,7 +488,7 @@ __global__ __launch_bounds__(kBlock) void mx4_matmul_join_kernel(const float* __
 // ------------------------------------------------------------------ few rows of A
 //
 // Bound by reading B once, and by its launch where B is small: 1 x 13824 x 5120 (38
-// MB) takes 9.4 us, 4.0 TB/s. A workgroup takes 16 rows of B; its wavefronts take a
+// MB) takes 9.0 us, 4.2 TB/s. A workgroup takes 16 rows of B; its wavefronts take a
 // part of k each, straight from global memory into registers, and add their
 // sums through LDS in order. Up to 16 FM rows of A; rows past the end are read
 // as the last one and not stored.
@@ -491,6 +499,7 @@ __global__ __launch_bounds__(kBlock) void mx4_matmul_join_kernel(const float* __
 // consecutive bytes of each row (a 32-row form of the instruction would make it
 // 32), and a row's scale bytes of four steps come in one.
 constexpr int kFewWaves = 8;
+constexpr int kFewAhead = 2;  // groups of four steps whose loads are in flight together
 
 template <int FM, class T>
 __global__ __launch_bounds__(kFewWaves* kWave) void mx4_matmul_few_kernel(const uint8_t* __restrict__ aq,
@@ -517,11 +526,10 @@ __global__ __launch_bounds__(kFewWaves* kWave) void mx4_matmul_few_kernel(const 
     f32x4 acc[FM];
 #pragma unroll
     for (int j = 0; j < FM; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int kAhead = 2;  // groups whose loads are in flight together
-    for (int g = g0; g < g1; g += kAhead) {
-        u32x4 b[kAhead][4], a[kAhead][FM][4], cb[kAhead], ca[kAhead][FM];
+    for (int g = g0; g < g1; g += kFewAhead) {
+        u32x4 b[kFewAhead][4], a[kFewAhead][FM][4], cb[kFewAhead], ca[kFewAhead][FM];
 #pragma unroll
-        for (int v = 0; v < kAhead; ++v) {
+        for (int v = 0; v < kFewAhead; ++v) {
             const int gv = g + v < g1 ? g + v : g1 - 1;
             cb[v] = *reinterpret_cast<const gu32x4*>(gp(psb) + gv * 16);
 #pragma unroll
@@ -535,7 +543,7 @@ __global__ __launch_bounds__(kFewWaves* kWave) void mx4_matmul_few_kernel(const 
             }
         }
 #pragma unroll
-        for (int v = 0; v < kAhead; ++v)
+        for (int v = 0; v < kFewAhead; ++v)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 // a step past this wavefront's part gets scale bytes 0, and adds nothing
@@ -572,7 +580,9 @@ __global__ __launch_bounds__(kFewWaves* kWave) void mx4_matmul_few_kernel(const 
 template <int FM, class T>
 int launch_few(const uint8_t* aq, const uint8_t* as, int64_t m, const uint8_t* bq, const uint8_t* bs, int64_t n, int64_t k,
                T* y, int64_t ld, hipStream_t st) {
-    const int64_t groups = div_up(k, 512), per = div_up(groups, kFewWaves);
+    // whole turns of the loop: 1 x 32000 x 4096 (8 groups) takes 14 us with 4
+    // wavefronts of two groups and 25 with 8 of one
+    const int64_t groups = div_up(k, 512), per = div_up(groups, kFewWaves * kFewAhead) * kFewAhead;
     hipLaunchKernelGGL((mx4_matmul_few_kernel<FM, T>), dim3((unsigned)div_up(n, 16)), dim3((unsigned)div_up(groups, per) * kWave),
                        0, st, aq, as, m, bq, bs, n, k, (int)per, y, ld);
     return launch_status();

@@ -97,9 +97,10 @@ inline double tile256_time(int64_t tiles, int64_t steps) {
 inline Product product_of(int64_t m, int64_t n, int64_t k) {
     Product p{Way::kSmall, 0, 0, 1, 0, 0, 0, m, n};
     if (k == 0 || k >= (1 << 22)) return p;  // longer rows than 32-bit offsets within a tile reach
-    // Up to 32 rows of A: 1 x 13824 x 5120 takes 10 us, 32 17 us; 64 take 21 that
-    // way and 16 in tiles.
-    if (m <= 32) {
+    // Few rows of A, which each 16 rows of B read again: 1 x 13824 x 5120 takes 9 us
+    // this way and 15 in tiles, 16 12 and 15, 32 17 and 15; 24 x 10000 x 5120 12 and
+    // 15, 16 x 32000 x 4096 20 and 15.
+    if (m <= 32 && m * n * k <= int64_t(7) << 28) {
         p.way = Way::kFew;
         return p;
     }

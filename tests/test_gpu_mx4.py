@@ -225,6 +225,19 @@ def test_product_of_whole_numbers(coat, m, n, k):
     assert np.array_equal(got, want)
 
 
+@pytest.mark.parametrize("m,n,k", [(20, 20000, 5000), (32, 4200, 14000)])
+def test_product_of_few_rows_with_much(coat, m, n, k):
+    """Few rows of A are not taken by themselves where B is large: the same bits as among more rows (exact sums)."""
+    g = torch.Generator(device="cuda").manual_seed(k)
+    aq, bq = (torch.randint(0, 256, (r, o.code_bytes(k)), dtype=torch.uint8, device="cuda", generator=g) for r in (200, n))
+    as_, bs = (torch.full((r, o.scale_bytes(k)), 127, dtype=torch.uint8, device="cuda") for r in (200, n))
+    few, many = torch.full((m + 1, n), 9.0, device="cuda"), torch.empty(200, n, device="cuda")
+    coat.mx4_matmul(aq[:m], as_[:m], bq, bs, few[:m])
+    coat.mx4_matmul(aq, as_, bq, bs, many)
+    torch.cuda.synchronize()
+    assert torch.equal(few[:m], many[:m]) and bool((few[m] == 9.0).all())
+
+
 @pytest.mark.parametrize("m,n,k", [(3, 5, 640), (130, 260, 640)])
 def test_product_takes_each_scale_at_its_block(coat, m, n, k):
     """One value a row, scales all different: a scale or a code at a wrong place shows."""
