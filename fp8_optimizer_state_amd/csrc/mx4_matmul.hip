@@ -436,7 +436,9 @@ __global__ __launch_bounds__(WN* WM* kWave) __attribute__((amdgpu_waves_per_eu(W
                     }
                 };
                 if (whole && lines) {
+                    asm volatile("; whole lines" ::: "memory");  // around the branch, which otherwise becomes
                     store_rows(std::bool_constant<(FN * FM > 4)>{});
+                    asm volatile("; of y" ::: "memory");  // one with the next, and its stores plain ones
                 } else if (whole) {
                     store_rows(std::false_type{});
                 } else {  // what exists of each chunk
