@@ -43,7 +43,7 @@ static void border(int64_t rows, int64_t cols, int64_t rpg, bool dgate) {
         }
     }
     for (int v : seen) EXPECT(v == 1);
-    EXPECT(s.blocks <= 2 * 4 * kCUs);
+    EXPECT(s.blocks <= 3 * 4 * kCUs);
     coat_border d{};
     d.rows = rows;
     d.cols = cols;
@@ -72,9 +72,9 @@ static void product(int64_t m, int64_t n, int64_t k) {
 }
 
 int main() {
-    for (int64_t rows : {1, 2, 7, 255, 256, 257, 700, 1031, 4096, 5001})
+    for (int64_t rows : {1, 2, 7, 255, 256, 257, 600, 700, 1031, 4096, 5001, 8000})
         for (int64_t cols : {1, 64, 512, 1024, 2731, 5120, 8192, 16384})
-            for (int64_t rpg : {int64_t(1), int64_t(2), int64_t(3), int64_t(5), int64_t(64), int64_t(257), rows / 2 + 1, rows, rows + 9})
+            for (int64_t rpg : {int64_t(1), int64_t(2), int64_t(3), int64_t(5), int64_t(31), int64_t(64), int64_t(257), rows / 2 + 1, rows, rows + 9})
                 for (bool dgate : {false, true}) border(rows, cols, rpg, dgate);
     EXPECT(border_split(0, 64, 1, true).blocks == 0);
 

@@ -138,12 +138,21 @@ def test_norms_without_weights(coat):
 
 @pytest.mark.parametrize("grads", TYPES)
 @pytest.mark.parametrize("rows,rpg", [(1, 1), (12, 1), (12, 5), (700, 1), (700, 2), (700, 3), (700, 699), (700, 700), (700, 4000),
-                                      (1031, 257), (2100, 4), (2100, 5), (2100, 7), (2100, 1050), (1537, 1536)])
+                                      (1031, 257), (2100, 4), (2100, 5), (2100, 7), (2100, 1050), (1537, 1536), (5000, 3), (5000, 7),
+                                      (5000, 301), (2600, 31)])
 def test_gates_of_sequences(coat, rows, rpg, grads):
     """Tokens that share a gate row, in every way that rows are dealt to workgroups; a last gate row with fewer tokens."""
     t, how = make(rows, 72, rows + rpg, rpg=rpg)
     check_forward(coat, t, how)
     check_backward(coat, t, how, TYPES[grads])
+
+
+@pytest.mark.parametrize("cols", [4099, 9000])
+@pytest.mark.parametrize("rpg", [2, 3, 5, 31])
+def test_gates_of_sequences_of_wide_rows(coat, rpg, cols):
+    """Few workgroups of many threads: several gate rows, one, and parts of one to a workgroup."""
+    t, how = make(600, cols, cols + rpg, rpg=rpg)
+    check_backward(coat, t, how, BF)
 
 
 def test_gate_for_all_by_default(coat):
