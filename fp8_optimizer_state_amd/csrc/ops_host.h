@@ -235,8 +235,8 @@ inline BorderSplit border_split(int64_t rows, int64_t cols, int64_t rows_per_gat
     for (int64_t round = 1; round <= 3; ++round) {
         const int64_t slots = round * kCUs * each;
         if (gates <= slots) {
-            const int64_t chunks = slots / gates < rpg ? slots / gates : rpg;
-            consider(div_up(rpg, chunks), chunks, gates * chunks);
+            const int64_t step = div_up(rpg, slots / gates), chunks = div_up(rpg, step);
+            consider(step, chunks, gates * chunks);
         } else {
             const int64_t step = div_up(gates, slots) * rpg;
             consider(step, 0, div_up(rows, step));

@@ -43,6 +43,7 @@ static void border(int64_t rows, int64_t cols, int64_t rpg, bool dgate) {
         }
     }
     for (int v : seen) EXPECT(v == 1);
+    if (s.chunks > 0) EXPECT((s.chunks - 1) * s.step < eff && s.chunks * s.step >= eff);  // no empty part of a whole gate row
     EXPECT(s.blocks <= 3 * 4 * kCUs);
     coat_border d{};
     d.rows = rows;
