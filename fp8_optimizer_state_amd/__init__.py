@@ -271,13 +271,14 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
 # torch.cuda.current_stream() builds a Stream object: 2 us, a fifth of a small call
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda gpu: torch.cuda.current_stream(gpu).cuda_stream)
+_current_gpu = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device  # of a process that has GPU tensors
 
 
 def _call(gpu: int, stream, function, what: str, *args) -> None:
     """function(*args, stream handle), with GPU `gpu` current."""
     if stream is not None and stream.device_index != gpu:
         raise ValueError(f"the stream belongs to GPU {stream.device_index}, the tensors are on GPU {gpu}")
-    if gpu == torch.cuda.current_device():
+    if gpu == _current_gpu():
         rc = function(*args, _raw_stream(gpu) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(gpu):
