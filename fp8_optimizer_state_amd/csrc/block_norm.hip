@@ -47,6 +47,11 @@ __device__ __forceinline__ void block_sum2(float (&scratch)[2][kMaxWaves][2], in
     }
 }
 
+// A value that every lane holds, in a scalar register.
+__device__ __forceinline__ float uniform(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
+}
+
 // How a row ends: with a whole chunk, inside one, or before the first one's end.
 enum Edge { kWhole, kInside, kTiny };
 
@@ -260,8 +265,11 @@ struct BorderBackward {
 
 // A workgroup takes consecutive rows and sums the gradients of the weights (and
 // of a gate row, while its tokens last) in registers.
-//   pre:  with u = w_pre dh, s2 = sum r u:  d = dr_out + rho u - r rho^3 s2 / cols
-//   post: with u = w_post scale g d, s4 = sum y u:  dy = sig u - y sig^3 s4 / cols
+//   pre:  with u = w_pre dh, s2 = sum r u:  d = dr_out + rho (u - (r rho) (rho (s2 / cols)))
+//   post: with u = w_post scale g d, s4 = sum y u:  dy = sig (u - y (sig (s4 / cols)) sig)
+// The products are formed in this order: rho^3 leaves fp32's range for rows of 1e13
+// and for rows of zeros with eps under 2e-26, while r rho is at most sqrt(cols).
+// (y sig multiplied first, as r rho is, costs registers: 16384 x 13824 650 us.)
 // MAXT: threads at most. Up to 768 leave registers for loading a row while the
 // one before it is worked on.
 template <class S, class P, int NV, int EDGE, int MAXT>
@@ -397,8 +405,8 @@ __global__ __launch_bounds__(MAXT) void border_backward_kernel(BorderBackward p)
             }
             block_sum2(scratch, buf, waves, s1, s2);
             buf ^= 1;
-            rho = __builtin_amdgcn_rsqf(__builtin_fmaf(s1, p.inv_cols, p.eps));
-            back = rho * rho * rho * (s2 * p.inv_cols);
+            rho = uniform(__builtin_amdgcn_rsqf(__builtin_fmaf(s1, p.inv_cols, p.eps)));
+            back = uniform(rho * (s2 * p.inv_cols));
         }
         float d[NV][8];
         float s3 = 0.0f, s4 = 0.0f;
@@ -413,9 +421,9 @@ __global__ __launch_bounds__(MAXT) void border_backward_kernel(BorderBackward p)
                 weight(w_pre[i], p.w_pre, 0, c, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float ru = rho * uv[j];
-                    acc_pre[i][j] = __builtin_fmaf(xv[j], ru, acc_pre[i][j]);
-                    d[i][j] += __builtin_fmaf(ru, w[j], -xv[j] * back);
+                    const float xn = xv[j] * rho;
+                    acc_pre[i][j] = __builtin_fmaf(xn, uv[j], acc_pre[i][j]);
+                    d[i][j] = __builtin_fmaf(rho, __builtin_fmaf(uv[j], w[j], -xn * back), d[i][j]);
                 }
             }
             store8<EDGE == kWhole>(static_cast<S*>(p.dr) + base + c, n, d[i]);
@@ -438,8 +446,8 @@ __global__ __launch_bounds__(MAXT) void border_backward_kernel(BorderBackward p)
         if (p.post) {
             block_sum2(scratch, buf, waves, s3, s4);
             buf ^= 1;
-            sig = __builtin_amdgcn_rsqf(__builtin_fmaf(s3, p.inv_cols, p.eps));
-            back = sig * sig * sig * (s4 * p.inv_cols);
+            sig = uniform(__builtin_amdgcn_rsqf(__builtin_fmaf(s3, p.inv_cols, p.eps)));
+            back = uniform(sig * (s4 * p.inv_cols));
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -455,7 +463,7 @@ __global__ __launch_bounds__(MAXT) void border_backward_kernel(BorderBackward p)
                 const float yn = yv[j] * sig, gd = g[j] * d[i][j];
                 post[j] = __builtin_fmaf(gd, yn, post[j]);
                 gates[j] = __builtin_fmaf(d[i][j] * w[j], yn, gates[j]);
-                out[j] = __builtin_fmaf(sig * w[j], gd, -yv[j] * back);
+                out[j] = sig * __builtin_fmaf(yv[j] * back, -sig, w[j] * gd);
             }
             put(0, i, acc_post[i], post);
             put(1, i, acc_gate[i], gates);

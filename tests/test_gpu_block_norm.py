@@ -287,3 +287,43 @@ def test_gradient_against_differences(coat):
             assert abs((formula[grad][0] * way).sum() - want) <= 1e-6 * (1 + size), name
             bound = 1e-6 * (1 + size) + (o.half_step(out[grad].dtype) + o.U32 * o.dw_steps(rows)) * np.abs(got * way).sum()
             assert abs((got * way).sum() - want) <= bound, name
+
+
+def gradients_at(coat, t, how, eps):
+    """check_backward with another eps, as fp32 holds it."""
+    how = dict(how, eps=eps)
+    eps = float(np.float32(eps))
+    rows = t["r"].shape[0]
+    out = backward(coat, t, how, t["r"])
+    want = o.border_backward(n64(t["y"]), n64(t["r"]), n64(t["dr_out"]), n64(t["dh"]), n64(t["w_post"]), n64(t["w_pre"]),
+                             n64(t["gate"]), how["rows_per_gate"], how["scale"], eps, how["post"], -(-rows // how["rows_per_gate"]))
+    steps = dict(dr=o.DR_STEPS, dy=o.DY_STEPS, dw_post=o.dw_steps(rows), dw_pre=o.dw_steps(rows), dgate=o.dw_steps(rows))
+    for name, got in out.items():
+        within(got, want[name][0], o.U32 * steps[name] * want[name][1], got.dtype, name)
+
+
+@pytest.mark.parametrize("stream", TYPES)
+@pytest.mark.parametrize("cols", [5, 40, 1029, 4096, 9000])
+@pytest.mark.parametrize("size", [1e-12, 1e8, 1e13, 1e14, 1e15, 1e16, 1e17])
+def test_gradients_of_rows_of_any_size(coat, size, cols, stream):
+    """Rows whose factor's cube leaves fp32's range (sums of squares up to 9e37 here, inside
+    it): the projections on the rows keep their accuracy. dr_out is as large as they are."""
+    t, how = make(6, cols, cols, TYPES[stream], F32, rpg=2)
+    g = torch.Generator().manual_seed(cols + 1)
+    for name, mag in (("r", size), ("y", size), ("dr_out", min(1.0, 1.0 / size))):
+        t[name] = (torch.randn(6, cols, generator=g) * mag).to(t[name].dtype).cuda()
+    check_forward(coat, t, how)
+    gradients_at(coat, t, how, EPS)
+    t["dr_out"] = None
+    gradients_at(coat, t, how, EPS)
+
+
+@pytest.mark.parametrize("stream", TYPES)
+@pytest.mark.parametrize("eps", [1e-20, 1e-30, 2.0 ** -126])
+def test_gradients_of_rows_of_zeros_with_a_small_eps(coat, eps, stream):
+    """The factor of such a row is eps^-1/2, whose cube passes fp32; its gradient does not."""
+    t, how = make(6, 520, 31, TYPES[stream], F32, rpg=2)
+    t["r"][0] = 0.0
+    t["y"][3] = 0.0
+    t["r"][4] *= 1e-15 / t["r"][4].float().abs().max()
+    gradients_at(coat, t, how, eps)
