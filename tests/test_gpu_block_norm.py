@@ -327,3 +327,17 @@ def test_gradients_of_rows_of_zeros_with_a_small_eps(coat, eps, stream):
     t["y"][3] = 0.0
     t["r"][4] *= 1e-15 / t["r"][4].float().abs().max()
     gradients_at(coat, t, how, eps)
+
+
+@pytest.mark.parametrize("cols", [40, 1029, 9000])
+def test_gradient_of_an_output_that_is_not_normalised(coat, cols):
+    """Without the post-norm dy = scale gate dr_out: an Inf or NaN in y shows in the gate's gradient alone."""
+    t, how = make(6, cols, 17, post=False, pre=False, rpg=3)
+    clean = backward(coat, t, how, t["r"])
+    t["y"][1, 7] = float("inf")
+    t["y"][4, cols - 1] = float("nan")
+    out = backward(coat, t, how, t["r"])
+    assert torch.equal(out["dr"], clean["dr"]) and torch.equal(out["dy"], clean["dy"])
+    bad = torch.zeros_like(out["dgate"], dtype=torch.bool)
+    bad[0, 7] = bad[1, cols - 1] = True
+    assert torch.equal(out["dgate"][~bad], clean["dgate"][~bad]) and not bool(out["dgate"][bad].isfinite().any())
