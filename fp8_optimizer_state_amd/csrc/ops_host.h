@@ -4,6 +4,7 @@
 // UndefinedBehaviorSanitizer.
 #pragma once
 
+#include <float.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -160,7 +161,8 @@ inline int check_border(const coat_border* b) {
     if (!b) return COAT_EINVAL;
     if (b->rows < 0 || b->rows > kMaxDim || b->cols < 1 || b->cols > COAT_BORDER_MAX_COLS || b->rows_per_gate < 1)
         return COAT_EINVAL;
-    if (!finite_f(b->eps) || !(b->eps > 0.0f) || !finite_f(b->scale)) return COAT_EINVAL;
+    // the reciprocal root takes no subnormal, and beside a smaller eps the squares that fp32 loses would count
+    if (!finite_f(b->eps) || !(b->eps >= FLT_MIN) || !finite_f(b->scale)) return COAT_EINVAL;
     if ((b->post != 0 && b->post != 1) || !type_ok(b->stream_type) || !type_ok(b->param_type) ||
         !type_ok(b->grad_type))
         return COAT_EINVAL;

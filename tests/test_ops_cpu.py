@@ -160,3 +160,15 @@ def test_binding_refuses_shapes_and_types():
         coat.block_norm(None, x, None, x, rows_per_gate=0)
     with pytest.raises(ValueError, match="matrix"):
         coat.block_norm(None, x[0], None, x[0])
+
+
+def test_block_norm_refuses_a_subnormal_eps():
+    """The factor of a row of zeros would be infinite, and its values NaN."""
+    L = coat.lib()
+    for eps in (2.0 ** -149, 1e-40, 1e-38, 2.0 ** -126 * (1 - 2.0 ** -23)):
+        b = border(eps=eps)
+        assert 0.0 < b.eps < 2.0 ** -126
+        assert L.coat_block_norm(ctypes.byref(b), FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, None, None, 0, 0, None) == EINVAL
+        assert L.coat_block_norm_backward_workspace_bytes(ctypes.byref(b)) == 0
+        assert L.coat_block_norm_backward(ctypes.byref(b), *[FAKE] * 13, 1 << 30, None) == EINVAL
+    assert L.coat_block_norm_backward_workspace_bytes(ctypes.byref(border(eps=2.0 ** -126))) > 0
