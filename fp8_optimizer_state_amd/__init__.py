@@ -387,6 +387,7 @@ def _border(ref, w_post, w_pre, gate, rows_per_gate, scale, eps, post, res_type)
     rpg = max(1, int(rows_per_gate)) if rows == 0 else int(rows_per_gate)
     if rpg < 1:
         raise ValueError("rows_per_gate must be at least 1")
+    rpg = min(rpg, max(1, rows))  # more is the same, and may pass the 64 bits of the C call
     gates = (rows + rpg - 1) // rpg
     return _Border(rows, cols, rpg, eps, scale, 1 if post else 0, res_type, kind, 0), dtype, (gates, cols)
 
@@ -412,6 +413,8 @@ def block_norm(y, r, r_out=None, h=None, *, w_post=None, w_pre=None, gate=None, 
     bf16 = torch.bfloat16
     if q_scale is None and q is not None or q is None and q_scale is not None:
         raise ValueError("q and q_scale come as a pair")
+    if q is not None and fmt not in (FMT_E4M3, FMT_E5M2, FMT_MX4):  # the C call would see the low 32 bits alone
+        raise ValueError(f"fmt must be FMT_E4M3, FMT_E5M2 or FMT_MX4, got {fmt}")
     if q is not None and fmt != FMT_MX4 and (group < 1 or cols % group):
         raise ValueError(f"group {group} must divide the {cols} channels")
     gpu = _gpu_of(r, "r")
@@ -476,7 +479,8 @@ def block_norm_backward(y, r_out, dr_out, dh, dr, dy=None, *, w_post=None, w_pre
 
 
 def block_norm_backward_workspace_bytes(rows: int, cols: int, rows_per_gate: Optional[int] = None) -> int:
-    b = _Border(rows, cols, max(1, rows if rows_per_gate is None else rows_per_gate), 1e-5, 1.0, 0, 0, 0, 0)
+    rpg = rows if rows_per_gate is None else min(rows, rows_per_gate)
+    b = _Border(rows, cols, max(1, rpg), 1e-5, 1.0, 0, 0, 0, 0)
     return lib().coat_block_norm_backward_workspace_bytes(ctypes.byref(b))
 
 

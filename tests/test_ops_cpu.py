@@ -172,3 +172,18 @@ def test_block_norm_refuses_a_subnormal_eps():
         assert L.coat_block_norm_backward_workspace_bytes(ctypes.byref(b)) == 0
         assert L.coat_block_norm_backward(ctypes.byref(b), *[FAKE] * 13, 1 << 30, None) == EINVAL
     assert L.coat_block_norm_backward_workspace_bytes(ctypes.byref(border(eps=2.0 ** -126))) > 0
+
+
+def test_binding_numbers_past_the_c_types():
+    """A count that ctypes would cut to its low bits describes other memory than the binding has checked."""
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    for rpg in (5, 2 ** 63, 2 ** 64 + 1):
+        b, _, gate_shape = coat._border(x, None, None, x, rpg, 1.0, 1e-5, False, 0)
+        assert (b.rows_per_gate, gate_shape) == (4, (1, 64))
+        assert coat.block_norm_backward_workspace_bytes(4, 64, rpg) == coat.block_norm_backward_workspace_bytes(4, 64, 4)
+    b, _, gate_shape = coat._border(x[:0], None, None, None, 2 ** 64 + 1, 1.0, 1e-5, False, 0)
+    assert (b.rows_per_gate, gate_shape) == (1, (0, 64))
+    q, s = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 2)
+    for fmt in (2 ** 32 + coat.FMT_MX4, 2 ** 32, -1, 3):
+        with pytest.raises(ValueError, match="fmt"):
+            coat.block_norm(None, x, None, x, q=q, q_scale=s, group=32, fmt=fmt)
