@@ -174,7 +174,7 @@ __device__ __forceinline__ void quantize_down(const float (&tile)[kTileRows][kTi
 
 template <class T, bool ROWS>
 __global__ __launch_bounds__(kBlock) void mx4_quantize_tile_kernel(const T* __restrict__ x, int64_t rows, int64_t cols,
-                                                                   int64_t ld, uint32_t tiles_r,
+                                                                   int64_t ld, uint32_t tiles_r, uint32_t tiles,
                                                                    uint8_t* __restrict__ q, uint8_t* __restrict__ s,
                                                                    uint8_t* __restrict__ qt, uint8_t* __restrict__ st) {
     __shared__ __attribute__((aligned(16))) T tile[kTileRows][kTileCols];
@@ -183,6 +183,8 @@ __global__ __launch_bounds__(kBlock) void mx4_quantize_tile_kernel(const T* __re
     // other on one XCD: consecutive workgroups run on different XCDs.
     uint32_t t = blockIdx.x;
     if (gridDim.x % 8 == 0) t = (t & 7) * (gridDim.x / 8) + (t >> 3);
+    t += blockIdx.y * gridDim.x;
+    if (t >= tiles) return;
     const uint32_t patch = t / 16, patches_r = tiles_r / 4;
     const int64_t r0 = (int64_t)(patch % patches_r * 4 + t % 4) * kTileRows;
     const int64_t c0 = (int64_t)(patch / patches_r * 4 + t / 4 % 4) * kTileCols;
@@ -219,12 +221,13 @@ int launch_quantize(const T* x, int64_t rows, int64_t cols, int64_t ld, uint8_t*
     // the tiles reach to the end of the scale bytes of either direction: four of them, 512 values
     const int64_t tr = div_up(32 * mx4_scale_bytes(rows), kTileRows), tc = div_up(32 * mx4_scale_bytes(cols), kTileCols);
     if (tr * tc > 0x7FFFFFFFll) return COAT_EINVAL;
+    const Grid g = grid_xy(tr * tc, kBlock);
     if (q)
-        hipLaunchKernelGGL((mx4_quantize_tile_kernel<T, true>), dim3((unsigned)(tr * tc)), dim3(kBlock), 0, stream, x,
-                           rows, cols, ld, (uint32_t)tr, q, s, qt, st);
+        hipLaunchKernelGGL((mx4_quantize_tile_kernel<T, true>), dim3(g.x, g.y), dim3(kBlock), 0, stream, x, rows, cols, ld,
+                           (uint32_t)tr, (uint32_t)(tr * tc), q, s, qt, st);
     else
-        hipLaunchKernelGGL((mx4_quantize_tile_kernel<T, false>), dim3((unsigned)(tr * tc)), dim3(kBlock), 0, stream, x,
-                           rows, cols, ld, (uint32_t)tr, q, s, qt, st);
+        hipLaunchKernelGGL((mx4_quantize_tile_kernel<T, false>), dim3(g.x, g.y), dim3(kBlock), 0, stream, x, rows, cols, ld,
+                           (uint32_t)tr, (uint32_t)(tr * tc), q, s, qt, st);
     return launch_status();
 }
 

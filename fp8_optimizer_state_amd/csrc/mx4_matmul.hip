@@ -35,8 +35,10 @@ __global__ __launch_bounds__(kBlock) void mx4_matmul_small_kernel(const uint8_t*
                                                                   const uint8_t* __restrict__ bs, int64_t n, int64_t k,
                                                                   uint32_t tiles_n, T* __restrict__ y, int64_t ld) {
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int64_t n0 = (int64_t)(blockIdx.x % tiles_n) * 64 + (wave & 1) * 32;
-    const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * 64 + (wave >> 1) * 32;
+    const uint32_t tile = blockIdx.y * gridDim.x + blockIdx.x;
+    const int64_t n0 = (int64_t)(tile % tiles_n) * 64 + (wave & 1) * 32;
+    const int64_t m0 = (int64_t)(tile / tiles_n) * 64 + (wave >> 1) * 32;
+    if (m0 >= m) return;
     const int row = lane & 31, half = lane >> 5;
     const int64_t qb = mx4_code_bytes(k), sb = mx4_scale_bytes(k);
     const int64_t ra = m0 + row < m ? m0 + row : m - 1, rb = n0 + row < n ? n0 + row : n - 1;
@@ -512,7 +514,8 @@ __global__ __launch_bounds__(kFewWaves* kWave) void mx4_matmul_few_kernel(const 
     __shared__ float sums[kFewWaves][4 * FM][kWave];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int block = lane >> 4, l16 = lane & 15;
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int64_t n0 = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 16;
+    if (n0 >= n) return;
     const int64_t qb = mx4_code_bytes(k), sb = mx4_scale_bytes(k);
     const int steps = (int)(qb / 64), groups = (steps + 3) / 4;  // groups of four steps
     const int g0 = wave * per, g1 = g0 + per < groups ? g0 + per : groups;
@@ -585,8 +588,10 @@ int launch_few(const uint8_t* aq, const uint8_t* as, int64_t m, const uint8_t* b
     // whole turns of the loop: 1 x 32000 x 4096 (8 groups) takes 14 us with 4
     // wavefronts of two groups and 25 with 8 of one
     const int64_t groups = div_up(k, 512), per = div_up(groups, kFewWaves * kFewAhead) * kFewAhead;
-    hipLaunchKernelGGL((mx4_matmul_few_kernel<FM, T>), dim3((unsigned)div_up(n, 16)), dim3((unsigned)div_up(groups, per) * kWave),
-                       0, st, aq, as, m, bq, bs, n, k, (int)per, y, ld);
+    const unsigned threads = (unsigned)div_up(groups, per) * kWave;
+    const Grid g = grid_xy(div_up(n, 16), threads);
+    hipLaunchKernelGGL((mx4_matmul_few_kernel<FM, T>), dim3(g.x, g.y), dim3(threads), 0, st, aq, as, m, bq, bs, n, k, (int)per, y,
+                       ld);
     return launch_status();
 }
 
@@ -600,8 +605,9 @@ int launch_matmul(const uint8_t* aq, const uint8_t* as, int64_t m, const uint8_t
     if (p.way == Way::kSmall) {
         const int64_t tn = div_up(n, 64), tiles = tn * div_up(m, 64);
         if (tiles > 0x7FFFFFFFll) return COAT_EINVAL;
-        hipLaunchKernelGGL(mx4_matmul_small_kernel<T>, dim3((unsigned)tiles), dim3(kBlock), 0, st, aq, as, m, bq, bs, n, k,
-                           (uint32_t)tn, y, ld);
+        const Grid g = grid_xy(tiles, kBlock);
+        hipLaunchKernelGGL(mx4_matmul_small_kernel<T>, dim3(g.x, g.y), dim3(kBlock), 0, st, aq, as, m, bq, bs, n, k, (uint32_t)tn,
+                           y, ld);
         return launch_status();
     }
     auto grid_of = [](int64_t items) { return dim3((unsigned)(items < kCUs ? items : kCUs)); };

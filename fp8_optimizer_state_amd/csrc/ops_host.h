@@ -18,6 +18,17 @@ constexpr int kCUs = 256;  // of an MI355X; launch shapes that decide an order o
 
 constexpr int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// A launch of `count` workgroups, numbered x first. One axis of a grid holds fewer
+// than 2^32 work-items, so more workgroups go over y; those behind `count` return.
+struct Grid {
+    uint32_t x, y;
+};
+inline Grid grid_xy(int64_t count, int64_t threads) {
+    const int64_t most = 0xFFFFFFFFll / threads / 16 * 16;  // whole patches of 16 workgroups
+    const int64_t x = count < most ? count : most;
+    return Grid{(uint32_t)x, (uint32_t)div_up(count, x)};
+}
+
 constexpr int64_t mx4_code_bytes(int64_t k) { return 64 * div_up(k, 128); }
 constexpr int64_t mx4_scale_bytes(int64_t k) { return 16 * div_up(k, 512); }
 

@@ -72,7 +72,18 @@ static void product(int64_t m, int64_t n, int64_t k) {
     if (p.splits > 1) EXPECT(p.lw >= n && p.lw % 4 == 0 && need == (size_t)p.splits * (size_t)m * (size_t)p.lw * 4);
 }
 
+// Every workgroup has a number, none of them is far behind, and no axis holds 2^32 work-items.
+static void grid(int64_t count, int64_t threads) {
+    const Grid g = grid_xy(count, threads);
+    EXPECT((uint64_t)g.x * (uint64_t)threads < (uint64_t(1) << 32) && g.y < 65536);
+    EXPECT((int64_t)g.x * g.y >= count && (int64_t)g.x * (g.y - 1) < count && (uint64_t)g.x * g.y < (uint64_t(1) << 32));
+    EXPECT(g.y == 1 || g.x % 16 == 0);
+}
+
 int main() {
+    for (int64_t count : {int64_t(1), int64_t(17), int64_t(256), (int64_t(1) << 24) - 16, int64_t(1) << 24, (int64_t(1) << 24) + 32,
+                          (int64_t(1) << 26) + 3, int64_t(0x7FFFFFFF)})
+        for (int64_t threads : {64, 256, 512}) grid(count, threads);
     for (int64_t rows : {1, 2, 7, 255, 256, 257, 600, 700, 1031, 4096, 5001, 8000})
         for (int64_t cols : {1, 64, 512, 1024, 2731, 5120, 8192, 16384})
             for (int64_t rpg : {int64_t(1), int64_t(2), int64_t(3), int64_t(5), int64_t(31), int64_t(64), int64_t(257), rows / 2 + 1, rows, rows + 9})

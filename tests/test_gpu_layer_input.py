@@ -349,3 +349,46 @@ def test_product_over_a_very_long_k(coat):
     want, mag = o.mx4_matmul(*(v[list(sub[0])].cpu().numpy() for v in ops[0]), *(v[list(sub[1])].cpu().numpy() for v in ops[1]), kp)
     got = o.f64(y)[np.ix_(*sub)]
     assert (np.abs(got - want) <= o.matmul_bound(want, mag, kp, torch.float32)).all()
+
+
+def test_quantize_in_more_tiles_than_an_axis_of_a_grid(coat):
+    """Over 2^24 tiles of 256 threads: one long column down the tiles, the same values as a row."""
+    n = (1 << 29) + 600
+    x = torch.empty(n, 1, dtype=BF, device="cuda")
+    for at in range(0, n, 1 << 27):
+        x[at:at + (1 << 27)] = randn(min(1 << 27, n - at), 1, seed=at + 1)
+    got, want = coat.mx4_empty(1, n), coat.mx4_empty(1, n)
+    for v in (*got, *want):
+        v.fill_(0xA5)
+    print("quantize", n, flush=True)
+    coat.mx4_quantize(x, None, None, *got)
+    coat.mx4_quantize(x.view(1, n), *want)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_product_in_more_workgroups_than_an_axis_of_a_grid(coat):
+    """Over 2^24 workgroups of 256 threads (no terms: zeros) and over 2^26 of 64 (one row, one term)."""
+    m = (1 << 30) + 70
+    y = torch.full((m + 1, 1), 9.0, dtype=BF, device="cuda")
+    print("product", m, 1, 0, flush=True)
+    coat.mx4_matmul(*coat.mx4_empty(m, 0), *coat.mx4_empty(1, 0), y[:m])
+    torch.cuda.synchronize()
+    assert bool((y[:m] == 0).all()) and y[m].item() == 9.0
+    n = (1 << 30) + 40
+    y = y[:n].view(1, n).fill_(9.0)
+    bq, bs = (v.zero_() for v in coat.mx4_empty(n, 1))
+    bs[:, 0] = 127
+    step = 1 << 27
+    for at in range(0, n, step):  # each row's one code: its number and the eighth part of it, mod 16
+        i = torch.arange(at, min(n, at + step), device="cuda")
+        bq[at:at + step, 0] = ((i + i // 8) % 16).to(torch.uint8)
+    aq, as_ = (v.zero_() for v in coat.mx4_empty(1, 1))
+    aq[0, 0], as_[0, 0] = 5, 127  # 3
+    print("product", 1, n, 1, flush=True)
+    # the C call: the binding takes k as the codes hold it, 128, which so many rows are not few for
+    assert coat.lib().coat_mx4_matmul(aq.data_ptr(), as_.data_ptr(), 1, bq.data_ptr(), bs.data_ptr(), n, 1, y.data_ptr(), n, 0,
+                                      None, 0, torch.cuda.current_stream().cuda_stream) == coat.COAT_OK
+    table = torch.tensor([v * s * 3 for s in (1, -1) for v in o.GRID], dtype=BF, device="cuda")
+    for at in range(0, n, step):
+        assert torch.equal(y[0, at:at + step], table[bq[at:at + step, 0].long()])
