@@ -95,6 +95,20 @@ int main() {
             for (int64_t k : {1, 128, 511, 513, 5120, 13824, (1 << 22) - 1, 1 << 22, 0x7FFFFFFF}) product(m, n, k);
     EXPECT(product_of(4096, 5120, 5120).head_n == 16 * 256 && product_of(5120, 4096, 5120).head_m == 16 * 256);
     EXPECT(product_of(16384, 5120, 13824).head_n == 5120);  // whole rounds
+    // the products whose every element the GPU tests compare, k as the codes hold it: large
+    // tiles in more than one round, over several groups of steps but for one; the last four with a rest
+    struct Case {
+        int64_t m, n, k;
+        bool rest;
+    };
+    for (const Case& c : {Case{8192, 8192, 1152, false}, Case{8192, 8192, 1280, false}, Case{8192, 8192, 1408, false},
+                          Case{8192, 8192, 1536, false}, Case{8192, 8192, 384, false}, Case{16384, 4000, 1152, false},
+                          Case{8000, 8300, 1152, true}, Case{4096, 5120, 5120, true}, Case{5120, 4096, 5120, true}, Case{2600, 13824, 5120, true}}) {
+        const Product p = product_of(c.m, c.n, c.k);
+        EXPECT(p.way == Way::kTile256 && p.splits == 1);
+        EXPECT((p.head_m < c.m || p.head_n < c.n) == c.rest);
+        EXPECT(div_up(p.head_m, 256) * div_up(p.head_n, 256) > (c.rest ? kCUs - 1 : 2 * kCUs));
+    }
     EXPECT(product_workspace_bytes(0, 5, 5) == 0 && product_workspace_bytes(5, 5, -1) == 0);
 
     EXPECT(mx4_code_bytes(1) == 64 && mx4_code_bytes(129) == 128 && mx4_scale_bytes(512) == 16 && mx4_scale_bytes(513) == 32);

@@ -310,3 +310,42 @@ def test_linear_layer_and_its_gradients(coat):
         k = host[0].shape[1] * 2
         want, mag = o.mx4_matmul(*host, k)
         assert (np.abs(o.f64(y) - want) <= o.matmul_bound(want, mag, k, torch.float32)).all()
+
+
+def unpacked(q):
+    """The codes' values in fp32, on the GPU."""
+    table = torch.tensor([v * s for s in (1, -1) for v in o.GRID], dtype=torch.float32, device="cuda")
+    return table[torch.stack([q & 15, q >> 4], dim=2).view(q.shape[0], -1).int()]
+
+
+def check_all_of_y(coat, m, n, k, pad, dtype):
+    """Equal scales: every partial sum is a multiple of 1/4 under 36 k < 2^22, exact in fp32 in any
+    order, so y has to be the sum rounded once. Every element, on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(m + n + k)
+    ops = []
+    for rows in (m, n):
+        q, s = coat.mx4_empty(rows, k)
+        ops.append((q.random_(0, 256, generator=g), s.fill_(127)))
+    y = torch.full((m, n + pad), 9.0, dtype=dtype, device="cuda")
+    print("product", m, n, k, pad, dtype, flush=True)
+    coat.mx4_matmul(*ops[0], *ops[1], y[:, :n])
+    torch.cuda.synchronize()
+    a, b = (unpacked(q) for q, _ in ops)
+    assert a.shape[1] * 36 < 1 << 22
+    want = torch.matmul(a, b.t().contiguous()).to(dtype)
+    assert torch.equal(y[:, :n], want) and bool((y[:, n:] == 9.0).all())
+
+
+# Large tiles in the state that most products run them in (the host driver of the launch
+# shapes holds the same list): several tiles one after the other on a compute unit, whole
+# ones, each over several groups of steps that end after one, two, three or four of them;
+# rows of y that fill lines and rows that do not; edges among the whole tiles; and the
+# last columns or rows in small tiles.
+LARGE = [(8192, 8192, 1100, 0), (8192, 8192, 1280, 0), (8192, 8192, 1400, 3), (8192, 8192, 1536, 0), (8192, 8192, 300, 0),
+         (16384, 4000, 1100, 0), (8000, 8300, 1100, 0), (4096, 5120, 5120, 0), (5120, 4096, 5120, 8), (2600, 13824, 5120, 0)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m,n,k,pad", LARGE)
+def test_product_in_many_large_tiles(coat, m, n, k, pad, dtype):
+    check_all_of_y(coat, m, n, k, pad, TYPES[dtype])
