@@ -8,6 +8,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "coat_fp8.h"
 #include "coat_host.h"
 
@@ -122,10 +124,13 @@ inline Product product_of(int64_t m, int64_t n, int64_t k) {
     p.way = Way::kTile256;
     p.tiles_m = (uint32_t)div_up(m, 256);
     p.tiles_n = (uint32_t)div_up(n, 256);
-    // large tiles where they fill most of the card: 2048 x 5120 x 5120 (160 of them)
-    // takes 40 us and 46 in small ones, 1500 x 5120 x 13824 (120) 87 and 77
+    // Large tiles where they fill most of the card: 2048 x 5120 x 5120 (160 of them)
+    // takes 40 us and 46 in small ones, 1500 x 5120 x 13824 (120) 87 and 77. Not where
+    // one row of small ones covers a side, and half of each large one would lie past
+    // it: 128 x 128256 x 5120 takes 108 and 89, 33 x 65536 x 5120 42 and 34, 2^18 x 33
+    // x 8200 350 and 262; 129 x 65536 x 5120 49 and 52, 192 x 65536 x 5120 52 and 58.
     const int64_t large = (int64_t)p.tiles_m * p.tiles_n, steps = div_up(k, 128);
-    if (large >= 160) {
+    if (large >= 160 && m > 128 && n > 128) {
         const int64_t full = large / kCUs * kCUs;  // of them in whole rounds of workgroups
         // A last round of few large tiles is done in small ones instead, if the
         // estimate gains 6 % or more (the card is bound by power, and a round with

@@ -109,6 +109,13 @@ int main() {
         EXPECT((p.head_m < c.m || p.head_n < c.n) == c.rest);
         EXPECT(div_up(p.head_m, 256) * div_up(p.head_n, 256) > (c.rest ? kCUs - 1 : 2 * kCUs));
     }
+    // one side within a small tile: small ones, here in more than one round of workgroups
+    for (const Case& c : {Case{128, 40000, 1152, false}, Case{100, 40000, 1280, false}, Case{64, 40001, 1408, false}, Case{40000, 128, 1536, false},
+                          Case{70000, 33, 384, false}, Case{20, 128256, 5120, false}, Case{1 << 18, 33, 8200, false}}) {
+        const Product p = product_of(c.m, c.n, c.k);
+        EXPECT(p.way == Way::kTile128 && p.splits == 1 && p.tiles_m * p.tiles_n > (uint32_t)kCUs);
+    }
+    EXPECT(product_of(129, 65536, 5120).way == Way::kTile256 && product_of(65536, 129, 5120).way == Way::kTile256);
     EXPECT(product_workspace_bytes(0, 5, 5) == 0 && product_workspace_bytes(5, 5, -1) == 0);
 
     EXPECT(mx4_code_bytes(1) == 64 && mx4_code_bytes(129) == 128 && mx4_scale_bytes(512) == 16 && mx4_scale_bytes(513) == 32);

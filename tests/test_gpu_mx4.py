@@ -349,3 +349,13 @@ LARGE = [(8192, 8192, 1100, 0), (8192, 8192, 1280, 0), (8192, 8192, 1400, 3), (8
 @pytest.mark.parametrize("m,n,k,pad", LARGE)
 def test_product_in_many_large_tiles(coat, m, n, k, pad, dtype):
     check_all_of_y(coat, m, n, k, pad, TYPES[dtype])
+
+
+# one side within a small tile, the other over more of them than there are compute units
+NARROW = [(128, 40000, 1100, 0), (100, 40000, 1280, 0), (64, 40001, 1400, 3), (40000, 128, 1536, 0), (70000, 33, 300, 0), (20, 128256, 5120, 0)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m,n,k,pad", NARROW)
+def test_product_with_a_narrow_side(coat, m, n, k, pad, dtype):
+    check_all_of_y(coat, m, n, k, pad, TYPES[dtype])
