@@ -105,7 +105,7 @@ __device__ __forceinline__ void wait_vm_and_lds_then_barrier() {
 template <uint32_t AT>
 __device__ __forceinline__ void load_to_lds16(uint32_t lds, uint32_t off, const uint8_t* base) {
     asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base), "n"(AT)
-                 : "memory", "scc", "m0");
+                 : "memory", "scc");
 }
 
 __device__ __forceinline__ uint32_t float_bits(float v) { return __builtin_bit_cast(uint32_t, v); }
@@ -132,7 +132,7 @@ __device__ __forceinline__ void load_to_lds16_if(uint32_t on, uint32_t lds, uint
     asm volatile(
         "s_cmp_eq_u32 %4, 0\n\ts_cbranch_scc1 .Lskip%=\n\ts_add_u32 m0, %0, %3\n\ts_nop 0\n\t"
         "global_load_lds_dwordx4 %1, %2\n.Lskip%=:" ::"s"(lds), "v"(off), "s"(base), "n"(AT), "s"(on)
-        : "memory", "scc", "m0");
+        : "memory", "scc");
 }
 
 // f(0), f(1), ... f(N - 1) with the index known to the compiler.
