@@ -350,7 +350,11 @@ enum { COAT_FMT_MX4 = 2 }; /* a layer input stored as coat_mx4_quantize stores i
  * With h and q both NULL there is no norm before the next block (w_pre NULL);
  * at least one output is needed. Matrices of bf16 and fp32 need their type's
  * alignment, q 16 bytes, q_scale 4, and 16 for COAT_FMT_MX4 (COAT_EALIGN).
- * Sums of squares are held in fp32, so |values| over 1e19 overflow.
+ * Sums of squares are held in fp32. A row that holds a NaN has a norm of NaN. A row
+ * that holds an Inf, or whose sum of squares passes fp32 (a root mean square over
+ * 1.8e19 / sqrt(cols)), is divided by infinity: N is NaN where the Inf stands and 0
+ * elsewhere, so that h is 0 there, and r' = r after such a row of y. Other rows do
+ * not change.
  */
 int coat_block_norm(const coat_border* b, const uint16_t* y, const void* r, const void* w_post,
                     const void* w_pre, const void* gate, void* r_out, uint16_t* h, uint8_t* q,
@@ -373,6 +377,10 @@ int coat_block_norm(const coat_border* b, const uint16_t* y, const void* r, cons
  *   workspace  device memory, 256-byte aligned, at least
  *           coat_block_norm_backward_workspace_bytes(b) bytes; calls that may
  *           overlap in time need one each.
+ * A row of r' (with dh) or of y (with post) that holds a NaN or Inf gives NaN in all of
+ * its dr and dy, or its dy, and in the sums over tokens that those values enter. For a
+ * finite row whose sum of squares passes fp32 what goes through that norm is 0, or NaN
+ * if the sum of its products with the gradient passes fp32 too.
  */
 size_t coat_block_norm_backward_workspace_bytes(const coat_border* b);
 int coat_block_norm_backward(const coat_border* b, const uint16_t* y, const void* r_out,

@@ -341,3 +341,60 @@ def test_gradient_of_an_output_that_is_not_normalised(coat, cols):
     bad = torch.zeros_like(out["dgate"], dtype=torch.bool)
     bad[0, 7] = bad[1, cols - 1] = True
     assert torch.equal(out["dgate"][~bad], clean["dgate"][~bad]) and not bool(out["dgate"][bad].isfinite().any())
+
+
+@pytest.mark.parametrize("stream", TYPES)
+@pytest.mark.parametrize("cols", [40, 1029, 9000])
+def test_an_infinity_in_y(coat, cols, stream):
+    """Under the post-norm: NaN in its channel of r', r' = r in the row's others, NaN in all of h and dy;
+    the weights' gradients NaN in that channel. Other rows and gate rows are those without it."""
+    t, how = make(6, cols, 41, TYPES[stream], rpg=2)
+    clean_r, clean_h = forward(coat, t, how)
+    clean = backward(coat, t, how, t["r"])
+    t["y"][3, 7] = -float("inf")
+    r_out, h = forward(coat, t, how)
+    keep, others = [0, 1, 2, 4, 5], torch.arange(cols, device="cuda") != 7
+    assert torch.equal(r_out[keep], clean_r[keep]) and torch.equal(h[keep], clean_h[keep])
+    assert bool(r_out[3, 7].isnan()) and torch.equal(r_out[3, others], t["r"][3, others]) and bool(h[3].isnan().all())
+    out = backward(coat, t, how, t["r"])  # from a stream without it
+    assert torch.equal(out["dr"], clean["dr"]) and torch.equal(out["dw_pre"], clean["dw_pre"])
+    assert torch.equal(out["dy"][keep], clean["dy"][keep]) and bool(out["dy"][3].isnan().all())
+    assert bool(out["dw_post"][7].isnan()) and bool(out["dw_post"][others].isfinite().all())
+    assert torch.equal(out["dgate"][[0, 2]], clean["dgate"][[0, 2]])
+    assert bool(out["dgate"][1, 7].isnan()) and bool(out["dgate"][1, others].isfinite().all())
+
+
+@pytest.mark.parametrize("stream", TYPES)
+@pytest.mark.parametrize("cols", [40, 1029, 9000])
+def test_an_infinity_in_the_stream(coat, cols, stream):
+    """NaN in its channel of h and 0 in the row's others; NaN in the row's dr and dy."""
+    t, how = make(6, cols, 42, TYPES[stream], rpg=2)
+    clean_r, clean_h = forward(coat, t, how)
+    clean = backward(coat, t, how, t["r"])
+    t["r"][3, cols - 1] = float("inf")
+    r_out, h = forward(coat, t, how)
+    keep = [0, 1, 2, 4, 5]
+    assert torch.equal(r_out[keep], clean_r[keep]) and torch.equal(h[keep], clean_h[keep])
+    assert torch.equal(r_out[3, :-1], clean_r[3, :-1]) and bool(r_out[3, -1] == float("inf"))
+    assert bool(h[3, -1].isnan()) and bool((h[3, :-1] == 0).all())
+    out = backward(coat, t, how, t["r"])
+    for name in ("dr", "dy"):
+        assert torch.equal(out[name][keep], clean[name][keep]) and bool(out[name][3].isnan().all())
+    assert bool(out["dw_pre"][-1].isnan()) and bool(out["dw_pre"][:-1].isfinite().all())
+    assert bool(out["dw_post"].isnan().all())
+    assert torch.equal(out["dgate"][[0, 2]], clean["dgate"][[0, 2]]) and bool(out["dgate"][1].isnan().all())
+
+
+def test_rows_whose_squares_pass_fp32(coat):
+    """Finite rows, in y and in the stream, over the documented limit: divided by infinity."""
+    t, how = make(5, 1024, 43, F32, rpg=5)
+    for name in ("y", "r"):
+        t[name][1] = t[name][1].sign() * 1.2e18  # sum of squares 1.5e39
+        t[name][2] = t[name][2].sign() * 4.5e17  # 2.1e38: inside
+    r_out, h = forward(coat, t, how)
+    assert torch.equal(r_out[1], t["r"][1]) and bool((h[1] == 0).all())
+    want = o.layer_input(n64(r_out[2:3]), n64(t["w_pre"]), EPS)
+    within(h[2:3], want, o.U32 * (o.SUM / 2 + 6) * np.abs(want), BF, "h")
+    out = backward(coat, t, how, t["r"])
+    assert torch.equal(out["dr"][1], t["dr_out"][1]) and bool((out["dy"][1] == 0).all())
+    assert all(bool(v.isfinite().all()) for v in out.values())
