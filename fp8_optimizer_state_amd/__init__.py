@@ -395,7 +395,7 @@ def _border(ref, w_post, w_pre, gate, rows_per_gate, scale, eps, post, res_type)
 def block_norm(y, r, r_out=None, h=None, *, w_post=None, w_pre=None, gate=None, rows_per_gate=None, scale=1.0,
                eps=1e-5, post=None, q=None, q_scale=None, group: int = 0, fmt: int = 0, stream=None) -> None:
     """The border between two blocks: r_out = r + scale gate (w_post N(y)), h = w_pre N(r_out),
-    N(a) = a / sqrt(mean(a^2) + eps) over the channels.
+    N(a) = a / sqrt(mean(a^2) + eps) over the channels, eps at least 2^-126.
 
     y None: no addition, r itself is normalised. post: whether y is normalised
     (default: if w_post is given). gate: (ceil(rows / rows_per_gate), channels), token

@@ -94,8 +94,10 @@ __global__ __launch_bounds__(kBlock) void mx4_matmul_small_kernel(const uint8_t*
 // busy for 57 % of the cycles, at 1.7 to 1.85 GHz: on codes of zero, which switch
 // nothing, the same launch runs at 2.4 GHz and 5.3 PFLOP/s. What is left of the
 // cycles goes to writing y (5 to 7 us a tile, in part under the next one's loads).
-// Tiles of 128 x 128 are bound by LDS: reads and refills take four fifths of its
-// cycles (0.27 us a step of 128 values, against 0.5 for four times the work).
+// Tiles of 128 x 128 are bound by latency, with one wavefront a SIMD and a barrier a
+// pair: reads of LDS are active in 0.39 of the cycles, the matrix units in 0.39, and the
+// wavefronts wait in 0.28 (1500 x 5120 x 13824, 77 us). 16384 x 13824 x 5120 takes 747 us
+// in them.
 template <int N>
 __device__ __forceinline__ void wait_vm_and_lds_then_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
@@ -503,7 +505,10 @@ __global__ __launch_bounds__(kBlock) void mx4_matmul_join_kernel(const float* __
 // consecutive bytes of each row (a 32-row form of the instruction would make it
 // 32), and a row's scale bytes of four steps come in one.
 constexpr int kFewWaves = 8;
-constexpr int kFewAhead = 2;  // groups of four steps whose loads are in flight together
+// Groups of four steps in a turn of the loop. The compiler deals a turn's loads out
+// between its matrix instructions (59 registers, where all of them at once would take
+// over 80), so that the loads of one or two steps are in flight at a time.
+constexpr int kFewAhead = 2;
 
 template <int FM, class T>
 __global__ __launch_bounds__(kFewWaves* kWave) void mx4_matmul_few_kernel(const uint8_t* __restrict__ aq,
@@ -630,8 +635,9 @@ int launch_matmul(const uint8_t* aq, const uint8_t* as, int64_t m, const uint8_t
         return launch_status();
     }
     const dim3 grid = grid_of((int64_t)p.tiles_m * p.tiles_n * p.splits);
-    // Bound by LDS: eight wavefronts of 32 x 64 read half as much again from it as
-    // four of 64 x 64, but hide its latency. One round of split tiles gains (64 x
+    // Bound by latency (LDS reads active in 0.46 of the cycles, matrix units in 0.28,
+    // wavefronts waiting in 0.35): eight wavefronts of 32 x 64 read half as much again from
+    // LDS as four of 64 x 64, but hide more of it. One round of split tiles gains (64 x
     // 5120 x 13824 22 -> 20 us, 700 x 1000 x 8192 23 -> 20), whole ones lose (1500 x
     // 5120 x 13824 79 -> 86).
     hipLaunchKernelGGL((mx4_matmul_tile_kernel<4, 2, 1, 2, 4, 64, float>), grid, dim3(2 * kBlock), 0, st, aq, as, m, bq, bs, n,

@@ -322,7 +322,7 @@ typedef struct coat_border {
     int64_t cols;          /* channels, 1 .. COAT_BORDER_MAX_COLS */
     int64_t rows_per_gate; /* >= 1; the gate has ceil(rows / rows_per_gate) rows (1: one per token, rows: one for all) */
     float eps;             /* at least 2^-126 (the smallest normal fp32), finite */
-    float scale;           /* the residual scale, finite */
+    float scale;           /* the residual scale, finite (its products with a row's factor and with D are formed in fp32) */
     int32_t post;          /* 1: y is normalised, 0: it is not */
     int32_t stream_type;   /* COAT_BF16 or COAT_FP32: r, r_out, dr_out, dr */
     int32_t param_type;    /* of w_post, w_pre and gate */
