@@ -20,9 +20,9 @@ namespace {
 // and s at most 24, so a quotient that is not an fp32 number lies at least
 // 2^-49 (relative) from every midpoint between fp32 neighbours (the distance
 // is a nonzero multiple of 2^(e-24) / s's integer significand in the binade
-// [2^e, 2^(e+1)), likewise in the subnormal range), while x * RN64(1 / s),
-// rounded to fp64, is within 2^-52 of it. Rounding that product to fp32 thus
-// gives RN32(x / s) exactly; the hardware converts round it to the FP8 grid,
+// [2^e, 2^(e+1)), likewise in the subnormal range), while x times 1 / s to
+// within 2^-51 of it, rounded to fp64, is within 2^-50. Rounding that product
+// to fp32 thus gives RN32(x / s) exactly; the hardware converts round it to the FP8 grid,
 // nearest with ties to even, after a clamp to the largest finite magnitude.
 
 // Largest bf16 magnitude bits of the 2 NW values in w.

@@ -218,3 +218,25 @@ def test_act_beyond_2_32_elements(coat, G):
         assert same_f32(s.cpu().numpy(), os_)
         assert np.array_equal(qs, oq)
         assert same_bf16(bs, oracle.act_dequantize(oq, os_, 0, fmt))
+
+
+@pytest.mark.parametrize("fmt", [E4, E5])
+def test_every_scale_that_a_bf16_maximum_gives(coat, fmt):
+    """Each positive finite bf16 as a group's maximum, with the values of the 23 binades under
+    it, both signs: scales and codes of the quotients in 64 bits, rounded to fp32 and to the format."""
+    top, dt = (448.0, torch.float8_e4m3fn) if fmt == E4 else (57344.0, torch.float8_e5m2)
+    G, parts = 1024, 3
+    i = torch.arange(G - 1, device="cuda", dtype=torch.int32)
+    down = torch.stack([torch.cat([i[:1] * 0, i + p * (G - 1)]) for p in range(parts)])  # steps below the maximum
+    for lo in range(1, 0x7F80, 4096):
+        amax = torch.arange(lo, min(lo + 4096, 0x7F80), device="cuda", dtype=torch.int32)
+        bits = (amax[:, None, None] - down).clamp_(min=0)
+        bits = torch.where((down % 2 == 1) & (bits < amax[:, None, None]), bits | 0x8000, bits).reshape(-1, G)
+        x = bits.to(torch.int16).view(torch.bfloat16)
+        q = torch.empty(x.numel(), dtype=torch.uint8, device="cuda")
+        s = torch.empty(x.shape[0], dtype=torch.float32, device="cuda")
+        coat.act_quantize(x.reshape(-1), q, s, group=G, fmt=fmt)
+        want = (x[:, 0].double() / top).float()
+        assert torch.equal(s, want) and bool((want > 0).all())
+        y = (x.double() / want.double()[:, None]).float().clamp(-top, top)
+        assert torch.equal(q.view(-1, G), y.to(dt).view(torch.uint8)), hex(lo)
