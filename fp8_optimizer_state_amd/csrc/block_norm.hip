@@ -14,7 +14,7 @@ namespace {
 // wavefront, so a row reaches over to the next multiple of 512 channels (the
 // padding of the 4-bit form); the lanes behind the last channel hold zeros. Bound
 // by HBM: 16384 x 5120 in bf16 take 140 us forward (4.8 TB/s; 147 us to FP8, 118 to
-// 4 bits) and 210 us backward (4.8 TB/s); a copy of that size runs at 4.7. Rows of
+// 4 bits) and 212 us backward (4.7 TB/s); a copy of that size runs at 4.7. Rows of
 // odd width lie at any byte: 1031 x 2731 takes 29 us backward, the latency of three
 // rows one after the other and of the second launch.
 constexpr int kMaxWaves = 16;
