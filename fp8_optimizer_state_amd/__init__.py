@@ -24,6 +24,7 @@ FMT_E4M3 = 0
 FMT_E5M2 = 1
 FMT_MX4 = 2
 FMT_NO_EXPAND = 0x100
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)
 
 COAT_OK, COAT_EINVAL, COAT_EALIGN, COAT_EHIP, COAT_ERANGE = 0, -1, -2, -3, -4
 STATIC_MAX_TENSORS = 4096
@@ -49,6 +50,11 @@ class _Border(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("rows_per_gate", ctypes.c_int64),
                 ("eps", ctypes.c_float), ("scale", ctypes.c_float), ("post", ctypes.c_int32),
                 ("stream_type", ctypes.c_int32), ("param_type", ctypes.c_int32), ("grad_type", ctypes.c_int32)]
+
+
+class _Epilogue(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int32), ("scale", ctypes.c_float), ("p", ctypes.c_float), ("offset", ctypes.c_int64),
+                ("rng", ctypes.c_void_p)]
 
 
 class _Plan(ctypes.Structure):
@@ -94,6 +100,16 @@ def lib() -> ctypes.CDLL:
     L.coat_block_norm.argtypes = [border, P, P, P, P, P, P, P, P, P, i32, i32, P]
     L.coat_block_norm_backward_workspace_bytes.argtypes = [border]
     L.coat_block_norm_backward.argtypes = [border, P, P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+    epilogue, size = ctypes.POINTER(_Epilogue), ctypes.c_size_t
+    L.coat_linear.argtypes = [P, i64, i64, i64, P, i64, i64, epilogue, P, i32, P, i64, P, i64, P, i64, i32, P, size, P]
+    L.coat_linear_backward.argtypes = [P, i64, i32, P, i64, i64, i64, P, i64, i64, epilogue, P, i64, P, i64, P, i64, P, i32, P, size,
+                                       P]
+    L.coat_dropout.argtypes = [P, i64, i64, i64, i32, P, i64, f32, f32, P, i64, P, i64, i32, P]
+    L.coat_linear_cross_entropy.argtypes = [P, i64, i64, i64, P, i64, i64, P, i64, P, P, P, size, P]
+    L.coat_linear_cross_entropy_backward.argtypes = [P, i64, i64, i64, P, i64, i64, P, i64, P, P, i64, P, i64, P, i64, P, size, P]
+    for name in ("coat_linear", "coat_linear_backward", "coat_linear_cross_entropy", "coat_linear_cross_entropy_backward"):
+        getattr(L, name + "_workspace_bytes").argtypes = [i64, i64, i64, i32]
+        getattr(L, name + "_workspace_bytes").restype = size
     for name in ("coat_mx4_code_bytes", "coat_mx4_scale_bytes"):
         getattr(L, name).restype = i64
     for name in ("coat_mx4_matmul_workspace_bytes", "coat_block_norm_backward_workspace_bytes"):
@@ -105,7 +121,8 @@ def lib() -> ctypes.CDLL:
                  "coat_fp8_adamw_step_multi", "coat_fp8_adamw_step_multi_static", "coat_fp8_quantize", "coat_fp8_dequantize",
                  "coat_fp8_encode", "coat_fp8_decode", "coat_fp8_act_quantize",
                  "coat_fp8_act_dequantize", "coat_mx4_quantize", "coat_mx4_dequantize", "coat_mx4_matmul",
-                 "coat_block_norm", "coat_block_norm_backward"):
+                 "coat_block_norm", "coat_block_norm_backward", "coat_linear", "coat_linear_backward", "coat_dropout",
+                 "coat_linear_cross_entropy", "coat_linear_cross_entropy_backward"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -482,6 +499,228 @@ def block_norm_backward_workspace_bytes(rows: int, cols: int, rows_per_gate: Opt
     rpg = rows if rows_per_gate is None else min(rows, rows_per_gate)
     b = _Border(rows, cols, max(1, rpg), 1e-5, 1.0, 0, 0, 0, 0)
     return lib().coat_block_norm_backward_workspace_bytes(ctypes.byref(b))
+
+
+# ---------------------------------------------------------------- products of a training step
+#
+# Linear layers, dropout and the loss, on (tokens, channels) matrices whose rows
+# have no gaps (they may lie further apart), on the device that holds them. Weights
+# are bf16 with one row per output feature, as the optimizer step writes them
+# (``TensorState.params_bf16``), their gradients bf16 as it reads them
+# (``TensorState.grads``).
+
+def _matrix(t: torch.Tensor, dtype, shape, gpu: int, name: str):
+    """(address, elements from row to row) of a matrix with this type and shape on GPU `gpu`."""
+    if t.get_device() != gpu:
+        raise ValueError(f"{name} must be on GPU {gpu} like the other tensors, got {t.device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr(), _row_stride(t, name)
+
+
+def _optional(t: Optional[torch.Tensor], dtype, shape, gpu: int, name: str):
+    return (None, max(shape[1], 1)) if t is None else _matrix(t, dtype, shape, gpu, name)
+
+
+def _random(p: float, rng: Optional[torch.Tensor], offset: int, gpu: int) -> Optional[int]:
+    if not 0.0 <= p < 1.0:
+        raise ValueError(f"p must be in [0, 1), got {p}")
+    if not -2 ** 63 <= offset < 2 ** 63:
+        raise ValueError(f"offset must fit 64 bits, got {offset}")
+    if rng is None:
+        if p > 0.0:
+            raise ValueError("dropout needs rng, a tensor of two int64: (seed, step)")
+        return None
+    return _operand(rng, torch.int64, (2,), gpu, "rng")
+
+
+def _epilogue(act: int, scale: float, p: float, rng, offset: int, gpu: int) -> _Epilogue:
+    if act not in (ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU):
+        raise ValueError(f"act must be one of the ACT_ constants, got {act}")
+    return _Epilogue(act, scale, p, offset, _random(p, rng, offset, gpu))
+
+
+def _is_aligned(ptr: int, ld: int, cols: int) -> bool:
+    return ptr % 16 == 0 and ld % 8 == 0 and cols % 8 == 0
+
+
+def linear(x, w, y, *, bias=None, act: int = ACT_NONE, z=None, residual=None, scale: float = 1.0, p: float = 0.0, rng=None,
+           offset: int = 0, workspace=None, stream=None) -> None:
+    """A linear layer: z = x w^T + bias, y = residual + scale D(act(z)).
+
+    x: (m, k) and w: (n, k) bf16; bias: (n,) bf16 or fp32; y: (m, n) bf16 or fp32;
+    residual: like y, may be y itself; z: (m, n) bf16, out, kept for the backward pass
+    of an activation. D is dropout with probability p (``dropout``); rng: two int64 on
+    the GPU, (seed, step), read when the work runs. ``workspace``: uint8, at least
+    ``linear_workspace_bytes`` long; without one the call takes one from torch's
+    allocator."""
+    gpu = _gpu_of(x, "x")
+    m, k = x.shape
+    if w.dim() != 2:
+        raise ValueError("w must be a matrix, one row per output feature")
+    n = w.shape[0]
+    bf16 = torch.bfloat16
+    xp, ldx = _matrix(x, bf16, (m, k), gpu, "x")
+    wp, ldw = _matrix(w, bf16, (n, k), gpu, "w")
+    kind = _float_type(y, "y")
+    yp, ldy = _matrix(y, y.dtype, (m, n), gpu, "y")
+    rp, ldr = _optional(residual, y.dtype, (m, n), gpu, "residual")
+    zp, ldz = _optional(z, bf16, (m, n), gpu, "z")
+    bp, bt = (None, 0) if bias is None else (_operand(bias, bias.dtype, (n,), gpu, "bias"), _float_type(bias, "bias"))
+    e = _epilogue(act, scale, p, rng, offset, gpu)
+    L = lib()
+    nbytes = L.coat_linear_workspace_bytes(m, n, k, _is_aligned(xp, ldx, k) and _is_aligned(wp, ldw, k))
+    ws = _workspace(nbytes, workspace, gpu, stream)
+    _call(gpu, stream, L.coat_linear, "coat_linear", xp, m, k, ldx, wp, n, ldw, ctypes.byref(e), bp, bt, rp, ldr, zp, ldz, yp, ldy,
+          kind, ws.data_ptr() if ws is not None else None, nbytes)
+
+
+def linear_workspace_bytes(m: int, n: int, k: int, aligned: bool = True) -> int:
+    """aligned: whether x and w start at multiples of 16 bytes, k and their row strides being multiples of 8."""
+    return lib().coat_linear_workspace_bytes(m, n, k, aligned)
+
+
+def linear_backward(dy, x, w, dx=None, dw=None, dbias=None, *, act: int = ACT_NONE, z=None, scale: float = 1.0, p: float = 0.0,
+                    rng=None, offset: int = 0, workspace=None, stream=None) -> None:
+    """Backward of ``linear`` with the forward's act, scale, p, rng and offset:
+    dz = scale D(dy) act'(z), dx = dz w, dw = dz^T x, dbias = dz summed over the tokens,
+    each where it is given (the gradient of residual is dy).
+
+    dy: (m, n) bf16 or fp32; z: the forward's, needed with an activation; dx: (m, k) and
+    dw: (n, k) bf16; dbias: (n,) bf16 or fp32. ``workspace``: uint8, at least
+    ``linear_backward_workspace_bytes`` long; without one the call takes one from
+    torch's allocator."""
+    gpu = _gpu_of(dy, "dy")
+    m, n = dy.shape
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix, one row per token")
+    k = x.shape[1]
+    bf16 = torch.bfloat16
+    kind = _float_type(dy, "dy")
+    dyp, lddy = _matrix(dy, dy.dtype, (m, n), gpu, "dy")
+    xp, ldx = _matrix(x, bf16, (m, k), gpu, "x")
+    wp, ldw = _matrix(w, bf16, (n, k), gpu, "w")
+    if act != ACT_NONE and z is None:
+        raise ValueError("the backward pass of an activation needs z, as linear writes it")
+    zp, ldz = _optional(z, bf16, (m, n), gpu, "z")
+    dxp, lddx = _optional(dx, bf16, (m, k), gpu, "dx")
+    dwp, lddw = _optional(dw, bf16, (n, k), gpu, "dw")
+    if dx is None and dw is None and dbias is None:
+        raise ValueError("one of dx, dw and dbias at least is needed")
+    dbp, dbt = (None, 0) if dbias is None else (_operand(dbias, dbias.dtype, (n,), gpu, "dbias"), _float_type(dbias, "dbias"))
+    e = _epilogue(act, scale, p, rng, offset, gpu)
+    L = lib()
+    nbytes = L.coat_linear_backward_workspace_bytes(m, n, k, _is_aligned(xp, ldx, k) and _is_aligned(wp, ldw, k))
+    ws = _workspace(nbytes, workspace, gpu, stream)
+    _call(gpu, stream, L.coat_linear_backward, "coat_linear_backward", dyp, lddy, kind, xp, m, k, ldx, wp, n, ldw, ctypes.byref(e), zp,
+          ldz, dxp, lddx, dwp, lddw, dbp, dbt, ws.data_ptr() if ws is not None else None, nbytes)
+
+
+def linear_backward_workspace_bytes(m: int, n: int, k: int, aligned: bool = True) -> int:
+    """aligned: as in ``linear_workspace_bytes``."""
+    return lib().coat_linear_backward_workspace_bytes(m, n, k, aligned)
+
+
+def dropout(x, y, *, p: float, rng=None, offset: int = 0, residual=None, scale: float = 1.0, stream=None) -> None:
+    """y = residual + scale D(x), D(v) = v / (1 - p) where kept and 0 where dropped.
+
+    x, y: matrices of one shape, bf16 or fp32 each; residual: like y; y may be x or
+    residual itself. The mask is never stored: it follows from rng (two int64 on the
+    GPU: seed, step; needed if p > 0), offset and an element's row and column, so that
+    ``dropout_backward`` and the dropout within ``linear`` find it again. p is rounded
+    to a multiple of 2^-16."""
+    gpu = _gpu_of(x, "x")
+    shape = x.shape
+    xt, yt = _float_type(x, "x"), _float_type(y, "y")
+    xp, ldx = _matrix(x, x.dtype, shape, gpu, "x")
+    yp, ldy = _matrix(y, y.dtype, shape, gpu, "y")
+    rp, ldr = _optional(residual, y.dtype, shape, gpu, "residual")
+    _call(gpu, stream, lib().coat_dropout, "coat_dropout", xp, shape[0], shape[1], ldx, xt, rp, ldr, scale, p,
+          _random(p, rng, offset, gpu), offset, yp, ldy, yt)
+
+
+def dropout_backward(dy, dx, *, p: float, rng=None, offset: int = 0, scale: float = 1.0, stream=None) -> None:
+    """Backward of ``dropout`` with the forward's p, rng, offset and scale: dx = scale D(dy)
+    (the gradient of residual is dy)."""
+    dropout(dy, dx, p=p, rng=rng, offset=offset, scale=scale, stream=stream)
+
+
+def _xent_operands(x, w, labels, gpu: int):
+    tokens, cols = x.shape
+    if w.dim() != 2:
+        raise ValueError("w must be a matrix, one row per entry of the vocabulary")
+    vocab = w.shape[0]
+    if vocab < 1:
+        raise ValueError("the vocabulary is empty")
+    xp, ldx = _matrix(x, torch.bfloat16, (tokens, cols), gpu, "x")
+    wp, ldw = _matrix(w, torch.bfloat16, (vocab, cols), gpu, "w")
+    return (xp, tokens, cols, ldx, wp, vocab, ldw, _operand(labels, torch.int64, (tokens,), gpu, "labels"),
+            _is_aligned(xp, ldx, cols) and _is_aligned(wp, ldw, cols))
+
+
+def _index64(ignore_index: int) -> int:
+    if not -2 ** 63 <= ignore_index < 2 ** 63:
+        raise ValueError(f"ignore_index must fit 64 bits, got {ignore_index}")
+    return ignore_index
+
+
+def linear_cross_entropy(x, w, labels, loss, lse, *, ignore_index: int = -100, workspace=None, stream=None) -> None:
+    """Softmax cross entropy of the logits x w^T, which are never stored:
+    lse = log sum exp(l), loss = lse - l[label] per token.
+
+    x: (tokens, cols) and w: (vocab, cols) bf16; labels: (tokens,) int64; loss, lse:
+    (tokens,) fp32, out. A token whose label is ignore_index is left out: loss 0, lse 0,
+    whatever its row of x holds. Any other label outside the vocabulary gives a loss of
+    NaN. ``workspace``: uint8, at least ``linear_cross_entropy_workspace_bytes`` long;
+    without one the call takes one from torch's allocator."""
+    gpu = _gpu_of(x, "x")
+    *args, aligned = _xent_operands(x, w, labels, gpu)
+    tokens, cols, vocab = args[1], args[2], args[5]
+    out = _operand(loss, torch.float32, (tokens,), gpu, "loss"), _operand(lse, torch.float32, (tokens,), gpu, "lse")
+    L = lib()
+    nbytes = L.coat_linear_cross_entropy_workspace_bytes(tokens, vocab, cols, aligned)
+    ws = _workspace(nbytes, workspace, gpu, stream)
+    _call(gpu, stream, L.coat_linear_cross_entropy, "coat_linear_cross_entropy", *args, _index64(ignore_index), *out,
+          ws.data_ptr() if ws is not None else None, nbytes)
+
+
+def linear_cross_entropy_workspace_bytes(tokens: int, vocab: int, cols: int, aligned: bool = True) -> int:
+    """aligned: whether x and w start at multiples of 16 bytes, cols and their row strides being multiples of 8."""
+    return lib().coat_linear_cross_entropy_workspace_bytes(tokens, vocab, cols, aligned)
+
+
+def linear_cross_entropy_backward(x, w, labels, lse, dloss, dx=None, dw=None, *, ignore_index: int = -100, workspace=None,
+                                  stream=None) -> None:
+    """Backward of ``linear_cross_entropy`` from its lse: with g = dloss (softmax(l) - onehot(label)),
+    dx = g w and dw = g^T x, each where it is given.
+
+    dloss: fp32, (tokens,) or one value for all; dx: (tokens, cols) and dw: (vocab, cols)
+    bf16, one at least. A token that is left out has zeros in dx and no part in dw, whatever
+    its row of x holds. ``workspace``: uint8, at least
+    ``linear_cross_entropy_backward_workspace_bytes`` long; without one the call takes one
+    from torch's allocator."""
+    gpu = _gpu_of(x, "x")
+    *args, aligned = _xent_operands(x, w, labels, gpu)
+    tokens, cols, vocab = args[1], args[2], args[5]
+    if dx is None and dw is None:
+        raise ValueError("one of dx and dw at least is needed")
+    count = 1 if dloss.numel() == 1 else tokens
+    lp = _operand(lse, torch.float32, (tokens,), gpu, "lse")
+    dp = _operand(dloss, torch.float32, dloss.shape if count == 1 else (tokens,), gpu, "dloss")
+    dxp, lddx = _optional(dx, torch.bfloat16, (tokens, cols), gpu, "dx")
+    dwp, lddw = _optional(dw, torch.bfloat16, (vocab, cols), gpu, "dw")
+    L = lib()
+    nbytes = L.coat_linear_cross_entropy_backward_workspace_bytes(tokens, vocab, cols, aligned)
+    ws = _workspace(nbytes, workspace, gpu, stream)
+    _call(gpu, stream, L.coat_linear_cross_entropy_backward, "coat_linear_cross_entropy_backward", *args, _index64(ignore_index), lp, dp,
+          count, dxp, lddx, dwp, lddw, ws.data_ptr() if ws is not None else None, nbytes)
+
+
+def linear_cross_entropy_backward_workspace_bytes(tokens: int, vocab: int, cols: int, aligned: bool = True) -> int:
+    """aligned: as in ``linear_cross_entropy_workspace_bytes``."""
+    return lib().coat_linear_cross_entropy_backward_workspace_bytes(tokens, vocab, cols, aligned)
 
 
 # ---------------------------------------------------------------- parameter lists

@@ -10,9 +10,10 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 # the step kernels, state codec and core ABI; the activation codec; the 4-bit
-# codec and its product; the norms at a block's border
+# codec and its product; the norms at a block's border; the training products
 SOURCES = [os.path.join(CSRC, name) for name in
-           ("coat_fp8.hip", "act_fp8.hip", "mx4.hip", "mx4_matmul.hip", "block_norm.hip")]
+           ("coat_fp8.hip", "act_fp8.hip", "mx4.hip", "mx4_matmul.hip", "block_norm.hip", "linear.hip",
+            "cross_entropy.hip", "dropout.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libcoat_fp8.so")
 
@@ -38,7 +39,7 @@ def build(verbose: bool = False) -> str:
 
         # one compiler per source at a time, then one link
         compile_flags = [f for f in HIPCC_FLAGS if f != "-shared"]
-        with ThreadPoolExecutor(max_workers=4) as pool:
+        with ThreadPoolExecutor(max_workers=6) as pool:
             done = list(pool.map(run, ([hipcc, *compile_flags, "-I" + INCLUDE, "-c", "-o", o, src]
                                        for src, o in zip(SOURCES, objects))))
         if all(res.returncode == 0 for res in done):

@@ -1,0 +1,166 @@
+// HIP (gfx950) linear layer with its epilogue, and its backward pass.
+#include <type_traits>
+
+#include "train_common.h"
+
+namespace {
+
+// ------------------------------------------------------------------ the gradient before the activation
+//
+// dz = D(dy) act'(z) in bf16, without the factors that the products' sums are multiplied
+// by, and the sums of kBiasRows rows of it as they were before the rounding. A workgroup
+// takes 512 columns of those rows: a thread 8 columns of every fourth row, the four
+// rows' sums joined through LDS in order.
+template <class T>
+__global__ __launch_bounds__(kBlock) void dz_kernel(const T* __restrict__ dy, int64_t lddy, const uint16_t* __restrict__ z, int64_t ldz,
+                                                    int32_t act, Drop drop, int64_t m, int64_t n, uint16_t* __restrict__ dz,
+                                                    int64_t ld_dz, float* __restrict__ bias_part) {
+    __shared__ float sums[kWavesPerBlock][kWave][9];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    drop.begin();
+    const int64_t col = ((int64_t)blockIdx.x * kWave + lane) * 8, left = n - col, blocks = (n + 7) / 8;
+    const int64_t r0 = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * kBiasRows;
+    if (r0 >= m) return;
+    const int64_t r1 = r0 + kBiasRows < m ? r0 + kBiasRows : m;
+    float sum[8] = {};
+    if (left > 0) {
+        for (int64_t row = r0 + wave; row < r1; row += kWavesPerBlock) {
+            float v[8];
+            expand(load_raw8(dy + row * lddy + col, left), v);
+            if (drop.threshold) drop((uint64_t)(row * blocks + col / 8), v);
+            if (act != COAT_ACT_NONE) {
+                float zv[8];
+                expand(load_raw8(z + row * ldz + col, left), zv);
+                with_act(act, [&](auto a) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float s = slope<a.value>(zv[i]);
+                        // a dropped place stays zero whatever z holds there
+                        v[i] = v[i] == 0.0f ? 0.0f : v[i] * s;
+                    }
+                });
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (i >= left) v[i] = 0.0f;
+                sum[i] += v[i];
+            }
+            if (dz) store8<true>(dz + row * ld_dz + col, 8, v);
+        }
+    }
+    if (!bias_part) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sums[wave][lane][i] = sum[i];
+    __syncthreads();
+    if (wave == 0 && left > 0) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (sums[0][lane][i] + sums[1][lane][i]) + (sums[2][lane][i] + sums[3][lane][i]);
+        store8<true>(bias_part + (r0 / kBiasRows) * ld_dz + col, 8, v);
+    }
+}
+
+// dbias = scale times the parts' sums, a thread a column.
+template <class T>
+__global__ __launch_bounds__(kBlock) void bias_join_kernel(const float* __restrict__ part, int64_t ld, int64_t parts, int64_t n,
+                                                           float scale, T* __restrict__ dbias) {
+    const int64_t col = (int64_t)blockIdx.x * kBlock + threadIdx.x;
+    if (col >= n) return;
+    float sum = 0.0f;
+    for (int64_t i = 0; i < parts; ++i) sum += gp(part)[i * ld + col];
+    sum *= scale;
+    if constexpr (sizeof(T) == 4) gp(dbias)[col] = sum;
+    else gp(dbias)[col] = (uint16_t)bf16_bits(sum);
+}
+
+template <class T>
+int launch_dz(const T* dy, int64_t lddy, const uint16_t* z, int64_t ldz, int32_t act, const Drop& drop, int64_t m, int64_t n, uint16_t* dz,
+              int64_t ld_dz, float* part, hipStream_t st) {
+    const int64_t bands = div_up(m, kBiasRows), most = 32768;
+    const dim3 grid((unsigned)div_up(n, kWave * 8), (unsigned)(bands < most ? bands : most), (unsigned)div_up(bands, most));
+    hipLaunchKernelGGL(dz_kernel<T>, grid, dim3(kBlock), 0, st, dy, lddy, z, ldz, act, drop, m, n, dz, ld_dz, part);
+    return launch_status();
+}
+
+template <class T>
+int launch_linear(const Product16& p, const coat_epilogue* e, const void* bias, int32_t bias_type, const void* residual, int64_t ldr,
+                  uint16_t* z, int64_t ldz, void* y, int64_t ldy, hipStream_t st) {
+    const uint32_t t = drop_threshold(e->p);
+    const LinearOut<T> out{bias, static_cast<const T*>(residual), z, static_cast<T*>(y), ldr, ldz, ldy, div_up(p.n, 8),
+                           Drop{e->rng, e->offset, t, 0, 0}, e->scale * drop_factor(t), e->act, bias_type};
+    return launch_product<false, false>(p, out, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t coat_linear_workspace_bytes(int64_t, int64_t, int64_t, int32_t) { return 0; }
+
+int coat_linear(const uint16_t* x, int64_t m, int64_t k, int64_t ldx, const uint16_t* w, int64_t n, int64_t ldw,
+                const coat_epilogue* e, const void* bias, int32_t bias_type, const void* residual, int64_t ldr, uint16_t* z,
+                int64_t ldz, void* y, int64_t ldy, int32_t y_type, void* workspace, size_t workspace_bytes, coat_stream_t stream) {
+    const int rc = check_linear(x, m, k, ldx, w, n, ldw, e, bias, bias_type, residual, ldr, z, ldz, y, ldy, y_type);
+    if (rc || m == 0 || n == 0) return rc;
+    (void)workspace;
+    (void)workspace_bytes;
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    const Product16 p{x, w, ldx, ldw, nullptr, nullptr, nullptr, m, n, k};
+    if (y_type == COAT_FP32) return launch_linear<float>(p, e, bias, bias_type, residual, ldr, z, ldz, y, ldy, st);
+    return launch_linear<uint16_t>(p, e, bias, bias_type, residual, ldr, z, ldz, y, ldy, st);
+}
+
+size_t coat_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t) {
+    if (m < 1 || n < 1 || m > kMaxDim || n > kMaxDim) return 0;
+    return linear_backward_layout(m, n, k).end;
+}
+
+int coat_linear_backward(const void* dy, int64_t lddy, int32_t dy_type, const uint16_t* x, int64_t m, int64_t k, int64_t ldx,
+                         const uint16_t* w, int64_t n, int64_t ldw, const coat_epilogue* e, const uint16_t* z, int64_t ldz,
+                         uint16_t* dx, int64_t lddx, uint16_t* dw, int64_t lddw, void* dbias, int32_t dbias_type, void* workspace,
+                         size_t workspace_bytes, coat_stream_t stream) {
+    int rc = check_linear_backward(dy, lddy, dy_type, x, m, k, ldx, w, n, ldw, e, z, ldz, dx, lddx, dw, lddw, dbias, dbias_type);
+    if (rc) return rc;
+    const size_t need = coat_linear_backward_workspace_bytes(m, n, k, 0);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return COAT_EINVAL;
+        if (!aligned(workspace, 256)) return COAT_EALIGN;
+    }
+    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    const LinearBackwardLayout l = linear_backward_layout(m, n, k);
+    char* const ws = static_cast<char*>(workspace);
+    uint16_t* const dz = reinterpret_cast<uint16_t*>(ws + l.dz);
+    float* const part = reinterpret_cast<float*>(ws + l.bias);
+    const uint32_t t = drop_threshold(e->p);
+    const Drop drop{e->rng, e->offset, t, 0, 0};
+    const float scale = e->scale * drop_factor(t);
+    if (m > 0 && n > 0) {
+        if (dy_type == COAT_FP32)
+            rc = launch_dz(static_cast<const float*>(dy), lddy, z, ldz, e->act, drop, m, n, dz, l.ld_dz, dbias ? part : nullptr, st);
+        else
+            rc = launch_dz(static_cast<const uint16_t*>(dy), lddy, z, ldz, e->act, drop, m, n, dz, l.ld_dz, dbias ? part : nullptr, st);
+        if (rc) return rc;
+    }
+    if (dbias && n > 0) {
+        const dim3 grid((unsigned)div_up(n, kBlock));
+        const int64_t parts = div_up(m, kBiasRows);
+        if (dbias_type == COAT_FP32)
+            hipLaunchKernelGGL(bias_join_kernel<float>, grid, dim3(kBlock), 0, st, part, l.ld_dz, parts, n, scale, static_cast<float*>(dbias));
+        else
+            hipLaunchKernelGGL(bias_join_kernel<uint16_t>, grid, dim3(kBlock), 0, st, part, l.ld_dz, parts, n, scale,
+                               static_cast<uint16_t*>(dbias));
+        if ((rc = launch_status())) return rc;
+    }
+    if (dx) {
+        const ScaledOut out{nullptr, scale, nullptr, dx, lddx, nullptr, 0, true};
+        rc = launch_product<false, true>(Product16{dz, w, l.ld_dz, ldw, nullptr, nullptr, nullptr, m, k, n}, out, st);
+        if (rc) return rc;
+    }
+    if (dw) {
+        const ScaledOut out{nullptr, scale, nullptr, dw, lddw, nullptr, 0, true};
+        rc = launch_product<true, true>(Product16{dz, x, l.ld_dz, ldx, nullptr, nullptr, nullptr, n, k, m}, out, st);
+    }
+    return rc;
+}
+
+}  // extern "C"

@@ -1,0 +1,178 @@
+// Host-side logic of the training products (linear layer, dropout, cross entropy of
+// a vocabulary projection) that touches no GPU: argument checks, sizes and
+// workspaces. Plain C++ with no HIP dependency, so that the same code runs in a
+// host-only driver under AddressSanitizer and UndefinedBehaviorSanitizer.
+#pragma once
+
+#include "ops_host.h"
+
+namespace {
+
+// Dropout: an element is dropped if its 16 bits are under the threshold, which is
+// at most 65535 (p rounded to a multiple of 2^-16, something always kept).
+inline uint32_t drop_threshold(float p) {
+    const double t = (double)p * 65536.0 + 0.5;
+    return t >= 65536.0 ? 65535u : (uint32_t)t;
+}
+inline float drop_factor(uint32_t threshold) { return (float)(65536.0 / (65536.0 - (double)threshold)); }
+
+inline int check_epilogue(const coat_epilogue* e) {
+    if (!e) return COAT_EINVAL;
+    if (e->act < COAT_ACT_NONE || e->act > COAT_ACT_SILU || !finite_f(e->scale)) return COAT_EINVAL;
+    if (!(e->p >= 0.0f && e->p < 1.0f) || (e->p > 0.0f && !e->rng)) return COAT_EINVAL;
+    if (!aligned(e->rng, 8)) return COAT_EALIGN;
+    return COAT_OK;
+}
+
+// A matrix that may be absent; rows = 0 or cols = 0 needs no address.
+inline int check_optional(const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t dtype) {
+    if (!p) return COAT_OK;
+    const int rc = check_matrix(rows, cols, ld, dtype);
+    if (rc) return rc;
+    return aligned(p, type_bytes(dtype)) ? COAT_OK : COAT_EALIGN;
+}
+inline int check_present(const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t dtype) {
+    if (!p && rows > 0 && cols > 0) return COAT_EINVAL;
+    const int rc = check_matrix(rows, cols, ld, dtype);
+    if (rc) return rc;
+    return aligned(p, type_bytes(dtype)) ? COAT_OK : COAT_EALIGN;
+}
+// The first error among several checks, invalid arguments before alignments.
+inline int first_error(std::initializer_list<int> all) {
+    int align = COAT_OK;
+    for (const int rc : all) {
+        if (rc == COAT_EINVAL) return rc;
+        if (rc) align = rc;
+    }
+    return align;
+}
+
+inline int check_linear(const void* x, int64_t m, int64_t k, int64_t ldx, const void* w, int64_t n, int64_t ldw,
+                        const coat_epilogue* e, const void* bias, int32_t bias_type, const void* residual, int64_t ldr,
+                        const void* z, int64_t ldz, const void* y, int64_t ldy, int32_t y_type) {
+    if (!type_ok(bias_type)) return COAT_EINVAL;
+    return first_error({check_epilogue(e), check_present(x, m, k, ldx, COAT_BF16), check_present(w, n, k, ldw, COAT_BF16),
+                        check_present(y, m, n, ldy, y_type), check_optional(residual, m, n, ldr, y_type),
+                        check_optional(z, m, n, ldz, COAT_BF16),
+                        aligned(bias, type_bytes(bias_type)) ? COAT_OK : COAT_EALIGN});
+}
+
+inline int check_linear_backward(const void* dy, int64_t lddy, int32_t dy_type, const void* x, int64_t m, int64_t k, int64_t ldx,
+                                 const void* w, int64_t n, int64_t ldw, const coat_epilogue* e, const void* z, int64_t ldz,
+                                 const void* dx, int64_t lddx, const void* dw, int64_t lddw, const void* dbias,
+                                 int32_t dbias_type) {
+    if (!type_ok(dbias_type) || (!dx && !dw && !dbias && m > 0 && n > 0 && k > 0)) return COAT_EINVAL;
+    const int rc = check_epilogue(e);
+    if (rc == COAT_EINVAL) return rc;
+    if (e->act != COAT_ACT_NONE && !z && m > 0 && n > 0) return COAT_EINVAL;
+    return first_error({rc, check_present(dy, m, n, lddy, dy_type), dw ? check_present(x, m, k, ldx, COAT_BF16) : check_optional(x, m, k, ldx, COAT_BF16),
+                        dx ? check_present(w, n, k, ldw, COAT_BF16) : check_optional(w, n, k, ldw, COAT_BF16),
+                        check_optional(z, m, n, ldz, COAT_BF16), check_optional(dx, m, k, lddx, COAT_BF16),
+                        check_optional(dw, n, k, lddw, COAT_BF16), aligned(dbias, type_bytes(dbias_type)) ? COAT_OK : COAT_EALIGN,
+                        m > kMaxDim || n > kMaxDim || k > kMaxDim || m < 0 || n < 0 || k < 0 ? COAT_EINVAL : COAT_OK});
+}
+
+inline int check_dropout(const void* x, int64_t rows, int64_t cols, int64_t ldx, int32_t x_type, const void* residual,
+                         int64_t ldr, float scale, float p, const int64_t* rng, const void* y, int64_t ldy, int32_t y_type) {
+    if (!finite_f(scale) || !(p >= 0.0f && p < 1.0f) || (p > 0.0f && !rng)) return COAT_EINVAL;
+    return first_error({check_present(x, rows, cols, ldx, x_type), check_present(y, rows, cols, ldy, y_type),
+                        check_optional(residual, rows, cols, ldr, y_type), aligned(rng, 8) ? COAT_OK : COAT_EALIGN});
+}
+
+// ------------------------------------------------------------------ backward pass of the linear layer
+
+// Rows whose part of the bias gradient one workgroup adds up.
+constexpr int64_t kBiasRows = 64;
+
+// Workspace of the backward pass: dz in bf16 with rows of whole 128 bytes, the
+// partial sums of the bias gradient.
+struct LinearBackwardLayout {
+    int64_t ld_dz;
+    size_t dz, bias, end;
+};
+inline LinearBackwardLayout linear_backward_layout(int64_t m, int64_t n, int64_t k) {
+    (void)k;
+    LinearBackwardLayout l;
+    l.ld_dz = div_up(n, 64) * 64;
+    l.dz = 0;
+    l.bias = align_up((size_t)m * (size_t)l.ld_dz * 2, 256);
+    l.end = l.bias + align_up((size_t)div_up(m, kBiasRows) * (size_t)l.ld_dz * sizeof(float), 256);
+    return l;
+}
+
+// ------------------------------------------------------------------ cross entropy of a vocabulary projection
+
+inline int check_xent(const void* x, int64_t tokens, int64_t cols, int64_t ldx, const void* w, int64_t vocab, int64_t ldw,
+                      const int64_t* labels, const float* loss, const float* lse) {
+    if (vocab < 1 || (tokens > 0 && (!labels || !loss || !lse))) return COAT_EINVAL;
+    return first_error({check_present(x, tokens, cols, ldx, COAT_BF16), check_present(w, vocab, cols, ldw, COAT_BF16),
+                        aligned(labels, 8) ? COAT_OK : COAT_EALIGN, aligned(loss, 4) && aligned(lse, 4) ? COAT_OK : COAT_EALIGN});
+}
+
+inline int check_xent_backward(const void* x, int64_t tokens, int64_t cols, int64_t ldx, const void* w, int64_t vocab, int64_t ldw,
+                               const int64_t* labels, const float* lse, const float* dloss, int64_t dloss_count, const void* dx,
+                               int64_t lddx, const void* dw, int64_t lddw) {
+    if (dloss_count != 1 && dloss_count != tokens) return COAT_EINVAL;
+    if (tokens > 0 && !dloss) return COAT_EINVAL;
+    if (!dx && !dw && tokens > 0 && cols > 0) return COAT_EINVAL;
+    return first_error({check_xent(x, tokens, cols, ldx, w, vocab, ldw, labels, lse, lse), check_optional(dx, tokens, cols, lddx, COAT_BF16),
+                        check_optional(dw, vocab, cols, lddw, COAT_BF16), aligned(dloss, 4) ? COAT_OK : COAT_EALIGN});
+}
+
+constexpr int64_t kLseWidth = 32;  // columns of a partial log sum
+
+// Workspace of the loss: number of tokens that count, their places and labels, the
+// logits of their labels, and a (maximum, sum) for each of them and each part of
+// the vocabulary.
+struct XentLayout {
+    int64_t parts;
+    size_t count, at, label, zt, part, end;
+};
+inline XentLayout xent_layout(int64_t tokens, int64_t vocab) {
+    XentLayout l;
+    const size_t t = (size_t)tokens;
+    l.parts = div_up(vocab, kLseWidth);
+    l.count = 0;
+    l.at = 256;
+    l.label = l.at + align_up(t * 4, 256);
+    l.zt = l.label + align_up(t * 4, 256);
+    l.part = l.zt + align_up(t * 4, 256);
+    l.end = l.part + align_up((size_t)l.parts * t * 8, 256);
+    return l;
+}
+
+// Columns of the vocabulary that the backward pass takes at a time. The gradients of
+// a piece's logits are 2^26 numbers (128 MB, half of the last cache) or 2048
+// columns wide; pieces are of equal size.
+inline int64_t xent_piece(int64_t tokens, int64_t vocab) {
+    int64_t most = ((int64_t)1 << 26) / (tokens > 0 ? tokens : 1) / 256 * 256;
+    if (most < 2048) most = 2048;
+    if (most >= vocab) return vocab;
+    return div_up(div_up(vocab, div_up(vocab, most)), 256) * 256;
+}
+
+// Workspace of the backward pass: number of tokens that count and the largest
+// weight of a loss, the tokens' places in the packed rows and back, what a row of
+// logits needs, the packed rows of x, a piece's gradients, and the sums of dx over pieces.
+struct XentBackwardLayout {
+    int64_t piece, ld_x, ld_g;
+    size_t count, at, place, info, x, g, acc, end;
+};
+inline XentBackwardLayout xent_backward_layout(int64_t tokens, int64_t vocab, int64_t cols) {
+    XentBackwardLayout l;
+    const size_t t = (size_t)tokens;
+    l.piece = xent_piece(tokens, vocab);
+    l.ld_x = div_up(cols, 64) * 64;
+    l.ld_g = div_up(l.piece, 64) * 64;
+    l.count = 0;
+    l.at = 256;
+    l.place = l.at + align_up(t * 4, 256);
+    l.info = l.place + align_up(t * 4, 256);
+    l.x = l.info + align_up(t * 16, 256);
+    l.g = l.x + align_up(t * (size_t)l.ld_x * 2, 256);
+    l.acc = l.g + align_up(t * (size_t)l.ld_g * 2, 256);
+    l.end = l.acc + (l.piece < vocab ? align_up(t * (size_t)l.ld_x * 4, 256) : 0);
+    return l;
+}
+
+}  // namespace

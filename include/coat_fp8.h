@@ -389,6 +389,130 @@ int coat_block_norm_backward(const coat_border* b, const uint16_t* y, const void
                              void* dw_post, void* dw_pre, void* dgate, void* workspace,
                              size_t workspace_bytes, coat_stream_t stream);
 
+/*
+ * The products of a training step, over the bf16 weights that the optimizer step
+ * writes (one row per output feature): a linear layer with its epilogue, dropout
+ * without a stored mask, and the softmax cross entropy of a vocabulary projection
+ * without stored logits. All matrices have one row per token, row i at p + i ld,
+ * ld >= the columns, counting elements; elements between the columns and ld are
+ * neither read nor written. Sizes are limited to 2^31 - 1 each. Matrices need
+ * their type's alignment (COAT_EALIGN).
+ *
+ * Dropout. rng points to two 64-bit numbers in device memory, (seed, step), read
+ * when the work runs, so that a captured graph draws anew after they changed.
+ * Element (i, j) of a matrix with `cols` columns takes 16 bits of the Philox 4x32
+ * generator with 10 rounds (Salmon et al., "Parallel random numbers: as easy as 1,
+ * 2, 3"): key seed, counter (i ceil(cols / 8) + j / 8, step + offset), 64 bits
+ * each with the low words first; half word j % 8 of the four output words, low
+ * halves first. It is dropped if they are under t = round(65536 p), at most 65535;
+ *   D(v) = v 65536 / (65536 - t) where kept, 0 where dropped
+ * (whatever v was). offset tells the uses of one (seed, step) apart: a layer's
+ * number, say, with step advanced by the number of layers. p = 0 needs no rng.
+ */
+enum { COAT_ACT_NONE = 0, COAT_ACT_RELU = 1, COAT_ACT_GELU = 2, COAT_ACT_GELU_TANH = 3, COAT_ACT_SILU = 4 };
+
+typedef struct coat_epilogue {
+    int32_t act;        /* COAT_ACT_*: max(z, 0); z Phi(z); z sigmoid(sqrt(8 / pi) (z + 0.044715 z^3)); z sigmoid(z) */
+    float scale;        /* finite */
+    float p;            /* dropout, 0 <= p < 1 */
+    int64_t offset;     /* added to the step */
+    const int64_t* rng; /* (seed, step) in device memory, 8-byte aligned; may be NULL if p = 0 */
+} coat_epilogue;
+
+/*
+ * Linear layer: z = x w^T + bias, y = residual + scale D(act(z)).
+ *   x      bf16, m x k      w  bf16, n x k
+ *   bias   n values of bias_type, may be NULL
+ *   residual  m x n, the type of y; may be NULL, may be y itself (same ld)
+ *   z      bf16, m x n, out: kept for the backward pass; may be NULL
+ *   y      m x n, bf16 or fp32 (y_type), out
+ * Sums are held in fp32, in an order that depends on the sizes and on whether x and
+ * w are aligned (below) alone; y and z are each rounded once from them.
+ *   workspace  device memory, 256-byte aligned, at least
+ *          coat_linear_workspace_bytes(m, n, k, aligned) bytes (may be NULL if that
+ *          is 0); calls that may overlap in time need one each. aligned: whether x
+ *          and w are 16-byte aligned and k, ldx and ldw multiples of 8.
+ * m = 0 or n = 0 writes nothing; k = 0 gives z = bias.
+ */
+size_t coat_linear_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t aligned);
+int coat_linear(const uint16_t* x, int64_t m, int64_t k, int64_t ldx, const uint16_t* w, int64_t n, int64_t ldw,
+                const coat_epilogue* e, const void* bias, int32_t bias_type, const void* residual,
+                int64_t ldr, uint16_t* z, int64_t ldz, void* y, int64_t ldy, int32_t y_type,
+                void* workspace, size_t workspace_bytes, coat_stream_t stream);
+
+/*
+ * Its backward pass, with the forward's epilogue and random numbers:
+ *   dz = scale D(dy) act'(z),  dx = dz w,  dw = dz^T x,  dbias = sum of dz over the tokens
+ * (the gradient of residual is dy). act' is taken at the stored z; that of the
+ * first activation is 0 at 0.
+ *   dy     m x n, bf16 or fp32 (dy_type)
+ *   z      the forward's; needed with an activation, may be NULL without
+ *   dx     bf16, m x k, dw bf16, n x k, dbias n values of dbias_type: out, each may
+ *          be NULL, one at least is needed; x may be NULL without dw, w without dx
+ * The products take dz rounded to bf16, without the factors scale and 1 / (1 - p),
+ * which their sums are multiplied by; dbias adds dz as it was before. m = 0 gives
+ * dw and dbias of zeros, n = 0 a dx of zeros.
+ *   workspace  as above, at least coat_linear_backward_workspace_bytes(m, n, k,
+ *          aligned) bytes; aligned: whether x and w are, as above.
+ */
+size_t coat_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t aligned);
+int coat_linear_backward(const void* dy, int64_t lddy, int32_t dy_type, const uint16_t* x, int64_t m, int64_t k,
+                         int64_t ldx, const uint16_t* w, int64_t n, int64_t ldw, const coat_epilogue* e,
+                         const uint16_t* z, int64_t ldz, uint16_t* dx, int64_t lddx, uint16_t* dw, int64_t lddw,
+                         void* dbias, int32_t dbias_type, void* workspace, size_t workspace_bytes,
+                         coat_stream_t stream);
+
+/*
+ * Dropout of a matrix: y = residual + scale D(x).
+ *   x      rows x cols, bf16 or fp32 (x_type)
+ *   residual  the type of y; may be NULL
+ *   y      rows x cols, bf16 or fp32 (y_type), out; may be x or residual itself (same
+ *          type and ld)
+ * Its backward pass is the same call on dy, without the residual: dx = scale D(dy).
+ */
+int coat_dropout(const void* x, int64_t rows, int64_t cols, int64_t ldx, int32_t x_type, const void* residual,
+                 int64_t ldr, float scale, float p, const int64_t* rng, int64_t offset, void* y, int64_t ldy,
+                 int32_t y_type, coat_stream_t stream);
+
+/*
+ * Softmax cross entropy of a vocabulary projection, the logits never stored:
+ *   l = x w^T,  lse = log sum_v exp(l_v),  loss = lse - l_label   per token.
+ *   x      bf16, tokens x cols      w  bf16, vocab x cols, vocab >= 1
+ *   labels tokens 64-bit numbers; a token whose label is ignore_index is left out:
+ *          loss 0, lse 0, and its row of x is not used. Any other label outside
+ *          [0, vocab) makes that token's loss NaN (and its gradients).
+ *   loss, lse  tokens fp32, out
+ * The logits are sums in fp32 and are not rounded further.
+ *   workspace  as above, coat_linear_cross_entropy_workspace_bytes(tokens, vocab,
+ *          cols, aligned); aligned: whether x and w are, as for the linear layer.
+ */
+size_t coat_linear_cross_entropy_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols, int32_t aligned);
+int coat_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t cols, int64_t ldx, const uint16_t* w,
+                              int64_t vocab, int64_t ldw, const int64_t* labels, int64_t ignore_index,
+                              float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                              coat_stream_t stream);
+
+/*
+ * Its backward pass, from the forward's lse:
+ *   g = dloss (softmax(l) - onehot(label)),  dx = g w,  dw = g^T x,
+ * the logits computed again in pieces of the vocabulary.
+ *   dloss  fp32, the gradient of each token's loss (dloss_count = tokens), or one
+ *          value for all of them (dloss_count = 1)
+ *   dx     bf16, tokens x cols, dw bf16, vocab x cols: out, each may be NULL, one
+ *          at least is needed. A token that is left out has zeros in dx and no part
+ *          in dw, whatever its x holds.
+ * The products take g rounded to bf16, without dloss's largest magnitude, which
+ * their sums are multiplied by; sums are held in fp32. tokens = 0 gives a dw of zeros.
+ *   workspace  as above, coat_linear_cross_entropy_backward_workspace_bytes(tokens,
+ *          vocab, cols, aligned).
+ */
+size_t coat_linear_cross_entropy_backward_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols, int32_t aligned);
+int coat_linear_cross_entropy_backward(const uint16_t* x, int64_t tokens, int64_t cols, int64_t ldx, const uint16_t* w,
+                                       int64_t vocab, int64_t ldw, const int64_t* labels, int64_t ignore_index,
+                                       const float* lse, const float* dloss, int64_t dloss_count, uint16_t* dx,
+                                       int64_t lddx, uint16_t* dw, int64_t lddw, void* workspace,
+                                       size_t workspace_bytes, coat_stream_t stream);
+
 /* Static description of a status code. */
 const char* coat_strerror(int status);
 
