@@ -543,7 +543,7 @@ def _epilogue(act: int, scale: float, p: float, rng, offset: int, gpu: int) -> _
 
 
 def _is_aligned(ptr: int, ld: int, cols: int) -> bool:
-    return ptr % 16 == 0 and ld % 8 == 0 and cols % 8 == 0
+    return ptr % 16 == 0 and ld % 8 == 0 and cols % 8 == 0 and ld < 1 << 22
 
 
 def linear(x, w, y, *, bias=None, act: int = ACT_NONE, z=None, residual=None, scale: float = 1.0, p: float = 0.0, rng=None,

@@ -1,0 +1,512 @@
+// Products of bf16 matrices on the matrix units (gfx950), with an epilogue of the caller's.
+#pragma once
+
+#include <type_traits>
+
+#include "train_common.h"
+
+namespace {
+
+// ------------------------------------------------------------------ the product
+//
+// sum over k of A(i, k) B(j, k), A m x k and B n x k in bf16. An operand's memory has
+// rows of k (k runs along a row), or of i (k is the row: "tall").
+
+struct Product16 {
+    const uint16_t *a, *b;
+    int64_t lda, ldb;       // elements from row to row of memory
+    const int32_t* a_rows;  // row i of A is row a_rows[i] of memory; NULL: row i (not with a tall A)
+    const int32_t* m_at;    // in device memory: the rows of A that exist, at most m; NULL: m
+    const int32_t* k_at;    // the same of k
+    int64_t m, n, k;
+};
+
+__device__ __forceinline__ f32x16 mfma16(const u32x4& b, const u32x4& a, const f32x16& acc) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), acc, 0, 0, 0);
+}
+
+// One matrix instruction takes 32 rows of each operand over 16 values of k: lane l
+// holds the 8 values k = 8 (l / 32) .. of row l % 32. B is the first operand, so that
+// a lane's four consecutive accumulators are four consecutive columns: accumulator r
+// of lane l is row l % 32, column 8 (r / 4) + 4 (l / 32) + r % 4.
+//
+// The plain product, straight from global memory: each wavefront a 32 x 32 tile, a
+// workgroup 64 x 64; any strides and alignments.
+template <bool TALL_A, bool TALL_B, class Out>
+__global__ __launch_bounds__(kBlock) void product_plain_kernel(Product16 p, uint32_t tiles_n, Out out) {
+    __shared__ float lds[kWavesPerBlock][32][33];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int64_t tile = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    const int64_t m = p.m_at ? (int64_t)__builtin_amdgcn_readfirstlane(*gp(p.m_at)) : p.m, k = p.k_at ? (int64_t)__builtin_amdgcn_readfirstlane(*gp(p.k_at)) : p.k;
+    const int64_t n0 = tile % tiles_n * 64 + (wave & 1) * 32, m0 = tile / tiles_n * 64 + (wave >> 1) * 32;
+    if (m0 >= m || n0 >= p.n) return;
+    out.begin();
+    const int row = lane & 31, half = lane >> 5;
+    // rows past the end are read as the last one and not used
+    const int64_t ra = m0 + row < m ? m0 + row : m - 1, rb = n0 + row < p.n ? n0 + row : p.n - 1;
+    const int64_t ma = p.a_rows ? (int64_t)gp(p.a_rows)[ra] : ra;
+    const uint16_t* const pa = p.a + (TALL_A ? ra : ma * p.lda);
+    const uint16_t* const pb = p.b + (TALL_B ? rb : rb * p.ldb);
+    f32x16 acc;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+    for (int64_t k0 = 0; k0 < k; k0 += 16) {
+        u32x4 a{0u, 0u, 0u, 0u}, b{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t at = k0 + half * 8 + e;
+            if (at < k) {
+                a[e / 2] |= (uint32_t)gp(pa)[TALL_A ? at * p.lda : at] << (16 * (e & 1));
+                b[e / 2] |= (uint32_t)gp(pb)[TALL_B ? at * p.ldb : at] << (16 * (e & 1));
+            }
+        }
+        acc = mfma16(b, a, acc);
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) lds[wave][row][8 * (r / 4) + 4 * half + r % 4] = acc[r];
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if constexpr (Out::kLogSum) {
+        if (lane < 32 && m0 + lane < m) {
+            const int64_t label = out.label_of(m0 + lane) - n0;
+            const int cols = (int)(p.n - n0 < 32 ? p.n - n0 : 32);
+            float top = -__builtin_inff(), sum = 0.0f;
+            for (int c = 0; c < cols; ++c)
+                if (c == label) out.keep(m0 + lane, lds[wave][lane][c]);
+                else top = fmaxf(top, lds[wave][lane][c]);
+            const float from = top == -__builtin_inff() ? 0.0f : top;
+            for (int c = 0; c < cols; ++c)
+                if (c != label) sum += exp_fast(lds[wave][lane][c] - from);
+            out.put(m0 + lane, n0 / 32, from, sum);
+        }
+    } else {
+        for (int i = lane; i < 32 * 4; i += kWave) {
+            const int r = i / 4, c = i % 4 * 8;
+            if (m0 + r >= m || n0 + c >= p.n) continue;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = lds[wave][r][c + e];
+            out(m0 + r, n0 + c, v, p.n - n0 - c);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ tiles
+//
+// A workgroup of WN x WM wavefronts, each with 32 FN rows of B by 32 FM rows of A,
+// computes tiles one after the other; the k of all its tiles forms one stream of
+// steps of 64 values. A step's values (128 bytes for each row of the tile, B's before
+// A's) go straight from global memory into one of SLOTS slots of LDS, SLOTS steps
+// before they are used. A step is computed in phases of HALVES runs of 16 values:
+// while one phase's matrix instructions run, the next one's fragments are read from
+// LDS. One barrier a step, before its last phase: behind it every wavefront has read
+// the step (its slot may be refilled) and the next one has arrived.
+//
+// In LDS an operand whose k runs along its rows lies as rows of 128 bytes, chunk c of
+// row r at position c ^ (r / 2 % 8), so that 16 rows' reads reach 16 different 16-byte
+// columns of the banks. A tall one lies as 64 rows of k, its 64-byte segments s at
+// s ^ (k % 4): the transposing read takes 4 rows of k by 32 columns from 32 lanes, which
+// are four different segments of the banks' 256 bytes.
+template <int N>
+__device__ __forceinline__ void wait_vm_and_lds_then_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// 16 bytes a lane from base + off to LDS, lane after lane from byte address lds + AT.
+template <uint32_t AT>
+__device__ __forceinline__ void load_to_lds16(uint32_t lds, uint32_t off, const uint8_t* base) {
+    asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base), "n"(AT)
+                 : "memory", "scc");
+}
+// The same, or nothing if `on` is 0 (one branch within a long run of code).
+template <uint32_t AT>
+__device__ __forceinline__ void load_to_lds16_if(uint32_t on, uint32_t lds, uint32_t off, const uint8_t* base) {
+    asm volatile(
+        "s_cmp_eq_u32 %4, 0\n\ts_cbranch_scc1 .Lskip%=\n\ts_add_u32 m0, %0, %3\n\ts_nop 0\n\t"
+        "global_load_lds_dwordx4 %1, %2\n.Lskip%=:" ::"s"(lds), "v"(off), "s"(base), "n"(AT), "s"(on)
+        : "memory", "scc");
+}
+
+// f(0), f(1), ... f(N - 1) with the index known to the compiler.
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void each(F&& f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        each<N, I + 1>(f);
+    }
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x2 read_transposed(const uint8_t* p) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
+}
+
+// Items: with splits > 1 item t is the product over the steps [s per_split, (s + 1)
+// per_split), s = t / tiles, of tile t % tiles, and goes to part + s stride (sums that
+// another kernel adds).
+struct Items {
+    uint32_t tiles_n, splits, per_split;
+    float* part;
+    int64_t ld, stride;
+};
+
+template <int WN_, int WM_, int FN_, int FM_, int SLOTS_, int HALVES_, int PIECE_>
+struct TileShape {
+    static constexpr int WN = WN_, WM = WM_, FN = FN_, FM = FM_, SLOTS = SLOTS_, HALVES = HALVES_, PIECE = PIECE_;
+    static constexpr int WAVES = WN * WM, BN = 32 * WN * FN, BM = 32 * WM * FM, kLds = SLOTS * (BN + BM) * 128 + WAVES * 32 * PIECE * 4;
+    static constexpr int kWavesPerSimd = WAVES / 4 * (kLds <= 81920 ? 2 : 1);
+};
+typedef TileShape<2, 2, 4, 4, 2, 1, 64> Tile256;
+typedef TileShape<2, 2, 2, 2, 2, 2, 32> Tile128;
+
+template <class S, bool TALL_A, bool TALL_B, class Out>
+__global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu(S::kWavesPerSimd, S::kWavesPerSimd))) void product_tile_kernel(
+    Product16 p, Items items_of, Out out) {
+    constexpr int WN = S::WN, FN = S::FN, FM = S::FM, SLOTS = S::SLOTS, HALVES = S::HALVES, PIECE = S::PIECE;
+    constexpr int WAVES = S::WAVES, BN = S::BN, BM = S::BM, D = FN + FM, PHASES = 4 / HALVES;
+    constexpr int L = (BN + BM) / 8 / WAVES, LB = BN / 8 / WAVES;  // loads of a step by each wavefront, LB of them B's
+    static_assert(LB * 8 * WAVES == BN && L * 8 * WAVES == BN + BM && L % 2 == 0 && WAVES % 2 == 0 && PHASES >= 2, "loads are dealt evenly");
+    constexpr uint32_t kSlotBytes = (BN + BM) * 128;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[S::kLds];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int half = lane >> 5, l32 = lane & 31;
+    const int64_t m = p.m_at ? (int64_t)__builtin_amdgcn_readfirstlane(*gp(p.m_at)) : p.m, n = p.n, k = p.k_at ? (int64_t)__builtin_amdgcn_readfirstlane(*gp(p.k_at)) : p.k;
+    const uint32_t tiles_n = items_of.tiles_n, tiles_m = (uint32_t)((m + BM - 1) / BM);
+    const uint32_t tiles = tiles_m * tiles_n, items = tiles * items_of.splits;
+    const uint32_t steps = (uint32_t)((k + 63) / 64), per_split = items_of.per_split;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+
+    // tile t: patches of 8 x 4 tiles are consecutive
+    auto place = [&](uint32_t t, int64_t& m0, int64_t& n0) __attribute__((always_inline)) {
+        const uint32_t per = 8 * tiles_n, band = t / per, in = t - band * per;
+        const uint32_t high = tiles_m - band * 8 < 8 ? tiles_m - band * 8 : 8;
+        m0 = (int64_t)(band * 8 + in % high) * BM;
+        n0 = (int64_t)(in / high) * BN;
+    };
+    // values of k in step g, at most 64 (none only if k is 0 or a split's part is empty)
+    auto values_of = [&](uint32_t g) __attribute__((always_inline)) {
+        const int64_t left = k - (int64_t)g * 64;
+        return (uint32_t)(left < 0 ? 0 : (left < 64 ? left : 64));
+    };
+    auto first_step = [&](uint32_t t) __attribute__((always_inline)) { return t / tiles * per_split; };
+    auto last_step = [&](uint32_t t) __attribute__((always_inline)) {  // one past it; an item has one step at least
+        const uint32_t g0 = first_step(t), g1 = g0 + per_split < steps ? g0 + per_split : steps;
+        return g1 > g0 ? g1 : g0 + 1;
+    };
+
+    // Byte offsets of this lane's 16 bytes in each load. What is past the end of the
+    // matrix or of k is not read: another row, column or value is fetched in its place,
+    // and not used, or zeroed in LDS.
+    uint32_t off[L];
+    auto offsets = [&](int64_t m0, int64_t n0, uint32_t values) __attribute__((always_inline)) {
+        each<L>([&](auto i) {
+            constexpr bool is_b = i < LB, tall = is_b ? TALL_B : TALL_A;
+            constexpr int own = is_b ? i : i - LB, width = is_b ? BN : BM;
+            const uint32_t ld2 = (uint32_t)(is_b ? p.ldb : p.lda) * 2;
+            const int64_t left = is_b ? n - n0 : m - m0;
+            if constexpr (tall) {
+                constexpr int lanes = width / 8, rows = kWave / lanes;  // lanes of a row of k, rows of a load
+                uint32_t row = (own * WAVES + wave) * rows + lane / lanes;
+                const uint32_t at = lane % lanes, seg = (at >> 2) ^ (row & 3);
+                uint32_t col = (seg * 4 + (at & 3)) * 8;
+                if (col >= left) col = 0;
+                if (row >= values) row = values > 0 ? values - 1 : 0;
+                off[i] = row * ld2 + col * 2;
+            } else {
+                uint32_t row = (own * WAVES + wave) * 8 + lane / 8, chunk = (lane & 7) ^ ((wave & 1) * 4 + (lane >> 4));
+                if (row >= left) row = (uint32_t)left - 1;
+                if (chunk * 8 >= values) chunk = 0;
+                if (!is_b && p.a_rows) off[i] = (uint32_t)gp(p.a_rows)[m0 + row] * ld2 + chunk * 16;
+                else off[i] = row * ld2 + chunk * 16;
+            }
+        });
+    };
+    const uint8_t *next_a, *next_b;  // first row of the step that is fetched next
+    auto start = [&](int64_t m0, int64_t n0, uint32_t g) __attribute__((always_inline)) {
+        const uint8_t *a = reinterpret_cast<const uint8_t*>(p.a), *b = reinterpret_cast<const uint8_t*>(p.b);
+        next_b = TALL_B ? b + ((int64_t)g * 64 * p.ldb + n0) * 2 : b + (n0 * p.ldb + (int64_t)g * 64) * 2;
+        next_a = TALL_A ? a + ((int64_t)g * 64 * p.lda + m0) * 2 : a + ((p.a_rows ? 0 : m0 * p.lda) + (int64_t)g * 64) * 2;
+    };
+    const uint32_t lds_wave = lds0 + wave * 1024;
+    auto fetch_part = [&](int slot, auto i, uint32_t on = 1) __attribute__((always_inline)) {
+        const uint8_t* from = i < LB ? next_b : next_a;
+        if (__builtin_constant_p(on)) load_to_lds16<i * WAVES * 1024>(lds_wave + slot * kSlotBytes, off[i], from);
+        else load_to_lds16_if<i * WAVES * 1024>(on, lds_wave + slot * kSlotBytes, off[i], from);
+    };
+
+    const int wn = wave % WN * FN * 32, wm = wave / WN * FM * 32;
+    u32x4 fb[2][HALVES][FN], fa[2][HALVES][FM];  // fragments, by parity of the phase
+    auto read_one = [&](const uint8_t* base, auto tall, auto width, int w0, int i, int h) __attribute__((always_inline)) {
+        if constexpr (tall.value) {
+            const int g = lane >> 4, q = lane & 15;
+            const uint8_t* at = base + (16 * h + 8 * (g >> 1) + (q >> 2)) * (width.value * 2) + ((w0 / 32 + i) ^ (q >> 2)) * 64 + (g & 1) * 32 + (q & 3) * 8;
+            const u32x2 lo = read_transposed(at), hi = read_transposed(at + 4 * width.value * 2);
+            return u32x4{lo[0], lo[1], hi[0], hi[1]};
+        } else {
+            return *reinterpret_cast<const u32x4*>(base + (w0 + i * 32 + l32) * 128 + ((2 * h + half) ^ ((l32 >> 1) & 7)) * 16);
+        }
+    };
+    // fragment i of run h of 16 values, A's first, which every row of matrix instructions needs
+    auto read_frag = [&](int slot, int set, int run, int h, int i) __attribute__((always_inline)) {
+        const uint8_t* base = lds + slot * kSlotBytes;
+        if (i < FM) fa[set][run][i] = read_one(base + BN * 128, std::bool_constant<TALL_A>{}, std::integral_constant<int, BM>{}, wm, i, h);
+        else fb[set][run][i - FM] = read_one(base, std::bool_constant<TALL_B>{}, std::integral_constant<int, BN>{}, wn, i - FM, h);
+    };
+    // Zeroes what a step of fewer than 64 values has fetched in excess.
+    auto clear_excess = [&](int slot, uint32_t values) __attribute__((always_inline)) {
+        uint8_t* base = lds + slot * kSlotBytes;
+        const u32x4 none{0u, 0u, 0u, 0u};
+        for (uint32_t c = threadIdx.x; c < (BN + BM) * 8; c += WAVES * kWave) {
+            const bool is_b = c < BN * 8, tall = is_b ? TALL_B : TALL_A;
+            const uint32_t own = is_b ? c : c - BN * 8, lanes = (is_b ? BN : BM) / 8;
+            const uint32_t at = tall ? own / lanes : ((own & 7) ^ (own >> 4 & 7)) * 8;
+            if (at >= values) *reinterpret_cast<u32x4*>(base + c * 16) = none;
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    };
+
+    // consecutive workgroups run on different XCDs: each XCD takes consecutive items of a round
+    const uint32_t first = gridDim.x % 8 == 0 ? (blockIdx.x & 7) * (gridDim.x / 8) + (blockIdx.x >> 3) : blockIdx.x;
+    if (first >= items) return;
+    out.begin();
+    uint32_t ft = first, fg = first_step(first), fg_end = last_step(first);  // step fg of item ft is fetched next
+    int64_t m0, n0;
+    place(ft % tiles, m0, n0);
+    offsets(m0, n0, values_of(fg));
+    start(m0, n0, fg);
+    auto advance = [&]() __attribute__((always_inline)) {
+        if (++fg < fg_end) {
+            next_b += TALL_B ? p.ldb * 128 : 128;
+            next_a += TALL_A ? p.lda * 128 : 128;
+            if (values_of(fg) < 64) offsets(m0, n0, values_of(fg));
+            return;
+        }
+        if (ft + gridDim.x < items) {  // behind the last item its steps are fetched once more and not used
+            ft += gridDim.x;
+            place(ft % tiles, m0, n0);
+        }
+        fg = first_step(ft);
+        fg_end = last_step(ft);
+        offsets(m0, n0, values_of(fg));
+        start(m0, n0, fg);
+    };
+    // With two slots the last step's later loads follow before the first phase.
+    constexpr int kLast = SLOTS > 2 ? L / 2 : L;
+    each<SLOTS>([&](auto s) {
+        if constexpr (s > 0) advance();
+        each<(s + 1 < SLOTS ? L : kLast)>([&](auto i) { fetch_part(s, i); });
+    });
+    wait_vm_and_lds_then_barrier<0>();
+    if (values_of(first_step(first)) < 64) clear_excess(0, values_of(first_step(first)));
+#pragma unroll
+    for (int r = 0; r < HALVES; ++r)
+#pragma unroll
+        for (int i = 0; i < D; ++i) read_frag(0, 0, r, r, i);
+    int slot = 0;
+    auto next_slot = [&] { return SLOTS == 2 ? slot ^ 1 : (slot + 1 < SLOTS ? slot + 1 : 0); };
+    auto last_slot = [&] { return SLOTS == 2 ? slot ^ 1 : (slot > 0 ? slot - 1 : SLOTS - 1); };
+
+    f32x16 acc[FN][FM];
+    // A phase. A wavefront issues in order, and a matrix instruction occupies its unit
+    // for 32 cycles: the few other instructions that the phase needs are dealt out
+    // between them, first the reads of the next phase's fragments, then loads into LDS:
+    // half of a step's in the last phase, the others (carry) in the phase behind that.
+    auto phase = [&](auto f, uint32_t carry) __attribute__((always_inline)) {
+        constexpr int kInstr = HALVES * FN * FM, set = f & 1;
+        constexpr bool last = f == PHASES - 1;
+        constexpr int kReads = HALVES * D, kItems = kReads + (last || f == 0 ? L / 2 : 0);
+        each<kInstr>([&](auto q) {
+            each<(q + 1) * kItems / kInstr - q * kItems / kInstr>([&](auto r) {
+                constexpr int item = q * kItems / kInstr + r;
+                if constexpr (item < kReads) {
+                    constexpr int nf = (f + 1) % PHASES, run = item / D;
+                    read_frag(last ? next_slot() : slot, 1 - set, run, nf * HALVES + run, item % D);
+                } else if constexpr (last) {
+                    fetch_part(slot, std::integral_constant<int, item - kReads>{});
+                } else {
+                    fetch_part(last_slot(), std::integral_constant<int, item - kReads + L / 2>{}, SLOTS > 2 ? 1 : carry);
+                }
+            });
+            __builtin_amdgcn_sched_barrier(0);
+            constexpr int run = q / (FN * FM), i = q / FM % FN, j = q % FM;
+            acc[i][j] = mfma16(fb[set][run][i], fa[set][run][j], acc[i][j]);
+            asm volatile("" : "+a"(acc[i][j]));  // keeps the order
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    for (uint32_t t = first; t < items; t += gridDim.x) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+        int64_t cm0, cn0;
+        place(t % tiles, cm0, cn0);
+        const uint32_t g0 = first_step(t), g1 = last_step(t);
+#pragma nounroll
+        for (uint32_t g = g0; g < g1; ++g) {
+            uint32_t carry = __builtin_amdgcn_readfirstlane(g != g0 ? 1 : 0);
+            asm volatile("" : "+s"(carry));  // the loop stays one loop
+            each<PHASES - 1>([&](auto f) { phase(f, carry); });
+            // still running at most: the loads of the steps behind the next one
+            if (SLOTS > 2 && (g != g0 || t == first)) wait_vm_and_lds_then_barrier<(SLOTS - 2) * L>();
+            else wait_vm_and_lds_then_barrier<0>();
+            const uint32_t values = g + 1 < g1 ? values_of(g + 1) : (t + gridDim.x < items ? values_of(first_step(t + gridDim.x)) : 64);
+            if (values < 64) clear_excess(next_slot(), values);
+            advance();
+            phase(std::integral_constant<int, PHASES - 1>{}, 0);
+            slot = next_slot();
+        }
+        if constexpr (SLOTS == 2) each<L / 2>([&](auto i) { fetch_part(last_slot(), std::integral_constant<int, i + L / 2>{}); });
+        if constexpr (Out::kLogSum) {
+            constexpr int kCols = FN * 32;
+            const int64_t col0 = cn0 + wn;
+            const int cols = (int)(n - col0 < kCols ? n - col0 : kCols);
+            if (cols > 0) {
+#pragma unroll
+                for (int j = 0; j < FM; ++j) {
+                    const int64_t row = cm0 + wm + j * 32 + l32;
+                    const int64_t label = row < m ? (int64_t)out.label_of(row) - col0 : -1;
+                    const float ninf = -__builtin_inff();
+                    f32x16 v[FN];
+#pragma unroll
+                    for (int i = 0; i < FN; ++i) v[i] = acc[i][j];
+                    if (cols < kCols) {
+#pragma unroll
+                        for (int i = 0; i < FN; ++i)
+#pragma unroll
+                            for (int r = 0; r < 16; ++r)
+                                if (i * 32 + 8 * (r / 4) + 4 * half + r % 4 >= cols) v[i][r] = ninf;
+                    }
+                    if (__any(label >= 0 && label < cols)) {
+#pragma unroll
+                        for (int i = 0; i < FN; ++i)
+#pragma unroll
+                            for (int r = 0; r < 16; ++r)
+                                if (i * 32 + 8 * (r / 4) + 4 * half + r % 4 == label) {
+                                    out.keep(row, v[i][r]);
+                                    v[i][r] = ninf;
+                                }
+                    }
+                    float top = ninf, sum = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < FN; ++i)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) top = fmaxf(top, v[i][r]);
+                    top = fmaxf(top, __shfl_xor(top, 32, kWave));
+                    if (top == ninf) top = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < FN; ++i)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) sum += exp_fast(v[i][r] - top);
+                    sum += __shfl_xor(sum, 32, kWave);
+                    if (half == 0 && row < m) out.put(row, col0 / kCols, top, sum);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        } else {
+            // Out through LDS of this wavefront's own, 32 rows of PIECE fp32 at a time, so that
+            // a lane has 8 columns of a row: chunk c of row r lies at position c ^ (r % chunks).
+            uint8_t* const mine = lds + SLOTS * kSlotBytes + wave * 32 * PIECE * 4;
+            constexpr int kChunks = PIECE / 4, kLanes = PIECE / 8, kFrags = PIECE / 32;
+            const int lr = lane / kLanes, lc = lane % kLanes;
+            float* const part = items_of.splits > 1 ? items_of.part + t / tiles * items_of.stride : nullptr;
+#pragma unroll
+            for (int j = 0; j < FM; ++j) {
+#pragma unroll
+                for (int pc = 0; pc < FN / kFrags; ++pc) {
+#pragma unroll
+                    for (int b = 0; b < kFrags; ++b)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const f32x16& v = acc[pc * kFrags + b][j];
+                            const int c = b * 8 + 2 * q + half;
+                            *reinterpret_cast<f32x4*>(mine + l32 * PIECE * 4 + (c ^ (l32 & (kChunks - 1))) * 16) =
+                                f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+                        }
+                    const int64_t row0 = cm0 + wm + j * 32, col = cn0 + wn + pc * PIECE + lc * 8;
+#pragma nounroll
+                    for (int r = lr; r < 32; r += kWave / kLanes) {
+                        const f32x4 lo = *reinterpret_cast<const f32x4*>(mine + r * PIECE * 4 + ((2 * lc) ^ (r & (kChunks - 1))) * 16);
+                        const f32x4 hi = *reinterpret_cast<const f32x4*>(mine + r * PIECE * 4 + ((2 * lc + 1) ^ (r & (kChunks - 1))) * 16);
+                        float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                        if (row0 + r < m && col < n) {
+                            if (part) store8<true>(part + (row0 + r) * items_of.ld + col, 8, v);
+                            else out(row0 + r, col, v, n - col);
+                        }
+                    }
+                }
+            }
+        }
+    }
+    // nothing may still be on its way into LDS when the workgroup ends
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// Adds the partial sums of the splits, in their order: 8 columns a thread.
+template <class Out>
+__global__ __launch_bounds__(kBlock) void product_join_kernel(Items items, const int32_t* __restrict__ m_at, int64_t m, int64_t n, Out out) {
+    if (m_at) m = (int64_t)*gp(m_at);
+    const int64_t blocks = items.ld / 8, total = m * blocks;
+    out.begin();
+    for (int64_t i = (int64_t)blockIdx.x * kBlock + threadIdx.x; i < total; i += (int64_t)gridDim.x * kBlock) {
+        const int64_t row = i / blocks, col = (i - row * blocks) * 8;
+        if (col >= n) continue;
+        const float* const at = items.part + row * items.ld + col;
+        float v[8];
+        expand(load_raw8<true>(at, 8), v);
+        for (uint32_t s = 1; s < items.splits; ++s) {
+            float w[8];
+            expand(load_raw8<true>(at + s * items.stride, 8), w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += w[e];
+        }
+        out(row, col, v, n - col);
+    }
+}
+
+// The product by the plan that the host logic makes for it; ws: the partial sums of its splits.
+template <class S, bool TALL_A, bool TALL_B, class Out>
+int launch_tiles(const Product16& p, const Plan16& plan, float* ws, const Out& out, hipStream_t st) {
+    const Items items{plan.tiles_n, plan.splits, plan.per_split, ws, plan.ld, plan.stride};
+    const int64_t count = (int64_t)plan.tiles_m * plan.tiles_n * plan.splits, most = kCUs * (S::kWavesPerSimd * 4 / S::WAVES);
+    hipLaunchKernelGGL((product_tile_kernel<S, TALL_A, TALL_B, Out>), dim3((unsigned)(count < most ? count : most)), dim3(S::WAVES * kWave), 0, st,
+                       p, items, out);
+    if constexpr (!Out::kLogSum) {
+        if (plan.splits > 1) {
+            const int64_t groups = div_up(p.m * (plan.ld / 8), kBlock);
+            hipLaunchKernelGGL(product_join_kernel<Out>, dim3((unsigned)(groups < 16 * kCUs ? groups : 16 * kCUs)), dim3(kBlock), 0, st, items,
+                               p.m_at, p.m, p.n, out);
+        }
+    }
+    return launch_status();
+}
+
+// The first `cols` values of each row, and zeros up to ld (a multiple of 8), 8 a thread.
+__global__ __launch_bounds__(kBlock) void pack_rows_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ldx,
+                                                           uint16_t* __restrict__ packed, int64_t ld) {
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (int64_t c = threadIdx.x * 8; c < ld; c += kBlock * 8)
+            *reinterpret_cast<gu32x4*>(gp(packed) + r * ld + c) = load_raw8(x + r * ldx + c, cols - c).w;
+}
+inline int launch_pack(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx, uint16_t* packed, hipStream_t st) {
+    hipLaunchKernelGGL(pack_rows_kernel, dim3((unsigned)(rows < 64 * kCUs ? rows : 64 * kCUs)), dim3(kBlock), 0, st, x, rows, cols, ldx, packed,
+                       packed_ld(cols));
+    return launch_status();
+}
+
+template <bool TALL_A, bool TALL_B, class Out>
+int launch_product(const Product16& p, const Plan16& plan, float* ws, const Out& out, hipStream_t st) {
+    if (p.m == 0 || p.n == 0) return COAT_OK;
+    if (plan.way == Way16::kTile256) return launch_tiles<Tile256, TALL_A, TALL_B>(p, plan, ws, out, st);
+    if (plan.way == Way16::kTile128) return launch_tiles<Tile128, TALL_A, TALL_B>(p, plan, ws, out, st);
+    const int64_t tn = div_up(p.n, 64), tiles = tn * div_up(p.m, 64);
+    if (tiles > 0x7FFFFFFFll * 64) return COAT_EINVAL;
+    const Grid g = grid_xy(tiles, kBlock);
+    hipLaunchKernelGGL((product_plain_kernel<TALL_A, TALL_B, Out>), dim3(g.x, g.y), dim3(kBlock), 0, st, p, (uint32_t)tn, out);
+    return launch_status();
+}
+
+}  // namespace

@@ -1,7 +1,5 @@
 // HIP (gfx950) softmax cross entropy of a vocabulary projection, the logits never stored.
-#include <type_traits>
-
-#include "train_common.h"
+#include "bf16_product.h"
 
 namespace {
 
@@ -190,9 +188,9 @@ __global__ __launch_bounds__(kBlock) void xent_pack_kernel(const uint16_t* __res
 
 extern "C" {
 
-size_t coat_linear_cross_entropy_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols, int32_t) {
+size_t coat_linear_cross_entropy_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols, int32_t aligned) {
     if (tokens < 1 || vocab < 1 || cols < 0 || tokens > kMaxDim || vocab > kMaxDim || cols > kMaxDim) return 0;
-    return xent_layout(tokens, vocab).end;
+    return xent_layout(tokens, vocab, cols, aligned != 0).end;
 }
 
 int coat_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t cols, int64_t ldx, const uint16_t* w, int64_t vocab,
@@ -200,7 +198,8 @@ int coat_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t cols, i
                               size_t workspace_bytes, coat_stream_t stream) {
     int rc = check_xent(x, tokens, cols, ldx, w, vocab, ldw, labels, loss, lse);
     if (rc || tokens == 0) return rc;
-    const XentLayout l = xent_layout(tokens, vocab);
+    const bool ready = tiles_take(x, ldx, cols) && tiles_take(w, ldw, cols);
+    const XentLayout l = xent_layout(tokens, vocab, cols, ready);
     if (!workspace || workspace_bytes < l.end) return COAT_EINVAL;
     if (!aligned(workspace, 256)) return COAT_EALIGN;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
@@ -210,11 +209,17 @@ int coat_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t cols, i
     int32_t* const label = reinterpret_cast<int32_t*>(ws + l.label);
     float* const zt = reinterpret_cast<float*>(ws + l.zt);
     f32x2* const part = reinterpret_cast<f32x2*>(ws + l.part);
+    Product16 p{x, w, ldx, ldw, at, count, nullptr, tokens, vocab, cols};
+    if (!ready && l.plan.way != Way16::kPlain) {
+        uint16_t *const px = reinterpret_cast<uint16_t*>(ws + l.x), *const pw = reinterpret_cast<uint16_t*>(ws + l.w);
+        if ((rc = launch_pack(x, tokens, cols, ldx, px, st)) || (rc = launch_pack(w, vocab, cols, ldw, pw, st))) return rc;
+        p.a = px;
+        p.b = pw;
+        p.lda = p.ldb = packed_ld(cols);
+    }
     hipLaunchKernelGGL(xent_rows_kernel, dim3(1), dim3(kRowsBlock), 0, st, labels, tokens, ignore_index, vocab, count, at, label, zt, loss, lse);
     if ((rc = launch_status())) return rc;
-    rc = launch_product<false, false>(Product16{x, w, ldx, ldw, at, count, nullptr, tokens, vocab, cols},
-                                      LogSumOut{label, zt, part, tokens}, st);
-    if (rc) return rc;
+    if ((rc = launch_product<false, false>(p, l.plan, nullptr, LogSumOut{label, zt, part, tokens}, st))) return rc;
     const int each = tokens >= 32 * kCUs ? 8 : (tokens >= 32 ? 32 : kBlock);
     const int64_t groups = div_up(tokens, kBlock / each);
     hipLaunchKernelGGL(xent_join_kernel, dim3((unsigned)(groups < 16 * kCUs ? groups : 16 * kCUs)), dim3(kBlock), 0, st, part, tokens, l.parts,
@@ -222,9 +227,9 @@ int coat_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t cols, i
     return launch_status();
 }
 
-size_t coat_linear_cross_entropy_backward_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols, int32_t) {
+size_t coat_linear_cross_entropy_backward_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols, int32_t aligned) {
     if (tokens < 1 || vocab < 1 || cols < 0 || tokens > kMaxDim || vocab > kMaxDim || cols > kMaxDim) return 0;
-    return xent_backward_layout(tokens, vocab, cols).end;
+    return xent_backward_layout(tokens, vocab, cols, aligned != 0).end;
 }
 
 int coat_linear_cross_entropy_backward(const uint16_t* x, int64_t tokens, int64_t cols, int64_t ldx, const uint16_t* w, int64_t vocab,
@@ -236,10 +241,11 @@ int coat_linear_cross_entropy_backward(const uint16_t* x, int64_t tokens, int64_
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     if (tokens == 0) {
         if (!dw) return COAT_OK;
-        return launch_product<true, true>(Product16{x, x, 8, 8, nullptr, nullptr, nullptr, vocab, cols, 0},
-                                          ScaledOut{nullptr, 0.0f, nullptr, dw, lddw, nullptr, 0, true}, st);
+        return launch_product<true, true>(Product16{x, x, 8, 8, nullptr, nullptr, nullptr, vocab, cols, 0}, plan16_of(vocab, cols, 0, false),
+                                          nullptr, ScaledOut{nullptr, 0.0f, nullptr, dw, lddw, nullptr, 0, true}, st);
     }
-    const XentBackwardLayout l = xent_backward_layout(tokens, vocab, cols);
+    const bool ready = tiles_take(x, ldx, cols) && tiles_take(w, ldw, cols);
+    const XentBackwardLayout l = xent_backward_layout(tokens, vocab, cols, ready);
     if (!workspace || workspace_bytes < l.end) return COAT_EINVAL;
     if (!aligned(workspace, 256)) return COAT_EALIGN;
     char* const ws = static_cast<char*>(workspace);
@@ -251,26 +257,34 @@ int coat_linear_cross_entropy_backward(const uint16_t* x, int64_t tokens, int64_
     uint16_t* const px = reinterpret_cast<uint16_t*>(ws + l.x);
     uint16_t* const g = reinterpret_cast<uint16_t*>(ws + l.g);
     float* const acc = reinterpret_cast<float*>(ws + l.acc);
+    float* const sums = reinterpret_cast<float*>(ws + l.part);
     hipLaunchKernelGGL(xent_back_rows_kernel, dim3(1), dim3(kRowsBlock), 0, st, labels, tokens, ignore_index, vocab, lse, dloss, dloss_count,
                        count, at, place, info);
     hipLaunchKernelGGL(xent_pack_kernel, dim3((unsigned)(tokens < 64 * kCUs ? tokens : 64 * kCUs)), dim3(kBlock), 0, st, x, tokens, cols, ldx,
                        place, px, l.ld_x, dx, lddx);
     if ((rc = launch_status())) return rc;
+    if (!ready) {
+        uint16_t* const pw = reinterpret_cast<uint16_t*>(ws + l.w);
+        if ((rc = launch_pack(w, vocab, cols, ldw, pw, st))) return rc;
+        w = pw;
+        ldw = packed_ld(cols);
+    }
     for (int64_t v0 = 0; v0 < vocab; v0 += l.piece) {
         const int64_t v1 = v0 + l.piece < vocab ? v0 + l.piece : vocab;
         const uint16_t* const wp = w + v0 * ldw;
-        rc = launch_product<false, false>(Product16{px, wp, l.ld_x, ldw, nullptr, count, nullptr, tokens, v1 - v0, cols},
+        const XentPiece plans = xent_piece_plans(tokens, v1 - v0, cols);
+        rc = launch_product<false, false>(Product16{px, wp, l.ld_x, ldw, nullptr, count, nullptr, tokens, v1 - v0, cols}, plans.logits, sums,
                                           GradOut{info, g, l.ld_g, v0}, st);
         if (rc) return rc;
         if (dx) {
-            rc = launch_product<false, true>(Product16{g, wp, l.ld_g, ldw, nullptr, count, nullptr, tokens, cols, v1 - v0},
+            rc = launch_product<false, true>(Product16{g, wp, l.ld_g, ldw, nullptr, count, nullptr, tokens, cols, v1 - v0}, plans.dx, sums,
                                              ScaledOut{top, 0.0f, at, v1 == vocab ? dx : nullptr, lddx, l.piece < vocab ? acc : nullptr,
                                                        l.ld_x, v0 == 0},
                                              st);
             if (rc) return rc;
         }
         if (dw) {
-            rc = launch_product<true, true>(Product16{g, px, l.ld_g, l.ld_x, nullptr, nullptr, count, v1 - v0, cols, tokens},
+            rc = launch_product<true, true>(Product16{g, px, l.ld_g, l.ld_x, nullptr, nullptr, count, v1 - v0, cols, tokens}, plans.dw, sums,
                                             ScaledOut{top, 0.0f, nullptr, dw + v0 * lddw, lddw, nullptr, 0, true}, st);
             if (rc) return rc;
         }

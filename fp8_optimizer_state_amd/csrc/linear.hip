@@ -1,7 +1,5 @@
 // HIP (gfx950) linear layer with its epilogue, and its backward pass.
-#include <type_traits>
-
-#include "train_common.h"
+#include "bf16_product.h"
 
 namespace {
 
@@ -83,36 +81,53 @@ int launch_dz(const T* dy, int64_t lddy, const uint16_t* z, int64_t ldz, int32_t
 }
 
 template <class T>
-int launch_linear(const Product16& p, const coat_epilogue* e, const void* bias, int32_t bias_type, const void* residual, int64_t ldr,
+int launch_linear(const Product16& p, const Plan16& plan, float* ws, const coat_epilogue* e, const void* bias, int32_t bias_type, const void* residual, int64_t ldr,
                   uint16_t* z, int64_t ldz, void* y, int64_t ldy, hipStream_t st) {
     const uint32_t t = drop_threshold(e->p);
     const LinearOut<T> out{bias, static_cast<const T*>(residual), z, static_cast<T*>(y), ldr, ldz, ldy, div_up(p.n, 8),
                            Drop{e->rng, e->offset, t, 0, 0}, e->scale * drop_factor(t), e->act, bias_type};
-    return launch_product<false, false>(p, out, st);
+    return launch_product<false, false>(p, plan, ws, out, st);
 }
 
 }  // namespace
 
 extern "C" {
 
-size_t coat_linear_workspace_bytes(int64_t, int64_t, int64_t, int32_t) { return 0; }
+size_t coat_linear_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t aligned) {
+    if (m < 1 || n < 1 || k < 1 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return 0;
+    return linear_layout(m, n, k, aligned != 0).end;
+}
 
 int coat_linear(const uint16_t* x, int64_t m, int64_t k, int64_t ldx, const uint16_t* w, int64_t n, int64_t ldw,
                 const coat_epilogue* e, const void* bias, int32_t bias_type, const void* residual, int64_t ldr, uint16_t* z,
                 int64_t ldz, void* y, int64_t ldy, int32_t y_type, void* workspace, size_t workspace_bytes, coat_stream_t stream) {
-    const int rc = check_linear(x, m, k, ldx, w, n, ldw, e, bias, bias_type, residual, ldr, z, ldz, y, ldy, y_type);
+    int rc = check_linear(x, m, k, ldx, w, n, ldw, e, bias, bias_type, residual, ldr, z, ldz, y, ldy, y_type);
     if (rc || m == 0 || n == 0) return rc;
-    (void)workspace;
-    (void)workspace_bytes;
+    const bool ready = tiles_take(x, ldx, k) && tiles_take(w, ldw, k);
+    const size_t need = coat_linear_workspace_bytes(m, n, k, ready);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return COAT_EINVAL;
+        if (!aligned(workspace, 256)) return COAT_EALIGN;
+    }
+    const LinearLayout l = linear_layout(m, n, k, ready);
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-    const Product16 p{x, w, ldx, ldw, nullptr, nullptr, nullptr, m, n, k};
-    if (y_type == COAT_FP32) return launch_linear<float>(p, e, bias, bias_type, residual, ldr, z, ldz, y, ldy, st);
-    return launch_linear<uint16_t>(p, e, bias, bias_type, residual, ldr, z, ldz, y, ldy, st);
+    char* const ws = static_cast<char*>(workspace);
+    Product16 p{x, w, ldx, ldw, nullptr, nullptr, nullptr, m, n, k};
+    if (!ready && l.plan.way != Way16::kPlain) {
+        uint16_t *const px = reinterpret_cast<uint16_t*>(ws + l.x), *const pw = reinterpret_cast<uint16_t*>(ws + l.w);
+        if ((rc = launch_pack(x, m, k, ldx, px, st)) || (rc = launch_pack(w, n, k, ldw, pw, st))) return rc;
+        p.a = px;
+        p.b = pw;
+        p.lda = p.ldb = packed_ld(k);
+    }
+    float* const part = reinterpret_cast<float*>(ws + l.part);
+    if (y_type == COAT_FP32) return launch_linear<float>(p, l.plan, part, e, bias, bias_type, residual, ldr, z, ldz, y, ldy, st);
+    return launch_linear<uint16_t>(p, l.plan, part, e, bias, bias_type, residual, ldr, z, ldz, y, ldy, st);
 }
 
-size_t coat_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t) {
-    if (m < 1 || n < 1 || m > kMaxDim || n > kMaxDim) return 0;
-    return linear_backward_layout(m, n, k).end;
+size_t coat_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t aligned) {
+    if (m < 1 || n < 1 || k < 0 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return 0;
+    return linear_backward_layout(m, n, k, aligned != 0).end;
 }
 
 int coat_linear_backward(const void* dy, int64_t lddy, int32_t dy_type, const uint16_t* x, int64_t m, int64_t k, int64_t ldx,
@@ -121,24 +136,31 @@ int coat_linear_backward(const void* dy, int64_t lddy, int32_t dy_type, const ui
                          size_t workspace_bytes, coat_stream_t stream) {
     int rc = check_linear_backward(dy, lddy, dy_type, x, m, k, ldx, w, n, ldw, e, z, ldz, dx, lddx, dw, lddw, dbias, dbias_type);
     if (rc) return rc;
-    const size_t need = coat_linear_backward_workspace_bytes(m, n, k, 0);
+    const bool ready = tiles_take(x, ldx, k) && tiles_take(w, ldw, k);
+    const size_t need = coat_linear_backward_workspace_bytes(m, n, k, ready);
     if (need > 0) {
         if (!workspace || workspace_bytes < need) return COAT_EINVAL;
         if (!aligned(workspace, 256)) return COAT_EALIGN;
     }
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-    const LinearBackwardLayout l = linear_backward_layout(m, n, k);
+    const LinearBackwardLayout l = linear_backward_layout(m, n, k, ready);
     char* const ws = static_cast<char*>(workspace);
-    uint16_t* const dz = reinterpret_cast<uint16_t*>(ws + l.dz);
+    uint16_t* const dz_made = reinterpret_cast<uint16_t*>(ws + l.dz);
     float* const part = reinterpret_cast<float*>(ws + l.bias);
+    float* const sums = reinterpret_cast<float*>(ws + l.part);
     const uint32_t t = drop_threshold(e->p);
     const Drop drop{e->rng, e->offset, t, 0, 0};
     const float scale = e->scale * drop_factor(t);
-    if (m > 0 && n > 0) {
+    // dy itself is dz up to the factor
+    const bool as_it_is = dy_type == COAT_BF16 && e->act == COAT_ACT_NONE && t == 0 && tiles_take(dy, lddy, n);
+    const uint16_t* const dz = as_it_is ? static_cast<const uint16_t*>(dy) : dz_made;
+    const int64_t ld_dz = as_it_is ? lddy : l.ld_dz;
+    if (m > 0 && n > 0 && (dbias || !as_it_is)) {
+        uint16_t* const to = as_it_is || (!dx && !dw) ? nullptr : dz_made;
         if (dy_type == COAT_FP32)
-            rc = launch_dz(static_cast<const float*>(dy), lddy, z, ldz, e->act, drop, m, n, dz, l.ld_dz, dbias ? part : nullptr, st);
+            rc = launch_dz(static_cast<const float*>(dy), lddy, z, ldz, e->act, drop, m, n, to, l.ld_dz, dbias ? part : nullptr, st);
         else
-            rc = launch_dz(static_cast<const uint16_t*>(dy), lddy, z, ldz, e->act, drop, m, n, dz, l.ld_dz, dbias ? part : nullptr, st);
+            rc = launch_dz(static_cast<const uint16_t*>(dy), lddy, z, ldz, e->act, drop, m, n, to, l.ld_dz, dbias ? part : nullptr, st);
         if (rc) return rc;
     }
     if (dbias && n > 0) {
@@ -151,14 +173,21 @@ int coat_linear_backward(const void* dy, int64_t lddy, int32_t dy_type, const ui
                                static_cast<uint16_t*>(dbias));
         if ((rc = launch_status())) return rc;
     }
+    const bool packs = !ready && m > 0 && n > 0 && k > 0;
     if (dx) {
+        uint16_t* const pw = reinterpret_cast<uint16_t*>(ws + l.w);
+        if (packs && (rc = launch_pack(w, n, k, ldw, pw, st))) return rc;
         const ScaledOut out{nullptr, scale, nullptr, dx, lddx, nullptr, 0, true};
-        rc = launch_product<false, true>(Product16{dz, w, l.ld_dz, ldw, nullptr, nullptr, nullptr, m, k, n}, out, st);
+        rc = launch_product<false, true>(Product16{dz, packs ? pw : w, ld_dz, packs ? packed_ld(k) : ldw, nullptr, nullptr, nullptr, m, k, n},
+                                         l.plan_dx, sums, out, st);
         if (rc) return rc;
     }
     if (dw) {
+        uint16_t* const px = reinterpret_cast<uint16_t*>(ws + l.x);
+        if (packs && (rc = launch_pack(x, m, k, ldx, px, st))) return rc;
         const ScaledOut out{nullptr, scale, nullptr, dw, lddw, nullptr, 0, true};
-        rc = launch_product<true, true>(Product16{dz, x, l.ld_dz, ldx, nullptr, nullptr, nullptr, n, k, m}, out, st);
+        rc = launch_product<true, true>(Product16{dz, packs ? px : x, ld_dz, packs ? packed_ld(k) : ldx, nullptr, nullptr, nullptr, n, k, m},
+                                        l.plan_dw, sums, out, st);
     }
     return rc;
 }

@@ -236,99 +236,4 @@ struct GradOut {
     }
 };
 
-// ------------------------------------------------------------------ the product
-//
-// sum over k of A(i, k) B(j, k), A m x k and B n x k in bf16. An operand's memory has
-// rows of k (k runs along a row), or of i (k is the row: "tall").
-
-struct Product16 {
-    const uint16_t *a, *b;
-    int64_t lda, ldb;       // elements from row to row of memory
-    const int32_t* a_rows;  // row i of A is row a_rows[i] of memory; NULL: row i (not with a tall A)
-    const int32_t* m_at;    // in device memory: the rows of A that exist, at most m; NULL: m
-    const int32_t* k_at;    // the same of k
-    int64_t m, n, k;
-};
-
-__device__ __forceinline__ f32x16 mfma16(const u32x4& b, const u32x4& a, const f32x16& acc) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), acc, 0, 0, 0);
-}
-
-// One matrix instruction takes 32 rows of each operand over 16 values of k: lane l
-// holds the 8 values k = 8 (l / 32) .. of row l % 32. B is the first operand, so that
-// a lane's four consecutive accumulators are four consecutive columns: accumulator r
-// of lane l is row l % 32, column 8 (r / 4) + 4 (l / 32) + r % 4.
-//
-// The plain product, straight from global memory: each wavefront a 32 x 32 tile, a
-// workgroup 64 x 64; any strides and alignments.
-template <bool TALL_A, bool TALL_B, class Out>
-__global__ __launch_bounds__(kBlock) void product_plain_kernel(Product16 p, uint32_t tiles_n, Out out) {
-    __shared__ float lds[kWavesPerBlock][32][33];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int64_t tile = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-    const int64_t m = p.m_at ? (int64_t)*gp(p.m_at) : p.m, k = p.k_at ? (int64_t)*gp(p.k_at) : p.k;
-    const int64_t n0 = tile % tiles_n * 64 + (wave & 1) * 32, m0 = tile / tiles_n * 64 + (wave >> 1) * 32;
-    if (m0 >= m || n0 >= p.n) return;
-    out.begin();
-    const int row = lane & 31, half = lane >> 5;
-    // rows past the end are read as the last one and not used
-    const int64_t ra = m0 + row < m ? m0 + row : m - 1, rb = n0 + row < p.n ? n0 + row : p.n - 1;
-    const int64_t ma = p.a_rows ? (int64_t)gp(p.a_rows)[ra] : ra;
-    const uint16_t* const pa = p.a + (TALL_A ? ra : ma * p.lda);
-    const uint16_t* const pb = p.b + (TALL_B ? rb : rb * p.ldb);
-    f32x16 acc;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-    for (int64_t k0 = 0; k0 < k; k0 += 16) {
-        u32x4 a{0u, 0u, 0u, 0u}, b{0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int64_t at = k0 + half * 8 + e;
-            if (at < k) {
-                a[e / 2] |= (uint32_t)gp(pa)[TALL_A ? at * p.lda : at] << (16 * (e & 1));
-                b[e / 2] |= (uint32_t)gp(pb)[TALL_B ? at * p.ldb : at] << (16 * (e & 1));
-            }
-        }
-        acc = mfma16(b, a, acc);
-    }
-#pragma unroll
-    for (int r = 0; r < 16; ++r) lds[wave][row][8 * (r / 4) + 4 * half + r % 4] = acc[r];
-    __builtin_amdgcn_wave_barrier();
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if constexpr (Out::kLogSum) {
-        static_assert(kLseWidth == 32);
-        if (lane < 32 && m0 + lane < m) {
-            const int64_t label = out.label_of(m0 + lane) - n0;
-            const int cols = (int)(p.n - n0 < 32 ? p.n - n0 : 32);
-            float top = -__builtin_inff(), sum = 0.0f;
-            for (int c = 0; c < cols; ++c)
-                if (c == label) out.keep(m0 + lane, lds[wave][lane][c]);
-                else top = fmaxf(top, lds[wave][lane][c]);
-            const float from = top == -__builtin_inff() ? 0.0f : top;
-            for (int c = 0; c < cols; ++c)
-                if (c != label) sum += exp_fast(lds[wave][lane][c] - from);
-            out.put(m0 + lane, n0 / 32, from, sum);
-        }
-    } else {
-        for (int i = lane; i < 32 * 4; i += kWave) {
-            const int r = i / 4, c = i % 4 * 8;
-            if (m0 + r >= m || n0 + c >= p.n) continue;
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = lds[wave][r][c + e];
-            out(m0 + r, n0 + c, v, p.n - n0 - c);
-        }
-    }
-}
-
-template <bool TALL_A, bool TALL_B, class Out>
-int launch_product(const Product16& p, const Out& out, hipStream_t st) {
-    if (p.m == 0 || p.n == 0) return COAT_OK;
-    const int64_t tn = div_up(p.n, 64), tiles = tn * div_up(p.m, 64);
-    if (tiles > 0x7FFFFFFFll * 64) return COAT_EINVAL;
-    const Grid g = grid_xy(tiles, kBlock);
-    hipLaunchKernelGGL((product_plain_kernel<TALL_A, TALL_B, Out>), dim3(g.x, g.y), dim3(kBlock), 0, st, p, (uint32_t)tn, out);
-    return launch_status();
-}
-
 }  // namespace

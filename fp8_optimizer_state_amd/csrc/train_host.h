@@ -79,24 +79,107 @@ inline int check_dropout(const void* x, int64_t rows, int64_t cols, int64_t ldx,
                         check_optional(residual, rows, cols, ldr, y_type), aligned(rng, 8) ? COAT_OK : COAT_EALIGN});
 }
 
+// ------------------------------------------------------------------ products of bf16 matrices
+
+// How a product m x n over k is computed: in tiles of 256 x 256 or 128 x 128, whose k
+// may be dealt to `splits` workgroups of per_split steps of 64 values (their sums go
+// to the workspace, `stride` apart in rows of ld, and are added by another kernel), or
+// one 32 x 32 tile a wavefront straight from memory.
+enum class Way16 { kPlain, kTile256, kTile128 };
+struct Plan16 {
+    Way16 way;
+    uint32_t tiles_m, tiles_n, splits, per_split;
+    int64_t ld, stride;
+};
+
+constexpr int64_t kMaxLd = int64_t(1) << 22;  // of a tile's operand: 256 rows' bytes stay within 32 bits
+
+// Whether tiles can take an operand as it lies: rows of whole 16-byte chunks.
+inline bool tiles_take(const void* p, int64_t ld, int64_t cols) {
+    return aligned16(p) && ld % 8 == 0 && cols % 8 == 0 && ld < kMaxLd;
+}
+
+inline double tile16_time(int64_t tiles, int64_t m, int64_t ld, int64_t steps, int64_t splits) {
+    const double rounds = (double)div_up(tiles * splits, 2 * kCUs);
+    const double work = rounds * (double)div_up(steps, splits) * 1.0 + 4.0;
+    return splits == 1 ? work : work + 5.0 + 8.0 * (double)splits * (double)m * (double)ld / 3.5e6;
+}
+
+// can_split: the sums of a part of k may leave on their own.
+inline Plan16 plan16_of(int64_t m, int64_t n, int64_t k, bool can_split) {
+    Plan16 p{Way16::kPlain, 0, 0, 1, 0, 0, 0};
+    if (m < 1 || n < 1 || k < 1 || k >= kMaxLd || m > kMaxDim || n > kMaxDim) return p;
+    if (div_up(m, 128) * div_up(n, 128) > 0x3FFFFFFF) return p;
+    const int64_t steps = div_up(k, 64), large = div_up(m, 256) * div_up(n, 256);
+    p.per_split = (uint32_t)steps;
+    if (large >= 160 && m > 128 && n > 128) {
+        p.way = Way16::kTile256;
+        p.tiles_m = (uint32_t)div_up(m, 256);
+        p.tiles_n = (uint32_t)div_up(n, 256);
+        return p;
+    }
+    p.way = Way16::kTile128;
+    p.tiles_m = (uint32_t)div_up(m, 128);
+    p.tiles_n = (uint32_t)div_up(n, 128);
+    if (!can_split) return p;
+    p.ld = div_up(n, 64) * 64;
+    p.stride = m * p.ld;
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    int64_t best = 1;
+    for (int64_t s = 2; s <= steps / 4 && tiles * s <= 2 * kCUs; ++s)
+        if (tile16_time(tiles, m, p.ld, steps, s) < tile16_time(tiles, m, p.ld, steps, best)) best = s;
+    p.per_split = (uint32_t)div_up(steps, best);
+    p.splits = (uint32_t)div_up(steps, p.per_split);
+    return p;
+}
+inline size_t plan16_bytes(const Plan16& p) {
+    return p.splits > 1 ? align_up((size_t)p.splits * (size_t)p.stride * sizeof(float), 256) : 0;
+}
+
+// An operand that tiles do not take is copied to rows of whole 128 bytes first, with
+// zeros behind its columns.
+inline int64_t packed_ld(int64_t cols) { return div_up(cols, 64) * 64; }
+inline size_t packed_bytes(int64_t rows, int64_t cols) { return align_up((size_t)rows * (size_t)packed_ld(cols) * 2, 256); }
+
+struct LinearLayout {
+    Plan16 plan;
+    size_t part, x, w, end;
+};
+inline LinearLayout linear_layout(int64_t m, int64_t n, int64_t k, bool ready) {
+    LinearLayout l;
+    l.plan = plan16_of(m, n, k, true);
+    const bool pack = !ready && l.plan.way != Way16::kPlain;
+    l.part = 0;
+    l.x = plan16_bytes(l.plan);
+    l.w = l.x + (pack ? packed_bytes(m, k) : 0);
+    l.end = l.w + (pack ? packed_bytes(n, k) : 0);
+    return l;
+}
+
 // ------------------------------------------------------------------ backward pass of the linear layer
 
 // Rows whose part of the bias gradient one workgroup adds up.
 constexpr int64_t kBiasRows = 64;
 
-// Workspace of the backward pass: dz in bf16 with rows of whole 128 bytes, the
-// partial sums of the bias gradient.
+// Workspace of the backward pass: dz in bf16 with rows of whole 128 bytes, the partial
+// sums of the bias gradient and of the products, and copies of x and w.
 struct LinearBackwardLayout {
+    Plan16 plan_dx, plan_dw;
     int64_t ld_dz;
-    size_t dz, bias, end;
+    size_t dz, bias, part, x, w, end;
 };
-inline LinearBackwardLayout linear_backward_layout(int64_t m, int64_t n, int64_t k) {
-    (void)k;
+inline LinearBackwardLayout linear_backward_layout(int64_t m, int64_t n, int64_t k, bool ready) {
     LinearBackwardLayout l;
-    l.ld_dz = div_up(n, 64) * 64;
+    l.plan_dx = plan16_of(m, k, n, true);
+    l.plan_dw = plan16_of(n, k, m, true);
+    const size_t dx = plan16_bytes(l.plan_dx), dw = plan16_bytes(l.plan_dw);
+    l.ld_dz = packed_ld(n);
     l.dz = 0;
-    l.bias = align_up((size_t)m * (size_t)l.ld_dz * 2, 256);
-    l.end = l.bias + align_up((size_t)div_up(m, kBiasRows) * (size_t)l.ld_dz * sizeof(float), 256);
+    l.bias = packed_bytes(m, n);
+    l.part = l.bias + align_up((size_t)div_up(m, kBiasRows) * (size_t)l.ld_dz * sizeof(float), 256);
+    l.x = l.part + (dx > dw ? dx : dw);
+    l.w = l.x + (ready ? 0 : packed_bytes(m, k));
+    l.end = l.w + (ready ? 0 : packed_bytes(n, k));
     return l;
 }
 
@@ -119,25 +202,31 @@ inline int check_xent_backward(const void* x, int64_t tokens, int64_t cols, int6
                         check_optional(dw, vocab, cols, lddw, COAT_BF16), aligned(dloss, 4) ? COAT_OK : COAT_EALIGN});
 }
 
-constexpr int64_t kLseWidth = 32;  // columns of a partial log sum
+// Columns of a partial log sum, by the way the logits are computed.
+inline int64_t log_sum_width(Way16 way) { return way == Way16::kTile256 ? 128 : (way == Way16::kTile128 ? 64 : 32); }
 
 // Workspace of the loss: number of tokens that count, their places and labels, the
-// logits of their labels, and a (maximum, sum) for each of them and each part of
-// the vocabulary.
+// logits of their labels, a (maximum, sum) for each of them and each part of the
+// vocabulary, and copies of x and w.
 struct XentLayout {
+    Plan16 plan;
     int64_t parts;
-    size_t count, at, label, zt, part, end;
+    size_t count, at, label, zt, part, x, w, end;
 };
-inline XentLayout xent_layout(int64_t tokens, int64_t vocab) {
+inline XentLayout xent_layout(int64_t tokens, int64_t vocab, int64_t cols, bool ready) {
     XentLayout l;
     const size_t t = (size_t)tokens;
-    l.parts = div_up(vocab, kLseWidth);
+    l.plan = plan16_of(tokens, vocab, cols, false);
+    const bool pack = !ready && l.plan.way != Way16::kPlain;
+    l.parts = div_up(vocab, log_sum_width(l.plan.way));
     l.count = 0;
     l.at = 256;
     l.label = l.at + align_up(t * 4, 256);
     l.zt = l.label + align_up(t * 4, 256);
     l.part = l.zt + align_up(t * 4, 256);
-    l.end = l.part + align_up((size_t)l.parts * t * 8, 256);
+    l.x = l.part + align_up((size_t)l.parts * t * 8, 256);
+    l.w = l.x + (pack ? packed_bytes(tokens, cols) : 0);
+    l.end = l.w + (pack ? packed_bytes(vocab, cols) : 0);
     return l;
 }
 
@@ -153,17 +242,31 @@ inline int64_t xent_piece(int64_t tokens, int64_t vocab) {
 
 // Workspace of the backward pass: number of tokens that count and the largest
 // weight of a loss, the tokens' places in the packed rows and back, what a row of
-// logits needs, the packed rows of x, a piece's gradients, and the sums of dx over pieces.
+// logits needs, the packed rows of x, a piece's gradients, the sums of dx over
+// pieces, the partial sums of products and a copy of w.
 struct XentBackwardLayout {
     int64_t piece, ld_x, ld_g;
-    size_t count, at, place, info, x, g, acc, end;
+    size_t count, at, place, info, x, g, acc, part, w, end;
 };
-inline XentBackwardLayout xent_backward_layout(int64_t tokens, int64_t vocab, int64_t cols) {
+// The products of a piece of `width` columns.
+struct XentPiece {
+    Plan16 logits, dx, dw;
+};
+inline XentPiece xent_piece_plans(int64_t tokens, int64_t width, int64_t cols) {
+    return XentPiece{plan16_of(tokens, width, cols, true), plan16_of(tokens, cols, width, true), plan16_of(width, cols, tokens, true)};
+}
+inline XentBackwardLayout xent_backward_layout(int64_t tokens, int64_t vocab, int64_t cols, bool ready) {
     XentBackwardLayout l;
     const size_t t = (size_t)tokens;
     l.piece = xent_piece(tokens, vocab);
-    l.ld_x = div_up(cols, 64) * 64;
-    l.ld_g = div_up(l.piece, 64) * 64;
+    l.ld_x = packed_ld(cols);
+    l.ld_g = packed_ld(l.piece);
+    size_t part = 0;
+    for (const int64_t width : {l.piece, vocab - (vocab - 1) / l.piece * l.piece}) {
+        const XentPiece p = xent_piece_plans(tokens, width, cols);
+        for (const Plan16& q : {p.logits, p.dx, p.dw})
+            if (plan16_bytes(q) > part) part = plan16_bytes(q);
+    }
     l.count = 0;
     l.at = 256;
     l.place = l.at + align_up(t * 4, 256);
@@ -171,7 +274,9 @@ inline XentBackwardLayout xent_backward_layout(int64_t tokens, int64_t vocab, in
     l.x = l.info + align_up(t * 16, 256);
     l.g = l.x + align_up(t * (size_t)l.ld_x * 2, 256);
     l.acc = l.g + align_up(t * (size_t)l.ld_g * 2, 256);
-    l.end = l.acc + (l.piece < vocab ? align_up(t * (size_t)l.ld_x * 4, 256) : 0);
+    l.part = l.acc + (l.piece < vocab ? align_up(t * (size_t)l.ld_x * 4, 256) : 0);
+    l.w = l.part + part;
+    l.end = l.w + (ready ? 0 : packed_bytes(vocab, cols));
     return l;
 }
 
