@@ -95,12 +95,13 @@ __global__ __launch_bounds__(kBlock) void product_plain_kernel(Product16 p, uint
 //
 // A workgroup of WN x WM wavefronts, each with 32 FN rows of B by 32 FM rows of A,
 // computes tiles one after the other; the k of all its tiles forms one stream of
-// steps of 64 values. A step's values (128 bytes for each row of the tile, B's before
-// A's) go straight from global memory into one of SLOTS slots of LDS, SLOTS steps
-// before they are used. A step is computed in phases of HALVES runs of 16 values:
-// while one phase's matrix instructions run, the next one's fragments are read from
-// LDS. One barrier a step, before its last phase: behind it every wavefront has read
-// the step (its slot may be refilled) and the next one has arrived.
+// steps of 64 values. An operand's part of a step (128 bytes for each row of the tile)
+// goes straight from global memory into one of five parts of LDS, two steps before it
+// is used; the fifth lets the loads run on evenly, and between two tiles the sums leave
+// through it. A step is computed in four phases of 16 values: while one phase's matrix
+// instructions run, the fragments of the one after the next are read from LDS. One
+// barrier a step, in its middle: behind it every wavefront has read the step (its parts
+// may be refilled) and the next one has arrived.
 //
 // In LDS an operand whose k runs along its rows lies as rows of 128 bytes, chunk c of
 // row r at position c ^ (r / 2 % 8), so that 16 rows' reads reach 16 different 16-byte
@@ -118,15 +119,6 @@ __device__ __forceinline__ void load_to_lds16(uint32_t lds, uint32_t off, const 
     asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base), "n"(AT)
                  : "memory", "scc");
 }
-// The same, or nothing if `on` is 0 (one branch within a long run of code).
-template <uint32_t AT>
-__device__ __forceinline__ void load_to_lds16_if(uint32_t on, uint32_t lds, uint32_t off, const uint8_t* base) {
-    asm volatile(
-        "s_cmp_eq_u32 %4, 0\n\ts_cbranch_scc1 .Lskip%=\n\ts_add_u32 m0, %0, %3\n\ts_nop 0\n\t"
-        "global_load_lds_dwordx4 %1, %2\n.Lskip%=:" ::"s"(lds), "v"(off), "s"(base), "n"(AT), "s"(on)
-        : "memory", "scc");
-}
-
 // f(0), f(1), ... f(N - 1) with the index known to the compiler.
 template <int N, int I = 0, class F>
 __device__ __forceinline__ void each(F&& f) {
@@ -150,23 +142,24 @@ struct Items {
     int64_t ld, stride;
 };
 
-template <int WN_, int WM_, int FN_, int FM_, int SLOTS_, int HALVES_, int PIECE_>
+template <int WN_, int WM_, int FN_, int FM_>
 struct TileShape {
-    static constexpr int WN = WN_, WM = WM_, FN = FN_, FM = FM_, SLOTS = SLOTS_, HALVES = HALVES_, PIECE = PIECE_;
-    static constexpr int WAVES = WN * WM, BN = 32 * WN * FN, BM = 32 * WM * FM, kLds = SLOTS * (BN + BM) * 128 + WAVES * 32 * PIECE * 4;
+    static constexpr int WN = WN_, WM = WM_, FN = FN_, FM = FM_, WAVES = WN * WM, BN = 32 * WN * FN, BM = 32 * WM * FM;
+    static constexpr int kPart = BN * 128, kLds = 5 * kPart;  // bytes of an operand's part of a step; of LDS
+    static constexpr int PIECE = kPart / WAVES / 128;         // fp32 columns of 32 rows that a wavefront writes out at a time
     static constexpr int kWavesPerSimd = WAVES / 4 * (kLds <= 81920 ? 2 : 1);
 };
-typedef TileShape<2, 2, 4, 4, 2, 1, 64> Tile256;
-typedef TileShape<2, 2, 2, 2, 2, 2, 32> Tile128;
+typedef TileShape<2, 2, 4, 4> Tile256;
+typedef TileShape<2, 2, 2, 2> Tile128;
 
 template <class S, bool TALL_A, bool TALL_B, class Out>
 __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu(S::kWavesPerSimd, S::kWavesPerSimd))) void product_tile_kernel(
     Product16 p, Items items_of, Out out) {
-    constexpr int WN = S::WN, FN = S::FN, FM = S::FM, SLOTS = S::SLOTS, HALVES = S::HALVES, PIECE = S::PIECE;
-    constexpr int WAVES = S::WAVES, BN = S::BN, BM = S::BM, D = FN + FM, PHASES = 4 / HALVES;
-    constexpr int L = (BN + BM) / 8 / WAVES, LB = BN / 8 / WAVES;  // loads of a step by each wavefront, LB of them B's
-    static_assert(LB * 8 * WAVES == BN && L * 8 * WAVES == BN + BM && L % 2 == 0 && WAVES % 2 == 0 && PHASES >= 2, "loads are dealt evenly");
-    constexpr uint32_t kSlotBytes = (BN + BM) * 128;
+    constexpr int WN = S::WN, FN = S::FN, FM = S::FM, PIECE = S::PIECE;
+    constexpr int WAVES = S::WAVES, BN = S::BN, BM = S::BM;
+    constexpr int LA = BM / 8 / WAVES, LB = BN / 8 / WAVES;  // loads of a step by each wavefront
+    static_assert(BN == BM && LB * 8 * WAVES == BN && LB % 4 == 0 && WAVES % 2 == 0, "loads are dealt evenly");
+    constexpr uint32_t kPart = S::kPart;
     __shared__ __attribute__((aligned(16))) uint8_t lds[S::kLds];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -198,11 +191,12 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
     // Byte offsets of this lane's 16 bytes in each load. What is past the end of the
     // matrix or of k is not read: another row, column or value is fetched in its place,
     // and not used, or zeroed in LDS.
-    uint32_t off[L];
+    uint32_t off_a[LA], off_b[LB];
     auto offsets = [&](int64_t m0, int64_t n0, uint32_t values) __attribute__((always_inline)) {
-        each<L>([&](auto i) {
+        each<LA + LB>([&](auto i) __attribute__((always_inline)) {
             constexpr bool is_b = i < LB, tall = is_b ? TALL_B : TALL_A;
             constexpr int own = is_b ? i : i - LB, width = is_b ? BN : BM;
+            uint32_t& off = is_b ? off_b[is_b ? own : 0] : off_a[is_b ? 0 : own];
             const uint32_t ld2 = (uint32_t)(is_b ? p.ldb : p.lda) * 2;
             const int64_t left = is_b ? n - n0 : m - m0;
             if constexpr (tall) {
@@ -212,13 +206,13 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
                 uint32_t col = (seg * 4 + (at & 3)) * 8;
                 if (col >= left) col = 0;
                 if (row >= values) row = values > 0 ? values - 1 : 0;
-                off[i] = row * ld2 + col * 2;
+                off = row * ld2 + col * 2;
             } else {
                 uint32_t row = (own * WAVES + wave) * 8 + lane / 8, chunk = (lane & 7) ^ ((wave & 1) * 4 + (lane >> 4));
                 if (row >= left) row = (uint32_t)left - 1;
                 if (chunk * 8 >= values) chunk = 0;
-                if (!is_b && p.a_rows) off[i] = (uint32_t)gp(p.a_rows)[m0 + row] * ld2 + chunk * 16;
-                else off[i] = row * ld2 + chunk * 16;
+                if (!is_b && p.a_rows) off = (uint32_t)gp(p.a_rows)[m0 + row] * ld2 + chunk * 16;
+                else off = row * ld2 + chunk * 16;
             }
         });
     };
@@ -229,14 +223,15 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
         next_a = TALL_A ? a + ((int64_t)g * 64 * p.lda + m0) * 2 : a + ((p.a_rows ? 0 : m0 * p.lda) + (int64_t)g * 64) * 2;
     };
     const uint32_t lds_wave = lds0 + wave * 1024;
-    auto fetch_part = [&](int slot, auto i, uint32_t on = 1) __attribute__((always_inline)) {
-        const uint8_t* from = i < LB ? next_b : next_a;
-        if (__builtin_constant_p(on)) load_to_lds16<i * WAVES * 1024>(lds_wave + slot * kSlotBytes, off[i], from);
-        else load_to_lds16_if<i * WAVES * 1024>(on, lds_wave + slot * kSlotBytes, off[i], from);
+    auto fetch_a = [&](int part, auto i) __attribute__((always_inline)) {
+        load_to_lds16<i * WAVES * 1024>(lds_wave + part * kPart, off_a[i], next_a);
+    };
+    auto fetch_b = [&](int part, auto i) __attribute__((always_inline)) {
+        load_to_lds16<i * WAVES * 1024>(lds_wave + part * kPart, off_b[i], next_b);
     };
 
     const int wn = wave % WN * FN * 32, wm = wave / WN * FM * 32;
-    u32x4 fb[2][HALVES][FN], fa[2][HALVES][FM];  // fragments, by parity of the phase
+    u32x4 fb[4][FN], fa[4][FM];  // fragments of the phases
     auto read_one = [&](const uint8_t* base, auto tall, auto width, int w0, int i, int h) __attribute__((always_inline)) {
         if constexpr (tall.value) {
             const int g = lane >> 4, q = lane & 15;
@@ -247,21 +242,18 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
             return *reinterpret_cast<const u32x4*>(base + (w0 + i * 32 + l32) * 128 + ((2 * h + half) ^ ((l32 >> 1) & 7)) * 16);
         }
     };
-    // fragment i of run h of 16 values, A's first, which every row of matrix instructions needs
-    auto read_frag = [&](int slot, int set, int run, int h, int i) __attribute__((always_inline)) {
-        const uint8_t* base = lds + slot * kSlotBytes;
-        if (i < FM) fa[set][run][i] = read_one(base + BN * 128, std::bool_constant<TALL_A>{}, std::integral_constant<int, BM>{}, wm, i, h);
-        else fb[set][run][i - FM] = read_one(base, std::bool_constant<TALL_B>{}, std::integral_constant<int, BN>{}, wn, i - FM, h);
+    // fragment i of phase f, A's first, which every row of matrix instructions needs
+    auto read_frag = [&](int part_a, int part_b, int f, int i) __attribute__((always_inline)) {
+        if (i < FM) fa[f][i] = read_one(lds + part_a * kPart, std::bool_constant<TALL_A>{}, std::integral_constant<int, BM>{}, wm, i, f);
+        else fb[f][i - FM] = read_one(lds + part_b * kPart, std::bool_constant<TALL_B>{}, std::integral_constant<int, BN>{}, wn, i - FM, f);
     };
     // Zeroes what a step of fewer than 64 values has fetched in excess.
-    auto clear_excess = [&](int slot, uint32_t values) __attribute__((always_inline)) {
-        uint8_t* base = lds + slot * kSlotBytes;
+    auto clear_excess = [&](int part_a, int part_b, uint32_t values) __attribute__((always_inline)) {
         const u32x4 none{0u, 0u, 0u, 0u};
-        for (uint32_t c = threadIdx.x; c < (BN + BM) * 8; c += WAVES * kWave) {
-            const bool is_b = c < BN * 8, tall = is_b ? TALL_B : TALL_A;
-            const uint32_t own = is_b ? c : c - BN * 8, lanes = (is_b ? BN : BM) / 8;
-            const uint32_t at = tall ? own / lanes : ((own & 7) ^ (own >> 4 & 7)) * 8;
-            if (at >= values) *reinterpret_cast<u32x4*>(base + c * 16) = none;
+        for (uint32_t c = threadIdx.x; c < BN * 8; c += WAVES * kWave) {
+            const uint32_t tall = c / (BN / 8), wide = ((c & 7) ^ (c >> 4 & 7)) * 8;
+            if ((TALL_A ? tall : wide) >= values) *reinterpret_cast<u32x4*>(lds + part_a * kPart + c * 16) = none;
+            if ((TALL_B ? tall : wide) >= values) *reinterpret_cast<u32x4*>(lds + part_b * kPart + c * 16) = none;
         }
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     };
@@ -291,46 +283,42 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
         offsets(m0, n0, values_of(fg));
         start(m0, n0, fg);
     };
-    // With two slots the last step's later loads follow before the first phase.
-    constexpr int kLast = SLOTS > 2 ? L / 2 : L;
-    each<SLOTS>([&](auto s) {
+    each<2>([&](auto s) __attribute__((always_inline)) {
         if constexpr (s > 0) advance();
-        each<(s + 1 < SLOTS ? L : kLast)>([&](auto i) { fetch_part(s, i); });
+        each<LA>([&](auto i) __attribute__((always_inline)) { fetch_a(2 * s, i); });
+        each<LB>([&](auto i) __attribute__((always_inline)) { fetch_b(2 * s + 1, i); });
     });
     wait_vm_and_lds_then_barrier<0>();
-    if (values_of(first_step(first)) < 64) clear_excess(0, values_of(first_step(first)));
+    if (values_of(first_step(first)) < 64) clear_excess(0, 1, values_of(first_step(first)));
 #pragma unroll
-    for (int r = 0; r < HALVES; ++r)
+    for (int f = 0; f < 2; ++f)
 #pragma unroll
-        for (int i = 0; i < D; ++i) read_frag(0, 0, r, r, i);
-    int slot = 0;
-    auto next_slot = [&] { return SLOTS == 2 ? slot ^ 1 : (slot + 1 < SLOTS ? slot + 1 : 0); };
-    auto last_slot = [&] { return SLOTS == 2 ? slot ^ 1 : (slot > 0 ? slot - 1 : SLOTS - 1); };
+        for (int i = 0; i < FN + FM; ++i) read_frag(0, 1, f, i);
+    // The parts of LDS in the order of their use, from A's of the step in work: A's and
+    // B's of this step and of the next, and a free one.
+    int here = 0;
+    auto ring = [&](int i) __attribute__((always_inline)) { return here + i < 5 ? here + i : here + i - 5; };
 
     f32x16 acc[FN][FM];
     // A phase. A wavefront issues in order, and a matrix instruction occupies its unit
     // for 32 cycles: the few other instructions that the phase needs are dealt out
-    // between them, first the reads of the next phase's fragments, then loads into LDS:
-    // half of a step's in the last phase, the others (carry) in the phase behind that.
-    auto phase = [&](auto f, uint32_t carry) __attribute__((always_inline)) {
-        constexpr int kInstr = HALVES * FN * FM, set = f & 1;
-        constexpr bool last = f == PHASES - 1;
-        constexpr int kReads = HALVES * D, kItems = kReads + (last || f == 0 ? L / 2 : 0);
-        each<kInstr>([&](auto q) {
-            each<(q + 1) * kItems / kInstr - q * kItems / kInstr>([&](auto r) {
+    // between them, first the reads of the fragments for two phases on, then loads. A
+    // compute unit takes a load of 1024 bytes in 16 cycles or more, so that the loads are
+    // spread: A's over the first two phases, B's, which are needed sooner after them,
+    // over the others, three in four in the earlier one.
+    auto phase = [&](auto f) __attribute__((always_inline)) {
+        constexpr int D = FN + FM, kInstr = FN * FM, kFrom = f == 0 || f == 2 ? 0 : (f == 1 ? LA / 2 : LB * 3 / 4);
+        constexpr int kTo = f == 0 ? LA / 2 : (f == 1 ? LA : (f == 2 ? LB * 3 / 4 : LB)), kItems = D + kTo - kFrom;
+        each<kInstr>([&](auto q) __attribute__((always_inline)) {
+            each<(q + 1) * kItems / kInstr - q * kItems / kInstr>([&](auto r) __attribute__((always_inline)) {
                 constexpr int item = q * kItems / kInstr + r;
-                if constexpr (item < kReads) {
-                    constexpr int nf = (f + 1) % PHASES, run = item / D;
-                    read_frag(last ? next_slot() : slot, 1 - set, run, nf * HALVES + run, item % D);
-                } else if constexpr (last) {
-                    fetch_part(slot, std::integral_constant<int, item - kReads>{});
-                } else {
-                    fetch_part(last_slot(), std::integral_constant<int, item - kReads + L / 2>{}, SLOTS > 2 ? 1 : carry);
-                }
+                if constexpr (item < D) read_frag(ring(f < 2 ? 0 : 2), ring(f < 2 ? 1 : 3), (f + 2) % 4, item);
+                else if constexpr (f < 2) fetch_a(ring(4), std::integral_constant<int, kFrom + item - D>{});
+                else fetch_b(ring(0), std::integral_constant<int, kFrom + item - D>{});
             });
             __builtin_amdgcn_sched_barrier(0);
-            constexpr int run = q / (FN * FM), i = q / FM % FN, j = q % FM;
-            acc[i][j] = mfma16(fb[set][run][i], fa[set][run][j], acc[i][j]);
+            constexpr int i = q / FM, j = q % FM;
+            acc[i][j] = mfma16(fb[f][i], fa[f][j], acc[i][j]);
             asm volatile("" : "+a"(acc[i][j]));  // keeps the order
             __builtin_amdgcn_sched_barrier(0);
         });
@@ -347,19 +335,17 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
         const uint32_t g0 = first_step(t), g1 = last_step(t);
 #pragma nounroll
         for (uint32_t g = g0; g < g1; ++g) {
-            uint32_t carry = __builtin_amdgcn_readfirstlane(g != g0 ? 1 : 0);
-            asm volatile("" : "+s"(carry));  // the loop stays one loop
-            each<PHASES - 1>([&](auto f) { phase(f, carry); });
-            // still running at most: the loads of the steps behind the next one
-            if (SLOTS > 2 && (g != g0 || t == first)) wait_vm_and_lds_then_barrier<(SLOTS - 2) * L>();
-            else wait_vm_and_lds_then_barrier<0>();
-            const uint32_t values = g + 1 < g1 ? values_of(g + 1) : (t + gridDim.x < items ? values_of(first_step(t + gridDim.x)) : 64);
-            if (values < 64) clear_excess(next_slot(), values);
             advance();
-            phase(std::integral_constant<int, PHASES - 1>{}, 0);
-            slot = next_slot();
+            phase(std::integral_constant<int, 0>{});
+            phase(std::integral_constant<int, 1>{});
+            // still running at most: A's loads of the step after the next
+            wait_vm_and_lds_then_barrier<LA>();
+            const uint32_t values = g + 1 < g1 ? values_of(g + 1) : (t + gridDim.x < items ? values_of(first_step(t + gridDim.x)) : 64);
+            if (values < 64) clear_excess(ring(2), ring(3), values);
+            phase(std::integral_constant<int, 2>{});
+            phase(std::integral_constant<int, 3>{});
+            here = ring(2);
         }
-        if constexpr (SLOTS == 2) each<L / 2>([&](auto i) { fetch_part(last_slot(), std::integral_constant<int, i + L / 2>{}); });
         if constexpr (Out::kLogSum) {
             constexpr int kCols = FN * 32;
             const int64_t col0 = cn0 + wn;
@@ -409,7 +395,7 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
         } else {
             // Out through LDS of this wavefront's own, 32 rows of PIECE fp32 at a time, so that
             // a lane has 8 columns of a row: chunk c of row r lies at position c ^ (r % chunks).
-            uint8_t* const mine = lds + SLOTS * kSlotBytes + wave * 32 * PIECE * 4;
+            uint8_t* const mine = lds + ring(4) * kPart + wave * 32 * PIECE * 4;
             constexpr int kChunks = PIECE / 4, kLanes = PIECE / 8, kFrags = PIECE / 32;
             const int lr = lane / kLanes, lc = lane % kLanes;
             float* const part = items_of.splits > 1 ? items_of.part + t / tiles * items_of.stride : nullptr;
@@ -439,6 +425,8 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
                     }
                 }
             }
+            // the free part is every wavefront's before the next step is loaded into it
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         }
     }
     // nothing may still be on its way into LDS when the workgroup ends
