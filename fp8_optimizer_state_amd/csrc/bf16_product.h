@@ -223,11 +223,12 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
         next_a = TALL_A ? a + ((int64_t)g * 64 * p.lda + m0) * 2 : a + ((p.a_rows ? 0 : m0 * p.lda) + (int64_t)g * 64) * 2;
     };
     const uint32_t lds_wave = lds0 + wave * 1024;
-    auto fetch_a = [&](int part, auto i) __attribute__((always_inline)) {
-        load_to_lds16<i * WAVES * 1024>(lds_wave + part * kPart, off_a[i], next_a);
+    // `part`: an offset into LDS
+    auto fetch_a = [&](uint32_t part, auto i) __attribute__((always_inline)) {
+        load_to_lds16<i * WAVES * 1024>(lds_wave + part, off_a[i], next_a);
     };
-    auto fetch_b = [&](int part, auto i) __attribute__((always_inline)) {
-        load_to_lds16<i * WAVES * 1024>(lds_wave + part * kPart, off_b[i], next_b);
+    auto fetch_b = [&](uint32_t part, auto i) __attribute__((always_inline)) {
+        load_to_lds16<i * WAVES * 1024>(lds_wave + part, off_b[i], next_b);
     };
 
     const int wn = wave % WN * FN * 32, wm = wave / WN * FM * 32;
@@ -243,17 +244,17 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
         }
     };
     // fragment i of phase f, A's first, which every row of matrix instructions needs
-    auto read_frag = [&](int part_a, int part_b, int f, int i) __attribute__((always_inline)) {
-        if (i < FM) fa[f][i] = read_one(lds + part_a * kPart, std::bool_constant<TALL_A>{}, std::integral_constant<int, BM>{}, wm, i, f);
-        else fb[f][i - FM] = read_one(lds + part_b * kPart, std::bool_constant<TALL_B>{}, std::integral_constant<int, BN>{}, wn, i - FM, f);
+    auto read_frag = [&](uint32_t part_a, uint32_t part_b, int f, int i) __attribute__((always_inline)) {
+        if (i < FM) fa[f][i] = read_one(lds + part_a, std::bool_constant<TALL_A>{}, std::integral_constant<int, BM>{}, wm, i, f);
+        else fb[f][i - FM] = read_one(lds + part_b, std::bool_constant<TALL_B>{}, std::integral_constant<int, BN>{}, wn, i - FM, f);
     };
     // Zeroes what a step of fewer than 64 values has fetched in excess.
-    auto clear_excess = [&](int part_a, int part_b, uint32_t values) __attribute__((always_inline)) {
+    auto clear_excess = [&](uint32_t part_a, uint32_t part_b, uint32_t values) __attribute__((always_inline)) {
         const u32x4 none{0u, 0u, 0u, 0u};
         for (uint32_t c = threadIdx.x; c < BN * 8; c += WAVES * kWave) {
             const uint32_t tall = c / (BN / 8), wide = ((c & 7) ^ (c >> 4 & 7)) * 8;
-            if ((TALL_A ? tall : wide) >= values) *reinterpret_cast<u32x4*>(lds + part_a * kPart + c * 16) = none;
-            if ((TALL_B ? tall : wide) >= values) *reinterpret_cast<u32x4*>(lds + part_b * kPart + c * 16) = none;
+            if ((TALL_A ? tall : wide) >= values) *reinterpret_cast<u32x4*>(lds + part_a + c * 16) = none;
+            if ((TALL_B ? tall : wide) >= values) *reinterpret_cast<u32x4*>(lds + part_b + c * 16) = none;
         }
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     };
@@ -285,19 +286,18 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
     };
     each<2>([&](auto s) __attribute__((always_inline)) {
         if constexpr (s > 0) advance();
-        each<LA>([&](auto i) __attribute__((always_inline)) { fetch_a(2 * s, i); });
-        each<LB>([&](auto i) __attribute__((always_inline)) { fetch_b(2 * s + 1, i); });
+        each<LA>([&](auto i) __attribute__((always_inline)) { fetch_a(2 * s * kPart, i); });
+        each<LB>([&](auto i) __attribute__((always_inline)) { fetch_b((2 * s + 1) * kPart, i); });
     });
     wait_vm_and_lds_then_barrier<0>();
-    if (values_of(first_step(first)) < 64) clear_excess(0, 1, values_of(first_step(first)));
+    if (values_of(first_step(first)) < 64) clear_excess(0, kPart, values_of(first_step(first)));
 #pragma unroll
     for (int f = 0; f < 2; ++f)
 #pragma unroll
-        for (int i = 0; i < FN + FM; ++i) read_frag(0, 1, f, i);
-    // The parts of LDS in the order of their use, from A's of the step in work: A's and
-    // B's of this step and of the next, and a free one.
-    int here = 0;
-    auto ring = [&](int i) __attribute__((always_inline)) { return here + i < 5 ? here + i : here + i - 5; };
+        for (int i = 0; i < FN + FM; ++i) read_frag(0, kPart, f, i);
+    // The parts of LDS in the order of their use: A's and B's of the step in work and of
+    // the next, and a free one.
+    uint32_t ring[5] = {0, kPart, 2 * kPart, 3 * kPart, 4 * kPart};
 
     f32x16 acc[FN][FM];
     // A phase. A wavefront issues in order, and a matrix instruction occupies its unit
@@ -312,9 +312,9 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
         each<kInstr>([&](auto q) __attribute__((always_inline)) {
             each<(q + 1) * kItems / kInstr - q * kItems / kInstr>([&](auto r) __attribute__((always_inline)) {
                 constexpr int item = q * kItems / kInstr + r;
-                if constexpr (item < D) read_frag(ring(f < 2 ? 0 : 2), ring(f < 2 ? 1 : 3), (f + 2) % 4, item);
-                else if constexpr (f < 2) fetch_a(ring(4), std::integral_constant<int, kFrom + item - D>{});
-                else fetch_b(ring(0), std::integral_constant<int, kFrom + item - D>{});
+                if constexpr (item < D) read_frag(ring[f < 2 ? 0 : 2], ring[f < 2 ? 1 : 3], (f + 2) % 4, item);
+                else if constexpr (f < 2) fetch_a(ring[4], std::integral_constant<int, kFrom + item - D>{});
+                else fetch_b(ring[0], std::integral_constant<int, kFrom + item - D>{});
             });
             __builtin_amdgcn_sched_barrier(0);
             constexpr int i = q / FM, j = q % FM;
@@ -332,22 +332,45 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
         int64_t cm0, cn0;
         place(t % tiles, cm0, cn0);
-        const uint32_t g0 = first_step(t), g1 = last_step(t);
-#pragma nounroll
-        for (uint32_t g = g0; g < g1; ++g) {
-            advance();
+        // A step. Scalar work between two phases would let the matrix unit run empty: in the
+        // plain ones, whose fetched step lies 64 whole values on, there is next to none.
+        uint32_t g = first_step(t);
+        const uint32_t g1 = last_step(t);
+        auto step = [&](auto plain) __attribute__((always_inline)) {
+            if constexpr (plain) {
+                next_b += TALL_B ? p.ldb * 128 : 128;
+                next_a += TALL_A ? p.lda * 128 : 128;
+            } else {
+                advance();
+            }
             phase(std::integral_constant<int, 0>{});
             phase(std::integral_constant<int, 1>{});
             // still running at most: A's loads of the step after the next
             wait_vm_and_lds_then_barrier<LA>();
-            const uint32_t values = g + 1 < g1 ? values_of(g + 1) : (t + gridDim.x < items ? values_of(first_step(t + gridDim.x)) : 64);
-            if (values < 64) clear_excess(ring(2), ring(3), values);
+            if constexpr (!plain) {
+                const uint32_t values = g + 1 < g1 ? values_of(g + 1) : (t + gridDim.x < items ? values_of(first_step(t + gridDim.x)) : 64);
+                if (values < 64) clear_excess(ring[2], ring[3], values);
+            }
             phase(std::integral_constant<int, 2>{});
             phase(std::integral_constant<int, 3>{});
-            here = ring(2);
-        }
+            const uint32_t r0 = ring[0], r1 = ring[1];
+            ring[0] = ring[2];
+            ring[1] = ring[3];
+            ring[2] = ring[4];
+            ring[3] = r0;
+            ring[4] = r1;
+        };
+        const uint32_t whole = fg_end == steps && (k & 63) != 0 ? fg_end - 1 : fg_end;
+        uint32_t plain = ft == t && fg + 1 < whole ? whole - 1 - fg : 0;
+        fg += plain;
+        g += plain;
+#pragma nounroll
+        for (; plain > 0; --plain) step(std::true_type{});
+#pragma nounroll
+        for (; g < g1; ++g) step(std::false_type{});
         if constexpr (Out::kLogSum) {
             constexpr int kCols = FN * 32;
+            static_assert(kCols == log_sum_width(BN == 256 ? Way16::kTile256 : Way16::kTile128), "as the workspace is laid out");
             const int64_t col0 = cn0 + wn;
             const int cols = (int)(n - col0 < kCols ? n - col0 : kCols);
             if (cols > 0) {
@@ -395,7 +418,7 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
         } else {
             // Out through LDS of this wavefront's own, 32 rows of PIECE fp32 at a time, so that
             // a lane has 8 columns of a row: chunk c of row r lies at position c ^ (r % chunks).
-            uint8_t* const mine = lds + ring(4) * kPart + wave * 32 * PIECE * 4;
+            uint8_t* const mine = lds + ring[4] + wave * 32 * PIECE * 4;
             constexpr int kChunks = PIECE / 4, kLanes = PIECE / 8, kFrags = PIECE / 32;
             const int lr = lane / kLanes, lc = lane % kLanes;
             float* const part = items_of.splits > 1 ? items_of.part + t / tiles * items_of.stride : nullptr;

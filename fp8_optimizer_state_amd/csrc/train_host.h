@@ -203,7 +203,7 @@ inline int check_xent_backward(const void* x, int64_t tokens, int64_t cols, int6
 }
 
 // Columns of a partial log sum, by the way the logits are computed.
-inline int64_t log_sum_width(Way16 way) { return way == Way16::kTile256 ? 128 : (way == Way16::kTile128 ? 64 : 32); }
+constexpr int64_t log_sum_width(Way16 way) { return way == Way16::kTile256 ? 128 : (way == Way16::kTile128 ? 64 : 32); }
 
 // Workspace of the loss: number of tokens that count, their places and labels, the
 // logits of their labels, a (maximum, sum) for each of them and each part of the
