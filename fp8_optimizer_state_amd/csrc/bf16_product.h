@@ -21,6 +21,17 @@ struct Product16 {
     int64_t m, n, k;
 };
 
+// The same of 16 rows of each operand over 32 values of k: lane l holds the 8 values
+// k = 8 (l / 16) .. of row l % 16; accumulator r of lane l is row l % 16, column
+// 4 (l / 16) + r. Written out, because the compiler moves 64 such accumulators about
+// between accumulation registers. It knows of no wait for it: who reads a result waits,
+// and no vector instruction may have written an operand in the two states before (the
+// fragments come from LDS reads alone; a test looks at the compiled code). Waiting here
+// would cost 5 % (8192 x 8192 x 8192 732 -> 772 us).
+__device__ __forceinline__ void mfma16x16(const u32x4& b, const u32x4& a, f32x4& acc) {
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+}
+
 __device__ __forceinline__ f32x16 mfma16(const u32x4& b, const u32x4& a, const f32x16& acc) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), acc, 0, 0, 0);
 }
@@ -144,13 +155,13 @@ struct Items {
 
 template <int WN_, int WM_, int FN_, int FM_>
 struct TileShape {
-    static constexpr int WN = WN_, WM = WM_, FN = FN_, FM = FM_, WAVES = WN * WM, BN = 32 * WN * FN, BM = 32 * WM * FM;
+    static constexpr int WN = WN_, WM = WM_, FN = FN_, FM = FM_, WAVES = WN * WM, BN = 16 * WN * FN, BM = 16 * WM * FM;
     static constexpr int kPart = BN * 128, kLds = 5 * kPart;  // bytes of an operand's part of a step; of LDS
     static constexpr int PIECE = kPart / WAVES / 128;         // fp32 columns of 32 rows that a wavefront writes out at a time
     static constexpr int kWavesPerSimd = WAVES / 4 * (kLds <= 81920 ? 2 : 1);
 };
-typedef TileShape<2, 2, 4, 4> Tile256;
-typedef TileShape<2, 2, 2, 2> Tile128;
+typedef TileShape<2, 2, 8, 8> Tile256;
+typedef TileShape<2, 2, 4, 4> Tile128;
 
 template <class S, bool TALL_A, bool TALL_B, class Out>
 __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu(S::kWavesPerSimd, S::kWavesPerSimd))) void product_tile_kernel(
@@ -163,7 +174,7 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
     __shared__ __attribute__((aligned(16))) uint8_t lds[S::kLds];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int half = lane >> 5, l32 = lane & 31;
+    const int quad = lane >> 4, l16 = lane & 15;
     const int64_t m = p.m_at ? (int64_t)__builtin_amdgcn_readfirstlane(*gp(p.m_at)) : p.m, n = p.n, k = p.k_at ? (int64_t)__builtin_amdgcn_readfirstlane(*gp(p.k_at)) : p.k;
     const uint32_t tiles_n = items_of.tiles_n, tiles_m = (uint32_t)((m + BM - 1) / BM);
     const uint32_t tiles = tiles_m * tiles_n, items = tiles * items_of.splits;
@@ -202,8 +213,8 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
             if constexpr (tall) {
                 constexpr int lanes = width / 8, rows = kWave / lanes;  // lanes of a row of k, rows of a load
                 uint32_t row = (own * WAVES + wave) * rows + lane / lanes;
-                const uint32_t at = lane % lanes, seg = (at >> 2) ^ (row & 3);
-                uint32_t col = (seg * 4 + (at & 3)) * 8;
+                const uint32_t at = lane % lanes, run = (at >> 1) ^ ((row & 3) * 2 + (row >> 3 & 1));
+                uint32_t col = (run * 2 + (at & 1)) * 8;
                 if (col >= left) col = 0;
                 if (row >= values) row = values > 0 ? values - 1 : 0;
                 off = row * ld2 + col * 2;
@@ -231,16 +242,16 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
         load_to_lds16<i * WAVES * 1024>(lds_wave + part, off_b[i], next_b);
     };
 
-    const int wn = wave % WN * FN * 32, wm = wave / WN * FM * 32;
-    u32x4 fb[4][FN], fa[4][FM];  // fragments of the phases
-    auto read_one = [&](const uint8_t* base, auto tall, auto width, int w0, int i, int h) __attribute__((always_inline)) {
+    const int wn = wave % WN * FN * 16, wm = wave / WN * FM * 16;
+    u32x4 fb[2][FN], fa[2][FM];  // fragments of the phases
+    auto read_one = [&](const uint8_t* base, auto tall, auto width, int w0, int i, int f) __attribute__((always_inline)) {
         if constexpr (tall.value) {
-            const int g = lane >> 4, q = lane & 15;
-            const uint8_t* at = base + (16 * h + 8 * (g >> 1) + (q >> 2)) * (width.value * 2) + ((w0 / 32 + i) ^ (q >> 2)) * 64 + (g & 1) * 32 + (q & 3) * 8;
+            const int row = 32 * f + 8 * quad + (l16 >> 2), run = (w0 / 16 + i) ^ ((l16 >> 2) * 2 + (quad & 1));
+            const uint8_t* at = base + row * (width.value * 2) + run * 32 + (l16 & 3) * 8;
             const u32x2 lo = read_transposed(at), hi = read_transposed(at + 4 * width.value * 2);
             return u32x4{lo[0], lo[1], hi[0], hi[1]};
         } else {
-            return *reinterpret_cast<const u32x4*>(base + (w0 + i * 32 + l32) * 128 + ((2 * h + half) ^ ((l32 >> 1) & 7)) * 16);
+            return *reinterpret_cast<const u32x4*>(base + (w0 + i * 16 + l16) * 128 + ((4 * f + quad) ^ (l16 >> 1)) * 16);
         }
     };
     // fragment i of phase f, A's first, which every row of matrix instructions needs
@@ -292,34 +303,40 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
     wait_vm_and_lds_then_barrier<0>();
     if (values_of(first_step(first)) < 64) clear_excess(0, kPart, values_of(first_step(first)));
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
-#pragma unroll
-        for (int i = 0; i < FN + FM; ++i) read_frag(0, kPart, f, i);
+    for (int i = 0; i < FN + FM; ++i) read_frag(0, kPart, 0, i);
     // The parts of LDS in the order of their use: A's and B's of the step in work and of
     // the next, and a free one.
     uint32_t ring[5] = {0, kPart, 2 * kPart, 3 * kPart, 4 * kPart};
 
-    f32x16 acc[FN][FM];
+    f32x4 acc[FN][FM];
+    // Between what the compiler knows to be done with the accumulators and what it does not.
+    auto settle = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j) asm volatile("" : "+a"(acc[i][j]));
+        asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j) asm volatile("" : "+a"(acc[i][j]));
+    };
     // A phase. A wavefront issues in order, and a matrix instruction occupies its unit
-    // for 32 cycles: the few other instructions that the phase needs are dealt out
-    // between them, first the reads of the fragments for two phases on, then loads. A
-    // compute unit takes a load of 1024 bytes in 16 cycles or more, so that the loads are
-    // spread: A's over the first two phases, B's, which are needed sooner after them,
-    // over the others, three in four in the earlier one.
+    // for 16 cycles: the few other instructions that the phase needs are dealt out
+    // between them, reads of the next phase's fragments and loads, A's of a step in its
+    // first phase and B's in the second.
     auto phase = [&](auto f) __attribute__((always_inline)) {
-        constexpr int D = FN + FM, kInstr = FN * FM, kFrom = f == 0 || f == 2 ? 0 : (f == 1 ? LA / 2 : LB * 3 / 4);
-        constexpr int kTo = f == 0 ? LA / 2 : (f == 1 ? LA : (f == 2 ? LB * 3 / 4 : LB)), kItems = D + kTo - kFrom;
+        constexpr int D = FN + FM, kInstr = FN * FM, kLoads = f == 0 ? LA : LB, kItems = D + kLoads, kRun = D / kLoads + 1;
         each<kInstr>([&](auto q) __attribute__((always_inline)) {
             each<(q + 1) * kItems / kInstr - q * kItems / kInstr>([&](auto r) __attribute__((always_inline)) {
                 constexpr int item = q * kItems / kInstr + r;
-                if constexpr (item < D) read_frag(ring[f < 2 ? 0 : 2], ring[f < 2 ? 1 : 3], (f + 2) % 4, item);
-                else if constexpr (f < 2) fetch_a(ring[4], std::integral_constant<int, kFrom + item - D>{});
-                else fetch_b(ring[0], std::integral_constant<int, kFrom + item - D>{});
+                if constexpr (item % kRun < kRun - 1) read_frag(ring[f == 0 ? 0 : 2], ring[f == 0 ? 1 : 3], 1 - f, item - item / kRun);
+                else if constexpr (f == 0) fetch_a(ring[4], std::integral_constant<int, item / kRun>{});
+                else fetch_b(ring[0], std::integral_constant<int, item / kRun>{});
             });
             __builtin_amdgcn_sched_barrier(0);
             constexpr int i = q / FM, j = q % FM;
-            acc[i][j] = mfma16(fb[f][i], fa[f][j], acc[i][j]);
-            asm volatile("" : "+a"(acc[i][j]));  // keeps the order
+            mfma16x16(fb[f][i], fa[f][j], acc[i][j]);
             __builtin_amdgcn_sched_barrier(0);
         });
     };
@@ -329,7 +346,8 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
 #pragma unroll
             for (int j = 0; j < FM; ++j)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+                for (int r = 0; r < 4; ++r) acc[i][j][r] = 0.0f;
+        settle();
         int64_t cm0, cn0;
         place(t % tiles, cm0, cn0);
         // A step. Scalar work between two phases would let the matrix unit run empty: in the
@@ -344,15 +362,13 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
                 advance();
             }
             phase(std::integral_constant<int, 0>{});
-            phase(std::integral_constant<int, 1>{});
             // still running at most: A's loads of the step after the next
             wait_vm_and_lds_then_barrier<LA>();
             if constexpr (!plain) {
                 const uint32_t values = g + 1 < g1 ? values_of(g + 1) : (t + gridDim.x < items ? values_of(first_step(t + gridDim.x)) : 64);
                 if (values < 64) clear_excess(ring[2], ring[3], values);
             }
-            phase(std::integral_constant<int, 2>{});
-            phase(std::integral_constant<int, 3>{});
+            phase(std::integral_constant<int, 1>{});
             const uint32_t r0 = ring[0], r1 = ring[1];
             ring[0] = ring[2];
             ring[1] = ring[3];
@@ -368,33 +384,34 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
         for (; plain > 0; --plain) step(std::true_type{});
 #pragma nounroll
         for (; g < g1; ++g) step(std::false_type{});
+        settle();
         if constexpr (Out::kLogSum) {
-            constexpr int kCols = FN * 32;
+            constexpr int kCols = FN * 16;
             static_assert(kCols == log_sum_width(BN == 256 ? Way16::kTile256 : Way16::kTile128), "as the workspace is laid out");
             const int64_t col0 = cn0 + wn;
             const int cols = (int)(n - col0 < kCols ? n - col0 : kCols);
             if (cols > 0) {
 #pragma unroll
                 for (int j = 0; j < FM; ++j) {
-                    const int64_t row = cm0 + wm + j * 32 + l32;
+                    const int64_t row = cm0 + wm + j * 16 + l16;
                     const int64_t label = row < m ? (int64_t)out.label_of(row) - col0 : -1;
                     const float ninf = -__builtin_inff();
-                    f32x16 v[FN];
+                    f32x4 v[FN];
 #pragma unroll
                     for (int i = 0; i < FN; ++i) v[i] = acc[i][j];
                     if (cols < kCols) {
 #pragma unroll
                         for (int i = 0; i < FN; ++i)
 #pragma unroll
-                            for (int r = 0; r < 16; ++r)
-                                if (i * 32 + 8 * (r / 4) + 4 * half + r % 4 >= cols) v[i][r] = ninf;
+                            for (int r = 0; r < 4; ++r)
+                                if (i * 16 + 4 * quad + r >= cols) v[i][r] = ninf;
                     }
                     if (__any(label >= 0 && label < cols)) {
 #pragma unroll
                         for (int i = 0; i < FN; ++i)
 #pragma unroll
-                            for (int r = 0; r < 16; ++r)
-                                if (i * 32 + 8 * (r / 4) + 4 * half + r % 4 == label) {
+                            for (int r = 0; r < 4; ++r)
+                                if (i * 16 + 4 * quad + r == label) {
                                     out.keep(row, v[i][r]);
                                     v[i][r] = ninf;
                                 }
@@ -403,15 +420,17 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
 #pragma unroll
                     for (int i = 0; i < FN; ++i)
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) top = fmaxf(top, v[i][r]);
+                        for (int r = 0; r < 4; ++r) top = fmaxf(top, v[i][r]);
+                    top = fmaxf(top, __shfl_xor(top, 16, kWave));
                     top = fmaxf(top, __shfl_xor(top, 32, kWave));
                     if (top == ninf) top = 0.0f;
 #pragma unroll
                     for (int i = 0; i < FN; ++i)
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) sum += exp_fast(v[i][r] - top);
+                        for (int r = 0; r < 4; ++r) sum += exp_fast(v[i][r] - top);
+                    sum += __shfl_xor(sum, 16, kWave);
                     sum += __shfl_xor(sum, 32, kWave);
-                    if (half == 0 && row < m) out.put(row, col0 / kCols, top, sum);
+                    if (quad == 0 && row < m) out.put(row, col0 / kCols, top, sum);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
@@ -419,21 +438,19 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
             // Out through LDS of this wavefront's own, 32 rows of PIECE fp32 at a time, so that
             // a lane has 8 columns of a row: chunk c of row r lies at position c ^ (r % chunks).
             uint8_t* const mine = lds + ring[4] + wave * 32 * PIECE * 4;
-            constexpr int kChunks = PIECE / 4, kLanes = PIECE / 8, kFrags = PIECE / 32;
+            constexpr int kChunks = PIECE / 4, kLanes = PIECE / 8, kFrags = PIECE / 16;
             const int lr = lane / kLanes, lc = lane % kLanes;
             float* const part = items_of.splits > 1 ? items_of.part + t / tiles * items_of.stride : nullptr;
 #pragma unroll
-            for (int j = 0; j < FM; ++j) {
+            for (int j = 0; j < FM / 2; ++j) {
 #pragma unroll
                 for (int pc = 0; pc < FN / kFrags; ++pc) {
 #pragma unroll
-                    for (int b = 0; b < kFrags; ++b)
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const f32x16& v = acc[pc * kFrags + b][j];
-                            const int c = b * 8 + 2 * q + half;
-                            *reinterpret_cast<f32x4*>(mine + l32 * PIECE * 4 + (c ^ (l32 & (kChunks - 1))) * 16) =
-                                f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+                        for (int b = 0; b < kFrags; ++b) {
+                            const int row = h * 16 + l16, c = b * 4 + quad;
+                            *reinterpret_cast<f32x4*>(mine + row * PIECE * 4 + (c ^ (row & (kChunks - 1))) * 16) = acc[pc * kFrags + b][2 * j + h];
                         }
                     const int64_t row0 = cm0 + wm + j * 32, col = cn0 + wn + pc * PIECE + lc * 8;
 #pragma nounroll
