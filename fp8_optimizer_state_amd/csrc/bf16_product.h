@@ -309,17 +309,18 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
     uint32_t ring[5] = {0, kPart, 2 * kPart, 3 * kPart, 4 * kPart};
 
     f32x4 acc[FN][FM];
-    // Between what the compiler knows to be done with the accumulators and what it does not.
+    // Between what the compiler knows to be done with the accumulators and what it does
+    // not; where it reads one again it does so through its own line, one by one.
     auto settle = [&]() __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
             for (int j = 0; j < FM; ++j) asm volatile("" : "+a"(acc[i][j]));
         asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
-#pragma unroll
-        for (int i = 0; i < FN; ++i)
-#pragma unroll
-            for (int j = 0; j < FM; ++j) asm volatile("" : "+a"(acc[i][j]));
+    };
+    auto sums = [&](int i, int j) __attribute__((always_inline)) {
+        asm volatile("" : "+a"(acc[i][j]));
+        return acc[i][j];
     };
     // A phase. A wavefront issues in order, and a matrix instruction occupies its unit
     // for 16 cycles: the few other instructions that the phase needs are dealt out
@@ -398,7 +399,7 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
                     const float ninf = -__builtin_inff();
                     f32x4 v[FN];
 #pragma unroll
-                    for (int i = 0; i < FN; ++i) v[i] = acc[i][j];
+                    for (int i = 0; i < FN; ++i) v[i] = sums(i, j);
                     if (cols < kCols) {
 #pragma unroll
                         for (int i = 0; i < FN; ++i)
@@ -406,15 +407,18 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
                             for (int r = 0; r < 4; ++r)
                                 if (i * 16 + 4 * quad + r >= cols) v[i][r] = ninf;
                     }
-                    if (__any(label >= 0 && label < cols)) {
+                    const bool holds = label >= 0 && label < cols;
+                    if (__any(holds)) {
+                        float own = 0.0f;
 #pragma unroll
                         for (int i = 0; i < FN; ++i)
 #pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                if (i * 16 + 4 * quad + r == label) {
-                                    out.keep(row, v[i][r]);
-                                    v[i][r] = ninf;
-                                }
+                            for (int r = 0; r < 4; ++r) {
+                                const bool hit = i * 16 + 4 * quad + r == label;
+                                own = hit ? v[i][r] : own;
+                                v[i][r] = hit ? ninf : v[i][r];
+                            }
+                        if (holds && quad == (label >> 2 & 3)) out.keep(row, own);
                     }
                     float top = ninf, sum = 0.0f;
 #pragma unroll
@@ -450,7 +454,7 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
 #pragma unroll
                         for (int b = 0; b < kFrags; ++b) {
                             const int row = h * 16 + l16, c = b * 4 + quad;
-                            *reinterpret_cast<f32x4*>(mine + row * PIECE * 4 + (c ^ (row & (kChunks - 1))) * 16) = acc[pc * kFrags + b][2 * j + h];
+                            *reinterpret_cast<f32x4*>(mine + row * PIECE * 4 + (c ^ (row & (kChunks - 1))) * 16) = sums(pc * kFrags + b, 2 * j + h);
                         }
                     const int64_t row0 = cm0 + wm + j * 32, col = cn0 + wn + pc * PIECE + lc * 8;
 #pragma nounroll

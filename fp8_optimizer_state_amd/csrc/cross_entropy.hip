@@ -70,7 +70,7 @@ __global__ __launch_bounds__(kRowsBlock) void xent_rows_kernel(const int64_t* __
 // lse and loss of the tokens that count from their parts: with S the sum of exp(l - M)
 // over all columns but the label's, and d = M - l_label,
 //   loss = log(1 + S exp(d)) = d + log(S + exp(-d)),  lse = l_label + loss.
-// A workgroup takes kBlock / each rows, `each` threads a row.
+// A workgroup takes kBlock / each rows, `each` (a power of two) threads a row.
 __global__ __launch_bounds__(kBlock) void xent_join_kernel(const f32x2* __restrict__ part, int64_t stride, int64_t parts, int each,
                                                            const int32_t* __restrict__ count, const int32_t* __restrict__ at,
                                                            const float* __restrict__ zt, float* __restrict__ loss,
@@ -88,12 +88,15 @@ __global__ __launch_bounds__(kBlock) void xent_join_kernel(const f32x2* __restri
             m = top;
         };
         if (row < rows)
+#pragma unroll 4
             for (int64_t i = threadIdx.x / per; i < parts; i += each) add(reinterpret_cast<const gf32x2*>(gp(part))[i * stride + row]);
-        __syncthreads();
-        sums[threadIdx.x] = f32x2{m, s};
-        __syncthreads();
-        if (threadIdx.x < per && row < rows) {
-            for (int i = 1; i < each; ++i) add(sums[i * per + r]);
+        for (int d = each / 2; d > 0; d /= 2) {
+            __syncthreads();
+            sums[threadIdx.x] = f32x2{m, s};
+            __syncthreads();
+            if ((int)threadIdx.x < d * per) add(sums[threadIdx.x + d * per]);
+        }
+        if ((int)threadIdx.x < per && row < rows) {
             const float l = gp(zt)[row], d = m - l;
             float v, whole;
             if (d > 0.0f) {
@@ -220,7 +223,7 @@ int coat_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t cols, i
     hipLaunchKernelGGL(xent_rows_kernel, dim3(1), dim3(kRowsBlock), 0, st, labels, tokens, ignore_index, vocab, count, at, label, zt, loss, lse);
     if ((rc = launch_status())) return rc;
     if ((rc = launch_product<false, false>(p, l.plan, nullptr, LogSumOut{label, zt, part, tokens}, st))) return rc;
-    const int each = tokens >= 32 * kCUs ? 8 : (tokens >= 32 ? 32 : kBlock);
+    const int each = tokens >= 16 * kCUs ? 16 : (tokens >= 32 ? 32 : kBlock);
     const int64_t groups = div_up(tokens, kBlock / each);
     hipLaunchKernelGGL(xent_join_kernel, dim3((unsigned)(groups < 16 * kCUs ? groups : 16 * kCUs)), dim3(kBlock), 0, st, part, tokens, l.parts,
                        each, count, at, zt, loss, lse);

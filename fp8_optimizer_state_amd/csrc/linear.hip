@@ -6,20 +6,20 @@ namespace {
 // ------------------------------------------------------------------ the gradient before the activation
 //
 // dz = D(dy) act'(z) in bf16, without the factors that the products' sums are multiplied
-// by, and the sums of kBiasRows rows of it as they were before the rounding. A workgroup
-// takes 512 columns of those rows: a thread 8 columns of every fourth row, the four
+// by, and the sums of a band of rows of it as they were before the rounding. A workgroup
+// takes 512 columns of a band: a thread 8 columns of every fourth row, the four
 // rows' sums joined through LDS in order.
 template <class T>
 __global__ __launch_bounds__(kBlock) void dz_kernel(const T* __restrict__ dy, int64_t lddy, const uint16_t* __restrict__ z, int64_t ldz,
                                                     int32_t act, Drop drop, int64_t m, int64_t n, uint16_t* __restrict__ dz,
-                                                    int64_t ld_dz, float* __restrict__ bias_part) {
+                                                    int64_t ld_dz, float* __restrict__ bias_part, int32_t band) {
     __shared__ float sums[kWavesPerBlock][kWave][9];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     drop.begin();
     const int64_t col = ((int64_t)blockIdx.x * kWave + lane) * 8, left = n - col, blocks = (n + 7) / 8;
-    const int64_t r0 = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * kBiasRows;
+    const int64_t r0 = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * band;
     if (r0 >= m) return;
-    const int64_t r1 = r0 + kBiasRows < m ? r0 + kBiasRows : m;
+    const int64_t r1 = r0 + band < m ? r0 + band : m;
     float sum[8] = {};
     if (left > 0) {
         for (int64_t row = r0 + wave; row < r1; row += kWavesPerBlock) {
@@ -54,19 +54,27 @@ __global__ __launch_bounds__(kBlock) void dz_kernel(const T* __restrict__ dy, in
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = (sums[0][lane][i] + sums[1][lane][i]) + (sums[2][lane][i] + sums[3][lane][i]);
-        store8<true>(bias_part + (r0 / kBiasRows) * ld_dz + col, 8, v);
+        store8<true>(bias_part + r0 / band * ld_dz + col, 8, v);
     }
 }
 
-// dbias = scale times the parts' sums, a thread a column.
+// dbias = scale times the parts' sums: a workgroup takes 64 columns, its wavefronts every
+// fourth part.
 template <class T>
 __global__ __launch_bounds__(kBlock) void bias_join_kernel(const float* __restrict__ part, int64_t ld, int64_t parts, int64_t n,
                                                            float scale, T* __restrict__ dbias) {
-    const int64_t col = (int64_t)blockIdx.x * kBlock + threadIdx.x;
-    if (col >= n) return;
+    __shared__ float sums[kWavesPerBlock][kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int64_t col = (int64_t)blockIdx.x * kWave + lane;
     float sum = 0.0f;
-    for (int64_t i = 0; i < parts; ++i) sum += gp(part)[i * ld + col];
-    sum *= scale;
+    if (col < n) {
+#pragma unroll 8
+        for (int64_t i = wave; i < parts; i += kWavesPerBlock) sum += gp(part)[i * ld + col];
+    }
+    sums[wave][lane] = sum;
+    __syncthreads();
+    if (wave != 0 || col >= n) return;
+    sum = ((sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane])) * scale;
     if constexpr (sizeof(T) == 4) gp(dbias)[col] = sum;
     else gp(dbias)[col] = (uint16_t)bf16_bits(sum);
 }
@@ -74,9 +82,10 @@ __global__ __launch_bounds__(kBlock) void bias_join_kernel(const float* __restri
 template <class T>
 int launch_dz(const T* dy, int64_t lddy, const uint16_t* z, int64_t ldz, int32_t act, const Drop& drop, int64_t m, int64_t n, uint16_t* dz,
               int64_t ld_dz, float* part, hipStream_t st) {
-    const int64_t bands = div_up(m, kBiasRows), most = 32768;
+    const int64_t band = bias_band(m, n), bands = div_up(m, band), most = 32768;
     const dim3 grid((unsigned)div_up(n, kWave * 8), (unsigned)(bands < most ? bands : most), (unsigned)div_up(bands, most));
-    hipLaunchKernelGGL(dz_kernel<T>, grid, dim3(kBlock), 0, st, dy, lddy, z, ldz, act, drop, m, n, dz, ld_dz, part);
+    hipLaunchKernelGGL(dz_kernel<T>, grid, dim3(kBlock), 0, st, dy, lddy, z, ldz, act, drop, m, n, dz, ld_dz, part,
+                       (int32_t)band);
     return launch_status();
 }
 
@@ -164,8 +173,8 @@ int coat_linear_backward(const void* dy, int64_t lddy, int32_t dy_type, const ui
         if (rc) return rc;
     }
     if (dbias && n > 0) {
-        const dim3 grid((unsigned)div_up(n, kBlock));
-        const int64_t parts = div_up(m, kBiasRows);
+        const dim3 grid((unsigned)div_up(n, kWave));
+        const int64_t parts = div_up(m, bias_band(m, n));
         if (dbias_type == COAT_FP32)
             hipLaunchKernelGGL(bias_join_kernel<float>, grid, dim3(kBlock), 0, st, part, l.ld_dz, parts, n, scale, static_cast<float*>(dbias));
         else

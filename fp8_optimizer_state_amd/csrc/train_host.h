@@ -158,8 +158,13 @@ inline LinearLayout linear_layout(int64_t m, int64_t n, int64_t k, bool ready) {
 
 // ------------------------------------------------------------------ backward pass of the linear layer
 
-// Rows whose part of the bias gradient one workgroup adds up.
-constexpr int64_t kBiasRows = 64;
+// Rows of a band, whose part of the bias gradient one workgroup adds up: 64, or fewer
+// where those would leave compute units without work (1031 x 2731: 32 us with 64, 9 with 8).
+inline int64_t bias_band(int64_t m, int64_t n) {
+    int64_t band = 64;
+    while (band > 8 && div_up(m, band) * div_up(n, 512) < 4 * kCUs) band /= 2;
+    return band;
+}
 
 // Workspace of the backward pass: dz in bf16 with rows of whole 128 bytes, the partial
 // sums of the bias gradient and of the products, and copies of x and w.
@@ -176,7 +181,7 @@ inline LinearBackwardLayout linear_backward_layout(int64_t m, int64_t n, int64_t
     l.ld_dz = packed_ld(n);
     l.dz = 0;
     l.bias = packed_bytes(m, n);
-    l.part = l.bias + align_up((size_t)div_up(m, kBiasRows) * (size_t)l.ld_dz * sizeof(float), 256);
+    l.part = l.bias + align_up((size_t)div_up(m, bias_band(m, n)) * (size_t)l.ld_dz * sizeof(float), 256);
     l.x = l.part + (dx > dw ? dx : dw);
     l.w = l.x + (ready ? 0 : packed_bytes(m, k));
     l.end = l.w + (ready ? 0 : packed_bytes(n, k));

@@ -125,8 +125,9 @@ def linear_backward(dy, x, w, z, act, f, scale):
     out["dx"] = g, edz @ w.abs() + sum_error(mag, n) + 4 * U32 * mag
     g, mag = product(dz.t(), x.t())
     out["dw"] = g, edz.t() @ x.abs() + sum_error(mag, m) + 4 * U32 * mag
-    # a band's 64 rows are added 16 in a thread and joined, then the bands one by one
-    out["dbias"] = dz.sum(0), exact.sum(0) + U32 * (24 + -(-m // 64)) * dz.abs().sum(0)
+    # a band's rows (8 to 64) are added at most 16 in a thread and joined in 2 more additions,
+    # the bands (m / 8 at most) every fourth in a thread and joined in 2 more, and scaled
+    out["dbias"] = dz.sum(0), exact.sum(0) + U32 * (24 + -(-m // 32)) * dz.abs().sum(0)
     return out
 
 
