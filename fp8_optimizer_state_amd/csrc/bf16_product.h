@@ -36,6 +36,11 @@ __device__ __forceinline__ f32x16 mfma16(const u32x4& b, const u32x4& a, const f
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), acc, 0, 0, 0);
 }
 
+template <class Out>
+__device__ __forceinline__ void finish(const Out& out, int64_t row, int64_t col, float (&v)[8], int64_t n) {
+    out(row, col, v, n, out.column(col, n), out.row(row, col, n));
+}
+
 // One matrix instruction takes 32 rows of each operand over 16 values of k: lane l
 // holds the 8 values k = 8 (l / 32) .. of row l % 32. B is the first operand, so that
 // a lane's four consecutive accumulators are four consecutive columns: accumulator r
@@ -97,7 +102,7 @@ __global__ __launch_bounds__(kBlock) void product_plain_kernel(Product16 p, uint
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = lds[wave][r][c + e];
-            out(m0 + r, n0 + c, v, p.n - n0 - c);
+            finish(out, m0 + r, n0 + c, v, p.n - n0 - c);
         }
     }
 }
@@ -193,7 +198,7 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
         const int64_t left = k - (int64_t)g * 64;
         return (uint32_t)(left < 0 ? 0 : (left < 64 ? left : 64));
     };
-    auto first_step = [&](uint32_t t) __attribute__((always_inline)) { return t / tiles * per_split; };
+    auto first_step = [&](uint32_t t) __attribute__((always_inline)) { return items_of.splits == 1 ? 0 : t / tiles * per_split; };
     auto last_step = [&](uint32_t t) __attribute__((always_inline)) {  // one past it; an item has one step at least
         const uint32_t g0 = first_step(t), g1 = g0 + per_split < steps ? g0 + per_split : steps;
         return g1 > g0 ? g1 : g0 + 1;
@@ -310,7 +315,8 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
 
     f32x4 acc[FN][FM];
     // Between what the compiler knows to be done with the accumulators and what it does
-    // not; where it reads one again it does so through its own line, one by one.
+    // not. Behind that they are read by lines of their own, where they are needed: the
+    // compiler would read all of them first, and spill.
     auto settle = [&]() __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < FN; ++i)
@@ -319,8 +325,14 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
         asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
     };
     auto sums = [&](int i, int j) __attribute__((always_inline)) {
-        asm volatile("" : "+a"(acc[i][j]));
-        return acc[i][j];
+        f32x4 v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float one;
+            asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(one) : "a"(acc[i][j][r]));
+            v[r] = one;
+        }
+        return v;
     };
     // A phase. A wavefront issues in order, and a matrix instruction occupies its unit
     // for 16 cycles: the few other instructions that the phase needs are dealt out
@@ -349,8 +361,8 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[i][j][r] = 0.0f;
         settle();
-        int64_t cm0, cn0;
-        place(t % tiles, cm0, cn0);
+        int64_t cm0 = m0, cn0 = n0;
+        if (ft != t) place(t % tiles, cm0, cn0);
         // A step. Scalar work between two phases would let the matrix unit run empty: in the
         // plain ones, whose fetched step lies 64 whole values on, there is next to none.
         uint32_t g = first_step(t);
@@ -392,10 +404,16 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
             const int64_t col0 = cn0 + wn;
             const int cols = (int)(n - col0 < kCols ? n - col0 : kCols);
             if (cols > 0) {
+                int32_t labels[FM];
 #pragma unroll
                 for (int j = 0; j < FM; ++j) {
                     const int64_t row = cm0 + wm + j * 16 + l16;
-                    const int64_t label = row < m ? (int64_t)out.label_of(row) - col0 : -1;
+                    labels[j] = out.label_of(row < m ? row : m - 1);
+                }
+#pragma unroll
+                for (int j = 0; j < FM; ++j) {
+                    const int64_t row = cm0 + wm + j * 16 + l16;
+                    const int64_t label = row < m ? (int64_t)labels[j] - col0 : -1;
                     const float ninf = -__builtin_inff();
                     f32x4 v[FN];
 #pragma unroll
@@ -442,30 +460,51 @@ __global__ __launch_bounds__(S::WAVES* kWave) __attribute__((amdgpu_waves_per_eu
             // Out through LDS of this wavefront's own, 32 rows of PIECE fp32 at a time, so that
             // a lane has 8 columns of a row: chunk c of row r lies at position c ^ (r % chunks).
             uint8_t* const mine = lds + ring[4] + wave * 32 * PIECE * 4;
-            constexpr int kChunks = PIECE / 4, kLanes = PIECE / 8, kFrags = PIECE / 16;
+            constexpr int kChunks = PIECE / 4, kLanes = PIECE / 8, kFrags = PIECE / 16, kRows = 32 * kLanes / kWave;
+            constexpr int kAcross = FN / kFrags, kPieces = FM / 2 * kAcross;
             const int lr = lane / kLanes, lc = lane % kLanes;
             float* const part = items_of.splits > 1 ? items_of.part + t / tiles * items_of.stride : nullptr;
-#pragma unroll
-            for (int j = 0; j < FM / 2; ++j) {
-#pragma unroll
-                for (int pc = 0; pc < FN / kFrags; ++pc) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int b = 0; b < kFrags; ++b) {
-                            const int row = h * 16 + l16, c = b * 4 + quad;
-                            *reinterpret_cast<f32x4*>(mine + row * PIECE * 4 + (c ^ (row & (kChunks - 1))) * 16) = sums(pc * kFrags + b, 2 * j + h);
-                        }
-                    const int64_t row0 = cm0 + wm + j * 32, col = cn0 + wn + pc * PIECE + lc * 8;
 #pragma nounroll
-                    for (int r = lr; r < 32; r += kWave / kLanes) {
-                        const f32x4 lo = *reinterpret_cast<const f32x4*>(mine + r * PIECE * 4 + ((2 * lc) ^ (r & (kChunks - 1))) * 16);
-                        const f32x4 hi = *reinterpret_cast<const f32x4*>(mine + r * PIECE * 4 + ((2 * lc + 1) ^ (r & (kChunks - 1))) * 16);
-                        float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                        if (row0 + r < m && col < n) {
-                            if (part) store8<true>(part + (row0 + r) * items_of.ld + col, 8, v);
-                            else out(row0 + r, col, v, n - col);
-                        }
+            for (int piece = 0; piece < kPieces; ++piece) {
+                const int64_t row0 = cm0 + wm + piece / kAcross * 32 + lr, col = cn0 + wn + piece % kAcross * PIECE + lc * 8;
+                const bool here = col < n;
+                typename Out::Column column = {};
+                typename Out::Row rows[kRows] = {};
+                if (!part && here) {
+                    column = out.column(col, n - col);
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r)
+                        if (row0 + r * (32 / kRows) < m) rows[r] = out.row(row0 + r * (32 / kRows), col, n - col);
+                }
+                each<kPieces>([&](auto which) __attribute__((always_inline)) {
+                    if (which == piece) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int b = 0; b < kFrags; ++b) {
+                                const int row = h * 16 + l16, c = b * 4 + quad;
+                                *reinterpret_cast<f32x4*>(mine + row * PIECE * 4 + (c ^ (row & (kChunks - 1))) * 16) =
+                                    sums(which % kAcross * kFrags + b, which / kAcross * 2 + h);
+                            }
+                    }
+                });
+                float v[kRows][8];
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    const int row = lr + r * (32 / kRows);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const f32x4 q = *reinterpret_cast<const f32x4*>(mine + row * PIECE * 4 + ((2 * lc + h) ^ (row & (kChunks - 1))) * 16);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[r][4 * h + e] = q[e];
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    const int64_t row = row0 + r * (32 / kRows);
+                    if (here && row < m) {
+                        if (part) store8<true>(part + row * items_of.ld + col, 8, v[r]);
+                        else out(row, col, v[r], n - col, column, rows[r]);
                     }
                 }
             }
@@ -495,7 +534,7 @@ __global__ __launch_bounds__(kBlock) void product_join_kernel(Items items, const
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += w[e];
         }
-        out(row, col, v, n - col);
+        finish(out, row, col, v, n - col);
     }
 }
 

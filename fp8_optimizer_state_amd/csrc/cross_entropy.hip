@@ -245,7 +245,7 @@ int coat_linear_cross_entropy_backward(const uint16_t* x, int64_t tokens, int64_
     if (tokens == 0) {
         if (!dw) return COAT_OK;
         return launch_product<true, true>(Product16{x, x, 8, 8, nullptr, nullptr, nullptr, vocab, cols, 0}, plan16_of(vocab, cols, 0, false),
-                                          nullptr, ScaledOut{nullptr, 0.0f, nullptr, dw, lddw, nullptr, 0, true}, st);
+                                          nullptr, ScaledOut{nullptr, 0.0f, dw, lddw}, st);
     }
     const bool ready = tiles_take(x, ldx, cols) && tiles_take(w, ldw, cols);
     const XentBackwardLayout l = xent_backward_layout(tokens, vocab, cols, ready);
@@ -281,14 +281,12 @@ int coat_linear_cross_entropy_backward(const uint16_t* x, int64_t tokens, int64_
         if (rc) return rc;
         if (dx) {
             rc = launch_product<false, true>(Product16{g, wp, l.ld_g, ldw, nullptr, count, nullptr, tokens, cols, v1 - v0}, plans.dx, sums,
-                                             ScaledOut{top, 0.0f, at, v1 == vocab ? dx : nullptr, lddx, l.piece < vocab ? acc : nullptr,
-                                                       l.ld_x, v0 == 0},
-                                             st);
+                                             PiecesOut{top, at, v1 == vocab ? dx : nullptr, lddx, acc, l.ld_x, v0 == 0, 0.0f}, st);
             if (rc) return rc;
         }
         if (dw) {
             rc = launch_product<true, true>(Product16{g, px, l.ld_g, l.ld_x, nullptr, nullptr, count, v1 - v0, cols, tokens}, plans.dw, sums,
-                                            ScaledOut{top, 0.0f, nullptr, dw + v0 * lddw, lddw, nullptr, 0, true}, st);
+                                            ScaledOut{top, 0.0f, dw + v0 * lddw, lddw}, st);
             if (rc) return rc;
         }
     }

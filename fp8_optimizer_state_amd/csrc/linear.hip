@@ -186,7 +186,7 @@ int coat_linear_backward(const void* dy, int64_t lddy, int32_t dy_type, const ui
     if (dx) {
         uint16_t* const pw = reinterpret_cast<uint16_t*>(ws + l.w);
         if (packs && (rc = launch_pack(w, n, k, ldw, pw, st))) return rc;
-        const ScaledOut out{nullptr, scale, nullptr, dx, lddx, nullptr, 0, true};
+        const ScaledOut out{nullptr, scale, dx, lddx};
         rc = launch_product<false, true>(Product16{dz, packs ? pw : w, ld_dz, packs ? packed_ld(k) : ldw, nullptr, nullptr, nullptr, m, k, n},
                                          l.plan_dx, sums, out, st);
         if (rc) return rc;
@@ -194,7 +194,7 @@ int coat_linear_backward(const void* dy, int64_t lddy, int32_t dy_type, const ui
     if (dw) {
         uint16_t* const px = reinterpret_cast<uint16_t*>(ws + l.x);
         if (packs && (rc = launch_pack(x, m, k, ldx, px, st))) return rc;
-        const ScaledOut out{nullptr, scale, nullptr, dw, lddw, nullptr, 0, true};
+        const ScaledOut out{nullptr, scale, dw, lddw};
         rc = launch_product<true, true>(Product16{dz, packs ? px : x, ld_dz, packs ? packed_ld(k) : ldx, nullptr, nullptr, nullptr, n, k, m},
                                         l.plan_dw, sums, out, st);
     }

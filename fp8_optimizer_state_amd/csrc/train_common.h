@@ -120,7 +120,9 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
 // ------------------------------------------------------------------ epilogues
 //
 // What becomes of a product's sums. A kernel hands over 8 consecutive columns of a
-// row at a time, the first a multiple of 8; n of them exist (n may be over 8).
+// row at a time, the first a multiple of 8; n of them exist (n may be over 8). What it
+// needs from memory for 8 columns (Column) and for them in one row (Row) is loaded apart
+// from that, so that the loads of several rows are under way together.
 
 // y = residual + scale D(act(sum + bias)), z = sum + bias.
 template <class T>
@@ -134,14 +136,26 @@ struct LinearOut {
     Drop drop;
     float scale;  // the dropout's factor in it
     int32_t act, bias_type;
+    struct Column {
+        float b[8];
+    };
+    typedef Raw8<T> Row;
     __device__ void begin() { drop.begin(); }
-    __device__ __forceinline__ void operator()(int64_t row, int64_t col, float (&v)[8], int64_t n) const {
+    __device__ __forceinline__ Column column(int64_t col, int64_t n) const {
+        Column c = {};
         if (bias) {
-            float b[8];
-            if (bias_type == COAT_FP32) expand(load_raw8(static_cast<const float*>(bias) + col, n), b);
-            else expand(load_raw8(static_cast<const uint16_t*>(bias) + col, n), b);
+            if (bias_type == COAT_FP32) expand(load_raw8(static_cast<const float*>(bias) + col, n), c.b);
+            else expand(load_raw8(static_cast<const uint16_t*>(bias) + col, n), c.b);
+        }
+        return c;
+    }
+    __device__ __forceinline__ Row row(int64_t row, int64_t col, int64_t n) const {
+        return residual ? load_raw8(residual + row * ldr + col, n) : Row{};
+    }
+    __device__ __forceinline__ void operator()(int64_t row, int64_t col, float (&v)[8], int64_t n, const Column& c, const Row& raw) const {
+        if (bias) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += b[i];
+            for (int i = 0; i < 8; ++i) v[i] += c.b[i];
         }
         if (z) store8(z + row * ldz + col, n, v);
         with_act(act, [&](auto a) {
@@ -149,9 +163,9 @@ struct LinearOut {
             for (int i = 0; i < 8; ++i) v[i] = activate<a.value>(v[i]);
         });
         if (drop.threshold) drop((uint64_t)(row * blocks + col / 8), v);
-        float r[8] = {};
         if (residual) {
-            expand(load_raw8(residual + row * ldr + col, n), r);
+            float r[8];
+            expand(raw, r);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], scale, r[i]);
         } else {
@@ -162,38 +176,58 @@ struct LinearOut {
     }
 };
 
-// y = scale sum in bf16, on top of the sums of earlier pieces and into those for later
-// ones where there are any; row i of y is row rows[i] of memory.
+// y = scale sum in bf16.
 struct ScaledOut {
     static constexpr bool kLogSum = false;
     const float* scale_at;  // in device memory, or
     float scale;
-    const int32_t* rows;
-    uint16_t* y;  // NULL: not the last piece
+    uint16_t* y;
     int64_t ldy;
-    float* acc;  // NULL: the only piece
-    int64_t lda;
-    bool first;
+    struct Column {};
+    struct Row {};
     __device__ void begin() {
         if (scale_at) scale = *gp(scale_at);
     }
-    __device__ __forceinline__ void operator()(int64_t row, int64_t col, float (&v)[8], int64_t n) const {
-        if (acc) {
-            float* const at = acc + row * lda + col;  // its rows hold whole blocks
-            if (!first) {
-                float a[8];
-                expand(load_raw8<true>(at, 8), a);
+    __device__ __forceinline__ Column column(int64_t, int64_t) const { return Column{}; }
+    __device__ __forceinline__ Row row(int64_t, int64_t, int64_t) const { return Row{}; }
+    __device__ __forceinline__ void operator()(int64_t row, int64_t col, float (&v)[8], int64_t n, const Column&, const Row&) const {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] += a[i];
-            }
-            if (!y) {
-                store8<true>(at, 8, v);
-                return;
-            }
+        for (int i = 0; i < 8; ++i) v[i] *= scale;
+        store8(y + row * ldy + col, n, v);
+    }
+};
+
+// The same of sums that come in pieces: on top of those of earlier pieces, and into
+// those for later ones or, behind the last, to row rows[i] of y for row i.
+struct PiecesOut {
+    static constexpr bool kLogSum = false;
+    const float* scale_at;
+    const int32_t* rows;
+    uint16_t* y;  // NULL: not the last piece
+    int64_t ldy;
+    float* acc;
+    int64_t lda;
+    bool first;
+    float scale;
+    struct Column {};
+    typedef Raw8<float> Row;
+    __device__ void begin() { scale = *gp(scale_at); }
+    __device__ __forceinline__ Column column(int64_t, int64_t) const { return Column{}; }
+    __device__ __forceinline__ Row row(int64_t row, int64_t col, int64_t) const {
+        return first ? Row{} : load_raw8<true>(acc + row * lda + col, 8);  // its rows hold whole blocks
+    }
+    __device__ __forceinline__ void operator()(int64_t row, int64_t col, float (&v)[8], int64_t n, const Column&, const Row& r) const {
+        float a[8];
+        expand(r, a);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += a[i];
+        if (!y) {
+            store8<true>(acc + row * lda + col, 8, v);
+            return;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= scale;
-        store8(y + (rows ? (int64_t)gp(rows)[row] : row) * ldy + col, n, v);
+        store8(y + (int64_t)gp(rows)[row] * ldy + col, n, v);
     }
 };
 
@@ -222,9 +256,12 @@ struct GradOut {
     const f32x4* info;
     uint16_t* g;
     int64_t ldg, col0;  // first column of the piece in the vocabulary
+    struct Column {};
+    typedef f32x4 Row;
     __device__ void begin() {}
-    __device__ __forceinline__ void operator()(int64_t row, int64_t col, float (&v)[8], int64_t n) const {
-        const f32x4 r = reinterpret_cast<const gf32x4*>(gp(info))[row];
+    __device__ __forceinline__ Column column(int64_t, int64_t) const { return Column{}; }
+    __device__ __forceinline__ Row row(int64_t row, int64_t, int64_t) const { return reinterpret_cast<const gf32x4*>(gp(info))[row]; }
+    __device__ __forceinline__ void operator()(int64_t row, int64_t col, float (&v)[8], int64_t n, const Column&, const Row& r) const {
         const float label = r[2];  // a bit cast of an element of a vector would take its first
         const int64_t hit = (int64_t)__builtin_bit_cast(int32_t, label) - col0 - col;
 #pragma unroll

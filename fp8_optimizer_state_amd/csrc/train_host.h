@@ -99,10 +99,24 @@ inline bool tiles_take(const void* p, int64_t ld, int64_t cols) {
     return aligned16(p) && ld % 8 == 0 && cols % 8 == 0 && ld < kMaxLd;
 }
 
-inline double tile16_time(int64_t tiles, int64_t m, int64_t ld, int64_t steps, int64_t splits) {
-    const double rounds = (double)div_up(tiles * splits, 2 * kCUs);
-    const double work = rounds * (double)div_up(steps, splits) * 1.0 + 4.0;
-    return splits == 1 ? work : work + 5.0 + 8.0 * (double)splits * (double)m * (double)ld / 3.5e6;
+// Estimated microseconds of 128 x 128 tiles with their k in `splits` parts: a compute
+// unit takes 0.83 a step of 64 values with two of them, 0.47 with one, and 4.3 a round to
+// begin and end; with splits the partial sums' way out and back on top. Measured:
+// 1500 x 5120 x 13824 (480 tiles, 216 steps) 179, 4096 x 5120 x 5120 (three rounds of 80)
+// 208, 333 x 5120 x 13824 (120 tiles) 104 in one part, 64 in two, 55 in four.
+inline double tile128x_time(int64_t tiles, int64_t m, int64_t ld, int64_t steps, int64_t splits) {
+    const int64_t items = tiles * splits, each = div_up(steps, splits);
+    const double work = items <= kCUs ? 0.47 * (double)each + 4.3 : (double)div_up(items, 2 * kCUs) * (0.83 * (double)each + 4.3);
+    return splits == 1 ? work : work + 4.0 + (double)splits * (double)m * (double)ld / 1e6;
+}
+// The same of 256 x 256 tiles: 1.3 a step with all compute units at work (the card's power
+// sets the clock), 1.0 with half of them, and 14 to write a tile out. Measured: 16384 x
+// 13824 x 5120 (14 rounds of 80) 1629, 4096 x 5120 x 5120 (two rounds) 233, 1023 x 50257
+// x 768 (four rounds of 12) 124 and 100 in small tiles.
+inline double tile256x_time(int64_t tiles, int64_t steps) {
+    const int64_t left = tiles % kCUs;
+    const double step = 0.7 + 0.6 * (left == 0 ? 1.0 : (double)left / kCUs);
+    return (double)(tiles / kCUs) * (1.3 * (double)steps + 14.0) + (left ? (step < 1.0 ? 1.0 : step) * (double)steps + 14.0 : 0.0);
 }
 
 // can_split: the sums of a part of k may leave on their own.
@@ -110,26 +124,26 @@ inline Plan16 plan16_of(int64_t m, int64_t n, int64_t k, bool can_split) {
     Plan16 p{Way16::kPlain, 0, 0, 1, 0, 0, 0};
     if (m < 1 || n < 1 || k < 1 || k >= kMaxLd || m > kMaxDim || n > kMaxDim) return p;
     if (div_up(m, 128) * div_up(n, 128) > 0x3FFFFFFF) return p;
-    const int64_t steps = div_up(k, 64), large = div_up(m, 256) * div_up(n, 256);
-    p.per_split = (uint32_t)steps;
-    if (large >= 160 && m > 128 && n > 128) {
-        p.way = Way16::kTile256;
-        p.tiles_m = (uint32_t)div_up(m, 256);
-        p.tiles_n = (uint32_t)div_up(n, 256);
-        return p;
+    const int64_t steps = div_up(k, 64), large = div_up(m, 256) * div_up(n, 256), tiles = div_up(m, 128) * div_up(n, 128);
+    p.ld = div_up(n, 64) * 64;
+    p.stride = m * p.ld;
+    int64_t best = 1;
+    if (can_split) {
+        for (int64_t s = 2; s <= steps / 4 && tiles * s <= 2 * kCUs; ++s)
+            if (tile128x_time(tiles, m, p.ld, steps, s) < tile128x_time(tiles, m, p.ld, steps, best)) best = s;
     }
+    p.per_split = (uint32_t)div_up(steps, best);
+    p.splits = (uint32_t)div_up(steps, p.per_split);
     p.way = Way16::kTile128;
     p.tiles_m = (uint32_t)div_up(m, 128);
     p.tiles_n = (uint32_t)div_up(n, 128);
-    if (!can_split) return p;
-    p.ld = div_up(n, 64) * 64;
-    p.stride = m * p.ld;
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-    int64_t best = 1;
-    for (int64_t s = 2; s <= steps / 4 && tiles * s <= 2 * kCUs; ++s)
-        if (tile16_time(tiles, m, p.ld, steps, s) < tile16_time(tiles, m, p.ld, steps, best)) best = s;
-    p.per_split = (uint32_t)div_up(steps, best);
-    p.splits = (uint32_t)div_up(steps, p.per_split);
+    if (tile256x_time(large, steps) < tile128x_time(tiles, m, p.ld, steps, best)) {
+        p.way = Way16::kTile256;
+        p.tiles_m = (uint32_t)div_up(m, 256);
+        p.tiles_n = (uint32_t)div_up(n, 256);
+        p.splits = 1;
+        p.per_split = (uint32_t)steps;
+    }
     return p;
 }
 inline size_t plan16_bytes(const Plan16& p) {
