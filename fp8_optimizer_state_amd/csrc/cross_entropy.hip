@@ -213,7 +213,7 @@ int coat_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t cols, i
     float* const zt = reinterpret_cast<float*>(ws + l.zt);
     f32x2* const part = reinterpret_cast<f32x2*>(ws + l.part);
     Product16 p{x, w, ldx, ldw, at, count, nullptr, tokens, vocab, cols};
-    if (!ready && l.plan.way != Way16::kPlain) {
+    if (!ready && l.plan.way != Way16::kPlain && l.plan.way != Way16::kFew) {
         uint16_t *const px = reinterpret_cast<uint16_t*>(ws + l.x), *const pw = reinterpret_cast<uint16_t*>(ws + l.w);
         if ((rc = launch_pack(x, tokens, cols, ldx, px, st)) || (rc = launch_pack(w, vocab, cols, ldw, pw, st))) return rc;
         p.a = px;
@@ -244,7 +244,7 @@ int coat_linear_cross_entropy_backward(const uint16_t* x, int64_t tokens, int64_
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     if (tokens == 0) {
         if (!dw) return COAT_OK;
-        return launch_product<true, true>(Product16{x, x, 8, 8, nullptr, nullptr, nullptr, vocab, cols, 0}, plan16_of(vocab, cols, 0, false),
+        return launch_product<true, true>(Product16{x, x, 8, 8, nullptr, nullptr, nullptr, vocab, cols, 0}, plan16_of(vocab, cols, 0, false, false),
                                           nullptr, ScaledOut{nullptr, 0.0f, dw, lddw}, st);
     }
     const bool ready = tiles_take(x, ldx, cols) && tiles_take(w, ldw, cols);

@@ -122,7 +122,7 @@ int coat_linear(const uint16_t* x, int64_t m, int64_t k, int64_t ldx, const uint
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     char* const ws = static_cast<char*>(workspace);
     Product16 p{x, w, ldx, ldw, nullptr, nullptr, nullptr, m, n, k};
-    if (!ready && l.plan.way != Way16::kPlain) {
+    if (!ready && l.plan.way != Way16::kPlain && l.plan.way != Way16::kFew) {
         uint16_t *const px = reinterpret_cast<uint16_t*>(ws + l.x), *const pw = reinterpret_cast<uint16_t*>(ws + l.w);
         if ((rc = launch_pack(x, m, k, ldx, px, st)) || (rc = launch_pack(w, n, k, ldw, pw, st))) return rc;
         p.a = px;

@@ -83,9 +83,9 @@ inline int check_dropout(const void* x, int64_t rows, int64_t cols, int64_t ldx,
 
 // How a product m x n over k is computed: in tiles of 256 x 256 or 128 x 128, whose k
 // may be dealt to `splits` workgroups of per_split steps of 64 values (their sums go
-// to the workspace, `stride` apart in rows of ld, and are added by another kernel), or
-// one 32 x 32 tile a wavefront straight from memory.
-enum class Way16 { kPlain, kTile256, kTile128 };
+// to the workspace, `stride` apart in rows of ld, and are added by another kernel), in
+// 16 rows of B a workgroup (kFew), or one 32 x 32 tile a wavefront straight from memory.
+enum class Way16 { kPlain, kTile256, kTile128, kFew };
 struct Plan16 {
     Way16 way;
     uint32_t tiles_m, tiles_n, splits, per_split;
@@ -115,14 +115,24 @@ inline double tile128x_time(int64_t tiles, int64_t m, int64_t ld, int64_t steps,
 // x 768 (four rounds of 12) 124 and 100 in small tiles.
 inline double tile256x_time(int64_t tiles, int64_t steps) {
     const int64_t left = tiles % kCUs;
-    const double step = 0.7 + 0.6 * (left == 0 ? 1.0 : (double)left / kCUs);
-    return (double)(tiles / kCUs) * (1.3 * (double)steps + 14.0) + (left ? (step < 1.0 ? 1.0 : step) * (double)steps + 14.0 : 0.0);
+    const double step = tiles > kCUs ? 1.3 : (left <= kCUs / 2 ? 1.0 : 0.7 + 0.6 * (double)left / kCUs);
+    return (double)(tiles / kCUs) * (1.3 * (double)steps + 14.0) + (left ? step * (double)steps + 14.0 : 0.0);
 }
 
-// can_split: the sums of a part of k may leave on their own.
-inline Plan16 plan16_of(int64_t m, int64_t n, int64_t k, bool can_split) {
+// can_split: the sums of a part of k may leave on their own. rows: k runs along both
+// operands' rows.
+inline Plan16 plan16_of(int64_t m, int64_t n, int64_t k, bool can_split, bool rows) {
     Plan16 p{Way16::kPlain, 0, 0, 1, 0, 0, 0};
     if (m < 1 || n < 1 || k < 1 || k >= kMaxLd || m > kMaxDim || n > kMaxDim) return p;
+    // Few rows of A. Each 16 rows of B read all of A again, so that more rows pay only where
+    // B is small: 4 x 13824 x 5120 takes 30 us this way and 29 in tiles, 16 40 and 30, 1 x
+    // 4096 x 4096 9 and 17. Where tiles cannot share k, they pay only if they fill the
+    // card: 1 x 32000 x 4096 takes 52 us and 47, 16 x 13824 x 5120 48 and 52, 16 x 5120 x
+    // 13824 59 and 110.
+    if (rows && m <= 16 && (can_split ? m <= 4 || n * k <= (1 << 24) : n <= 25600)) {
+        p.way = Way16::kFew;
+        return p;
+    }
     if (div_up(m, 128) * div_up(n, 128) > 0x3FFFFFFF) return p;
     const int64_t steps = div_up(k, 64), large = div_up(m, 256) * div_up(n, 256), tiles = div_up(m, 128) * div_up(n, 128);
     p.ld = div_up(n, 64) * 64;
@@ -161,8 +171,8 @@ struct LinearLayout {
 };
 inline LinearLayout linear_layout(int64_t m, int64_t n, int64_t k, bool ready) {
     LinearLayout l;
-    l.plan = plan16_of(m, n, k, true);
-    const bool pack = !ready && l.plan.way != Way16::kPlain;
+    l.plan = plan16_of(m, n, k, true, true);
+    const bool pack = !ready && l.plan.way != Way16::kPlain && l.plan.way != Way16::kFew;
     l.part = 0;
     l.x = plan16_bytes(l.plan);
     l.w = l.x + (pack ? packed_bytes(m, k) : 0);
@@ -189,8 +199,8 @@ struct LinearBackwardLayout {
 };
 inline LinearBackwardLayout linear_backward_layout(int64_t m, int64_t n, int64_t k, bool ready) {
     LinearBackwardLayout l;
-    l.plan_dx = plan16_of(m, k, n, true);
-    l.plan_dw = plan16_of(n, k, m, true);
+    l.plan_dx = plan16_of(m, k, n, true, false);
+    l.plan_dw = plan16_of(n, k, m, true, false);
     const size_t dx = plan16_bytes(l.plan_dx), dw = plan16_bytes(l.plan_dw);
     l.ld_dz = packed_ld(n);
     l.dz = 0;
@@ -222,7 +232,7 @@ inline int check_xent_backward(const void* x, int64_t tokens, int64_t cols, int6
 }
 
 // Columns of a partial log sum, by the way the logits are computed.
-constexpr int64_t log_sum_width(Way16 way) { return way == Way16::kTile256 ? 128 : (way == Way16::kTile128 ? 64 : 32); }
+constexpr int64_t log_sum_width(Way16 way) { return way == Way16::kTile256 ? 128 : (way == Way16::kTile128 ? 64 : (way == Way16::kFew ? 16 : 32)); }
 
 // Workspace of the loss: number of tokens that count, their places and labels, the
 // logits of their labels, a (maximum, sum) for each of them and each part of the
@@ -235,8 +245,8 @@ struct XentLayout {
 inline XentLayout xent_layout(int64_t tokens, int64_t vocab, int64_t cols, bool ready) {
     XentLayout l;
     const size_t t = (size_t)tokens;
-    l.plan = plan16_of(tokens, vocab, cols, false);
-    const bool pack = !ready && l.plan.way != Way16::kPlain;
+    l.plan = plan16_of(tokens, vocab, cols, false, true);
+    const bool pack = !ready && l.plan.way != Way16::kPlain && l.plan.way != Way16::kFew;
     l.parts = div_up(vocab, log_sum_width(l.plan.way));
     l.count = 0;
     l.at = 256;
@@ -272,7 +282,8 @@ struct XentPiece {
     Plan16 logits, dx, dw;
 };
 inline XentPiece xent_piece_plans(int64_t tokens, int64_t width, int64_t cols) {
-    return XentPiece{plan16_of(tokens, width, cols, true), plan16_of(tokens, cols, width, true), plan16_of(width, cols, tokens, true)};
+    return XentPiece{plan16_of(tokens, width, cols, true, true), plan16_of(tokens, cols, width, true, false),
+                     plan16_of(width, cols, tokens, true, false)};
 }
 inline XentBackwardLayout xent_backward_layout(int64_t tokens, int64_t vocab, int64_t cols, bool ready) {
     XentBackwardLayout l;
