@@ -578,7 +578,8 @@ def linear(x, w, y, *, bias=None, act: int = ACT_NONE, z=None, residual=None, sc
 
 
 def linear_workspace_bytes(m: int, n: int, k: int, aligned: bool = True) -> int:
-    """aligned: whether x and w start at multiples of 16 bytes, k and their row strides being multiples of 8."""
+    """aligned: whether x and w start at multiples of 16 bytes, k and their row strides being multiples of 8, the
+    strides under 2^22."""
     return lib().coat_linear_workspace_bytes(m, n, k, aligned)
 
 
@@ -657,7 +658,7 @@ def _xent_operands(x, w, labels, gpu: int):
     xp, ldx = _matrix(x, torch.bfloat16, (tokens, cols), gpu, "x")
     wp, ldw = _matrix(w, torch.bfloat16, (vocab, cols), gpu, "w")
     return (xp, tokens, cols, ldx, wp, vocab, ldw, _operand(labels, torch.int64, (tokens,), gpu, "labels"),
-            _is_aligned(xp, ldx, cols) and _is_aligned(wp, ldw, cols))
+            _is_aligned(xp, ldx, cols) and _is_aligned(wp, ldw, cols) and tokens * ldx < 1 << 31)
 
 
 def _index64(ignore_index: int) -> int:
@@ -687,7 +688,8 @@ def linear_cross_entropy(x, w, labels, loss, lse, *, ignore_index: int = -100, w
 
 
 def linear_cross_entropy_workspace_bytes(tokens: int, vocab: int, cols: int, aligned: bool = True) -> int:
-    """aligned: whether x and w start at multiples of 16 bytes, cols and their row strides being multiples of 8."""
+    """aligned: whether x and w start at multiples of 16 bytes, cols and their row strides being multiples of 8, the
+    strides under 2^22 and x under 2^31 elements long."""
     return lib().coat_linear_cross_entropy_workspace_bytes(tokens, vocab, cols, aligned)
 
 

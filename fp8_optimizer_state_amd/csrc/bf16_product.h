@@ -644,16 +644,22 @@ int launch_tiles(const Product16& p, const Plan16& plan, float* ws, const Out& o
     return launch_status();
 }
 
-// The first `cols` values of each row, and zeros up to ld (a multiple of 8), 8 a thread.
+// The first `cols` values of each row, and zeros up to ld (a multiple of 8), 8 a thread:
+// of rows at[0] .. at[*count - 1], if they are given.
 __global__ __launch_bounds__(kBlock) void pack_rows_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ldx,
+                                                           const int32_t* __restrict__ at, const int32_t* __restrict__ count,
                                                            uint16_t* __restrict__ packed, int64_t ld) {
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+    if (count) rows = (int64_t)*gp(count);
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const uint16_t* const from = x + (at ? (int64_t)gp(at)[r] : r) * ldx;
         for (int64_t c = threadIdx.x * 8; c < ld; c += kBlock * 8)
-            *reinterpret_cast<gu32x4*>(gp(packed) + r * ld + c) = load_raw8(x + r * ldx + c, cols - c).w;
+            *reinterpret_cast<gu32x4*>(gp(packed) + r * ld + c) = load_raw8(from + c, cols - c).w;
+    }
 }
-inline int launch_pack(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx, uint16_t* packed, hipStream_t st) {
-    hipLaunchKernelGGL(pack_rows_kernel, dim3((unsigned)(rows < 64 * kCUs ? rows : 64 * kCUs)), dim3(kBlock), 0, st, x, rows, cols, ldx, packed,
-                       packed_ld(cols));
+inline int launch_pack(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx, const int32_t* at, const int32_t* count, uint16_t* packed,
+                       hipStream_t st) {
+    hipLaunchKernelGGL(pack_rows_kernel, dim3((unsigned)(rows < 64 * kCUs ? rows : 64 * kCUs)), dim3(kBlock), 0, st, x, rows, cols, ldx, at, count,
+                       packed, packed_ld(cols));
     return launch_status();
 }
 

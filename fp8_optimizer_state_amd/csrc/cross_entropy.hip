@@ -201,7 +201,7 @@ int coat_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t cols, i
                               size_t workspace_bytes, coat_stream_t stream) {
     int rc = check_xent(x, tokens, cols, ldx, w, vocab, ldw, labels, loss, lse);
     if (rc || tokens == 0) return rc;
-    const bool ready = tiles_take(x, ldx, cols) && tiles_take(w, ldw, cols);
+    const bool ready = tiles_gather(x, tokens, ldx, cols) && tiles_take(w, ldw, cols);
     const XentLayout l = xent_layout(tokens, vocab, cols, ready);
     if (!workspace || workspace_bytes < l.end) return COAT_EINVAL;
     if (!aligned(workspace, 256)) return COAT_EALIGN;
@@ -213,15 +213,17 @@ int coat_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t cols, i
     float* const zt = reinterpret_cast<float*>(ws + l.zt);
     f32x2* const part = reinterpret_cast<f32x2*>(ws + l.part);
     Product16 p{x, w, ldx, ldw, at, count, nullptr, tokens, vocab, cols};
+    hipLaunchKernelGGL(xent_rows_kernel, dim3(1), dim3(kRowsBlock), 0, st, labels, tokens, ignore_index, vocab, count, at, label, zt, loss, lse);
+    if ((rc = launch_status())) return rc;
     if (!ready && l.plan.way != Way16::kPlain && l.plan.way != Way16::kFew) {
         uint16_t *const px = reinterpret_cast<uint16_t*>(ws + l.x), *const pw = reinterpret_cast<uint16_t*>(ws + l.w);
-        if ((rc = launch_pack(x, tokens, cols, ldx, px, st)) || (rc = launch_pack(w, vocab, cols, ldw, pw, st))) return rc;
+        if ((rc = launch_pack(x, tokens, cols, ldx, at, count, px, st)) || (rc = launch_pack(w, vocab, cols, ldw, nullptr, nullptr, pw, st)))
+            return rc;
         p.a = px;
         p.b = pw;
         p.lda = p.ldb = packed_ld(cols);
+        p.a_rows = nullptr;
     }
-    hipLaunchKernelGGL(xent_rows_kernel, dim3(1), dim3(kRowsBlock), 0, st, labels, tokens, ignore_index, vocab, count, at, label, zt, loss, lse);
-    if ((rc = launch_status())) return rc;
     if ((rc = launch_product<false, false>(p, l.plan, nullptr, LogSumOut{label, zt, part, tokens}, st))) return rc;
     const int each = tokens >= 16 * kCUs ? 16 : (tokens >= 32 ? 32 : kBlock);
     const int64_t groups = div_up(tokens, kBlock / each);
@@ -244,10 +246,10 @@ int coat_linear_cross_entropy_backward(const uint16_t* x, int64_t tokens, int64_
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     if (tokens == 0) {
         if (!dw) return COAT_OK;
-        return launch_product<true, true>(Product16{x, x, 8, 8, nullptr, nullptr, nullptr, vocab, cols, 0}, plan16_of(vocab, cols, 0, false, false),
+        return launch_product<true, true>(Product16{x, x, 8, 8, nullptr, nullptr, nullptr, vocab, cols, 0}, plan16_of(vocab, cols, 0, false, true, true),
                                           nullptr, ScaledOut{nullptr, 0.0f, dw, lddw}, st);
     }
-    const bool ready = tiles_take(x, ldx, cols) && tiles_take(w, ldw, cols);
+    const bool ready = tiles_gather(x, tokens, ldx, cols) && tiles_take(w, ldw, cols);
     const XentBackwardLayout l = xent_backward_layout(tokens, vocab, cols, ready);
     if (!workspace || workspace_bytes < l.end) return COAT_EINVAL;
     if (!aligned(workspace, 256)) return COAT_EALIGN;
@@ -268,7 +270,7 @@ int coat_linear_cross_entropy_backward(const uint16_t* x, int64_t tokens, int64_
     if ((rc = launch_status())) return rc;
     if (!ready) {
         uint16_t* const pw = reinterpret_cast<uint16_t*>(ws + l.w);
-        if ((rc = launch_pack(w, vocab, cols, ldw, pw, st))) return rc;
+        if ((rc = launch_pack(w, vocab, cols, ldw, nullptr, nullptr, pw, st))) return rc;
         w = pw;
         ldw = packed_ld(cols);
     }

@@ -65,7 +65,7 @@ __global__ __launch_bounds__(kBlock) void bias_join_kernel(const float* __restri
                                                            float scale, T* __restrict__ dbias) {
     __shared__ float sums[kWavesPerBlock][kWave];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int64_t col = (int64_t)blockIdx.x * kWave + lane;
+    const int64_t col = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kWave + lane;
     float sum = 0.0f;
     if (col < n) {
 #pragma unroll 8
@@ -93,8 +93,11 @@ template <class T>
 int launch_linear(const Product16& p, const Plan16& plan, float* ws, const coat_epilogue* e, const void* bias, int32_t bias_type, const void* residual, int64_t ldr,
                   uint16_t* z, int64_t ldz, void* y, int64_t ldy, hipStream_t st) {
     const uint32_t t = drop_threshold(e->p);
+    // Large outputs of whole lines in bf16: 16384 x 13824 x 5120 with z 1870 -> 1784 us. Small
+    // ones stay in the caches for who reads them next.
+    auto past = [&](const void* to, int64_t ld) { return aligned(to, 128) && ld % 64 == 0 && p.m * p.n >= (int64_t(1) << 25); };
     const LinearOut<T> out{bias, static_cast<const T*>(residual), z, static_cast<T*>(y), ldr, ldz, ldy, div_up(p.n, 8),
-                           Drop{e->rng, e->offset, t, 0, 0}, e->scale * drop_factor(t), e->act, bias_type};
+                           Drop{e->rng, e->offset, t, 0, 0}, e->scale * drop_factor(t), e->act, bias_type, past(y, ldy), past(z, ldz)};
     return launch_product<false, false>(p, plan, ws, out, st);
 }
 
@@ -124,7 +127,7 @@ int coat_linear(const uint16_t* x, int64_t m, int64_t k, int64_t ldx, const uint
     Product16 p{x, w, ldx, ldw, nullptr, nullptr, nullptr, m, n, k};
     if (!ready && l.plan.way != Way16::kPlain && l.plan.way != Way16::kFew) {
         uint16_t *const px = reinterpret_cast<uint16_t*>(ws + l.x), *const pw = reinterpret_cast<uint16_t*>(ws + l.w);
-        if ((rc = launch_pack(x, m, k, ldx, px, st)) || (rc = launch_pack(w, n, k, ldw, pw, st))) return rc;
+        if ((rc = launch_pack(x, m, k, ldx, nullptr, nullptr, px, st)) || (rc = launch_pack(w, n, k, ldw, nullptr, nullptr, pw, st))) return rc;
         p.a = px;
         p.b = pw;
         p.lda = p.ldb = packed_ld(k);
@@ -173,7 +176,8 @@ int coat_linear_backward(const void* dy, int64_t lddy, int32_t dy_type, const ui
         if (rc) return rc;
     }
     if (dbias && n > 0) {
-        const dim3 grid((unsigned)div_up(n, kWave));
+        const Grid g = grid_xy(div_up(n, kWave), kBlock);
+        const dim3 grid(g.x, g.y);
         const int64_t parts = div_up(m, bias_band(m, n));
         if (dbias_type == COAT_FP32)
             hipLaunchKernelGGL(bias_join_kernel<float>, grid, dim3(kBlock), 0, st, part, l.ld_dz, parts, n, scale, static_cast<float*>(dbias));
@@ -185,7 +189,7 @@ int coat_linear_backward(const void* dy, int64_t lddy, int32_t dy_type, const ui
     const bool packs = !ready && m > 0 && n > 0 && k > 0;
     if (dx) {
         uint16_t* const pw = reinterpret_cast<uint16_t*>(ws + l.w);
-        if (packs && (rc = launch_pack(w, n, k, ldw, pw, st))) return rc;
+        if (packs && (rc = launch_pack(w, n, k, ldw, nullptr, nullptr, pw, st))) return rc;
         const ScaledOut out{nullptr, scale, dx, lddx};
         rc = launch_product<false, true>(Product16{dz, packs ? pw : w, ld_dz, packs ? packed_ld(k) : ldw, nullptr, nullptr, nullptr, m, k, n},
                                          l.plan_dx, sums, out, st);
@@ -193,7 +197,7 @@ int coat_linear_backward(const void* dy, int64_t lddy, int32_t dy_type, const ui
     }
     if (dw) {
         uint16_t* const px = reinterpret_cast<uint16_t*>(ws + l.x);
-        if (packs && (rc = launch_pack(x, m, k, ldx, px, st))) return rc;
+        if (packs && (rc = launch_pack(x, m, k, ldx, nullptr, nullptr, px, st))) return rc;
         const ScaledOut out{nullptr, scale, dw, lddw};
         rc = launch_product<true, true>(Product16{dz, packs ? px : x, ld_dz, packs ? packed_ld(k) : ldx, nullptr, nullptr, nullptr, n, k, m},
                                         l.plan_dw, sums, out, st);

@@ -117,6 +117,18 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
     }
 }
 
+// 8 columns past the caches' usual order where whole lines leave for memory anyway, and
+// would drive the operands out of them.
+__device__ __forceinline__ void store8_past(bool past, uint16_t* p, int64_t n, const float (&v)[8]) {
+    if (past && n >= 8) {
+        const u32x4 w{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
+        __builtin_nontemporal_store(w, reinterpret_cast<gu32x4_a2*>(gp(p)));
+    } else {
+        store8(p, n, v);
+    }
+}
+__device__ __forceinline__ void store8_past(bool, float* p, int64_t n, const float (&v)[8]) { store8(p, n, v); }
+
 // ------------------------------------------------------------------ epilogues
 //
 // What becomes of a product's sums. A kernel hands over 8 consecutive columns of a
@@ -136,6 +148,7 @@ struct LinearOut {
     Drop drop;
     float scale;  // the dropout's factor in it
     int32_t act, bias_type;
+    bool y_past, z_past;
     struct Column {
         float b[8];
     };
@@ -157,7 +170,7 @@ struct LinearOut {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] += c.b[i];
         }
-        if (z) store8(z + row * ldz + col, n, v);
+        if (z) store8_past(z_past, z + row * ldz + col, n, v);
         with_act(act, [&](auto a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = activate<a.value>(v[i]);
@@ -172,7 +185,7 @@ struct LinearOut {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] *= scale;
         }
-        store8(y + row * ldy + col, n, v);
+        store8_past(y_past, y + row * ldy + col, n, v);
     }
 };
 

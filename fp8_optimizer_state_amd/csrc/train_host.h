@@ -119,11 +119,13 @@ inline double tile256x_time(int64_t tiles, int64_t steps) {
     return (double)(tiles / kCUs) * (1.3 * (double)steps + 14.0) + (left ? step * (double)steps + 14.0 : 0.0);
 }
 
-// can_split: the sums of a part of k may leave on their own. rows: k runs along both
-// operands' rows.
-inline Plan16 plan16_of(int64_t m, int64_t n, int64_t k, bool can_split, bool rows) {
+// can_split: the sums of a part of k may leave on their own. tall_a, tall_b: an operand
+// whose rows in memory are those of k.
+inline Plan16 plan16_of(int64_t m, int64_t n, int64_t k, bool can_split, bool tall_a, bool tall_b) {
     Plan16 p{Way16::kPlain, 0, 0, 1, 0, 0, 0};
-    if (m < 1 || n < 1 || k < 1 || k >= kMaxLd || m > kMaxDim || n > kMaxDim) return p;
+    if (m < 1 || n < 1 || k < 1 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return p;
+    if ((tall_a ? m : k) >= kMaxLd || (tall_b ? n : k) >= kMaxLd) return p;
+    const bool rows = !tall_a && !tall_b;
     // Few rows of A. Each 16 rows of B read all of A again, so that more rows pay only where
     // B is small: 4 x 13824 x 5120 takes 30 us this way and 29 in tiles, 16 40 and 30, 1 x
     // 4096 x 4096 9 and 17. Where tiles cannot share k, they pay only if they fill the
@@ -171,7 +173,7 @@ struct LinearLayout {
 };
 inline LinearLayout linear_layout(int64_t m, int64_t n, int64_t k, bool ready) {
     LinearLayout l;
-    l.plan = plan16_of(m, n, k, true, true);
+    l.plan = plan16_of(m, n, k, true, false, false);
     const bool pack = !ready && l.plan.way != Way16::kPlain && l.plan.way != Way16::kFew;
     l.part = 0;
     l.x = plan16_bytes(l.plan);
@@ -199,8 +201,8 @@ struct LinearBackwardLayout {
 };
 inline LinearBackwardLayout linear_backward_layout(int64_t m, int64_t n, int64_t k, bool ready) {
     LinearBackwardLayout l;
-    l.plan_dx = plan16_of(m, k, n, true, false);
-    l.plan_dw = plan16_of(n, k, m, true, false);
+    l.plan_dx = plan16_of(m, k, n, true, false, true);
+    l.plan_dw = plan16_of(n, k, m, true, true, true);
     const size_t dx = plan16_bytes(l.plan_dx), dw = plan16_bytes(l.plan_dw);
     l.ld_dz = packed_ld(n);
     l.dz = 0;
@@ -245,7 +247,7 @@ struct XentLayout {
 inline XentLayout xent_layout(int64_t tokens, int64_t vocab, int64_t cols, bool ready) {
     XentLayout l;
     const size_t t = (size_t)tokens;
-    l.plan = plan16_of(tokens, vocab, cols, false, true);
+    l.plan = plan16_of(tokens, vocab, cols, false, false, false);
     const bool pack = !ready && l.plan.way != Way16::kPlain && l.plan.way != Way16::kFew;
     l.parts = div_up(vocab, log_sum_width(l.plan.way));
     l.count = 0;
@@ -259,12 +261,19 @@ inline XentLayout xent_layout(int64_t tokens, int64_t vocab, int64_t cols, bool 
     return l;
 }
 
+// Whether the loss's tiles can gather x's rows as they lie: their byte offsets have 32 bits.
+inline bool tiles_gather(const void* x, int64_t tokens, int64_t ldx, int64_t cols) {
+    return tiles_take(x, ldx, cols) && tokens * ldx < (int64_t(1) << 31);
+}
+
 // Columns of the vocabulary that the backward pass takes at a time. The gradients of
-// a piece's logits are 2^26 numbers (128 MB, half of the last cache) or 2048
-// columns wide; pieces are of equal size.
+// a piece's logits are 2^27 numbers (256 MB) or 2048 columns wide; pieces are of equal
+// size. 8192 x 32000 x 5120 takes 6300 us in pieces of 2^26, 5900 of 2^27 and 5740 of
+// 2^28, which would be all of its logits.
 inline int64_t xent_piece(int64_t tokens, int64_t vocab) {
-    int64_t most = ((int64_t)1 << 26) / (tokens > 0 ? tokens : 1) / 256 * 256;
+    int64_t most = ((int64_t)1 << 27) / (tokens > 0 ? tokens : 1) / 256 * 256;
     if (most < 2048) most = 2048;
+    if (most > kMaxLd / 2) most = kMaxLd / 2;
     if (most >= vocab) return vocab;
     return div_up(div_up(vocab, div_up(vocab, most)), 256) * 256;
 }
@@ -282,8 +291,8 @@ struct XentPiece {
     Plan16 logits, dx, dw;
 };
 inline XentPiece xent_piece_plans(int64_t tokens, int64_t width, int64_t cols) {
-    return XentPiece{plan16_of(tokens, width, cols, true, true), plan16_of(tokens, cols, width, true, false),
-                     plan16_of(width, cols, tokens, true, false)};
+    return XentPiece{plan16_of(tokens, width, cols, true, false, false), plan16_of(tokens, cols, width, true, false, true),
+                     plan16_of(width, cols, tokens, true, true, true)};
 }
 inline XentBackwardLayout xent_backward_layout(int64_t tokens, int64_t vocab, int64_t cols, bool ready) {
     XentBackwardLayout l;

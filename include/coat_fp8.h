@@ -431,7 +431,8 @@ typedef struct coat_epilogue {
  *   workspace  device memory, 256-byte aligned, at least
  *          coat_linear_workspace_bytes(m, n, k, aligned) bytes (may be NULL if that
  *          is 0); calls that may overlap in time need one each. aligned: whether x
- *          and w are 16-byte aligned and k, ldx and ldw multiples of 8.
+ *          and w are 16-byte aligned and k, ldx and ldw multiples of 8, ldx and ldw
+ *          under 2^22.
  * m = 0 or n = 0 writes nothing; k = 0 gives z = bias.
  */
 size_t coat_linear_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t aligned);
@@ -484,7 +485,8 @@ int coat_dropout(const void* x, int64_t rows, int64_t cols, int64_t ldx, int32_t
  *   loss, lse  tokens fp32, out
  * The logits are sums in fp32 and are not rounded further.
  *   workspace  as above, coat_linear_cross_entropy_workspace_bytes(tokens, vocab,
- *          cols, aligned); aligned: whether x and w are, as for the linear layer.
+ *          cols, aligned); aligned: whether x and w are, as for the linear layer, and
+ *          tokens ldx is under 2^31.
  */
 size_t coat_linear_cross_entropy_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols, int32_t aligned);
 int coat_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t cols, int64_t ldx, const uint16_t* w,

@@ -95,6 +95,26 @@ def test_linear_many_tiles():
     run_linear(4200, 4300, 96, "relu", 0.0, F32, 6, sample=(0, 300))
 
 
+@pytest.mark.parametrize("size,pad,shift", [((8100, 4090, 1600), (0, 0, 0), 0), ((4090, 8190, 2003), (0, 0, 1), 0), ((8192, 4096, 1536), (8, 0, 0), 8),
+                                            ((4300, 12288, 1032), (0, 0, 0), 0)])
+def test_large_tiles(size, pad, shift):
+    """Sizes whose products are made in large tiles, several of them a workgroup, with edges and a short last step."""
+    m, n, k = size
+    run_linear(m, n, k, "gelu", 0.0, BF16, 5, pad=pad, shift=shift, sample=(m - 70, m))
+    run_linear(m, n, k, "silu", 0.0, F32, 6, pad=pad, shift=shift, sample=(200, 300))
+    x, w, _, _, _ = inputs(m, n, k, 7, BF16, False, False)
+    dy = torch.randn(m, n, generator=gen(8)).to(BF16)
+    dx, dw = torch.empty(m, k, dtype=BF16, device=DEV), torch.empty(n, k, dtype=BF16, device=DEV)
+    db = torch.empty(n, device=DEV)
+    coat.linear_backward(strided(dy, n + pad[0], shift), strided(x, k + pad[1], shift), strided(w, k + pad[1], shift), dx, dw, db, scale=0.5)
+    D, X, W = (t.to(DEV).double() for t in (dy, x, w))
+    for got, want, terms in ((dx, 0.5 * (D @ W), 0.5 * (D.abs() @ W.abs())),
+                             (dw, 0.5 * (D.t().contiguous() @ X), 0.5 * (D.abs().t().contiguous() @ X.abs()))):
+        depth = n if got is dx else m
+        ref.check("gradient", got, want.cpu(), (ref.sum_error(terms, depth) + 4 * ref.U32 * terms).cpu())
+    assert float((db.double() - 0.5 * D.sum(0)).abs().max()) < 1e-3
+
+
 def test_linear_extremes():
     """No columns of x, no rows, and what NaN and Inf reach."""
     x, w, b, r, rng = inputs(4, 24, 16, 1, F32)
