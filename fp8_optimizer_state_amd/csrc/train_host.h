@@ -128,10 +128,10 @@ inline Plan16 plan16_of(int64_t m, int64_t n, int64_t k, bool can_split, bool ta
     const bool rows = !tall_a && !tall_b;
     // Few rows of A. Each 16 rows of B read all of A again, so that more rows pay only where
     // B is small: 4 x 13824 x 5120 takes 30 us this way and 29 in tiles, 16 40 and 30, 1 x
-    // 4096 x 4096 9 and 17. Where tiles cannot share k, they pay only if they fill the
-    // card: 1 x 32000 x 4096 takes 52 us and 47, 16 x 13824 x 5120 48 and 52, 16 x 5120 x
-    // 13824 59 and 110.
-    if (rows && m <= 16 && (can_split ? m <= 4 || n * k <= (1 << 24) : n <= 25600)) {
+    // 4096 x 4096 9 and 17. Where tiles cannot share k they pay later: the loss of 1 x
+    // 32000 x 4096 takes 57 us and 72, of 16 x 32000 x 4096 71 and 54, of 16 x 13824 x 5120
+    // 48 and 52, of 16 x 5120 x 13824 59 and 110.
+    if (rows && m <= 16 && (m <= 4 || (can_split ? n * k <= (1 << 24) : n <= 25600))) {
         p.way = Way16::kFew;
         return p;
     }
