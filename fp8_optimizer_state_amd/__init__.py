@@ -511,6 +511,8 @@ def block_norm_backward_workspace_bytes(rows: int, cols: int, rows_per_gate: Opt
 
 def _matrix(t: torch.Tensor, dtype, shape, gpu: int, name: str):
     """(address, elements from row to row) of a matrix with this type and shape on GPU `gpu`."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == gpu and t.is_contiguous():
+        return t.data_ptr(), shape[1] or 1
     if t.get_device() != gpu:
         raise ValueError(f"{name} must be on GPU {gpu} like the other tensors, got {t.device}")
     if t.dtype is not dtype:

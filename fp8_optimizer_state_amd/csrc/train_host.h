@@ -20,6 +20,7 @@ inline int check_epilogue(const coat_epilogue* e) {
     if (!e) return COAT_EINVAL;
     if (e->act < COAT_ACT_NONE || e->act > COAT_ACT_SILU || !finite_f(e->scale)) return COAT_EINVAL;
     if (!(e->p >= 0.0f && e->p < 1.0f) || (e->p > 0.0f && !e->rng)) return COAT_EINVAL;
+    if (!finite_f(e->scale * drop_factor(drop_threshold(e->p)))) return COAT_EINVAL;
     if (!aligned(e->rng, 8)) return COAT_EALIGN;
     return COAT_OK;
 }
@@ -75,6 +76,7 @@ inline int check_linear_backward(const void* dy, int64_t lddy, int32_t dy_type, 
 inline int check_dropout(const void* x, int64_t rows, int64_t cols, int64_t ldx, int32_t x_type, const void* residual,
                          int64_t ldr, float scale, float p, const int64_t* rng, const void* y, int64_t ldy, int32_t y_type) {
     if (!finite_f(scale) || !(p >= 0.0f && p < 1.0f) || (p > 0.0f && !rng)) return COAT_EINVAL;
+    if (!finite_f(scale * drop_factor(drop_threshold(p)))) return COAT_EINVAL;
     return first_error({check_present(x, rows, cols, ldx, x_type), check_present(y, rows, cols, ldy, y_type),
                         check_optional(residual, rows, cols, ldr, y_type), aligned(rng, 8) ? COAT_OK : COAT_EALIGN});
 }

@@ -413,7 +413,7 @@ enum { COAT_ACT_NONE = 0, COAT_ACT_RELU = 1, COAT_ACT_GELU = 2, COAT_ACT_GELU_TA
 
 typedef struct coat_epilogue {
     int32_t act;        /* COAT_ACT_*: max(z, 0); z Phi(z); z sigmoid(sqrt(8 / pi) (z + 0.044715 z^3)); z sigmoid(z) */
-    float scale;        /* finite */
+    float scale;        /* finite, also times the factor of D */
     float p;            /* dropout, 0 <= p < 1 */
     int64_t offset;     /* added to the step */
     const int64_t* rng; /* (seed, step) in device memory, 8-byte aligned; may be NULL if p = 0 */

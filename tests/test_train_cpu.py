@@ -20,7 +20,7 @@ def epilogue(act=0, scale=1.0, p=0.0, offset=0, rng=None):
 
 
 BAD_EPILOGUES = [dict(act=-1), dict(act=5), dict(scale=float("nan")), dict(scale=float("inf")), dict(p=-0.1), dict(p=1.0),
-                 dict(p=float("nan")), dict(p=0.5)]  # the last: no random numbers
+                 dict(p=float("nan")), dict(p=0.5), dict(p=0.5, rng=FAKE, scale=3e38)]  # no random numbers; a factor past fp32
 
 
 def test_constants_and_reference():
@@ -78,7 +78,7 @@ def test_dropout_arguments():
 
     assert call(rows=-1) == call(cols=BIG, ldx=BIG, ldy=BIG) == call(ldx=7) == call(ldy=7) == call(r=FAKE, ldr=7) == EINVAL
     assert call(x=None) == call(y=None) == call(rng=None) == call(xt=2) == call(yt=-1) == EINVAL
-    assert call(p=1.0) == call(p=-1.0) == call(p=float("nan")) == call(scale=float("inf")) == EINVAL
+    assert call(p=1.0) == call(p=-1.0) == call(p=float("nan")) == call(scale=float("inf")) == call(scale=3e38) == EINVAL
     assert call(x=FAKE + 1) == call(x=FAKE + 2, xt=1) == call(y=FAKE + 1) == call(r=FAKE + 1) == call(rng=FAKE + 4) == EALIGN
     assert call(rows=0, x=None, y=None) == call(cols=0, x=None, y=None) == OK
 
