@@ -8,7 +8,7 @@ whole list. Prints one JSON line on stdout; progress goes to stderr.
 
   python bench.py [--gpus 1] [--steps 20] [--warmup 3] [--workload llama13b]
                   [--no-cpu-baseline] [--no-reference] [--copy-calibration]
-                  [--sweep | --act | --layer-input | --codec | --ceiling]
+                  [--sweep | --act | --layer-input | --train-products | --codec | --ceiling]
 
 After the measured steps it also times, unless --no-reference, the same step
 without expansion (every group k = 1: the same bytes with the least
@@ -41,6 +41,12 @@ With --layer-input it times what makes and multiplies a layer input, on 16384
 tokens at Llama-2-13B's widths: the norms at a block's border (5120 channels;
 to bf16, FP8 and 4-bit form, and backward), the 4-bit codec and the gate
 projection's 4-bit products: one JSON line per launch kind.
+
+With --train-products it times the products of a training step at those widths:
+the up projection (16384 tokens, 5120 to 13824, bias and GELU) and its backward
+pass, the down projection onto the residual stream with dropout, dropout alone,
+and the cross entropy of 8192 tokens over 32000 entries with its gradients: one
+JSON line per call.
 """
 from __future__ import annotations
 
@@ -291,6 +297,62 @@ def layer_input_bench(args) -> int:
         ms = ev0.elapsed_time(ev1) / args.steps
         row = {"layer_input": name, "tokens": t, "channels": c, "features": f, "ms": ms,
                "achieved_GBps": nbytes / (ms * 1e-3) / 1e9, "achieved_TFLOPps": flops / (ms * 1e-3) / 1e12}
+        print(json.dumps(row), flush=True)
+        log(f"{name}: {ms * 1e3:.1f} us, {row['achieved_GBps']:.0f} GB/s, {row['achieved_TFLOPps']:.0f} TFLOP/s")
+    return 0
+
+
+def train_products_bench(args) -> int:
+    """Times of the training products' entry points, inputs resident in HBM."""
+    import torch
+
+    import fp8_optimizer_state_amd as coat
+    import synth
+
+    dev = torch.device("cuda:0")
+    torch.cuda.set_device(dev)
+    coat.lib()
+    t, c, f, lt, v = 16384, 5120, 13824, 8192, 32000
+    bf16 = torch.bfloat16
+    new = lambda *s, dtype=bf16: torch.empty(*s, dtype=dtype, device=dev)
+    normal = lambda r, n, seed, scale=1.0: (torch.randn(r, n, generator=gen.manual_seed(seed), device=dev) * scale).to(bf16)
+    gen = torch.Generator(device=dev)
+    x, dy, r = normal(t, c, 31), normal(t, f, 32), normal(t, c, 33)
+    up = synth.params(f * c, 13, device=dev).view(f, c).to(bf16)
+    down = synth.params(c * f, 14, device=dev).view(c, f).to(bf16)
+    vocab = synth.params(v * c, 15, device=dev).view(v, c).to(bf16)
+    bias, dbias = torch.zeros(f, dtype=bf16, device=dev), new(f, dtype=torch.float32)
+    rng = torch.tensor([1, 0], device=dev)
+    a, z, r2, dx, dup, dd = new(t, f), new(t, f), new(t, c), new(t, c), new(f, c), new(t, c)
+    labels = torch.randint(0, v, (lt,), generator=gen.manual_seed(34), device=dev)
+    loss, lse = new(lt, dtype=torch.float32), new(lt, dtype=torch.float32)
+    one, dxl, dv = torch.full((1,), 1.0 / lt, device=dev), new(lt, c), new(v, c)
+    h = x[:lt]
+    g = 2 * t * c * f
+    ops = (
+        ("linear up, bias, GELU, z kept", lambda: coat.linear(x, up, a, bias=bias, act=coat.ACT_GELU, z=z), 2 * (t * c + f * c + 2 * t * f), g),
+        ("linear down, dropout, residual", lambda: coat.linear(a, down, r2, residual=r, p=0.1, rng=rng), 2 * (t * f + f * c + 2 * t * c), g),
+        ("linear_backward up", lambda: coat.linear_backward(dy, x, up, dx, dup, dbias, act=coat.ACT_GELU, z=z),
+         2 * (2 * t * f + 2 * t * c + 2 * f * c), 2 * g),
+        ("dropout onto the residual", lambda: coat.dropout(x, dd, p=0.1, rng=rng, residual=r), 6 * t * c, 0),
+        ("linear_cross_entropy", lambda: coat.linear_cross_entropy(h, vocab, labels, loss, lse), 2 * (lt + v) * c, 2 * lt * v * c),
+        ("linear_cross_entropy_backward", lambda: coat.linear_cross_entropy_backward(h, vocab, labels, lse, one, dxl, dv),
+         4 * (lt + v) * c, 4 * lt * v * c),
+    )
+    stream = torch.cuda.current_stream()
+    for name, fn, nbytes, flops in ops:
+        for _ in range(args.warmup):
+            fn()
+        ev0, ev1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        ev0.record(stream)
+        for _ in range(args.steps):
+            fn()
+        ev1.record(stream)
+        torch.cuda.synchronize()
+        ms = ev0.elapsed_time(ev1) / args.steps
+        row = {"train_product": name, "ms": ms, "achieved_GBps": nbytes / (ms * 1e-3) / 1e9,
+               "achieved_TFLOPps": flops / (ms * 1e-3) / 1e12}
         print(json.dumps(row), flush=True)
         log(f"{name}: {ms * 1e3:.1f} us, {row['achieved_GBps']:.0f} GB/s, {row['achieved_TFLOPps']:.0f} TFLOP/s")
     return 0
@@ -566,6 +628,8 @@ def main() -> int:
     ap.add_argument("--act", action="store_true", help="time the FP8 activation codec instead of the step")
     ap.add_argument("--layer-input", action="store_true",
                     help="time the block-border norms, the 4-bit codec and its products instead of the step")
+    ap.add_argument("--train-products", action="store_true",
+                    help="time linear layers, dropout and the cross entropy of a vocabulary projection instead of the step")
     ap.add_argument("--codec", action="store_true",
                     help="time the FP8 state codec (quantize / dequantize of moments) instead of the step")
     ap.add_argument("--ceiling", action="store_true",
@@ -585,6 +649,8 @@ def main() -> int:
         return act_bench(args)
     if args.layer_input:
         return layer_input_bench(args)
+    if args.train_products:
+        return train_products_bench(args)
     if args.codec:
         return codec_bench(args)
     if args.ceiling:
