@@ -655,22 +655,28 @@ int launch_tiles(const Product16& p, const Plan16& plan, float* ws, const Out& o
     return launch_status();
 }
 
-// The first `cols` values of each row, and zeros up to ld (a multiple of 8), 8 a thread:
-// of rows at[0] .. at[*count - 1], if they are given.
-__global__ __launch_bounds__(kBlock) void pack_rows_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ldx,
-                                                           const int32_t* __restrict__ at, const int32_t* __restrict__ count,
-                                                           uint16_t* __restrict__ packed, int64_t ld) {
-    if (count) rows = (int64_t)*gp(count);
+// Rows of an operand that tiles do not take: the first `cols` values of each, to rows of ld
+// (a multiple of 8) with zeros behind them; of rows at[0] .. at[*count - 1], if they are given.
+struct Pack {
+    const uint16_t* x;
+    int64_t rows, ldx;
+    const int32_t *at, *count;
+    uint16_t* packed;
+};
+// Up to two operands in one launch, 8 values a thread.
+__global__ __launch_bounds__(kBlock) void pack_rows_kernel(Pack first, Pack second, int64_t cols, int64_t ld) {
+    const Pack p = blockIdx.y == 0 ? first : second;
+    const int64_t rows = p.count ? (int64_t)*gp(p.count) : p.rows;
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const uint16_t* const from = x + (at ? (int64_t)gp(at)[r] : r) * ldx;
+        const uint16_t* const from = p.x + (p.at ? (int64_t)gp(p.at)[r] : r) * p.ldx;
         for (int64_t c = threadIdx.x * 8; c < ld; c += kBlock * 8)
-            *reinterpret_cast<gu32x4*>(gp(packed) + r * ld + c) = load_raw8(from + c, cols - c).w;
+            *reinterpret_cast<gu32x4*>(gp(p.packed) + r * ld + c) = load_raw8(from + c, cols - c).w;
     }
 }
-inline int launch_pack(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx, const int32_t* at, const int32_t* count, uint16_t* packed,
-                       hipStream_t st) {
-    hipLaunchKernelGGL(pack_rows_kernel, dim3((unsigned)(rows < 64 * kCUs ? rows : 64 * kCUs)), dim3(kBlock), 0, st, x, rows, cols, ldx, at, count,
-                       packed, packed_ld(cols));
+inline int launch_pack(const Pack& first, const Pack& second, int64_t cols, hipStream_t st) {
+    const int64_t rows = first.rows > second.rows ? first.rows : second.rows;
+    hipLaunchKernelGGL(pack_rows_kernel, dim3((unsigned)(rows < 64 * kCUs ? rows : 64 * kCUs), second.rows > 0 ? 2u : 1u), dim3(kBlock), 0, st,
+                       first, second, cols, packed_ld(cols));
     return launch_status();
 }
 

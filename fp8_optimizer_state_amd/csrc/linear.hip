@@ -128,7 +128,7 @@ int coat_linear(const uint16_t* x, int64_t m, int64_t k, int64_t ldx, const uint
     Product16 p{x, w, ldx, ldw, nullptr, nullptr, nullptr, m, n, k};
     if (!ready && l.plan.way != Way16::kPlain && l.plan.way != Way16::kFew) {
         uint16_t *const px = reinterpret_cast<uint16_t*>(ws + l.x), *const pw = reinterpret_cast<uint16_t*>(ws + l.w);
-        if ((rc = launch_pack(x, m, k, ldx, nullptr, nullptr, px, st)) || (rc = launch_pack(w, n, k, ldw, nullptr, nullptr, pw, st))) return rc;
+        if ((rc = launch_pack(Pack{x, m, ldx, nullptr, nullptr, px}, Pack{w, n, ldw, nullptr, nullptr, pw}, k, st))) return rc;
         p.a = px;
         p.b = pw;
         p.lda = p.ldb = packed_ld(k);
@@ -188,17 +188,18 @@ int coat_linear_backward(const void* dy, int64_t lddy, int32_t dy_type, const ui
         if ((rc = launch_status())) return rc;
     }
     const bool packs = !ready && m > 0 && n > 0 && k > 0;
+    uint16_t *const px = reinterpret_cast<uint16_t*>(ws + l.x), *const pw = reinterpret_cast<uint16_t*>(ws + l.w);
+    if (packs && (dx || dw)) {
+        const Pack of_x{x, m, ldx, nullptr, nullptr, px}, of_w{w, n, ldw, nullptr, nullptr, pw}, none{};
+        if ((rc = launch_pack(dx ? of_w : of_x, dx && dw ? of_x : none, k, st))) return rc;
+    }
     if (dx) {
-        uint16_t* const pw = reinterpret_cast<uint16_t*>(ws + l.w);
-        if (packs && (rc = launch_pack(w, n, k, ldw, nullptr, nullptr, pw, st))) return rc;
         const ScaledOut out{nullptr, scale, dx, lddx};
         rc = launch_product<false, true>(Product16{dz, packs ? pw : w, ld_dz, packs ? packed_ld(k) : ldw, nullptr, nullptr, nullptr, m, k, n},
                                          l.plan_dx, sums, out, st);
         if (rc) return rc;
     }
     if (dw) {
-        uint16_t* const px = reinterpret_cast<uint16_t*>(ws + l.x);
-        if (packs && (rc = launch_pack(x, m, k, ldx, nullptr, nullptr, px, st))) return rc;
         const ScaledOut out{nullptr, scale, dw, lddw};
         rc = launch_product<true, true>(Product16{dz, packs ? px : x, ld_dz, packs ? packed_ld(k) : ldx, nullptr, nullptr, nullptr, n, k, m},
                                         l.plan_dw, sums, out, st);

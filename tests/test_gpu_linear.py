@@ -115,6 +115,49 @@ def test_large_tiles(size, pad, shift):
     assert float((db.double() - 0.5 * D.sum(0)).abs().max()) < 1e-3
 
 
+def test_rows_past_what_tiles_take():
+    """Rows of 2^22 values and more."""
+    m, n, k = 3, 5, (1 << 22) + 8
+    g = gen(3)
+    x, w = torch.randn(m, k, generator=g).to(BF16).to(DEV), torch.randn(n, k, generator=g).to(BF16).to(DEV)
+    y = torch.empty(m, n, device=DEV)
+    coat.linear(x, w, y)
+    X, W = x.double(), w.double()
+    # sums of 2^18 instructions of independent signs: the mean of squares, not the worst case
+    assert float((y.double() - X @ W.t().contiguous()).abs().max()) < 1e-3 * k ** 0.5
+    dy = torch.randn(m, n, generator=g).to(BF16).to(DEV)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    coat.linear_backward(dy, x, w, dx, dw)
+    D = dy.double()
+    for got, want, mag in ((dx, D @ W, D.abs() @ W.abs()), (dw, D.t().contiguous() @ X, D.abs().t().contiguous() @ X.abs())):
+        off = (got.double() - want).abs()
+        assert bool((off <= 2.0 ** -8 * want.abs() + 1e-5 * mag + 1e-30).all())
+
+
+def test_rows_far_apart():
+    """Rows nearly 2^22 elements apart, over 2^31 elements in all: the same results as close together."""
+    m, n, k, ld = 600, 200, 64, (1 << 22) - 8
+    flat = torch.empty(m * ld, dtype=BF16, device=DEV)
+    x = flat.view(m, ld)[:, :k]
+    x.copy_(torch.randn(m, k, generator=gen(4)))
+    close, w = x.contiguous(), torch.randn(n, k, generator=gen(5)).to(BF16).to(DEV)
+    y, z = torch.empty(m, n, device=DEV), torch.empty(m, n, device=DEV)
+    coat.linear(x, w, y)
+    coat.linear(close, w, z)
+    assert torch.equal(y, z)
+    labels = torch.randint(0, n, (m,), generator=gen(6)).to(DEV)
+    labels[::3] = -100
+    out = []
+    for t in (x, close):
+        loss, lse = torch.empty(m, device=DEV), torch.empty(m, device=DEV)
+        dx, dw = torch.empty_like(close), torch.empty_like(w)
+        coat.linear_cross_entropy(t, w, labels, loss, lse)
+        coat.linear_cross_entropy_backward(t, w, labels, lse, torch.ones(1, device=DEV), dx, dw)
+        out.append((loss, lse, dx, dw))
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+
+
 def test_linear_extremes():
     """No columns of x, no rows, and what NaN and Inf reach."""
     x, w, b, r, rng = inputs(4, 24, 16, 1, F32)
