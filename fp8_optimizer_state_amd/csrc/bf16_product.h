@@ -662,6 +662,7 @@ struct Pack {
     int64_t rows, ldx;
     const int32_t *at, *count;
     uint16_t* packed;
+    bool finite = false;  // with zeros for infinities and NaN
 };
 // Up to two operands in one launch, 8 values a thread.
 __global__ __launch_bounds__(kBlock) void pack_rows_kernel(Pack first, Pack second, int64_t cols, int64_t ld) {
@@ -669,8 +670,10 @@ __global__ __launch_bounds__(kBlock) void pack_rows_kernel(Pack first, Pack seco
     const int64_t rows = p.count ? (int64_t)*gp(p.count) : p.rows;
     for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
         const uint16_t* const from = p.x + (p.at ? (int64_t)gp(p.at)[r] : r) * p.ldx;
-        for (int64_t c = threadIdx.x * 8; c < ld; c += kBlock * 8)
-            *reinterpret_cast<gu32x4*>(gp(p.packed) + r * ld + c) = load_raw8(from + c, cols - c).w;
+        for (int64_t c = threadIdx.x * 8; c < ld; c += kBlock * 8) {
+            const u32x4 v = load_raw8(from + c, cols - c).w;
+            *reinterpret_cast<gu32x4*>(gp(p.packed) + r * ld + c) = p.finite ? finite_of(v) : v;
+        }
     }
 }
 inline int launch_pack(const Pack& first, const Pack& second, int64_t cols, hipStream_t st) {

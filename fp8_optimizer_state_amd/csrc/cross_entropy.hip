@@ -8,8 +8,9 @@
 //
 // Backward: the rows that count are packed (so that what the others hold, an infinity say,
 // reaches no sum), and for one piece of the vocabulary after the other the logits are
-// computed again, their gradients stored in bf16 and multiplied twice. The logits' second
-// product is a third of the work; storing them would take tokens x vocabulary numbers.
+// computed again, their gradients stored in bf16 (with second terms where tokens are few) and
+// multiplied twice. The logits' second product is a third of the work; storing them would
+// take tokens x vocabulary numbers.
 namespace {
 
 constexpr int kRowsBlock = 1024;
@@ -130,7 +131,8 @@ __global__ __launch_bounds__(kRowsBlock) void xent_back_rows_kernel(const int64_
                                                                     int64_t vocab, const float* __restrict__ lse,
                                                                     const float* __restrict__ dloss, int64_t dloss_count,
                                                                     int32_t* __restrict__ count, int32_t* __restrict__ at,
-                                                                    int32_t* __restrict__ place, f32x4* __restrict__ info) {
+                                                                    int32_t* __restrict__ place, int32_t* __restrict__ second,
+                                                                    f32x4* __restrict__ info) {
     __shared__ float tops[kRowsBlock / kWave];
     float top = 0.0f;
     for (int64_t t = threadIdx.x; t < tokens; t += kRowsBlock)
@@ -175,20 +177,25 @@ __global__ __launch_bounds__(kRowsBlock) void xent_back_rows_kernel(const int64_
     if (threadIdx.x == 0) {
         *gp(count) = done;
         reinterpret_cast<gfloat*>(gp(count))[1] = top;
+        gp(count)[2] = 2 * done;  // rows with second terms
     }
+    for (int64_t t = threadIdx.x; t < done; t += kRowsBlock) gp(second)[t] = (int32_t)(done + t);
 }
 
-// The rows of x that count, packed, with zeros up to ld; zeros in the others' rows of dx.
+// The rows of x that count, packed, with zeros up to ld (and once more behind them, for second
+// terms, if count is given); zeros in the others' rows of dx.
 __global__ __launch_bounds__(kBlock) void xent_pack_kernel(const uint16_t* __restrict__ x, int64_t tokens, int64_t cols, int64_t ldx,
                                                            const int32_t* __restrict__ place, uint16_t* __restrict__ packed, int64_t ld,
-                                                           uint16_t* __restrict__ dx, int64_t lddx) {
+                                                           uint16_t* __restrict__ dx, int64_t lddx, const int32_t* __restrict__ count) {
     for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
         const int32_t j = gp(place)[t];
         if (j < 0 && !dx) continue;
         for (int64_t c = threadIdx.x * 8; c < ld; c += kBlock * 8) {
             float v[8] = {};
             if (j >= 0) {
-                *reinterpret_cast<gu32x4*>(gp(packed) + j * ld + c) = load_raw8(x + t * ldx + c, cols - c).w;
+                const u32x4 w = load_raw8(x + t * ldx + c, cols - c).w;
+                *reinterpret_cast<gu32x4*>(gp(packed) + j * ld + c) = w;
+                if (count) *reinterpret_cast<gu32x4*>(gp(packed) + ((int64_t)*gp(count) + j) * ld + c) = finite_of(w);
             } else {
                 store8(dx + t * lddx + c, cols - c, v);
             }
@@ -268,15 +275,17 @@ int coat_linear_cross_entropy_backward(const uint16_t* x, int64_t tokens, int64_
     const float* const top = reinterpret_cast<const float*>(ws + l.count) + 1;
     int32_t* const at = reinterpret_cast<int32_t*>(ws + l.at);
     int32_t* const place = reinterpret_cast<int32_t*>(ws + l.place);
+    int32_t* const second = reinterpret_cast<int32_t*>(ws + l.second);
+    const int32_t* const two = l.two ? count : nullptr;
     f32x4* const info = reinterpret_cast<f32x4*>(ws + l.info);
     uint16_t* const px = reinterpret_cast<uint16_t*>(ws + l.x);
     uint16_t* const g = reinterpret_cast<uint16_t*>(ws + l.g);
     float* const acc = reinterpret_cast<float*>(ws + l.acc);
     float* const sums = reinterpret_cast<float*>(ws + l.part);
     hipLaunchKernelGGL(xent_back_rows_kernel, dim3(1), dim3(kRowsBlock), 0, st, labels, tokens, ignore_index, vocab, lse, dloss, dloss_count,
-                       count, at, place, info);
+                       count, at, place, second, info);
     hipLaunchKernelGGL(xent_pack_kernel, dim3((unsigned)(tokens < 64 * kCUs ? tokens : 64 * kCUs)), dim3(kBlock), 0, st, x, tokens, cols, ldx,
-                       place, px, l.ld_x, dx, lddx);
+                       place, px, l.ld_x, dx, lddx, two);
     if ((rc = launch_status())) return rc;
     if (!ready) {
         uint16_t* const pw = reinterpret_cast<uint16_t*>(ws + l.w);
@@ -287,18 +296,30 @@ int coat_linear_cross_entropy_backward(const uint16_t* x, int64_t tokens, int64_
     for (int64_t v0 = 0; v0 < vocab; v0 += l.piece) {
         const int64_t v1 = v0 + l.piece < vocab ? v0 + l.piece : vocab;
         const uint16_t* const wp = w + v0 * ldw;
-        const XentPiece plans = xent_piece_plans(tokens, v1 - v0, cols);
-        rc = launch_product<false, false>(Product16{px, wp, l.ld_x, ldw, nullptr, count, nullptr, tokens, v1 - v0, cols}, plans.logits, sums,
-                                          GradOut{info, g, l.ld_g, v0}, st);
+        const XentPiece plans = xent_piece_plans(tokens, v1 - v0, cols, l.two);
+        const Product16 logits{px, wp, l.ld_x, ldw, nullptr, count, nullptr, tokens, v1 - v0, cols};
+        rc = two ? launch_product<false, false>(logits, plans.logits, sums, GradOut<true>{info, g, l.ld_g, v0, two, 0}, st)
+                 : launch_product<false, false>(logits, plans.logits, sums, GradOut<false>{info, g, l.ld_g, v0, nullptr, 0}, st);
         if (rc) return rc;
         if (dx) {
-            rc = launch_product<false, true>(Product16{g, wp, l.ld_g, ldw, nullptr, count, nullptr, tokens, cols, v1 - v0}, plans.dx, sums,
-                                             PiecesOut{top, at, v1 == vocab ? dx : nullptr, lddx, acc, l.ld_x, v0 == 0, 0.0f}, st);
+            uint16_t* const to = v1 == vocab ? dx : nullptr;
+            Product16 p{g, wp, l.ld_g, ldw, nullptr, count, nullptr, tokens, cols, v1 - v0};
+            if (two) {
+                const PiecesOut<true> first{top, at, nullptr, lddx, acc, l.ld_x, v0 == 0, 0.0f, false};
+                if ((rc = launch_product<false, true>(p, plans.dx, sums, first, st))) return rc;
+                p.a_rows = second;
+                const PiecesOut<true> left{top, at, to, lddx, acc, l.ld_x, false, 0.0f, true};
+                rc = launch_product<false, true>(p, plans.dx, sums, left, st);
+            } else {
+                const PiecesOut<false> out{top, at, to, lddx, acc, l.ld_x, v0 == 0, 0.0f, false};
+                rc = launch_product<false, true>(p, plans.dx, sums, out, st);
+            }
             if (rc) return rc;
         }
         if (dw) {
-            rc = launch_product<true, true>(Product16{g, px, l.ld_g, l.ld_x, nullptr, nullptr, count, v1 - v0, cols, tokens}, plans.dw, sums,
-                                            ScaledOut{top, 0.0f, dw + v0 * lddw, lddw}, st);
+            const int64_t rows = l.two ? 2 * tokens : tokens;
+            const Product16 p{g, px, l.ld_g, l.ld_x, nullptr, nullptr, l.two ? count + 2 : count, v1 - v0, cols, rows};
+            rc = launch_product<true, true>(p, plans.dw, sums, ScaledOut{top, 0.0f, dw + v0 * lddw, lddw}, st);
             if (rc) return rc;
         }
     }

@@ -6,14 +6,14 @@ namespace {
 // ------------------------------------------------------------------ the gradient before the activation
 //
 // dz = D(dy) act'(z) in bf16 (the matrix units' type, and the one rounding on the way to dx
-// and dw), without the factors that the products' sums are multiplied by, and the sums
-// of a band of rows of it as they were before the rounding. A workgroup takes 512 columns
-// of a band: a thread 8 columns of every fourth row, the four rows' sums joined through
-// LDS in order. Bound by HBM: 8192 x 13824 in bf16 takes 132 us (5.1 TB/s).
+// and dw, unless few values take a second term), without the factors that the products' sums
+// are multiplied by, and the sums of a band of rows of it as they were before the rounding.
+// A workgroup takes 512 columns of a band: a thread 8 columns of every fourth row, the four
+// rows' sums joined through LDS in order. Bound by HBM: 8192 x 13824 in bf16 takes 132 us (5.1 TB/s).
 template <class T>
 __global__ __launch_bounds__(kBlock) void dz_kernel(const T* __restrict__ dy, int64_t lddy, const uint16_t* __restrict__ z, int64_t ldz,
                                                     int32_t act, Drop drop, int64_t m, int64_t n, uint16_t* __restrict__ dz,
-                                                    int64_t ld_dz, float* __restrict__ bias_part, int32_t band) {
+                                                    int64_t ld_dz, float* __restrict__ bias_part, int32_t band, bool two) {
     __shared__ float sums[kWavesPerBlock][kWave][9];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     drop.begin();
@@ -45,6 +45,10 @@ __global__ __launch_bounds__(kBlock) void dz_kernel(const T* __restrict__ dy, in
                 sum[i] += v[i];
             }
             if (dz) store8<true>(dz + row * ld_dz + col, 8, v);
+            if (dz && two) {  // what the rounding leaves, behind the m rows
+                left_of(v);
+                store8<true>(dz + (m + row) * ld_dz + col, 8, v);
+            }
         }
     }
     if (!bias_part) return;
@@ -82,11 +86,11 @@ __global__ __launch_bounds__(kBlock) void bias_join_kernel(const float* __restri
 
 template <class T>
 int launch_dz(const T* dy, int64_t lddy, const uint16_t* z, int64_t ldz, int32_t act, const Drop& drop, int64_t m, int64_t n, uint16_t* dz,
-              int64_t ld_dz, float* part, hipStream_t st) {
+              int64_t ld_dz, float* part, bool two, hipStream_t st) {
     const int64_t band = bias_band(m, n), bands = div_up(m, band), most = 32768;
     const dim3 grid((unsigned)div_up(n, kWave * 8), (unsigned)(bands < most ? bands : most), (unsigned)div_up(bands, most));
     hipLaunchKernelGGL(dz_kernel<T>, grid, dim3(kBlock), 0, st, dy, lddy, z, ldz, act, drop, m, n, dz, ld_dz, part,
-                       (int32_t)band);
+                       (int32_t)band, two);
     return launch_status();
 }
 
@@ -168,12 +172,15 @@ int coat_linear_backward(const void* dy, int64_t lddy, int32_t dy_type, const ui
     const bool as_it_is = dy_type == COAT_BF16 && e->act == COAT_ACT_NONE && t == 0 && tiles_take(dy, lddy, n);
     const uint16_t* const dz = as_it_is ? static_cast<const uint16_t*>(dy) : dz_made;
     const int64_t ld_dz = as_it_is ? lddy : l.ld_dz;
+    // dropping and cutting at zero leave bf16 values as they are
+    const bool exact = dy_type == COAT_BF16 && (e->act == COAT_ACT_NONE || e->act == COAT_ACT_RELU);
+    const bool two = !exact && m > 0 && n > 0 && k > 0 && dz_takes_two_terms(m, n);
     if (m > 0 && n > 0 && (dbias || !as_it_is)) {
         uint16_t* const to = as_it_is || (!dx && !dw) ? nullptr : dz_made;
         if (dy_type == COAT_FP32)
-            rc = launch_dz(static_cast<const float*>(dy), lddy, z, ldz, e->act, drop, m, n, to, l.ld_dz, dbias ? part : nullptr, st);
+            rc = launch_dz(static_cast<const float*>(dy), lddy, z, ldz, e->act, drop, m, n, to, l.ld_dz, dbias ? part : nullptr, two, st);
         else
-            rc = launch_dz(static_cast<const uint16_t*>(dy), lddy, z, ldz, e->act, drop, m, n, to, l.ld_dz, dbias ? part : nullptr, st);
+            rc = launch_dz(static_cast<const uint16_t*>(dy), lddy, z, ldz, e->act, drop, m, n, to, l.ld_dz, dbias ? part : nullptr, two, st);
         if (rc) return rc;
     }
     if (dbias && n > 0) {
@@ -189,20 +196,37 @@ int coat_linear_backward(const void* dy, int64_t lddy, int32_t dy_type, const ui
     }
     const bool packs = !ready && m > 0 && n > 0 && k > 0;
     uint16_t *const px = reinterpret_cast<uint16_t*>(ws + l.x), *const pw = reinterpret_cast<uint16_t*>(ws + l.w);
-    if (packs && (dx || dw)) {
-        const Pack of_x{x, m, ldx, nullptr, nullptr, px}, of_w{w, n, ldw, nullptr, nullptr, pw}, none{};
-        if ((rc = launch_pack(dx ? of_w : of_x, dx && dw ? of_x : none, k, st))) return rc;
-    }
+    const Pack of_x{x, m, ldx, nullptr, nullptr, px}, of_w{w, n, ldw, nullptr, nullptr, pw};
+    if (packs && dx && (rc = launch_pack(of_w, dw && !two ? of_x : Pack{}, k, st))) return rc;
+    if (packs && !dx && dw && !two && (rc = launch_pack(of_x, Pack{}, k, st))) return rc;
     if (dx) {
-        const ScaledOut out{nullptr, scale, dx, lddx};
-        rc = launch_product<false, true>(Product16{dz, packs ? pw : w, ld_dz, packs ? packed_ld(k) : ldw, nullptr, nullptr, nullptr, m, k, n},
-                                         l.plan_dx, sums, out, st);
+        const Product16 p{dz, packs ? pw : w, ld_dz, packs ? packed_ld(k) : ldw, nullptr, nullptr, nullptr, m, k, n};
+        if (two) {
+            float* const acc = reinterpret_cast<float*>(ws + l.acc);
+            const PiecesOut<true> first{nullptr, nullptr, nullptr, lddx, acc, packed_ld(k), true, scale, false};
+            if ((rc = launch_product<false, true>(p, l.plan_dx, sums, first, st))) return rc;
+            const PiecesOut<true> second{nullptr, nullptr, dx, lddx, acc, packed_ld(k), false, scale, true};
+            Product16 left = p;
+            left.a = dz + m * ld_dz;
+            rc = launch_product<false, true>(left, l.plan_dx, sums, second, st);
+        } else {
+            rc = launch_product<false, true>(p, l.plan_dx, sums, ScaledOut{nullptr, scale, dx, lddx}, st);
+        }
         if (rc) return rc;
     }
     if (dw) {
         const ScaledOut out{nullptr, scale, dw, lddw};
-        rc = launch_product<true, true>(Product16{dz, packs ? px : x, ld_dz, packs ? packed_ld(k) : ldx, nullptr, nullptr, nullptr, n, k, m},
-                                        l.plan_dw, sums, out, st);
+        if (two) {  // x's rows stand beside both terms
+            Pack again = of_x;
+            again.packed = px + m * packed_ld(k);
+            again.finite = true;
+            if ((rc = launch_pack(of_x, again, k, st))) return rc;
+            const Product16 p{dz, px, ld_dz, packed_ld(k), nullptr, nullptr, nullptr, n, k, 2 * m};
+            rc = launch_product<true, true>(p, l.plan_dw_two, sums, out, st);
+        } else {
+            rc = launch_product<true, true>(Product16{dz, packs ? px : x, ld_dz, packs ? packed_ld(k) : ldx, nullptr, nullptr, nullptr, n, k, m},
+                                            l.plan_dw, sums, out, st);
+        }
     }
     return rc;
 }

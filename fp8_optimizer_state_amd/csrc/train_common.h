@@ -117,6 +117,25 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
     }
 }
 
+// What rounding to bf16 leaves of 8 values (of a NaN or Inf nothing more).
+__device__ __forceinline__ void left_of(float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float left = v[i] - as_float(bf16_bits(v[i]) << 16);
+        v[i] = fabsf(left) < __builtin_inff() ? left : 0.0f;
+    }
+}
+
+// 8 values in bf16 with zeros for infinities and NaN, beside second terms: the first ones carry
+// those, and zero times infinity would make a NaN of them.
+__device__ __forceinline__ u32x4 finite_of(u32x4 w) {
+    for (int i = 0; i < 4; ++i) {
+        if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u;
+        if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0xFFFFu;
+    }
+    return w;
+}
+
 // 8 columns past the caches' usual order where whole lines leave for memory anyway, and
 // would drive the operands out of them.
 __device__ __forceinline__ void store8_past(bool past, uint16_t* p, int64_t n, const float (&v)[8]) {
@@ -212,19 +231,26 @@ struct ScaledOut {
 
 // The same of sums that come in pieces: on top of those of earlier pieces, and into
 // those for later ones or, behind the last, to row rows[i] of y for row i.
+// With second terms the factor and the rows may be given otherwise, and a second sum changes
+// nothing that is not finite already. That is a type of its own: as choices at run time, here
+// and in GradOut, it made the gradients of 8192 x 32000 x 5120 take 6370 us instead of 5830.
+template <bool TWO>
 struct PiecesOut {
     static constexpr bool kLogSum = false;
-    const float* scale_at;
-    const int32_t* rows;
-    uint16_t* y;  // NULL: not the last piece
+    const float* scale_at;  // in device memory; with second terms may be NULL: scale
+    const int32_t* rows;    // with second terms may be NULL: row i
+    uint16_t* y;            // NULL: not the last piece
     int64_t ldy;
     float* acc;
     int64_t lda;
     bool first;
     float scale;
+    bool second;            // these are sums of second terms
     struct Column {};
     typedef Raw8<float> Row;
-    __device__ void begin() { scale = *gp(scale_at); }
+    __device__ void begin() {
+        if (!TWO || scale_at) scale = *gp(scale_at);
+    }
     __device__ __forceinline__ Column column(int64_t, int64_t) const { return Column{}; }
     __device__ __forceinline__ Row row(int64_t row, int64_t col, int64_t) const {
         return first ? Row{} : load_raw8<true>(acc + row * lda + col, 8);  // its rows hold whole blocks
@@ -233,14 +259,14 @@ struct PiecesOut {
         float a[8];
         expand(r, a);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += a[i];
+        for (int i = 0; i < 8; ++i) v[i] = TWO && second && !(fabsf(a[i]) < __builtin_inff()) ? a[i] : v[i] + a[i];
         if (!y) {
             store8<true>(acc + row * lda + col, 8, v);
             return;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= scale;
-        store8(y + (int64_t)gp(rows)[row] * ldy + col, n, v);
+        store8(y + (!TWO || rows ? (int64_t)gp(rows)[row] : row) * ldy + col, n, v);
     }
 };
 
@@ -263,15 +289,20 @@ struct LogSumOut {
 
 // What a row of logits' gradients needs: {lse, weight over the largest weight, label's bits, 0}.
 // The gradient g = weight (exp(l - lse) - [the label]) in bf16; columns past the end up to a
-// whole block are zero.
+// whole block are zero. With second terms, what that rounding leaves goes to row i + *count.
+template <bool TWO>
 struct GradOut {
     static constexpr bool kLogSum = false;
     const f32x4* info;
     uint16_t* g;
-    int64_t ldg, col0;  // first column of the piece in the vocabulary
+    int64_t ldg, col0;     // first column of the piece in the vocabulary
+    const int32_t* count;  // with second terms
+    int64_t second;
     struct Column {};
     typedef f32x4 Row;
-    __device__ void begin() {}
+    __device__ void begin() {
+        if constexpr (TWO) second = (int64_t)*gp(count);
+    }
     __device__ __forceinline__ Column column(int64_t, int64_t) const { return Column{}; }
     __device__ __forceinline__ Row row(int64_t row, int64_t, int64_t) const { return reinterpret_cast<const gf32x4*>(gp(info))[row]; }
     __device__ __forceinline__ void operator()(int64_t row, int64_t col, float (&v)[8], int64_t n, const Column&, const Row& r) const {
@@ -283,6 +314,10 @@ struct GradOut {
             v[i] = i < n ? r[1] * (i == hit ? p - 1.0f : p) : 0.0f;
         }
         store8<true>(g + row * ldg + col, 8, v);
+        if constexpr (TWO) {
+            left_of(v);
+            store8<true>(g + (row + second) * ldg + col, 8, v);
+        }
     }
 };
 

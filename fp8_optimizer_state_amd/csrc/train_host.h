@@ -194,25 +194,42 @@ inline int64_t bias_band(int64_t m, int64_t n) {
     return band;
 }
 
-// Workspace of the backward pass: dz in bf16 with rows of whole 128 bytes, the partial
-// sums of the bias gradient and of the products, and copies of x and w.
+// A rounding to bf16 on the way to a gradient averages out over many values, and not over a
+// few, whose gradients would be off by up to 2.6 times what storing them rounds (1 x 8 values;
+// 1.5 to 1.6 at 64 to 1024, 1.4 from 4096 on; a loss of 1 token 1.6, of 16 1.3, of 64 1.1).
+// Where there are few the products take what it leaves as well, a second bf16 term, and
+// are off by 1.0 times: of up to 2048 values, and of the logits of up to 16 tokens, whose labels'
+// own gradients are most of them. It costs launches (the gradients of 16 x 128 values 19 -> 31 us)
+// and reading the weights once more (a loss of 1 x 32000 x 4096 208 -> 260 us).
+constexpr int64_t kTwoTermValues = 2048, kTwoTermTokens = 16;
+inline bool dz_takes_two_terms(int64_t m, int64_t n) { return m <= kTwoTermValues && n <= kTwoTermValues && m * n <= kTwoTermValues; }
+inline bool xent_takes_two_terms(int64_t tokens, int64_t vocab) { return tokens <= kTwoTermTokens || dz_takes_two_terms(tokens, vocab); }
+
+// Workspace of the backward pass: dz in bf16 with rows of whole 128 bytes (its second terms
+// behind it), the partial sums of the bias gradient and of the products, copies of x
+// and w, and the sums of dx over the two terms.
 struct LinearBackwardLayout {
-    Plan16 plan_dx, plan_dw;
+    Plan16 plan_dx, plan_dw, plan_dw_two;
     int64_t ld_dz;
-    size_t dz, bias, part, x, w, end;
+    size_t dz, bias, part, x, w, acc, end;
 };
 inline LinearBackwardLayout linear_backward_layout(int64_t m, int64_t n, int64_t k, bool ready) {
     LinearBackwardLayout l;
+    const bool two = dz_takes_two_terms(m, n);
     l.plan_dx = plan16_of(m, k, n, true, false, true);
     l.plan_dw = plan16_of(n, k, m, true, true, true);
-    const size_t dx = plan16_bytes(l.plan_dx), dw = plan16_bytes(l.plan_dw);
+    l.plan_dw_two = plan16_of(n, k, 2 * m, true, true, true);
+    size_t part = plan16_bytes(l.plan_dx);
+    if (plan16_bytes(l.plan_dw) > part) part = plan16_bytes(l.plan_dw);
+    if (two && plan16_bytes(l.plan_dw_two) > part) part = plan16_bytes(l.plan_dw_two);
     l.ld_dz = packed_ld(n);
     l.dz = 0;
-    l.bias = packed_bytes(m, n);
+    l.bias = packed_bytes(two ? 2 * m : m, n);
     l.part = l.bias + align_up((size_t)div_up(m, bias_band(m, n)) * (size_t)l.ld_dz * sizeof(float), 256);
-    l.x = l.part + (dx > dw ? dx : dw);
-    l.w = l.x + (ready ? 0 : packed_bytes(m, k));
-    l.end = l.w + (ready ? 0 : packed_bytes(n, k));
+    l.x = l.part + part;
+    l.w = l.x + (two ? packed_bytes(2 * m, k) : (ready ? 0 : packed_bytes(m, k)));
+    l.acc = l.w + (ready ? 0 : packed_bytes(n, k));
+    l.end = l.acc + (two ? 2 * packed_bytes(m, k) : 0);
     return l;
 }
 
@@ -280,42 +297,47 @@ inline int64_t xent_piece(int64_t tokens, int64_t vocab) {
     return div_up(div_up(vocab, div_up(vocab, most)), 256) * 256;
 }
 
-// Workspace of the backward pass: number of tokens that count and the largest
-// weight of a loss, the tokens' places in the packed rows and back, what a row of
-// logits needs, the packed rows of x, a piece's gradients, the sums of dx over
-// pieces, the partial sums of products and a copy of w.
+// Workspace of the backward pass: number of tokens that count, the largest weight of a
+// loss and twice that number, the tokens' places in the packed rows and back, the rows of
+// their second terms, what a row of logits needs, the packed rows of x and a piece's
+// gradients (each twice with second terms), the sums of dx over pieces and terms, the
+// partial sums of products and a copy of w.
 struct XentBackwardLayout {
+    bool two;
     int64_t piece, ld_x, ld_g;
-    size_t count, at, place, info, x, g, acc, part, w, end;
+    size_t count, at, place, second, info, x, g, acc, part, w, end;
 };
 // The products of a piece of `width` columns.
 struct XentPiece {
     Plan16 logits, dx, dw;
 };
-inline XentPiece xent_piece_plans(int64_t tokens, int64_t width, int64_t cols) {
+inline XentPiece xent_piece_plans(int64_t tokens, int64_t width, int64_t cols, bool two) {
     return XentPiece{plan16_of(tokens, width, cols, true, false, false), plan16_of(tokens, cols, width, true, false, true),
-                     plan16_of(width, cols, tokens, true, true, true)};
+                     plan16_of(width, cols, two ? 2 * tokens : tokens, true, true, true)};
 }
 inline XentBackwardLayout xent_backward_layout(int64_t tokens, int64_t vocab, int64_t cols, bool ready) {
     XentBackwardLayout l;
     const size_t t = (size_t)tokens;
+    l.two = xent_takes_two_terms(tokens, vocab);
     l.piece = xent_piece(tokens, vocab);
     l.ld_x = packed_ld(cols);
     l.ld_g = packed_ld(l.piece);
     size_t part = 0;
     for (const int64_t width : {l.piece, vocab - (vocab - 1) / l.piece * l.piece}) {
-        const XentPiece p = xent_piece_plans(tokens, width, cols);
+        const XentPiece p = xent_piece_plans(tokens, width, cols, l.two);
         for (const Plan16& q : {p.logits, p.dx, p.dw})
             if (plan16_bytes(q) > part) part = plan16_bytes(q);
     }
+    const size_t rows = l.two ? 2 * t : t;
     l.count = 0;
     l.at = 256;
     l.place = l.at + align_up(t * 4, 256);
-    l.info = l.place + align_up(t * 4, 256);
+    l.second = l.place + align_up(t * 4, 256);
+    l.info = l.second + align_up(t * 4, 256);
     l.x = l.info + align_up(t * 16, 256);
-    l.g = l.x + align_up(t * (size_t)l.ld_x * 2, 256);
-    l.acc = l.g + align_up(t * (size_t)l.ld_g * 2, 256);
-    l.part = l.acc + (l.piece < vocab ? align_up(t * (size_t)l.ld_x * 4, 256) : 0);
+    l.g = l.x + align_up(rows * (size_t)l.ld_x * 2, 256);
+    l.acc = l.g + align_up(rows * (size_t)l.ld_g * 2, 256);
+    l.part = l.acc + (l.two || l.piece < vocab ? align_up(t * (size_t)l.ld_x * 4, 256) : 0);
     l.w = l.part + part;
     l.end = l.w + (ready ? 0 : packed_bytes(vocab, cols));
     return l;

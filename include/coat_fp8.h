@@ -451,8 +451,9 @@ int coat_linear(const uint16_t* x, int64_t m, int64_t k, int64_t ldx, const uint
  *   dx     bf16, m x k, dw bf16, n x k, dbias n values of dbias_type: out, each may
  *          be NULL, one at least is needed; x may be NULL without dw, w without dx
  * The products take dz rounded to bf16, without the factors scale and 1 / (1 - p),
- * which their sums are multiplied by; dbias adds dz as it was before. m = 0 gives
- * dw and dbias of zeros, n = 0 a dx of zeros.
+ * which their sums are multiplied by; dbias adds dz as it was before. Up to 2048
+ * values of dz are taken as two bf16 terms. m = 0 gives dw and dbias of zeros, n = 0
+ * a dx of zeros.
  *   workspace  as above, at least coat_linear_backward_workspace_bytes(m, n, k,
  *          aligned) bytes; aligned: whether x and w are, as above.
  */
@@ -504,7 +505,8 @@ int coat_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t cols, i
  *          at least is needed. A token that is left out has zeros in dx and no part
  *          in dw, whatever its x holds.
  * The products take g rounded to bf16, without dloss's largest magnitude, which
- * their sums are multiplied by; sums are held in fp32. tokens = 0 gives a dw of zeros.
+ * their sums are multiplied by; sums are held in fp32. Up to 16 tokens, or 2048
+ * logits, have their g taken as two bf16 terms. tokens = 0 gives a dw of zeros.
  *   workspace  as above, coat_linear_cross_entropy_backward_workspace_bytes(tokens,
  *          vocab, cols, aligned).
  */

@@ -112,13 +112,13 @@ def linear(x, w, bias, act, f, scale, residual):
     return y, ey, z, ez
 
 
-def linear_backward(dy, x, w, z, act, f, scale):
-    """{name: (gradient, its error before it is stored)}."""
+def linear_backward(dy, x, w, z, act, f, scale, terms=1):
+    """{name: (gradient, its error before it is stored)}; dz taken as `terms` values in bf16."""
     s = activation_slope(z, act) if act != "none" else torch.ones_like(dy)
     d = dropped(f, dy)
     dz = scale * d * s
     exact = abs(scale) * d.abs() * ((0 if act == "none" else SLOPE) + 6 * U32 * s.abs())
-    edz = exact + half_step(torch.bfloat16) * (dz.abs() + exact)  # as the products take it
+    edz = exact + half_step(torch.bfloat16) ** terms * (dz.abs() + exact)  # as the products take it
     m, n = dy.shape
     out = {}
     g, mag = product(dz, w.t())
@@ -151,8 +151,8 @@ def cross_entropy(x, w, labels, ignore):
     return torch.where(kept, loss, zero), torch.where(kept, lse, zero), e + torch.where(kept, el[rows, at], zero), e
 
 
-def cross_entropy_backward(x, w, labels, dloss, ignore):
-    """{name: (gradient, its error before it is stored)}."""
+def cross_entropy_backward(x, w, labels, dloss, ignore, terms=1):
+    """{name: (gradient, its error before it is stored)}; the logits' taken as `terms` values in bf16."""
     kept = labels != ignore
     at = torch.where(kept, labels, torch.zeros_like(labels))
     x = torch.where(kept[:, None], x, torch.zeros_like(x))
@@ -167,7 +167,7 @@ def cross_entropy_backward(x, w, labels, dloss, ignore):
     # lse as it is stored, and the logits computed again
     exact = weight.abs() * (p * (elog[:, None] + sum_error(mag, x.shape[1]) + U32 * (16 + 3 * (l.abs() + lse[:, None].abs())))
                             + 4 * U32 * hot)
-    eg = exact + half_step(torch.bfloat16) * (g.abs() + exact)
+    eg = exact + half_step(torch.bfloat16) ** terms * (g.abs() + exact)
     out = {}
     d, m = product(g, w.t())
     out["dx"] = d, eg @ w.abs() + sum_error(m, w.shape[0], 128) + 4 * U32 * m

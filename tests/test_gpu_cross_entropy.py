@@ -232,6 +232,18 @@ def test_many_tokens_left_out_here_and_there():
     ref.check("dw", dw, *g["dw"])
 
 
+@pytest.mark.parametrize("size", [(1, 2, 8), (1, 300, 72), (5, 1000, 100), (60, 33, 129), (16, 515, 200), (900, 2, 40)])
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("ignored", [0.0, 0.4])
+def test_few_tokens_are_not_rounded_on_the_way(size, shift, ignored):
+    """Up to 16 tokens or 2048 logits: what the first bf16 term of a logit's gradient leaves counts too."""
+    x, w, labels, dloss = inputs(*size, 21, ignored=ignored)
+    _, _, dx, dw = run(x, w, labels, dloss, shift=shift)
+    grads = ref.cross_entropy_backward(ref.f64(x), ref.f64(w), labels, dloss.double(), IGNORE, terms=2)
+    ref.check("dx", dx, *grads["dx"])
+    ref.check("dw", dw, *grads["dw"])
+
+
 def test_gradients_against_differences():
     x, w, labels, dloss = inputs(30, 60, 24, 15)
     _, _, dx, dw = run(x, w, labels, dloss)

@@ -299,6 +299,43 @@ def test_backward_dropped_places_take_nothing_in():
     assert torch.isfinite(dx).all() and torch.isfinite(dw).all() and torch.isfinite(db).all()
 
 
+@pytest.mark.parametrize("size", [(1, 1, 1), (1, 2048, 72), (3, 40, 17), (32, 64, 200), (250, 8, 40), (2048, 1, 9), (20, 100, 1000)])
+@pytest.mark.parametrize("dy_type,act", [(F32, "none"), (F32, "relu"), (BF16, "gelu"), (F32, "silu")])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_few_values_are_not_rounded_on_the_way(size, dy_type, act, shift):
+    """Up to 2048 values of dz: what the first bf16 term leaves counts, so that only the stored rounding is left."""
+    m, n, k = size
+    x, w, _, _, rng = inputs(m, n, k, 5, F32, False, False)
+    g = gen(6)
+    dy, z = torch.randn(m, n, generator=g).to(dy_type), (2 * torch.randn(m, n, generator=g)).to(BF16)
+    f = ref.factors(m, n, 0.3, rng)
+    want = ref.linear_backward(ref.f64(dy), ref.f64(x), ref.f64(w), ref.f64(z), act, f, 0.7, terms=2)
+    dx, dw = torch.empty(m, k, dtype=BF16, device=DEV), torch.empty(n, k, dtype=BF16, device=DEV)
+    how = dict(act=ref.ACTS[act], z=z.to(DEV) if act != "none" else None, p=0.3, rng=rng.to(DEV), scale=0.7)
+    xs, ws, dys = strided(x, shift=shift), strided(w, shift=shift), strided(dy, shift=shift)
+    coat.linear_backward(dys, xs, ws, dx, dw, **how)
+    ref.check("dx", dx, *want["dx"])
+    ref.check("dw", dw, *want["dw"])
+    one = torch.empty_like(dw)
+    coat.linear_backward(dys, xs, ws, None, one, **how)
+    assert torch.equal(one, dw)
+
+
+def test_infinite_operands_stay_infinite():
+    g = gen(3)
+    for m, n, k in ((6, 24, 16), (6, 24, 15), (70, 72, 16)):
+        dy, x, w = torch.randn(m, n, generator=g), torch.randn(m, k, generator=g).to(BF16), torch.randn(n, k, generator=g).to(BF16)
+        dy[1, 3], dy[2, 3] = 1.0, float("inf")
+        x[0, 1], w[2, 3] = float("inf"), -float("inf")
+        dx, dw = torch.empty(m, k, dtype=BF16, device=DEV), torch.empty(n, k, dtype=BF16, device=DEV)
+        coat.linear_backward(dy.to(DEV), x.to(DEV), w.to(DEV), dx, dw)
+        for got, want in ((dx, dy.double() @ w.double()), (dw, dy.double().t() @ x.double())):
+            got = got.double().cpu()
+            assert torch.equal(torch.isnan(got), torch.isnan(want))
+            assert torch.equal(got[torch.isinf(want)], want[torch.isinf(want)]) and torch.isinf(want).any()
+            assert torch.equal(torch.isinf(got), torch.isinf(want))
+
+
 def test_gradients_against_differences():
     """A step along a direction changes the loss sum(y c) by the gradients' product with it."""
     m, n, k = 40, 56, 32
