@@ -336,7 +336,7 @@ def train_products_bench(args) -> int:
          2 * (2 * t * f + 2 * t * c + 2 * f * c), 2 * g),
         ("dropout onto the residual", lambda: coat.dropout(x, dd, p=0.1, rng=rng, residual=r), 6 * t * c, 0),
         ("linear_cross_entropy", lambda: coat.linear_cross_entropy(h, vocab, labels, loss, lse), 2 * (lt + v) * c, 2 * lt * v * c),
-        ("linear_cross_entropy_backward", lambda: coat.linear_cross_entropy_backward(h, vocab, labels, lse, one, dxl, dv),
+        ("linear_cross_entropy_backward", lambda: coat.linear_cross_entropy_backward(h, vocab, labels, lse, one, dxl, dv, loss=loss),
          4 * (lt + v) * c, 4 * lt * v * c),
     )
     stream = torch.cuda.current_stream()

@@ -107,6 +107,7 @@ def lib() -> ctypes.CDLL:
     L.coat_dropout.argtypes = [P, i64, i64, i64, i32, P, i64, f32, f32, P, i64, P, i64, i32, P]
     L.coat_linear_cross_entropy.argtypes = [P, i64, i64, i64, P, i64, i64, P, i64, P, P, P, size, P]
     L.coat_linear_cross_entropy_backward.argtypes = [P, i64, i64, i64, P, i64, i64, P, i64, P, P, i64, P, i64, P, i64, P, size, P]
+    L.coat_linear_cross_entropy_backward_loss.argtypes = [P, i64, i64, i64, P, i64, i64, P, i64, P, P, P, i64, P, i64, P, i64, P, size, P]
     for name in ("coat_linear", "coat_linear_backward", "coat_linear_cross_entropy", "coat_linear_cross_entropy_backward"):
         getattr(L, name + "_workspace_bytes").argtypes = [i64, i64, i64, i32]
         getattr(L, name + "_workspace_bytes").restype = size
@@ -122,7 +123,7 @@ def lib() -> ctypes.CDLL:
                  "coat_fp8_encode", "coat_fp8_decode", "coat_fp8_act_quantize",
                  "coat_fp8_act_dequantize", "coat_mx4_quantize", "coat_mx4_dequantize", "coat_mx4_matmul",
                  "coat_block_norm", "coat_block_norm_backward", "coat_linear", "coat_linear_backward", "coat_dropout",
-                 "coat_linear_cross_entropy", "coat_linear_cross_entropy_backward"):
+                 "coat_linear_cross_entropy", "coat_linear_cross_entropy_backward", "coat_linear_cross_entropy_backward_loss"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -695,14 +696,16 @@ def linear_cross_entropy_workspace_bytes(tokens: int, vocab: int, cols: int, ali
     return lib().coat_linear_cross_entropy_workspace_bytes(tokens, vocab, cols, aligned)
 
 
-def linear_cross_entropy_backward(x, w, labels, lse, dloss, dx=None, dw=None, *, ignore_index: int = -100, workspace=None,
-                                  stream=None) -> None:
-    """Backward of ``linear_cross_entropy`` from its lse: with g = dloss (softmax(l) - onehot(label)),
+def linear_cross_entropy_backward(x, w, labels, lse, dloss, dx=None, dw=None, *, loss=None, ignore_index: int = -100,
+                                  workspace=None, stream=None) -> None:
+    """Backward of ``linear_cross_entropy`` from its lse and loss: with g = dloss (softmax(l) - onehot(label)),
     dx = g w and dw = g^T x, each where it is given.
 
-    dloss: fp32, (tokens,) or one value for all; dx: (tokens, cols) and dw: (vocab, cols)
-    bf16, one at least. A token that is left out has zeros in dx and no part in dw, whatever
-    its row of x holds. ``workspace``: uint8, at least
+    loss: the forward's, (tokens,) fp32; without it the label's own g is taken from lse
+    alone, off by about 2^-23 |lse| dloss, which is much of it for a token that the model
+    is sure of. dloss: fp32, (tokens,) or one value for all; dx: (tokens, cols) and dw:
+    (vocab, cols) bf16, one at least. A token that is left out has zeros in dx and no part
+    in dw, whatever its row of x holds. ``workspace``: uint8, at least
     ``linear_cross_entropy_backward_workspace_bytes`` long; without one the call takes one
     from torch's allocator."""
     gpu = _gpu_of(x, "x")
@@ -712,14 +715,15 @@ def linear_cross_entropy_backward(x, w, labels, lse, dloss, dx=None, dw=None, *,
         raise ValueError("one of dx and dw at least is needed")
     count = 1 if dloss.numel() == 1 else tokens
     lp = _operand(lse, torch.float32, (tokens,), gpu, "lse")
+    op = None if loss is None else _operand(loss, torch.float32, (tokens,), gpu, "loss")
     dp = _operand(dloss, torch.float32, dloss.shape if count == 1 else (tokens,), gpu, "dloss")
     dxp, lddx = _optional(dx, torch.bfloat16, (tokens, cols), gpu, "dx")
     dwp, lddw = _optional(dw, torch.bfloat16, (vocab, cols), gpu, "dw")
     L = lib()
     nbytes = L.coat_linear_cross_entropy_backward_workspace_bytes(tokens, vocab, cols, aligned)
     ws = _workspace(nbytes, workspace, gpu, stream)
-    _call(gpu, stream, L.coat_linear_cross_entropy_backward, "coat_linear_cross_entropy_backward", *args, _index64(ignore_index), lp, dp,
-          count, dxp, lddx, dwp, lddw, ws.data_ptr() if ws is not None else None, nbytes)
+    _call(gpu, stream, L.coat_linear_cross_entropy_backward_loss, "coat_linear_cross_entropy_backward_loss", *args,
+          _index64(ignore_index), lp, op, dp, count, dxp, lddx, dwp, lddw, ws.data_ptr() if ws is not None else None, nbytes)
 
 
 def linear_cross_entropy_backward_workspace_bytes(tokens: int, vocab: int, cols: int, aligned: bool = True) -> int:

@@ -126,9 +126,10 @@ __global__ __launch_bounds__(kBlock) void xent_join_kernel(const f32x2* __restri
 
 // The backward pass's view of the tokens: those that count in order, each token's place
 // among them (-1: left out), the largest finite magnitude of their losses' weights, and
-// each row's {lse, weight over that, label, 0}. One workgroup.
+// each row's {lse, weight over that, label, expm1(-loss)} (without a loss 1). One workgroup.
 __global__ __launch_bounds__(kRowsBlock) void xent_back_rows_kernel(const int64_t* __restrict__ labels, int64_t tokens, int64_t ignore,
                                                                     int64_t vocab, const float* __restrict__ lse,
+                                                                    const float* __restrict__ loss,
                                                                     const float* __restrict__ dloss, int64_t dloss_count,
                                                                     int32_t* __restrict__ count, int32_t* __restrict__ at,
                                                                     int32_t* __restrict__ place, int32_t* __restrict__ second,
@@ -166,10 +167,11 @@ __global__ __launch_bounds__(kRowsBlock) void xent_back_rows_kernel(const int64_
             }
             const int32_t label = label_in(y[i], vocab);
             const float d = gp(dloss)[dloss_count == 1 ? 0 : t];
+            const float known = loss ? expm1f(-gp(loss)[t]) : 1.0f, own = loss && known > 0.0f ? 0.0f : known;
             gp(place)[t] = j;
             gp(at)[j] = (int32_t)t;
             reinterpret_cast<gf32x4*>(gp(info))[j] =
-                f32x4{gp(lse)[t], label < 0 ? __builtin_nanf("") : d / top, __builtin_bit_cast(float, label), 0.0f};
+                f32x4{gp(lse)[t], label < 0 ? __builtin_nanf("") : d / top, __builtin_bit_cast(float, label), own};
             ++j;
         }
         done += total;
@@ -254,11 +256,12 @@ size_t coat_linear_cross_entropy_backward_workspace_bytes(int64_t tokens, int64_
     return xent_backward_layout(tokens, vocab, cols, aligned != 0).end;
 }
 
-int coat_linear_cross_entropy_backward(const uint16_t* x, int64_t tokens, int64_t cols, int64_t ldx, const uint16_t* w, int64_t vocab,
-                                       int64_t ldw, const int64_t* labels, int64_t ignore_index, const float* lse, const float* dloss,
-                                       int64_t dloss_count, uint16_t* dx, int64_t lddx, uint16_t* dw, int64_t lddw, void* workspace,
-                                       size_t workspace_bytes, coat_stream_t stream) {
+int coat_linear_cross_entropy_backward_loss(const uint16_t* x, int64_t tokens, int64_t cols, int64_t ldx, const uint16_t* w, int64_t vocab,
+                                            int64_t ldw, const int64_t* labels, int64_t ignore_index, const float* lse, const float* loss,
+                                            const float* dloss, int64_t dloss_count, uint16_t* dx, int64_t lddx, uint16_t* dw, int64_t lddw,
+                                            void* workspace, size_t workspace_bytes, coat_stream_t stream) {
     int rc = check_xent_backward(x, tokens, cols, ldx, w, vocab, ldw, labels, lse, dloss, dloss_count, dx, lddx, dw, lddw);
+    if (!rc && !aligned(loss, 4)) rc = COAT_EALIGN;
     if (rc || cols == 0) return rc;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     if (tokens == 0) {
@@ -282,7 +285,7 @@ int coat_linear_cross_entropy_backward(const uint16_t* x, int64_t tokens, int64_
     uint16_t* const g = reinterpret_cast<uint16_t*>(ws + l.g);
     float* const acc = reinterpret_cast<float*>(ws + l.acc);
     float* const sums = reinterpret_cast<float*>(ws + l.part);
-    hipLaunchKernelGGL(xent_back_rows_kernel, dim3(1), dim3(kRowsBlock), 0, st, labels, tokens, ignore_index, vocab, lse, dloss, dloss_count,
+    hipLaunchKernelGGL(xent_back_rows_kernel, dim3(1), dim3(kRowsBlock), 0, st, labels, tokens, ignore_index, vocab, lse, loss, dloss, dloss_count,
                        count, at, place, second, info);
     hipLaunchKernelGGL(xent_pack_kernel, dim3((unsigned)(tokens < 64 * kCUs ? tokens : 64 * kCUs)), dim3(kBlock), 0, st, x, tokens, cols, ldx,
                        place, px, l.ld_x, dx, lddx, two);
@@ -324,6 +327,14 @@ int coat_linear_cross_entropy_backward(const uint16_t* x, int64_t tokens, int64_
         }
     }
     return COAT_OK;
+}
+
+int coat_linear_cross_entropy_backward(const uint16_t* x, int64_t tokens, int64_t cols, int64_t ldx, const uint16_t* w, int64_t vocab,
+                                       int64_t ldw, const int64_t* labels, int64_t ignore_index, const float* lse, const float* dloss,
+                                       int64_t dloss_count, uint16_t* dx, int64_t lddx, uint16_t* dw, int64_t lddw, void* workspace,
+                                       size_t workspace_bytes, coat_stream_t stream) {
+    return coat_linear_cross_entropy_backward_loss(x, tokens, cols, ldx, w, vocab, ldw, labels, ignore_index, lse, nullptr, dloss, dloss_count,
+                                                   dx, lddx, dw, lddw, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

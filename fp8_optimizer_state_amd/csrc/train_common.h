@@ -287,9 +287,12 @@ struct LogSumOut {
     }
 };
 
-// What a row of logits' gradients needs: {lse, weight over the largest weight, label's bits, 0}.
-// The gradient g = weight (exp(l - lse) - [the label]) in bf16; columns past the end up to a
-// whole block are zero. With second terms, what that rounding leaves goes to row i + *count.
+// What a row of logits' gradients needs: {lse, weight over the largest weight, label's bits,
+// own}. The gradient g = weight (exp(l - lse) - [the label]) in bf16; columns past the end up
+// to a whole block are zero. At the label that is -(1 - p) = expm1(-loss), `own`, which keeps
+// its digits where exp(l - lse) - 1 cancels (lse's rounding alone moves it by 2^-24 |lse|, of a
+// loss of 1e-5 at a logit of 60 a seventh). A positive own: the loss is not known, and the
+// difference is taken. With second terms, what the rounding to bf16 leaves goes to row i + *count.
 template <bool TWO>
 struct GradOut {
     static constexpr bool kLogSum = false;
@@ -308,10 +311,11 @@ struct GradOut {
     __device__ __forceinline__ void operator()(int64_t row, int64_t col, float (&v)[8], int64_t n, const Column&, const Row& r) const {
         const float label = r[2];  // a bit cast of an element of a vector would take its first
         const int64_t hit = (int64_t)__builtin_bit_cast(int32_t, label) - col0 - col;
+        const float own = r[3] > 0.0f ? -1.0f : r[3], times = r[3] > 0.0f ? 1.0f : 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float p = exp_fast(v[i] - r[0]);
-            v[i] = i < n ? r[1] * (i == hit ? p - 1.0f : p) : 0.0f;
+            v[i] = i < n ? r[1] * (i == hit ? fmaf(p, times, own) : p) : 0.0f;
         }
         store8<true>(g + row * ldg + col, 8, v);
         if constexpr (TWO) {

@@ -496,9 +496,13 @@ int coat_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t cols, i
                               coat_stream_t stream);
 
 /*
- * Its backward pass, from the forward's lse:
+ * Its backward pass, from the forward's lse and loss:
  *   g = dloss (softmax(l) - onehot(label)),  dx = g w,  dw = g^T x,
  * the logits computed again in pieces of the vocabulary.
+ *   loss   the forward's, tokens fp32; the label's own g is dloss expm1(-loss), good to
+ *          the digits that loss has. May be NULL, as in the form without it: that g is
+ *          then dloss (exp(l_label - lse) - 1), off by about 2^-23 |lse| dloss, which is
+ *          much of it for a token that the model is sure of.
  *   dloss  fp32, the gradient of each token's loss (dloss_count = tokens), or one
  *          value for all of them (dloss_count = 1)
  *   dx     bf16, tokens x cols, dw bf16, vocab x cols: out, each may be NULL, one
@@ -511,6 +515,12 @@ int coat_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t cols, i
  *          vocab, cols, aligned).
  */
 size_t coat_linear_cross_entropy_backward_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols, int32_t aligned);
+int coat_linear_cross_entropy_backward_loss(const uint16_t* x, int64_t tokens, int64_t cols, int64_t ldx, const uint16_t* w,
+                                            int64_t vocab, int64_t ldw, const int64_t* labels, int64_t ignore_index,
+                                            const float* lse, const float* loss, const float* dloss,
+                                            int64_t dloss_count, uint16_t* dx, int64_t lddx, uint16_t* dw,
+                                            int64_t lddw, void* workspace, size_t workspace_bytes,
+                                            coat_stream_t stream);
 int coat_linear_cross_entropy_backward(const uint16_t* x, int64_t tokens, int64_t cols, int64_t ldx, const uint16_t* w,
                                        int64_t vocab, int64_t ldw, const int64_t* labels, int64_t ignore_index,
                                        const float* lse, const float* dloss, int64_t dloss_count, uint16_t* dx,

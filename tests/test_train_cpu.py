@@ -111,6 +111,17 @@ def test_cross_entropy_backward_arguments():
     assert need > 0 and call(ws=None) == call(nb=need - 1) == EINVAL
 
 
+def test_cross_entropy_backward_from_the_loss():
+    f = coat.lib().coat_linear_cross_entropy_backward_loss
+
+    def call(x=FAKE, t=4, lse=FAKE, loss=FAKE, dl=FAKE, ws=FAKE, nb=BIG_WS):
+        return f(x, t, 16, 16, FAKE, 8, 16, FAKE, -100, lse, loss, dl, t, FAKE, 16, FAKE, 16, ws, nb, None)
+
+    assert call(loss=FAKE + 2) == EALIGN and call(loss=FAKE + 2, lse=None) == call(loss=FAKE + 2, t=-1) == EINVAL
+    need = coat.linear_cross_entropy_backward_workspace_bytes(4, 8, 16)
+    assert call(nb=need - 1) == call(loss=None, nb=need - 1) == call(ws=None) == EINVAL
+
+
 def test_workspaces():
     L = coat.lib()
     for name in ("coat_linear", "coat_linear_backward", "coat_linear_cross_entropy", "coat_linear_cross_entropy_backward"):
