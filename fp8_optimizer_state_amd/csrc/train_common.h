@@ -58,17 +58,21 @@ constexpr float kLog2e = 1.44269504f;
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_fast(-x)); }
 
-// Phi(z), the normal distribution function, and e = exp(-z^2 / 2), by Hastings'
-// rational approximation of the error function (Abramowitz and Stegun 7.1.26, off
-// by at most 1.5e-7): Phi(-|z|) = e (a1 t + .. + a5 t^5) / 2, t = 1 / (1 + 0.3275911 |z| / sqrt 2).
+// Phi(z), the normal distribution function, and e = exp(-z^2 / 2). Phi(-|z|) / e falls from 1/2
+// like 1 / |z|: it is t P(t) with t = 1 / (1 + 0.3 |z|) and a P of degree 7, whose largest
+// relative error up to |z| = 14, where e ends, was made least (1.5e-7; 4e-7 as computed here).
+// e itself is off by up to 1.5 z^2 half steps of itself, from its argument's rounding.
 __device__ __forceinline__ float normal_cdf(float z, float& e) {
     const float a = fabsf(z);
     e = __builtin_amdgcn_exp2f(-0.5f * kLog2e * a * a);
-    const float t = __builtin_amdgcn_rcpf(fmaf(0.231641888f, a, 1.0f));
-    float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
-    q = fmaf(q, t, 0.5f * 1.421413741f);
-    q = fmaf(q, t, 0.5f * -0.284496736f);
-    q = fmaf(q, t, 0.5f * 0.254829592f);
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3f, a, 1.0f));
+    float q = fmaf(t, 0.0356748769f, -0.157203499f);
+    q = fmaf(q, t, 0.206354196f);
+    q = fmaf(q, t, -0.0536842455f);
+    q = fmaf(q, t, 0.128561924f);
+    q = fmaf(q, t, 0.0999134088f);
+    q = fmaf(q, t, 0.120753968f);
+    q = fmaf(q, t, 0.119629298f);
     q = q * t * e;
     return z < 0.0f ? q : 1.0f - q;
 }
