@@ -8,9 +8,10 @@ namespace {
 // y = residual + scale D(x). Bound by HBM: 16384 x 5120 in bf16 with a residual takes 90 us
 // (5.6 TB/s), 8191 x 2731 from fp32 25 us. A thread takes blocks of 8 columns of a row,
 // whose random bits are one call of the generator: 16 bits an element, since 32 would make
-// the generator's 20 wide products twice the work and p needs no finer steps.
+// the generator's 20 wide products twice the work and p needs no finer steps. y may be x or
+// residual: each thread has read its 8 columns before it writes them.
 template <class X, class T, bool DROP>
-__global__ __launch_bounds__(kBlock) void dropout_kernel(const X* __restrict__ x, int64_t ldx, const T* residual, int64_t ldr,
+__global__ __launch_bounds__(kBlock) void dropout_kernel(const X* x, int64_t ldx, const T* residual, int64_t ldr,
                                                          float scale, Drop drop, T* y, int64_t ldy, int64_t rows, int64_t cols) {
     drop.begin();
     const int64_t blocks = (cols + 7) / 8, total = rows * blocks;
