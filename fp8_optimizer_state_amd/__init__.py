@@ -703,8 +703,9 @@ def linear_cross_entropy_backward(x, w, labels, lse, dloss, dx=None, dw=None, *,
 
     loss: the forward's, (tokens,) fp32; without it the label's own g is taken from lse
     alone, off by about 2^-23 |lse| dloss, which is much of it for a token that the model
-    is sure of. dloss: fp32, (tokens,) or one value for all; dx: (tokens, cols) and dw:
-    (vocab, cols) bf16, one at least. A token that is left out has zeros in dx and no part
+    is sure of. dloss: fp32, (tokens,) or one value for all; under 2^-100 of the largest it
+    loses digits, under 2^-126 it may count as zero. dx: (tokens, cols) and dw: (vocab, cols)
+    bf16, one at least. A token that is left out has zeros in dx and no part
     in dw, whatever its row of x holds. ``workspace``: uint8, at least
     ``linear_cross_entropy_backward_workspace_bytes`` long; without one the call takes one
     from torch's allocator."""

@@ -508,9 +508,11 @@ int coat_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t cols, i
  *   dx     bf16, tokens x cols, dw bf16, vocab x cols: out, each may be NULL, one
  *          at least is needed. A token that is left out has zeros in dx and no part
  *          in dw, whatever its x holds.
- * The products take g rounded to bf16, without dloss's largest magnitude, which
- * their sums are multiplied by; sums are held in fp32. Up to 16 tokens, or 2048
- * logits, have their g taken as two bf16 terms. tokens = 0 gives a dw of zeros.
+ * The products take g rounded to bf16, without dloss's largest finite magnitude
+ * among the tokens that count, which their sums are multiplied by; sums are held in
+ * fp32. A dloss under 2^-100 of that magnitude loses digits of its g, and one under
+ * 2^-126 of it may count as zero, also in its own row of dx. Up to 16 tokens, or
+ * 2048 logits, have their g taken as two bf16 terms. tokens = 0 gives a dw of zeros.
  *   workspace  as above, coat_linear_cross_entropy_backward_workspace_bytes(tokens,
  *          vocab, cols, aligned).
  */

@@ -258,3 +258,29 @@ def test_gradients_against_differences():
         size = float((grad.double().cpu() * d).norm())
         # the gradient and g are each rounded to bf16: two half steps of each term, independent of each other
         assert abs(float((grad.double().cpu() * d).sum()) - want) <= 40 * 2.0 ** -8 * size
+
+
+@pytest.mark.parametrize("tokens,terms", [(12, 2), (40, 1), (40, 2)])
+def test_weights_far_apart(tokens, terms):
+    """The largest weight on a token that counts, the others at 2^-100 of it (all digits kept), and so small that
+    their ratio is no fp32 number (taken as zero, as documented)."""
+    vocab = 50 if terms == 2 else 60
+    x, w, labels, _ = inputs(tokens, vocab, 24, 17, ignored=0.0)
+    top = 2.0 ** 40
+    weights = torch.full((tokens,), top * 2.0 ** -100)
+    weights[1] = -top
+    _, _, dx, dw = run(x, w, labels, weights)
+    X, W = ref.f64(x), ref.f64(w)
+    grads = ref.cross_entropy_backward(X, W, labels, weights.double(), IGNORE, terms=terms)
+    least = top * 2.0 ** -126  # what is under fp32's normal numbers before the factor
+    ref.check("dx", dx, grads["dx"][0], grads["dx"][1] + least * W.abs().sum(0))
+    ref.check("dw", dw, grads["dw"][0], grads["dw"][1] + least * X.abs().sum(0))
+    weights = torch.full((tokens,), 1e-30)
+    weights[1] = 3e30
+    _, _, dx, dw = run(x, w, labels, weights)
+    grads = ref.cross_entropy_backward(X, W, labels, weights.double(), IGNORE, terms=terms)
+    ref.check("dx", dx[1:2], grads["dx"][0][1:2], grads["dx"][1][1:2])
+    ref.check("dw", dw, *grads["dw"])
+    want, error = (t[torch.arange(tokens) != 1] for t in grads["dx"])
+    got = dx.double().cpu()[torch.arange(tokens) != 1]
+    assert ((got - want).abs() <= want.abs() + error).all()  # the value or as little as zero
