@@ -633,8 +633,10 @@ def dropout(x, y, *, p: float, rng=None, offset: int = 0, residual=None, scale: 
     x, y: matrices of one shape, bf16 or fp32 each; residual: like y; y may be x or
     residual itself. The mask is never stored: it follows from rng (two int64 on the
     GPU: seed, step; needed if p > 0), offset and an element's row and column, so that
-    ``dropout_backward`` and the dropout within ``linear`` find it again. p is rounded
-    to a multiple of 2^-16."""
+    ``dropout_backward`` and the dropout within ``linear`` find it again. Uses of one
+    (seed, step) take different offsets, 0 .. n - 1; a training step then advances step by
+    n (``rng[1] += n``) and leaves the seed, which tells ranks apart. p is rounded to a
+    multiple of 2^-16."""
     gpu = _gpu_of(x, "x")
     shape = x.shape
     xt, yt = _float_type(x, "x"), _float_type(y, "y")
