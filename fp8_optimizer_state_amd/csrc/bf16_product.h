@@ -695,7 +695,9 @@ inline int launch_pack(const Pack& first, const Pack& second, int64_t cols, hipS
 template <bool TALL_A, bool TALL_B, class Out>
 int launch_product(const Product16& p, const Plan16& plan, float* ws, const Out& out, hipStream_t st) {
     if (p.m == 0 || p.n == 0) return COAT_OK;
-    if (plan.way == Way16::kTile256) return launch_tiles<Tile256, TALL_A, TALL_B>(p, plan, ws, out, st);
+    if constexpr (Out::kLarge) {
+        if (plan.way == Way16::kTile256) return launch_tiles<Tile256, TALL_A, TALL_B>(p, plan, ws, out, st);
+    }
     if (plan.way == Way16::kTile128) return launch_tiles<Tile128, TALL_A, TALL_B>(p, plan, ws, out, st);
     if constexpr (!TALL_A && !TALL_B) {
         if (plan.way == Way16::kFew) return launch_few(p, out, st);

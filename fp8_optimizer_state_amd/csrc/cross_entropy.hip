@@ -181,7 +181,8 @@ __global__ __launch_bounds__(kRowsBlock) void xent_back_rows_kernel(const int64_
         reinterpret_cast<gfloat*>(gp(count))[1] = top;
         gp(count)[2] = 2 * done;  // rows with second terms
     }
-    for (int64_t t = threadIdx.x; t < done; t += kRowsBlock) gp(second)[t] = (int32_t)(done + t);
+    if (second)
+        for (int64_t t = threadIdx.x; t < done; t += kRowsBlock) gp(second)[t] = (int32_t)(done + t);
 }
 
 // The rows of x that count, packed, with zeros up to ld (and once more behind them, for second
@@ -278,7 +279,7 @@ int coat_linear_cross_entropy_backward_loss(const uint16_t* x, int64_t tokens, i
     const float* const top = reinterpret_cast<const float*>(ws + l.count) + 1;
     int32_t* const at = reinterpret_cast<int32_t*>(ws + l.at);
     int32_t* const place = reinterpret_cast<int32_t*>(ws + l.place);
-    int32_t* const second = reinterpret_cast<int32_t*>(ws + l.second);
+    int32_t* const second = l.two ? reinterpret_cast<int32_t*>(ws + l.second) : nullptr;
     const int32_t* const two = l.two ? count : nullptr;
     f32x4* const info = reinterpret_cast<f32x4*>(ws + l.info);
     uint16_t* const px = reinterpret_cast<uint16_t*>(ws + l.x);

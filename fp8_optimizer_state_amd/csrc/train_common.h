@@ -157,12 +157,13 @@ __device__ __forceinline__ void store8_past(bool, float* p, int64_t n, const flo
 // What becomes of a product's sums. A kernel hands over 8 consecutive columns of a
 // row at a time, the first a multiple of 8; n of them exist (n may be over 8). What it
 // needs from memory for 8 columns (Column) and for them in one row (Row) is loaded apart
-// from that, so that the loads of several rows are under way together.
+// from that, so that the loads of several rows are under way together. kLarge: its products may be
+// made in tiles of 256 x 256.
 
 // y = residual + scale D(act(sum + bias)), z = sum + bias.
 template <class T>
 struct LinearOut {
-    static constexpr bool kLogSum = false;
+    static constexpr bool kLogSum = false, kLarge = true;
     const void* bias;
     const T* residual;
     uint16_t* z;
@@ -214,7 +215,7 @@ struct LinearOut {
 
 // y = scale sum in bf16.
 struct ScaledOut {
-    static constexpr bool kLogSum = false;
+    static constexpr bool kLogSum = false, kLarge = true;
     const float* scale_at;  // in device memory, or
     float scale;
     uint16_t* y;
@@ -240,7 +241,7 @@ struct ScaledOut {
 // and in GradOut, it made the gradients of 8192 x 32000 x 5120 take 6370 us instead of 5830.
 template <bool TWO>
 struct PiecesOut {
-    static constexpr bool kLogSum = false;
+    static constexpr bool kLogSum = false, kLarge = !TWO;
     const float* scale_at;  // in device memory; with second terms may be NULL: scale
     const int32_t* rows;    // with second terms may be NULL: row i
     uint16_t* y;            // NULL: not the last piece
@@ -278,7 +279,7 @@ struct PiecesOut {
 // the sum of exp(l - m), the label's own logit left out and kept apart (so that the
 // loss of a token that the model is sure of keeps its digits).
 struct LogSumOut {
-    static constexpr bool kLogSum = true;
+    static constexpr bool kLogSum = true, kLarge = true;
     const int32_t* label;
     float* zt;
     f32x2* part;   // [part][row]
@@ -299,7 +300,7 @@ struct LogSumOut {
 // difference is taken. With second terms, what the rounding to bf16 leaves goes to row i + *count.
 template <bool TWO>
 struct GradOut {
-    static constexpr bool kLogSum = false;
+    static constexpr bool kLogSum = false, kLarge = !TWO;
     const f32x4* info;
     uint16_t* g;
     int64_t ldg, col0;     // first column of the piece in the vocabulary

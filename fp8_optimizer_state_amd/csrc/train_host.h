@@ -122,8 +122,9 @@ inline double tile256x_time(int64_t tiles, int64_t steps) {
 }
 
 // can_split: the sums of a part of k may leave on their own. tall_a, tall_b: an operand
-// whose rows in memory are those of k.
-inline Plan16 plan16_of(int64_t m, int64_t n, int64_t k, bool can_split, bool tall_a, bool tall_b) {
+// whose rows in memory are those of k. large: whether tiles of 256 x 256 may be taken (products
+// of second terms have no code for them: their few rows or columns never pay for one).
+inline Plan16 plan16_of(int64_t m, int64_t n, int64_t k, bool can_split, bool tall_a, bool tall_b, bool large = true) {
     Plan16 p{Way16::kPlain, 0, 0, 1, 0, 0, 0};
     if (m < 1 || n < 1 || k < 1 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return p;
     if ((tall_a ? m : k) >= kMaxLd || (tall_b ? n : k) >= kMaxLd) return p;
@@ -138,7 +139,7 @@ inline Plan16 plan16_of(int64_t m, int64_t n, int64_t k, bool can_split, bool ta
         return p;
     }
     if (div_up(m, 128) * div_up(n, 128) > 0x3FFFFFFF) return p;
-    const int64_t steps = div_up(k, 64), large = div_up(m, 256) * div_up(n, 256), tiles = div_up(m, 128) * div_up(n, 128);
+    const int64_t steps = div_up(k, 64), tiles256 = div_up(m, 256) * div_up(n, 256), tiles = div_up(m, 128) * div_up(n, 128);
     p.ld = div_up(n, 64) * 64;
     p.stride = m * p.ld;
     int64_t best = 1;
@@ -151,7 +152,7 @@ inline Plan16 plan16_of(int64_t m, int64_t n, int64_t k, bool can_split, bool ta
     p.way = Way16::kTile128;
     p.tiles_m = (uint32_t)div_up(m, 128);
     p.tiles_n = (uint32_t)div_up(n, 128);
-    if (tile256x_time(large, steps) < tile128x_time(tiles, m, p.ld, steps, best)) {
+    if (large && tile256x_time(tiles256, steps) < tile128x_time(tiles, m, p.ld, steps, best)) {
         p.way = Way16::kTile256;
         p.tiles_m = (uint32_t)div_up(m, 256);
         p.tiles_n = (uint32_t)div_up(n, 256);
@@ -216,7 +217,7 @@ struct LinearBackwardLayout {
 inline LinearBackwardLayout linear_backward_layout(int64_t m, int64_t n, int64_t k, bool ready) {
     LinearBackwardLayout l;
     const bool two = dz_takes_two_terms(m, n);
-    l.plan_dx = plan16_of(m, k, n, true, false, true);
+    l.plan_dx = plan16_of(m, k, n, true, false, true, !two);
     l.plan_dw = plan16_of(n, k, m, true, true, true);
     l.plan_dw_two = plan16_of(n, k, 2 * m, true, true, true);
     size_t part = plan16_bytes(l.plan_dx);
@@ -299,7 +300,7 @@ inline int64_t xent_piece(int64_t tokens, int64_t vocab) {
 
 // Workspace of the backward pass: number of tokens that count, the largest weight of a
 // loss and twice that number, the tokens' places in the packed rows and back, the rows of
-// their second terms, what a row of logits needs, the packed rows of x and a piece's
+// their second terms if they have any, what a row of logits needs, the packed rows of x and a piece's
 // gradients (each twice with second terms), the sums of dx over pieces and terms, the
 // partial sums of products and a copy of w.
 struct XentBackwardLayout {
@@ -312,7 +313,7 @@ struct XentPiece {
     Plan16 logits, dx, dw;
 };
 inline XentPiece xent_piece_plans(int64_t tokens, int64_t width, int64_t cols, bool two) {
-    return XentPiece{plan16_of(tokens, width, cols, true, false, false), plan16_of(tokens, cols, width, true, false, true),
+    return XentPiece{plan16_of(tokens, width, cols, true, false, false, !two), plan16_of(tokens, cols, width, true, false, true, !two),
                      plan16_of(width, cols, two ? 2 * tokens : tokens, true, true, true)};
 }
 inline XentBackwardLayout xent_backward_layout(int64_t tokens, int64_t vocab, int64_t cols, bool ready) {
@@ -333,7 +334,7 @@ inline XentBackwardLayout xent_backward_layout(int64_t tokens, int64_t vocab, in
     l.at = 256;
     l.place = l.at + align_up(t * 4, 256);
     l.second = l.place + align_up(t * 4, 256);
-    l.info = l.second + align_up(t * 4, 256);
+    l.info = l.second + (l.two ? align_up(t * 4, 256) : 0);
     l.x = l.info + align_up(t * 16, 256);
     l.g = l.x + align_up(rows * (size_t)l.ld_x * 2, 256);
     l.acc = l.g + align_up(rows * (size_t)l.ld_g * 2, 256);

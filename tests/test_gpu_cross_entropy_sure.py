@@ -81,7 +81,7 @@ def test_a_sure_token_keeps_its_gradients_digits():
         others = (vocab - 1) * torch.exp(-z)
         g = -others / (1 + others) * d
         # the loss is good to (64 * 2 + 32) steps; two bf16 terms, one rounding to bf16 stored
-        near = (64 * 2 + 64) * ref.U32 + 2.0 ** -18 + 2.0 ** -9
+        near = (64 * 2 + 64) * ref.U32 + ref.half_step(BF16) ** 2 + ref.half_step(BF16)
         assert ((dx[:, 0].cpu().double() - g).abs() <= near * g.abs()).all()
         assert abs(float(dw[3, 0]) - float((g * z).sum())) <= near * float((g * z).sum().abs())
         other = float((torch.exp(-z) / (1 + others) * d * z).sum())

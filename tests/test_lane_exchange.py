@@ -11,8 +11,13 @@ from fp8_optimizer_state_amd import _build
 from test_matrix_code import HIPCC
 
 
+CODE = {}  # of a source, compiled once
+
+
 def device_code(name, tmp_path):
     """Assembly of a source, its comments kept."""
+    if name in CODE:
+        return CODE[name]
     if shutil.which(HIPCC) is None:
         pytest.skip("needs hipcc")
     out = os.path.join(tmp_path, "device.s")
@@ -20,7 +25,8 @@ def device_code(name, tmp_path):
     done = subprocess.run([HIPCC, *flags, "-I" + _build.INCLUDE, "--offload-device-only", "-S", "-o", out, os.path.join(_build.CSRC, name)],
                           capture_output=True, text=True)
     assert done.returncode == 0, done.stderr[-2000:]
-    return open(out).read()
+    CODE[name] = open(out).read()
+    return CODE[name]
 
 
 def kernels(text, name):
