@@ -284,3 +284,31 @@ def test_weights_far_apart(tokens, terms):
     want, error = (t[torch.arange(tokens) != 1] for t in grads["dx"])
     got = dx.double().cpu()[torch.arange(tokens) != 1]
     assert ((got - want).abs() <= want.abs() + error).all()  # the value or as little as zero
+
+
+@pytest.mark.parametrize("tokens,ignored", [(3, 0.0), (16, 0.4)])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_few_tokens_over_several_pieces(tokens, ignored, shift):
+    """Second terms over a vocabulary of more than one piece (2^21 entries): their sums of dx lie in the workspace
+    from piece to piece."""
+    vocab, cols = (1 << 21) + 300, 8
+    x, w, labels, dloss = inputs(tokens, vocab, cols, 22, ignored=ignored)
+    labels[0] = vocab - 1
+    if tokens > 3:
+        labels[1], labels[2] = 0, (1 << 20) + 200
+    loss, lse, dx, dw = run(x, w, labels, dloss, shift=shift)
+    X, W = ref.f64(x), ref.f64(w)
+    kept = labels != IGNORE
+    at = labels.clamp(min=0)
+    l = X @ W.t()
+    want = torch.logsumexp(l, 1)
+    # sums of 2^17 partial sums a thread at most, joined in a tree: the mean of squares, not the worst case
+    assert float(((lse.cpu().double() - want) * kept).abs().max()) < 1e-5
+    g = torch.exp(l - want[:, None])
+    g[torch.arange(tokens), at] -= 1
+    g = g * (dloss.double() * kept)[:, None]
+    for out, exact in ((dx, g @ W), (dw, g.t() @ X)):
+        off = (out.double().cpu() - exact).norm(dim=1)
+        # the rounding that stores it: half a step of each element at most
+        assert bool((off <= 1.1 * ref.half_step(BF16) * exact.norm(dim=1) + 1e-30).all())
+    assert (dx.cpu()[~kept] == 0).all()
