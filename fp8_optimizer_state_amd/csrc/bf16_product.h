@@ -146,13 +146,6 @@ __device__ __forceinline__ void load_to_lds16(uint32_t lds, uint32_t off, const 
     asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base), "n"(AT)
                  : "memory", "scc");
 }
-// Between what lanes of a wavefront write to LDS and what others of it read, either way round:
-// LDS keeps a wavefront's order, and this has the compiler keep it too. No instruction.
-__device__ __forceinline__ void exchange_between_lanes() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
 // f(0), f(1), ... f(N - 1) with the index known to the compiler.
 template <int N, int I = 0, class F>
 __device__ __forceinline__ void each(F&& f) {

@@ -25,6 +25,14 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
+// Between what lanes of a wavefront write to LDS and what others of it read, either way round:
+// LDS keeps a wavefront's order, and this has the compiler keep it too. No instruction.
+__device__ __forceinline__ void exchange_between_lanes() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // 8 stored elements, as they come from memory.
 template <class E>
 struct Raw8;

@@ -429,6 +429,7 @@ __global__ __launch_bounds__(WN* WM* kWave) __attribute__((amdgpu_waves_per_eu(W
                         put(2 * b + half, u32x4{w0[0], w1[0], w0[1], w1[1]});
                     }
                 }
+                exchange_between_lanes();
                 const int lr = lane / kChunks, lc = lane % kChunks;
                 const int64_t row0 = cm0 + wm + j * 32, col0 = cn0 + wn + pc * kBlocks * 16;
                 auto store_rows = [&](auto past) {
@@ -459,6 +460,7 @@ __global__ __launch_bounds__(WN* WM* kWave) __attribute__((amdgpu_waves_per_eu(W
                         }
                     }
                 }
+                exchange_between_lanes();  // the next piece's take the place of these
             }
         }
         if (!whole) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");

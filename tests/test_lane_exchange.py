@@ -72,3 +72,12 @@ def test_tiles_leave_through_lds_in_order(name, tmp_path):
             assert orders >= 1, kernel
             seen += 1
     assert seen >= 4
+
+
+def test_the_4_bit_products_tiles_too(tmp_path):
+    seen = 0
+    for kernel, lines in kernels(device_code("mx4_matmul.hip", tmp_path), "mx4_matmul_tile_kernel"):
+        bad, orders = unordered(lines)
+        assert not bad and orders >= 2, (kernel, bad[:3])
+        seen += 1
+    assert seen >= 3
