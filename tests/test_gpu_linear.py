@@ -321,6 +321,20 @@ def test_few_values_are_not_rounded_on_the_way(size, dy_type, act, shift):
     assert torch.equal(one, dw)
 
 
+def test_gradients_of_zero_take_nothing_in():
+    """dz is 0 where dy is, also beside a z that is not finite."""
+    for m, n, k in ((6, 24, 16), (70, 72, 16)):
+        x, w, _, _, _ = inputs(m, n, k, 1, F32, False, False)
+        dy, z = torch.ones(m, n), torch.ones(m, n)
+        dy[1], dy[2, 3], z[1], z[2, 3] = 0.0, -0.0, float("nan"), float("inf")
+        want = ref.linear_backward(ref.f64(dy), ref.f64(x), ref.f64(w), torch.ones(m, n, dtype=torch.float64), "silu",
+                                   torch.ones(m, n, dtype=torch.float64), 1.0)
+        dx, dw, db = torch.ones(m, k, dtype=BF16, device=DEV), torch.ones(n, k, dtype=BF16, device=DEV), torch.ones(n, device=DEV)
+        coat.linear_backward(dy.to(DEV), x.to(DEV), w.to(DEV), dx, dw, db, act=coat.ACT_SILU, z=z.to(BF16).to(DEV))
+        for name, got in (("dx", dx), ("dw", dw), ("dbias", db)):
+            ref.check(name, got, *want[name])
+
+
 def test_infinite_operands_stay_infinite():
     g = gen(3)
     for m, n, k in ((6, 24, 16), (6, 24, 15), (70, 72, 16)):
