@@ -98,8 +98,8 @@ template <class T>
 int launch_linear(const Product16& p, const Plan16& plan, float* ws, const coat_epilogue* e, const void* bias, int32_t bias_type, const void* residual, int64_t ldr,
                   uint16_t* z, int64_t ldz, void* y, int64_t ldy, hipStream_t st) {
     const uint32_t t = drop_threshold(e->p);
-    // Large outputs of whole lines in bf16: 16384 x 13824 x 5120 with z 1870 -> 1784 us. Small
-    // ones stay in the caches for who reads them next.
+    // Large outputs of whole lines in bf16: 16384 x 13824 x 5120 with z 1870 -> 1743..1784 us, by
+    // box. Small ones stay in the caches for who reads them next.
     auto past = [&](const void* to, int64_t ld) { return aligned(to, 128) && ld % 64 == 0 && p.m * p.n >= (int64_t(1) << 25); };
     const LinearOut<T> out{bias, static_cast<const T*>(residual), z, static_cast<T*>(y), ldr, ldz, ldy, div_up(p.n, 8),
                            Drop{e->rng, e->offset, t, 0, 0}, e->scale * drop_factor(t), e->act, bias_type, past(y, ldy), past(z, ldz)};

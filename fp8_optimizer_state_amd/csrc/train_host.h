@@ -195,13 +195,16 @@ inline int64_t bias_band(int64_t m, int64_t n) {
     return band;
 }
 
-// A rounding to bf16 on the way to a gradient averages out over many values, and not over a
-// few, whose gradients would be off by up to 2.6 times what storing them rounds (1 x 8 values;
-// 1.5 to 1.6 at 64 to 1024, 1.4 from 4096 on; a loss of 1 token 1.6, of 16 1.3, of 64 1.1).
-// Where there are few the products take what it leaves as well, a second bf16 term, and
-// are off by 1.0 times: of up to 2048 values, and of the logits of up to 16 tokens, whose labels'
-// own gradients are most of them. It costs launches (the gradients of 16 x 128 values 19 -> 31 us)
-// and reading the weights once more (a loss of 1 x 32000 x 4096 208 -> 260 us).
+// A rounding to bf16 on the way to a gradient and the one that stores it are independent and
+// alike: together they leave the gradients off by sqrt 2 of what storing leaves, in the mean
+// of squares and at any size. Over many values that is what every call sees (1.4 from 4096
+// on); over few it spreads (1 x 8 values up to 2.6 times, 64 to 1024 1.5 to 1.6; a loss of 1
+// token 1.6, of 16 1.3, of 64 1.1). Where there are few the products take what the rounding
+// leaves as well, a second bf16 term, and are off by 1.0 times: of up to 2048 values, and of the
+// logits of up to 16 tokens, whose labels' own gradients are most of them. So the error steps
+// from 1.0 to 1.5 at 2049 values; a limit further up would cost more: launches (the gradients of
+// 16 x 128 values 19 -> 31 us), twice the products over the tokens, and reading the weights once
+// more (a loss of 1 x 32000 x 4096 with its gradients 208 -> 260 us).
 constexpr int64_t kTwoTermValues = 2048, kTwoTermTokens = 16;
 inline bool dz_takes_two_terms(int64_t m, int64_t n) { return m <= kTwoTermValues && n <= kTwoTermValues && m * n <= kTwoTermValues; }
 inline bool xent_takes_two_terms(int64_t tokens, int64_t vocab) { return tokens <= kTwoTermTokens || dz_takes_two_terms(tokens, vocab); }

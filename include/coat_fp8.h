@@ -445,7 +445,7 @@ int coat_linear(const uint16_t* x, int64_t m, int64_t k, int64_t ldx, const uint
  * Its backward pass, with the forward's epilogue and random numbers:
  *   dz = scale D(dy) act'(z),  dx = dz w,  dw = dz^T x,  dbias = sum of dz over the tokens
  * (the gradient of residual is dy). act' is taken at the stored z; that of the
- * first activation is 0 at 0.
+ * first activation is 0 at 0. Where D(dy) is 0 so is dz, whatever z holds.
  *   dy     m x n, bf16 or fp32 (dy_type)
  *   z      the forward's; needed with an activation, may be NULL without
  *   dx     bf16, m x k, dw bf16, n x k, dbias n values of dbias_type: out, each may
@@ -513,6 +513,7 @@ int coat_linear_cross_entropy(const uint16_t* x, int64_t tokens, int64_t cols, i
  * fp32. A dloss under 2^-100 of that magnitude loses digits of its g, and one under
  * 2^-126 of it may count as zero, also in its own row of dx. Up to 16 tokens, or
  * 2048 logits, have their g taken as two bf16 terms. tokens = 0 gives a dw of zeros.
+ * The workspace holds the g of a piece: of up to 2^27 logits, or 2048 columns.
  *   workspace  as above, coat_linear_cross_entropy_backward_workspace_bytes(tokens,
  *          vocab, cols, aligned).
  */
